@@ -1,4 +1,4 @@
-"""ctypes view of the C ABI declared in include/kda.h (argument marshalling only)."""
+"""ctypes view of the C ABI declared in include/kda.h and include/mixer.h (argument marshalling only)."""
 from __future__ import annotations
 
 import ctypes
@@ -93,6 +93,85 @@ class DplrBwdArgs(ctypes.Structure):
     ]
 
 
+# ------------------------------------------------------------ include/mixer.h
+SHORT_CONV_FLAG_SILU = 1
+SSM_FLAG_DELTA_SOFTPLUS = 1
+
+_I, _L, _U, _F, _Z, _P = (ctypes.c_int, ctypes.c_longlong, ctypes.c_uint, ctypes.c_float, ctypes.c_size_t,
+                          ctypes.c_void_p)
+
+
+class LayerNormFwdArgs(ctypes.Structure):
+    _fields_ = [("rows", _L), ("D", _I), ("dtype", _I), ("w_dtype", _I), ("eps", _F), ("x", _P), ("ld_x", _L),
+                ("weight", _P), ("bias", _P), ("y", _P), ("ld_y", _L), ("mean", _P), ("rstd", _P)]
+
+
+class LayerNormBwdArgs(ctypes.Structure):
+    _fields_ = [("rows", _L), ("D", _I), ("dtype", _I), ("w_dtype", _I), ("dy", _P), ("ld_dy", _L), ("x", _P),
+                ("ld_x", _L), ("weight", _P), ("mean", _P), ("rstd", _P), ("dx", _P), ("ld_dx", _L), ("dweight", _P),
+                ("dbias", _P), ("workspace", _P), ("workspace_bytes", _Z)]
+
+
+class ShortConvFwdArgs(ctypes.Structure):
+    _fields_ = [("B", _I), ("T", _I), ("D", _I), ("W", _I), ("dtype", _I), ("w_dtype", _I), ("flags", _U), ("x", _P),
+                ("ld_x", _L), ("weight", _P), ("bias", _P), ("h0", _P), ("y", _P), ("ld_y", _L), ("ht", _P),
+                ("cu_seqlens", _P)]
+
+
+class ShortConvBwdArgs(ctypes.Structure):
+    _fields_ = [("B", _I), ("T", _I), ("D", _I), ("W", _I), ("dtype", _I), ("w_dtype", _I), ("flags", _U), ("x", _P),
+                ("ld_x", _L), ("weight", _P), ("bias", _P), ("h0", _P), ("dy", _P), ("ld_dy", _L), ("dht", _P),
+                ("dx", _P), ("ld_dx", _L), ("dh0", _P), ("dweight", _P), ("dbias", _P), ("workspace", _P),
+                ("workspace_bytes", _Z), ("cu_seqlens", _P)]
+
+
+class ShortConvStepArgs(ctypes.Structure):
+    _fields_ = [("B", _I), ("D", _I), ("W", _I), ("slots", _I), ("dtype", _I), ("w_dtype", _I), ("flags", _U),
+                ("x", _P), ("ld_x", _L), ("weight", _P), ("bias", _P), ("state", _P), ("slot", _P), ("y", _P),
+                ("ld_y", _L)]
+
+
+class SsmScanFwdArgs(ctypes.Structure):
+    _fields_ = [("B", _I), ("T", _I), ("D", _I), ("N", _I), ("dtype", _I), ("flags", _U), ("x", _P), ("ld_x", _L),
+                ("delta", _P), ("ld_delta", _L), ("Bm", _P), ("ld_B", _L), ("Cm", _P), ("ld_C", _L), ("z", _P),
+                ("ld_z", _L), ("A", _P), ("Dskip", _P), ("delta_bias", _P), ("h0", _P), ("y", _P), ("ld_y", _L),
+                ("ht", _P), ("workspace", _P), ("workspace_bytes", _Z), ("cu_seqlens", _P)]
+
+
+class SsmScanBwdArgs(ctypes.Structure):
+    _fields_ = [("B", _I), ("T", _I), ("D", _I), ("N", _I), ("dtype", _I), ("flags", _U), ("x", _P), ("ld_x", _L),
+                ("delta", _P), ("ld_delta", _L), ("Bm", _P), ("ld_B", _L), ("Cm", _P), ("ld_C", _L), ("z", _P),
+                ("ld_z", _L), ("A", _P), ("Dskip", _P), ("delta_bias", _P), ("h0", _P), ("dy", _P), ("ld_dy", _L),
+                ("dht", _P), ("dx", _P), ("ld_dx", _L), ("ddelta", _P), ("ld_ddelta", _L), ("dBm", _P),
+                ("ld_dB", _L), ("dCm", _P), ("ld_dC", _L), ("dz", _P), ("ld_dz", _L), ("dA", _P), ("dDskip", _P),
+                ("ddelta_bias", _P), ("dh0", _P), ("workspace", _P), ("workspace_bytes", _Z), ("cu_seqlens", _P)]
+
+
+class SsmScanStepArgs(ctypes.Structure):
+    _fields_ = [("B", _I), ("D", _I), ("N", _I), ("slots", _I), ("dtype", _I), ("flags", _U), ("x", _P),
+                ("ld_x", _L), ("delta", _P), ("ld_delta", _L), ("Bm", _P), ("ld_B", _L), ("Cm", _P), ("ld_C", _L),
+                ("z", _P), ("ld_z", _L), ("A", _P), ("Dskip", _P), ("delta_bias", _P), ("state", _P), ("slot", _P),
+                ("y", _P), ("ld_y", _L)]
+
+
+# Every symbol include/mixer.h declares, with its argument block and whether it takes a stream
+# (launches) or answers a size (workspace queries).
+MIXER_EXPORTS = {
+    "layer_norm_fwd": (LayerNormFwdArgs, True),
+    "layer_norm_bwd_workspace": (LayerNormBwdArgs, False),
+    "layer_norm_bwd": (LayerNormBwdArgs, True),
+    "short_conv_fwd": (ShortConvFwdArgs, True),
+    "short_conv_bwd_workspace": (ShortConvBwdArgs, False),
+    "short_conv_bwd": (ShortConvBwdArgs, True),
+    "short_conv_step": (ShortConvStepArgs, True),
+    "ssm_scan_fwd_workspace": (SsmScanFwdArgs, False),
+    "ssm_scan_fwd": (SsmScanFwdArgs, True),
+    "ssm_scan_bwd_workspace": (SsmScanBwdArgs, False),
+    "ssm_scan_bwd": (SsmScanBwdArgs, True),
+    "ssm_scan_step": (SsmScanStepArgs, True),
+}
+
+
 class KdaError(RuntimeError):
     def __init__(self, code: int, what: str):
         super().__init__(f"{what}: {status_string(code)} ({code})")
@@ -136,6 +215,10 @@ def load() -> ctypes.CDLL:
         lib.kda_status_read.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
         lib.kda_status_string.restype = ctypes.c_char_p
         lib.kda_status_string.argtypes = [ctypes.c_int]
+        for name, (args, launches) in MIXER_EXPORTS.items():
+            fn = getattr(lib, name)
+            fn.restype = ctypes.c_int if launches else ctypes.c_size_t
+            fn.argtypes = [ctypes.POINTER(args)] + ([ctypes.c_void_p] if launches else [])
         _lib = lib
     return _lib
 

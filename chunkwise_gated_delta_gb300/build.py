@@ -17,7 +17,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libkda.so")
 
-SOURCES = ["kda_api.cu", "kda_fwd_simt.cu", "kda_fwd_tc.cu", "kda_noalloc.cu", "dplr_fwd_simt.cu", "kda_bwd_simt.cu", "dplr_bwd_simt.cu"]
+SOURCES = ["kda_api.cu", "kda_fwd_simt.cu", "kda_fwd_tc.cu", "kda_noalloc.cu", "dplr_fwd_simt.cu", "kda_bwd_simt.cu", "dplr_bwd_simt.cu",
+           "mixer_api.cu", "mixer_common.cu", "layer_norm.cu", "short_conv.cu", "ssm_scan_fwd.cu", "ssm_scan_bwd.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 
