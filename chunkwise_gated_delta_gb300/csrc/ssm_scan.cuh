@@ -29,6 +29,55 @@ __device__ __forceinline__ float log1p_unit(float u) {
 // softplus(v) = max(v, 0) + log(1 + exp(-|v|)).
 __device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1p_unit(ex2(-kLog2e * fabsf(v))); }
 
+// Two float32 values in one 64-bit register: the packed forms of the FMA pipe do both in one issue
+// slot (the same arithmetic rate, half the instructions, and issue slots are what runs short).
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(f2 v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 ex2_2(f2 v) {
+    float a, b;
+    unpack2(v, a, b);
+    return pack2(ex2(a), ex2(b));
+}
+struct alignas(16) f2x2 {
+    f2 a, b;
+};
+
+// softplus of two values at once.
+__device__ __forceinline__ f2 softplus2(float v, float w) {
+    const f2 u = pack2(ex2(-kLog2e * fabsf(v)), ex2(-kLog2e * fabsf(w)));
+    float lo, hi;
+    unpack2(add2(u, pack2(2.f, 2.f)), lo, hi);
+    const f2 s = mul2(u, pack2(rcp(lo), rcp(hi))), q = mul2(s, s);
+    f2 r = pack2(1.f / 15.f, 1.f / 15.f);
+    r = fma2(r, q, pack2(1.f / 13.f, 1.f / 13.f));
+    r = fma2(r, q, pack2(1.f / 11.f, 1.f / 11.f));
+    r = fma2(r, q, pack2(1.f / 9.f, 1.f / 9.f));
+    r = fma2(r, q, pack2(1.f / 7.f, 1.f / 7.f));
+    r = fma2(r, q, pack2(1.f / 5.f, 1.f / 5.f));
+    r = fma2(r, q, pack2(1.f / 3.f, 1.f / 3.f));
+    return fma2(fma2(mul2(s, q), r, s), pack2(2.f, 2.f), pack2(fmaxf(v, 0.f), fmaxf(w, 0.f)));
+}
+
 // Sums v[k] over the L lanes of a channel; lane i ends with the sums of k = i K / L ... in v[0 ..].
 // K is a multiple of L.
 template <int K, int L> __device__ __forceinline__ void spread_sum(float (&v)[K], int i) {
@@ -45,6 +94,61 @@ template <int K, int L> __device__ __forceinline__ void spread_sum(float (&v)[K]
             }
     }
 }
+
+// Four neighbouring elements as they lie in memory.
+template <class T> struct RawQuad;
+template <> struct RawQuad<float> {
+    using type = float4;
+    static __device__ __forceinline__ float4 floats(float4 v) { return v; }
+};
+template <> struct RawQuad<bf16> {
+    using type = uint2;
+    static __device__ __forceinline__ float4 floats(uint2 v) {
+        return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                           __uint_as_float(v.y & 0xffff0000u));
+    }
+};
+
+// Rows t0 .. t0 + TT - 1 of Bm or Cm in two halves: a thread's groups of four states into registers,
+// as they lie in memory (nothing waits for them there), and a tile later to shared memory.
+// VEC: N = NP and rows aligned to four elements.
+template <class T, int NP, int TT, bool VEC> struct RowFetch {
+    static constexpr int Q = NP / 4, U = (TT * Q + kScanThreads - 1) / kScanThreads;
+    static constexpr bool ALL = TT * Q % kScanThreads == 0;
+    using Raw = typename RawQuad<T>::type;
+    Raw v[VEC ? U : 1];
+    T e[VEC ? 1 : U][4];
+    __device__ __forceinline__ void load(const void *src, long long ld, int N, const Segment &g, int t0) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int u = threadIdx.x + k * kScanThreads, t = u / Q, n = u % Q * 4;
+            const bool in = (ALL || u < TT * Q) && t0 + t < g.len;
+            const T *r = static_cast<const T *>(src) + (g.row0 + g.t0 + t0 + t) * ld + n;
+            if (VEC) {
+                v[k] = Raw{};
+                if (in) v[k] = *reinterpret_cast<const Raw *>(r);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    e[k][q] = from_f<T>(0.f);
+                    if (in && n + q < N) e[k][q] = r[q];
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void store(float (*dst)[NP]) const {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int u = threadIdx.x + k * kScanThreads;
+            if (ALL || u < TT * Q) {
+                float4 o;
+                if (VEC) o = RawQuad<T>::floats(v[k]);
+                else o = make_float4(to_f(e[k][0]), to_f(e[k][1]), to_f(e[k][2]), to_f(e[k][3]));
+                *reinterpret_cast<float4 *>(&dst[u / Q][u % Q * 4]) = o;
+            }
+        }
+    }
+};
 
 // Rows t0 .. t0 + TT - 1 of Bm or Cm into shared memory as float32 [TT][NP], zero behind the
 // segment's end and past N.  One thread per group of four states.
