@@ -17,6 +17,14 @@ template <class T> __device__ __forceinline__ T from_f(float v);
 template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
 template <> __device__ __forceinline__ bf16 from_f<bf16>(float v) { return __float2bfloat16_rn(v); }
 
+// One element as it lies in memory, in a register of its own: pairs of 16-bit values would share
+// one, and the load would be waited for where they are put together.
+__device__ __forceinline__ uint32_t load_bits(const float *p) { return __float_as_uint(*p); }
+__device__ __forceinline__ uint32_t load_bits(const bf16 *p) { return *reinterpret_cast<const unsigned short *>(p); }
+template <class T> __device__ __forceinline__ float bits_f(uint32_t v) {
+    return __uint_as_float(sizeof(T) == 4 ? v : v << 16);
+}
+
 // A parameter vector stored as bfloat16 or float32 (uniform over the launch).
 __device__ __forceinline__ float load_w(const void *p, long long i, bool is_bf16) {
     return is_bf16 ? to_f(static_cast<const bf16 *>(p)[i]) : static_cast<const float *>(p)[i];

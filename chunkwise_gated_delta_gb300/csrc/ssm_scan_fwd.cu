@@ -22,11 +22,12 @@ namespace {
 // Both sides work on double buffers and meet once per tile.  Alone, a carrier warp waits for its
 // own shared-memory loads and exponentials two cycles of three, and one block of 32 channels per
 // 1.7 warps and scheduler is all that B 4, D 2048 has: the feeders fill those slots.
-constexpr int kFwdThreads = 2 * kScanThreads;
-constexpr int KT = 8;                      // tokens of a tile per lane
 
-template <int L> struct FwdTiles {
-    static constexpr int NP = 4 * L, CW = 32 / L, CH = 4 * CW, TT = KT * L, YS = CH + CW;
+// L lanes of NS states per channel; a tile has KT tokens per lane.
+template <int L, int NS, int KT> struct FwdTiles {
+    static constexpr int kFeeders = 16 * KT, kThreads = kScanThreads + kFeeders;   // one feeder per 8 channels of a token
+    static_assert(NS % 4 == 0 && 32 % L == 0, "16-byte shared-memory accesses take four states");
+    static constexpr int NP = NS * L, CW = 32 / L, CH = 4 * CW, TT = KT * L, YS = CH + CW;
     f2x2 d[2][TT * CH];                    // {dt, dt}, {dt x, dt x}; 16-byte words swizzled, see at()
     float B[2][TT][NP], C[2][TT][NP];
     float y[2][TT][YS];                    // row stride: the tokens of a channel's lanes in different banks
@@ -35,45 +36,40 @@ template <int L> struct FwdTiles {
     static __device__ __forceinline__ int at(int s) { return s ^ (s >> 3 & 7); }
 };
 
-__device__ __forceinline__ void meet() { asm volatile("bar.sync 1, %0;" ::"n"(kFwdThreads) : "memory"); }
+template <int N> __device__ __forceinline__ void meet_all() { asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void copy16(void *to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
 
 // Eight neighbouring channels of one token, as they lie in memory (XV: two or one 16-byte accesses).
 template <class T, bool XV> struct Eight {
     static constexpr int W = 8 * sizeof(T) / 16;
     uint4 v[XV ? W : 1];
-    T e[XV ? 1 : 8];
-    __device__ __forceinline__ void load(const T *p, int n) {        // n: channels that exist
+    uint32_t e[XV ? 1 : 8];
+    __device__ __forceinline__ void load(const T *p, int last) {     // element k past `last` repeats it
         if (XV) {
 #pragma unroll
             for (int k = 0; k < W; ++k) v[k] = reinterpret_cast<const uint4 *>(p)[k];
         } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k < n) e[k] = p[k];
+            for (int k = 0; k < 8; ++k) e[k] = load_bits(p + min(k, last));
         }
     }
-    __device__ __forceinline__ void zero() {
-        if (XV) {
-#pragma unroll
-            for (int k = 0; k < W; ++k) v[k] = make_uint4(0, 0, 0, 0);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) e[k] = from_f<T>(0.f);
-        }
-    }
-    __device__ __forceinline__ float get(int k) const {
-        if (!XV) return to_f(e[k]);
-        const uint4 &q = v[k * sizeof(T) / 16];
-        const int w = k * sizeof(T) / 4 % 4;
-        const uint32_t u = w == 0 ? q.x : w == 1 ? q.y : w == 2 ? q.z : q.w;
-        if (sizeof(T) == 4) return __uint_as_float(u);
-        return __uint_as_float(k & 1 ? u & 0xffff0000u : u << 16);
+    // elements k and k + 1, k even
+    __device__ __forceinline__ f2 pair(int k) const {
+        if (!XV) return pack2(bits_f<T>(e[k]), bits_f<T>(e[k + 1]));
+        if (sizeof(T) == 4) return k & 2 ? reinterpret_cast<const f2x2 &>(v[k / 4]).b : reinterpret_cast<const f2x2 &>(v[k / 4]).a;
+        const uint32_t u = k == 0 ? v[0].x : k == 2 ? v[0].y : k == 4 ? v[0].z : v[0].w;
+        return pack2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
     }
 };
 
-template <class T, int L, bool XV>
-__global__ void __launch_bounds__(kFwdThreads) scan_fwd_kernel(ScanParams p, int chan_blocks) {
-    using S = FwdTiles<L>;
+template <class T, int L, int NS, int KT, bool XV>
+__global__ void __launch_bounds__(16 * KT + kScanThreads) scan_fwd_kernel(ScanParams p, int chan_blocks) {
+    using S = FwdTiles<L, NS, KT>;
+    constexpr int kFeeders = S::kFeeders;
+    auto meet = [] { meet_all<S::kThreads>(); };
     constexpr int NP = S::NP, CW = S::CW, CH = S::CH, TT = S::TT;
     extern __shared__ __align__(16) unsigned char raw[];
     S &sm = *reinterpret_cast<S *>(raw);
@@ -90,123 +86,191 @@ __global__ void __launch_bounds__(kFwdThreads) scan_fwd_kernel(ScanParams p, int
         const int t = tid / (CH / 8), c0 = tid % (CH / 8) * 8;       // this thread's token and channels
         const int d = d0 + c0, n = p.D - d;                          // n <= 0: none of them exist
         const bool some = n > 0;
-        const long long r = row0 + t;
-        const T *x = static_cast<const T *>(p.x) + r * p.ld_x + d, *delta = static_cast<const T *>(p.delta) + r * p.ld_delta + d;
-        const T *z = p.z ? static_cast<const T *>(p.z) + r * p.ld_z + d : nullptr;
-        T *y = static_cast<T *>(p.y) + r * p.ld_y + d;
-        float dbias[8], skip[8];
+        // Loads into registers take no branch: tokens past the end repeat the last one and channels past
+        // the end the last ones, and what comes of them is set to 0 or not stored.  (Where two branches
+        // meet, a loaded value is waited for on the spot: 1000 cycles a tile.)
+        const int dl = XV ? min(d, p.D - 8) : min(d, p.D - 1), last = p.D - 1 - dl;
+        const T *x = static_cast<const T *>(p.x) + row0 * p.ld_x + dl, *delta = static_cast<const T *>(p.delta) + row0 * p.ld_delta + dl;
+        const T *z = p.z ? static_cast<const T *>(p.z) + row0 * p.ld_z + dl : nullptr;
+        T *y = static_cast<T *>(p.y) + (row0 + t) * p.ld_y + d;
+        f2 dbias[4], skip[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            dbias[k] = k < n && p.delta_bias ? p.delta_bias[d + k] : 0.f;
-            skip[k] = k < n && p.Dskip ? p.Dskip[d + k] : 0.f;
+        for (int k = 0; k < 4; ++k) {
+            const int e = 2 * k;
+            dbias[k] = pack2(e < n && p.delta_bias ? p.delta_bias[d + e] : 0.f, e + 1 < n && p.delta_bias ? p.delta_bias[d + e + 1] : 0.f);
+            skip[k] = pack2(e < n && p.Dskip ? p.Dskip[d + e] : 0.f, e + 1 < n && p.Dskip ? p.Dskip[d + e + 1] : 0.f);
         }
-        // Bm and Cm of a tile: elements tid, tid + 128, ...
-        constexpr int E = TT * NP < kScanThreads ? 1 : TT * NP / kScanThreads;
-        const int bt = tid / NP, bn = tid % NP;                      // NP divides 128
-        const bool bs = TT * NP >= kScanThreads || bt < TT;          // (L = 1: 32 elements)
-        const T *Bp = static_cast<const T *>(p.Bm) + (row0 + bt) * p.ld_B + bn;
-        const T *Cp = static_cast<const T *>(p.Cm) + (row0 + bt) * p.ld_C + bn;
-        constexpr int BT = kScanThreads / NP;                        // tokens between a thread's elements
-        Eight<T, XV> xn, dn, zn, xc, zc, xo, zo;                     // next, current, last tile
-        T be[E], ce[E];
-        auto fetch = [&](int tile) {
-            const int t0 = tile * TT;
-            xn.zero();
-            dn.zero();
-            zn.zero();
-            if (some && t0 + t < g.len) {
-                xn.load(x + t0 * p.ld_x, n);
-                dn.load(delta + t0 * p.ld_delta, n);
-                if (z) zn.load(z + t0 * p.ld_z, n);
+        // Bm and Cm of a tile: elements tid, tid + 256, ...
+        constexpr int E = TT * NP < kFeeders ? 1 : TT * NP / kFeeders;
+        const int bt = tid / NP, bn = tid % NP;                      // NP divides the feeders
+        const bool bs = TT * NP >= kFeeders || bt < TT;              // (N <= 8: more threads than elements)
+        const int bl = min(bn, p.N - 1);
+        const T *Bp = static_cast<const T *>(p.Bm) + row0 * p.ld_B + bl;
+        const T *Cp = static_cast<const T *>(p.Cm) + row0 * p.ld_C + bl;
+        constexpr int BT = kFeeders / NP;                            // tokens between a thread's elements
+        // x, delta and z on their way.  XV: asynchronous copies of three tiles, each thread its own
+        // eight channels into words of its own, so nobody else waits for them.  Otherwise one tile in registers.
+        using Data = Eight<T, XV>;
+        constexpr int RING = XV ? 3 : 0;
+        uint4 *const ring = reinterpret_cast<uint4 *>(raw + sizeof(S)) + tid;      // [RING][3][W][feeders]
+        Data f[XV ? 1 : 3] = {};
+        Data xc{}, zc{}, xo{}, zo{};                                 // x and z of the current and the last tile
+        uint32_t be[E], ce[E];                                       // the next tile's Bm and Cm
+        const T *const pz = z ? z : x;                               // (no gate: loaded all the same, not used)
+        const long long ldz = z ? p.ld_z : p.ld_x, sy = TT * p.ld_y;
+        int row = t, slot3 = 0;                                      // of the next fetch; its place in the ring
+        auto fetch = [&] {                                           // tile by tile; past the end the last row again
+            const long long r = min(row, g.len - 1);
+            const T *px = x + r * p.ld_x, *pd = delta + r * p.ld_delta, *pg = pz + r * ldz;
+            if (XV) {
+                if (row - t < g.len) {
+                    uint4 *to = ring + slot3 * (3 * Data::W * kFeeders);
+#pragma unroll
+                    for (int k = 0; k < Data::W; ++k) {
+                        copy16(to + k * kFeeders, px + k * (16 / sizeof(T)));
+                        copy16(to + (Data::W + k) * kFeeders, pd + k * (16 / sizeof(T)));
+                        if (z) copy16(to + (2 * Data::W + k) * kFeeders, pg + k * (16 / sizeof(T)));
+                    }
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                slot3 = slot3 == RING - 1 ? 0 : slot3 + 1;
+            } else {
+                f[0].load(px, last);
+                f[XV ? 0 : 1].load(pd, last);
+                f[XV ? 0 : 2].load(pg, last);
             }
+            row += TT;
+        };
+        int rowb = bt;
+        auto fetch_bc = [&] {
 #pragma unroll
             for (int k = 0; k < E; ++k) {
-                be[k] = ce[k] = from_f<T>(0.f);
-                if (bs && bn < p.N && t0 + bt + k * BT < g.len) {
-                    be[k] = Bp[(t0 + k * BT) * p.ld_B];
-                    ce[k] = Cp[(t0 + k * BT) * p.ld_C];
-                }
+                const long long r = min(rowb + k * BT, g.len - 1);
+                be[k] = load_bits(Bp + r * p.ld_B);
+                ce[k] = load_bits(Cp + r * p.ld_C);
             }
+            rowb += TT;
         };
-        auto stage = [&](int tile) {
+        auto stage_bc = [&](int tile) {
             const int b = tile & 1;
-            const bool in = tile * TT + t < g.len;                   // behind the end the state stays as it is
-#pragma unroll
-            for (int k = 0; k < 8; k += 2) {
-                float lo = dn.get(k) + dbias[k], hi = dn.get(k + 1) + dbias[k + 1];
-                if (p.softplus) unpack2(softplus2(lo, hi), lo, hi);
-                lo = in ? lo : 0.f;
-                hi = in ? hi : 0.f;
-                const float ul = lo * xn.get(k), uh = hi * xn.get(k + 1);
-                sm.d[b][S::at(tid * 8 + k)] = {pack2(lo, lo), pack2(ul, ul)};
-                sm.d[b][S::at(tid * 8 + k + 1)] = {pack2(hi, hi), pack2(uh, uh)};
-            }
 #pragma unroll
             for (int k = 0; k < E; ++k) {
                 if (!bs) break;
-                sm.B[b][bt + k * BT][bn] = to_f(be[k]);
-                sm.C[b][bt + k * BT][bn] = to_f(ce[k]);
+                sm.B[b][bt + k * BT][bn] = bn < p.N ? bits_f<T>(be[k]) : 0.f;
+                sm.C[b][bt + k * BT][bn] = bn < p.N ? bits_f<T>(ce[k]) : 0.f;
             }
-            xc = xn;
-            zc = zn;
         };
-        auto finish = [&](int tile) {
-            if (!some || tile * TT + t >= g.len) return;
-            const float *src = &sm.y[tile & 1][t][c0];
-            const float4 a = *reinterpret_cast<const float4 *>(src), b = *reinterpret_cast<const float4 *>(src + 4);
-            float o[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        f2x2 *const sd0 = &sm.d[0][tid * 8], *const sd1 = &sm.d[1][tid * 8];
+        const int sw = tid & 7;                                      // at(tid 8 + k) = tid 8 + (k ^ sw)
+        int from = 0;
+        // Stage one tile and finish another.  The two have nothing to do with each other, and there is no
+        // branch in either, so their long dependent chains (exponential, sum, reciprocal, ...) overlap.
+        auto work = [&](int staged, int finished, bool store) {
+            f2x2 *const sd = staged & 1 ? sd1 : sd0;
+            Data dc{}, xn{}, zn{};
+            if (XV) {
+                asm volatile("cp.async.wait_group 2;" ::: "memory");
+                const uint4 *src = ring + from * (3 * Data::W * kFeeders);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) o[k] = fmaf(skip[k], xo.get(k), o[k]);
-            if (z)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float zv = zo.get(k);
-                    o[k] *= zv * sigmoid(zv);
+                for (int k = 0; k < Data::W; ++k) {
+                    xn.v[k] = src[k * kFeeders];
+                    dc.v[k] = src[(Data::W + k) * kFeeders];
+                    zn.v[k] = src[(2 * Data::W + k) * kFeeders];
                 }
-            T *out = y + (long long)tile * TT * p.ld_y;
+                from = from == RING - 1 ? 0 : from + 1;
+            } else {
+                xn = f[0];
+                dc = f[XV ? 0 : 1];
+                zn = f[XV ? 0 : 2];
+            }
+            const f2x2 *src = reinterpret_cast<const f2x2 *>(&sm.y[finished & 1][t][c0]);
+            const f2x2 ya = src[0], yb = src[1];
+            f2 o[4] = {ya.a, ya.b, yb.a, yb.b};
+            const bool in = staged * TT + t < g.len;                 // behind the end the state stays as it is
+#pragma unroll
+            for (int k = 0; k < 8; k += 2) {
+                const f2 raw_dt = add2(dc.pair(k), dbias[k / 2]);
+                const f2 sp = softplus2(raw_dt);
+                const f2 dt = p.softplus ? sp : raw_dt;
+                o[k / 2] = fma2(skip[k / 2], xo.pair(k), o[k / 2]);
+                const f2 gated = mul2(o[k / 2], silu2(zo.pair(k)));
+                o[k / 2] = z ? gated : o[k / 2];
+                float lo, hi, ul, uh;
+                unpack2(dt, lo, hi);
+                unpack2(mul2(dt, xn.pair(k)), ul, uh);
+                lo = in ? lo : 0.f;
+                hi = in ? hi : 0.f;
+                ul = in ? ul : 0.f;
+                uh = in ? uh : 0.f;
+                sd[k ^ sw] = {both(lo), both(ul)};
+                sd[(k + 1) ^ sw] = {both(hi), both(uh)};
+            }
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) unpack2(o[k], v[2 * k], v[2 * k + 1]);
             if (XV) {
 #pragma unroll
                 for (int k = 0; k < 8; k += 16 / (int)sizeof(T)) {
                     Vec<T, 16 / sizeof(T)> q;
 #pragma unroll
-                    for (int e = 0; e < 16 / (int)sizeof(T); ++e) q.e[e] = from_f<T>(o[k + e]);
-                    store_vec<T, 16 / sizeof(T)>(out + k, q);
+                    for (int e = 0; e < 16 / (int)sizeof(T); ++e) q.e[e] = from_f<T>(v[k + e]);
+                    if (store) store_vec<T, 16 / sizeof(T)>(y + k, q);
                 }
             } else {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    if (k < n) out[k] = from_f<T>(o[k]);
+                    if (store && k < n) y[k] = from_f<T>(v[k]);
             }
+            xo = xc;
+            zo = zc;
+            xc = xn;
+            zc = zn;
         };
         if (tiles > 0) {
-            fetch(0);
-            stage(0);
-            if (tiles > 1) fetch(1);
+            fetch_bc();
+            fetch();
+            if (XV) {
+                fetch();
+                fetch();
+            }
+            stage_bc(0);
+            fetch_bc();
+            work(0, 0, false);
+            fetch();
         }
         for (int tile = 0; tile < tiles; ++tile) {
             meet();                              // tile staged; tile - 1 carried
-            if (tile > 0) finish(tile - 1);
-            xo = xc;
-            zo = zc;
-            if (tile + 1 < tiles) stage(tile + 1);
-            if (tile + 2 < tiles) fetch(tile + 2);
+            stage_bc(tile + 1);                  // (of the last tile's data again past the end: read by nobody)
+            fetch_bc();
+            work(tile + 1, tile - 1, tile > 0 && some && (tile - 1) * TT + t < g.len);
+            fetch();
+            if (tile > 0) y += sy;
         }
         meet();
-        if (tiles > 0) finish(tiles - 1);
+        if (tiles > 0) work(tiles + 1, tiles - 1, some && (tiles - 1) * TT + t < g.len);
         return;
     }
     // ---------------------------------------------------------------------- carriers
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane / L, i = lane % L, n0 = 4 * i;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane / L, i = lane % L, n0 = NS * i;
     const int d = d0 + warp * CW + c;
     const bool live = d < p.D;
-    float a2[4] = {0.f, 0.f, 0.f, 0.f}, h[4] = {0.f, 0.f, 0.f, 0.f};
-    if (live) {
-        load_states(a2, p.A + (long long)d * p.N, n0, p.N);
-        if (p.seg_state) load_states(h, p.seg_state + (slot * p.D + d) * NP, n0, NP);
-        else if (p.h0) load_states(h, p.h0 + ((long long)g.b * p.D + d) * p.N, n0, p.N);
+    constexpr int H = NS / 2;
+    f2 a2[H], h[H];
+    {
+        float av[NS], hv[NS];
+#pragma unroll
+        for (int k = 0; k < NS; ++k) av[k] = hv[k] = 0.f;
+        if (live) {
+            load_states(av, p.A + (long long)d * p.N, n0, p.N);
+            if (p.seg_state) load_states(hv, p.seg_state + (slot * p.D + d) * NP, n0, NP);
+            else if (p.h0) load_states(hv, p.h0 + ((long long)g.b * p.D + d) * p.N, n0, p.N);
+        }
+#pragma unroll
+        for (int k = 0; k < H; ++k) {
+            a2[k] = pack2(av[2 * k] * kLog2e, av[2 * k + 1] * kLog2e);
+            h[k] = pack2(hv[2 * k], hv[2 * k + 1]);
+        }
     }
-    const f2 a01 = pack2(a2[0] * kLog2e, a2[1] * kLog2e), a23 = pack2(a2[2] * kLog2e, a2[3] * kLog2e);
-    f2 h01 = pack2(h[0], h[1]), h23 = pack2(h[2], h[3]);
     // the swizzle's period in tokens: at() sees t CH / 8 modulo 8
     constexpr int P = L <= 2 ? 1 : L / 2;
     int off[P];
@@ -216,33 +280,65 @@ __global__ void __launch_bounds__(kFwdThreads) scan_fwd_kernel(ScanParams p, int
         meet();
         const int b = tile & 1;
         const f2x2 *sd = sm.d[b];
-        // L tokens at a time: their decays and inputs do not wait for the state, so they are
-        // prepared one group ahead.  No branch in here: the whole tile is one block to schedule.
-        f2 da[2][L][2], du[2][L][2];
-        auto prepare = [&](int j) {
+        // L tokens at a time, in three stages that overlap: the shared-memory loads of group j + 2, the
+        // decays and inputs of group j + 1 (which do not wait for the state), the recurrence of group j.
+        // A pair of states costs two exponentials (8 cycles of the special-function pipe) and four packed
+        // FMAs (8 cycles of theirs); they are written, and kept by `volatile`, in the order that feeds both
+        // pipes at once.  No branch in here: the whole tile is one block to schedule.
+        constexpr int G = KT;                  // groups of L tokens
+        f2x2 sv[L], bv[L][H / 2], cv[2][L][H / 2];
+        f2 e[2][L][H], u[2][L][H];
+        auto load = [&](int j) {               // raw operands of group j
 #pragma unroll
             for (int k = 0; k < L; ++k) {
                 const int t = j * L + k;
-                const f2x2 v = sd[t * CH + off[t % P]];
-                const f2x2 bq = *reinterpret_cast<const f2x2 *>(&sm.B[b][t][n0]);
-                da[j & 1][k][0] = ex2_2(mul2(v.a, a01));
-                da[j & 1][k][1] = ex2_2(mul2(v.a, a23));
-                du[j & 1][k][0] = mul2(v.b, bq.a);
-                du[j & 1][k][1] = mul2(v.b, bq.b);
+                sv[k] = sd[t * CH + off[t % P]];
+#pragma unroll
+                for (int q = 0; q < H / 2; ++q) {
+                    bv[k][q] = *reinterpret_cast<const f2x2 *>(&sm.B[b][t][n0 + 4 * q]);
+                    cv[j & 1][k][q] = *reinterpret_cast<const f2x2 *>(&sm.C[b][t][n0 + 4 * q]);
+                }
             }
         };
-        prepare(0);
+        auto half = [](const f2x2 &v, int q) { return q & 1 ? v.b : v.a; };
+        load(0);
 #pragma unroll
-        for (int j = 0; j < KT; ++j) {
-            if (j + 1 < KT) prepare(j + 1);
+        for (int k = 0; k < L; ++k)
+#pragma unroll
+            for (int q = 0; q < H; ++q) {
+                e[0][k][q] = ex2_2(mul2(sv[k].a, a2[q]));
+                u[0][k][q] = mul2(sv[k].b, half(bv[k][q / 2], q));
+            }
+        load(1);
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+            const int x = j & 1, y = x ^ 1;
+            if (j + 1 < G)
+#pragma unroll
+                for (int k = 0; k < L; ++k)
+#pragma unroll
+                    for (int q = 0; q < H; ++q) {
+                        e[y][k][q] = mul2v(sv[k].a, a2[q]);
+                        u[y][k][q] = mul2v(sv[k].b, half(bv[k][q / 2], q));
+                    }
             float ys[L];
+            f2x2 cj[L][H / 2];
+#pragma unroll
+            for (int k = 0; k < L; ++k)
+#pragma unroll
+                for (int q = 0; q < H / 2; ++q) cj[k][q] = cv[x][k][q];
+            if (j + 2 < G) load(j + 2);
 #pragma unroll
             for (int k = 0; k < L; ++k) {
-                const f2x2 q = *reinterpret_cast<const f2x2 *>(&sm.C[b][j * L + k][n0]);
-                h01 = fma2(da[j & 1][k][0], h01, du[j & 1][k][0]);
-                h23 = fma2(da[j & 1][k][1], h23, du[j & 1][k][1]);
+                f2 acc;
+#pragma unroll
+                for (int q = 0; q < H; ++q) {
+                    if (j + 1 < G) e[y][k][q] = ex2_2v(e[y][k][q]);
+                    h[q] = fma2v(e[x][k][q], h[q], u[x][k][q]);
+                    acc = q ? fma2v(h[q], half(cj[k][q / 2], q), acc) : mul2v(h[q], half(cj[k][q / 2], q));
+                }
                 float lo, hi;
-                unpack2(fma2(h01, q.a, mul2(h23, q.b)), lo, hi);
+                unpack2(acc, lo, hi);
                 ys[k] = lo + hi;
             }
             spread_sum<L, L>(ys, i);
@@ -251,9 +347,10 @@ __global__ void __launch_bounds__(kFwdThreads) scan_fwd_kernel(ScanParams p, int
     }
     meet();
     if (p.ht && live && g.i == g.n - 1) {
-        unpack2(h01, h[0], h[1]);
-        unpack2(h23, h[2], h[3]);
-        store_states(p.ht + ((long long)g.b * p.D + d) * p.N, h, n0, p.N);
+        float hv[NS];
+#pragma unroll
+        for (int k = 0; k < H; ++k) unpack2(h[k], hv[2 * k], hv[2 * k + 1]);
+        store_states(p.ht + ((long long)g.b * p.D + d) * p.N, hv, n0, p.N);
     }
 }
 
@@ -304,22 +401,24 @@ __global__ void __launch_bounds__(kScanThreads) scan_step_kernel(ScanParams p, i
     }
 }
 
-template <class T, int L, bool XV> cudaError_t fwd_start(const ScanParams &p, cudaStream_t s) {
-    const int cb = (p.D + FwdTiles<L>::CH - 1) / FwdTiles<L>::CH;
+template <class T, int L, int NS, int KT, bool XV> cudaError_t fwd_start(const ScanParams &p, cudaStream_t s) {
+    using S = FwdTiles<L, NS, KT>;
+    const int cb = (p.D + S::CH - 1) / S::CH;
     const long long blocks = scan_slots(p, p.seg) * cb;
     if (blocks > 0x7fffffffLL) return cudaErrorNotSupported;
-    constexpr int smem = sizeof(FwdTiles<L>);
-    const cudaError_t e = cudaFuncSetAttribute(scan_fwd_kernel<T, L, XV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    constexpr int smem = sizeof(S) + (XV ? 3 * 3 * Eight<T, XV>::W * 16 * S::kFeeders : 0);
+    const cudaError_t e =
+        cudaFuncSetAttribute(scan_fwd_kernel<T, L, NS, KT, XV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    scan_fwd_kernel<T, L, XV><<<(unsigned)blocks, kFwdThreads, smem, s>>>(p, cb);
+    scan_fwd_kernel<T, L, NS, KT, XV><<<(unsigned)blocks, S::kThreads, smem, s>>>(p, cb);
     return cudaGetLastError();
 }
 
 // 16-byte accesses to x, delta, z and y where all of them allow it.
-template <class T, int L> cudaError_t fwd_launch(const ScanParams &p, cudaStream_t s) {
+template <class T, int L, int NS, int KT> cudaError_t fwd_launch(const ScanParams &p, cudaStream_t s) {
     const bool xv = p.D % 8 == 0 && rows_aligned(p.x, p.ld_x, sizeof(T), 16) && rows_aligned(p.delta, p.ld_delta, sizeof(T), 16) &&
                     rows_aligned(p.z, p.ld_z, sizeof(T), 16) && rows_aligned(p.y, p.ld_y, sizeof(T), 16);
-    return xv ? fwd_start<T, L, true>(p, s) : fwd_start<T, L, false>(p, s);
+    return xv ? fwd_start<T, L, NS, KT, true>(p, s) : fwd_start<T, L, NS, KT, false>(p, s);
 }
 
 template <class T, int L> cudaError_t step_launch(const ScanParams &p, cudaStream_t s) {
@@ -331,12 +430,10 @@ template <class T, int L> cudaError_t step_launch(const ScanParams &p, cudaStrea
 }
 
 template <class T> cudaError_t fwd_type(const ScanParams &p, cudaStream_t s) {
-    switch (lanes_for(p.N)) {
-    case 1: return fwd_launch<T, 1>(p, s);
-    case 2: return fwd_launch<T, 2>(p, s);
-    case 4: return fwd_launch<T, 4>(p, s);
-    default: return fwd_launch<T, 8>(p, s);
-    }
+    if (p.N <= 4) return fwd_launch<T, 1, 4, 16>(p, s);
+    if (p.N <= 8) return fwd_launch<T, 1, 8, 16>(p, s);
+    if (p.N <= 16) return fwd_launch<T, 2, 8, 16>(p, s);
+    return fwd_launch<T, 4, 8, 16>(p, s);
 }
 template <class T> cudaError_t step_type(const ScanParams &p, cudaStream_t s) {
     switch (lanes_for(p.N)) {
