@@ -38,7 +38,8 @@ struct ConvParams {
 
 struct ScanParams {
     int B, T, D, N;
-    int seg;                          // tokens per segment; >= T: whole sequences
+    int seg;                          // tokens per segment that the forward walks alone; >= T: whole sequences
+    int lseg;                         // tokens per segment of the local pass (divides seg)
     bool softplus;
     const void *x, *delta, *Bm, *Cm, *z, *dy;
     long long ld_x, ld_delta, ld_B, ld_C, ld_z, ld_y, ld_dy;

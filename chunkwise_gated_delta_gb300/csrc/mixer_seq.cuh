@@ -62,4 +62,9 @@ __host__ __device__ inline bool segment_of(const int32_t *cu, int B, int T, int 
     return true;
 }
 
+// Slot of the segment that begins at token t0 of sequence b, for segments of another length.
+__host__ __device__ inline long long slot_at(const int32_t *cu, int T, int seg, int b, int t0) {
+    return (cu ? first_slot(cu, T, seg, b) : b * ((T + (long long)seg - 1) / seg)) + t0 / seg;
+}
+
 }  // namespace mixer

@@ -11,6 +11,7 @@ namespace mixer {
 
 constexpr int kScanThreads = 128;
 constexpr int kBwdSegment = 64;      // tokens between boundary states in the backward
+constexpr int kFwdLocal = 128;       // and in the split forward
 
 // log(1 + u) for u in [0, 1]: 2 atanh(s) with s = u / (2 + u) <= 1/3, atanh(s) = s + s^3 P(s^2) with P
 // fitted for the smallest relative error of atanh on that interval (Lawson's reweighted least
@@ -128,54 +129,13 @@ template <> struct RawQuad<bf16> {
     }
 };
 
-// Rows t0 .. t0 + TT - 1 of Bm or Cm in two halves: a thread's groups of four states into registers,
-// as they lie in memory (nothing waits for them there), and a tile later to shared memory.
-// VEC: N = NP and rows aligned to four elements.
-template <class T, int NP, int TT, bool VEC> struct RowFetch {
-    static constexpr int Q = NP / 4, U = (TT * Q + kScanThreads - 1) / kScanThreads;
-    static constexpr bool ALL = TT * Q % kScanThreads == 0;
-    using Raw = typename RawQuad<T>::type;
-    Raw v[VEC ? U : 1];
-    T e[VEC ? 1 : U][4];
-    __device__ __forceinline__ void load(const void *src, long long ld, int N, const Segment &g, int t0) {
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int u = threadIdx.x + k * kScanThreads, t = u / Q, n = u % Q * 4;
-            const bool in = (ALL || u < TT * Q) && t0 + t < g.len;
-            const T *r = static_cast<const T *>(src) + (g.row0 + g.t0 + t0 + t) * ld + n;
-            if (VEC) {
-                v[k] = Raw{};
-                if (in) v[k] = *reinterpret_cast<const Raw *>(r);
-            } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    e[k][q] = from_f<T>(0.f);
-                    if (in && n + q < N) e[k][q] = r[q];
-                }
-            }
-        }
-    }
-    __device__ __forceinline__ void store(float (*dst)[NP]) const {
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int u = threadIdx.x + k * kScanThreads;
-            if (ALL || u < TT * Q) {
-                float4 o;
-                if (VEC) o = RawQuad<T>::floats(v[k]);
-                else o = make_float4(to_f(e[k][0]), to_f(e[k][1]), to_f(e[k][2]), to_f(e[k][3]));
-                *reinterpret_cast<float4 *>(&dst[u / Q][u % Q * 4]) = o;
-            }
-        }
-    }
-};
-
 // Rows t0 .. t0 + TT - 1 of Bm or Cm into shared memory as float32 [TT][NP], zero behind the
 // segment's end and past N.  One thread per group of four states.
-template <class T, int NP, int TT>
+template <class T, int NP, int TT, int THREADS = kScanThreads>
 __device__ __forceinline__ void stage_rows(float (*dst)[NP], const void *src, long long ld, int N, const Segment &g, int t0,
                                            bool vec) {
     constexpr int Q = NP / 4;
-    for (int u = threadIdx.x; u < TT * Q; u += kScanThreads) {
+    for (int u = threadIdx.x; u < TT * Q; u += THREADS) {
         const int t = u / Q, n = u % Q * 4;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (t0 + t < g.len) {
@@ -210,11 +170,13 @@ template <class T> inline bool bc_vec_ok(const ScanParams &p, int NP) {
            rows_aligned(p.Cm, p.ld_C, sizeof(T), 4 * sizeof(T));
 }
 
+// Lanes (of four states) per channel of the single-token kernel, and the forward's padded states.
 inline int lanes_for(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : 8; }
+inline int padded_states(int N) { return 4 * lanes_for(N); }
 
 inline long long scan_slots(const ScanParams &p, int seg) { return segment_slots(p.B, p.T, seg, p.cu_seqlens != nullptr); }
 
-// Local pass over every segment of p.seg tokens: the state it ends with when it starts from zero
+// Local pass over every segment of p.lseg tokens: the state it ends with when it starts from zero
 // (seg_state), its sum of dt (seg_dt) and, where grad is set, the gradient of the state entering
 // it when none comes from behind (seg_grad).  Then the boundary pass turns them into the state
 // entering and the gradient leaving each segment, in place.

@@ -23,320 +23,385 @@ namespace {
 
 constexpr int SEG = kBwdSegment;
 
-template <class T, int L, bool GRAD>
-__global__ void __launch_bounds__(kScanThreads) scan_local_kernel(ScanParams p, int chan_blocks, bool vec) {
-    constexpr int NP = 4 * L, CW = 32 / L, TT = L == 1 ? 16 : 32, K = TT / L;
-    __shared__ float sB[TT][NP], sC[GRAD ? TT : 1][NP];
-    __shared__ float4 sd[4][TT][CW];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane / L, i = lane % L, n0 = 4 * i;
-    const long long slot = blockIdx.x / chan_blocks;
-    const int d = (int)(blockIdx.x - slot * chan_blocks) * (4 * CW) + warp * CW + c;
-    Segment g;
-    if (!segment_of(p.cu_seqlens, p.B, p.T, p.seg, slot, g)) return;
-    const bool live = d < p.D;
-    float a2[4] = {0.f, 0.f, 0.f, 0.f}, h[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};
-    float m[4] = {1.f, 1.f, 1.f, 1.f};      // a_1 ... a_t
-    float dbias = 0.f, sum = 0.f;
-    if (live) {
-        load_states(a2, p.A + (long long)d * p.N, n0, p.N);
-        if (p.delta_bias) dbias = p.delta_bias[d];
+// Four neighbouring channels of one token (XV: in one access).  Channels past the end repeat the last
+// ones (last: the last offset that exists).
+template <class T, bool XV> __device__ __forceinline__ void load_four(float (&o)[4], const T *p, int last) {
+    if (XV) {
+        const float4 v = RawQuad<T>::floats(*reinterpret_cast<const typename RawQuad<T>::type *>(p));
+        o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+    } else {
+        uint32_t v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = load_bits(p + min(k, last));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = bits_f<T>(v[k]);
     }
+}
+template <class T, bool XV> __device__ __forceinline__ void store_four(T *p, const float (&v)[4], int n) {
+    if (XV) {
+        Vec<T, 4> q;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) a2[k] *= kLog2e;
-    const T *x = static_cast<const T *>(p.x), *delta = static_cast<const T *>(p.delta);
-    const T *z = static_cast<const T *>(p.z), *dy = static_cast<const T *>(p.dy);
-    for (int t0 = 0; t0 < g.len; t0 += TT) {
-        __syncthreads();
-        stage_rows<T, NP, TT>(sB, p.Bm, p.ld_B, p.N, g, t0, vec);
-        if (GRAD) stage_rows<T, NP, TT>(reinterpret_cast<float(*)[NP]>(sC), p.Cm, p.ld_C, p.N, g, t0, vec);
+        for (int k = 0; k < 4; ++k) q.e[k] = from_f<T>(v[k]);
+        store_vec<T, 4>(p, q);
+    } else {
 #pragma unroll
-        for (int j = 0; j < K; ++j) {
-            const int t = t0 + j * L + i;
-            float dt = 0.f, xv = 0.f, gy = 0.f;
-            if (live && t < g.len) {
-                const long long r = g.row0 + g.t0 + t;
-                xv = to_f(x[r * p.ld_x + d]);
-                dt = to_f(delta[r * p.ld_delta + d]) + dbias;
-                if (p.softplus) dt = softplus(dt);
-                if (GRAD) {
-                    gy = to_f(dy[r * p.ld_dy + d]);
-                    if (z) {
-                        const float zv = to_f(z[r * p.ld_z + d]);
-                        gy *= zv * sigmoid(zv);
-                    }
-                }
-            }
-            sum += dt;
-            sd[warp][j * L + i][c] = make_float4(dt, dt * xv, gy, 0.f);
-        }
-        __syncthreads();
-#pragma unroll 8
-        for (int t = 0; t < TT; ++t) {
-            const float4 v = sd[warp][t][c];
-            const float4 b = *reinterpret_cast<const float4 *>(&sB[t][n0]);
-            float a[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) a[k] = ex2(v.x * a2[k]);
-            h[0] = fmaf(a[0], h[0], v.y * b.x);
-            h[1] = fmaf(a[1], h[1], v.y * b.y);
-            h[2] = fmaf(a[2], h[2], v.y * b.z);
-            h[3] = fmaf(a[3], h[3], v.y * b.w);
-            if (GRAD) {
-                const float4 q = *reinterpret_cast<const float4 *>(&sC[t][n0]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) m[k] *= a[k];
-                e[0] = fmaf(m[0], v.z * q.x, e[0]);
-                e[1] = fmaf(m[1], v.z * q.y, e[1]);
-                e[2] = fmaf(m[2], v.z * q.z, e[2]);
-                e[3] = fmaf(m[3], v.z * q.w, e[3]);
-            }
-        }
+        for (int k = 0; k < 4; ++k)
+            if (k < n) p[k] = from_f<T>(v[k]);
     }
-#pragma unroll
-    for (int s = L / 2; s; s >>= 1) sum += __shfl_xor_sync(~0u, sum, s);
-    if (!live) return;
-    const long long at = slot * p.D + d;
-    *reinterpret_cast<float4 *>(p.seg_state + at * NP + n0) = make_float4(h[0], h[1], h[2], h[3]);
-    if (GRAD) *reinterpret_cast<float4 *>(p.seg_grad + at * NP + n0) = make_float4(e[0], e[1], e[2], e[3]);
-    if (i == 0) p.seg_dt[at] = sum;
 }
 
-// One thread per (sequence, channel, state).
-template <bool GRAD> __global__ void __launch_bounds__(128) scan_boundary_kernel(ScanParams p, int NP) {
+// Local pass.  A block: 128 / L channels, a lane NS states of one of them.  Per 32 tokens, first dt, dt x
+// and g of all channels into shared memory (four channels per access), then the recurrences.  Four
+// blocks to an SM cover each other's phases.
+template <int L, int NS> struct LocalTiles {
+    static constexpr int TT = 32, CH = kScanThreads / L, NP = NS * L;
+    f2x2 d[TT][CH];                  // {dt, dt}, {dt x, dt x}; columns swizzled, see at()
+    f2 g[TT][CH];
+    float B[TT][NP], C[TT][NP];
+    float sum[TT][CH / 4][4];        // dt over a thread's tokens
+    // Column of channel c: threads that write every fourth channel and threads that read neighbouring
+    // ones both meet eight different 16-byte words.
+    static __device__ __forceinline__ int at(int c) { return c ^ (c >> 3 & 3); }
+};
+
+template <class T, int L, int NS, bool GRAD, bool XV>
+__global__ void __launch_bounds__(kScanThreads, 4) scan_local_kernel(ScanParams p, int chan_blocks, bool vec) {
+    using S = LocalTiles<L, NS>;
+    constexpr int TT = S::TT, CH = S::CH, NP = S::NP, H = NS / 2, Q = CH / 4, ROWS = kScanThreads / Q, K = TT / ROWS;
+    extern __shared__ __align__(16) unsigned char raw[];
+    S &sm = *reinterpret_cast<S *>(raw);
+    const long long slot = blockIdx.x / chan_blocks;
+    const int d0 = (int)(blockIdx.x - slot * chan_blocks) * CH;
+    Segment g;
+    if (!segment_of(p.cu_seqlens, p.B, p.T, p.lseg, slot, g)) return;
+    const int tid = threadIdx.x, c = tid / L, i = tid % L, n0 = NS * i, d = d0 + c;
+    const bool live = d < p.D;
+    f2 a2[H], h[H], e[H], m[H];
+    {
+        float av[NS];
+#pragma unroll
+        for (int k = 0; k < NS; ++k) av[k] = 0.f;
+        if (live) load_states(av, p.A + (long long)d * p.N, n0, p.N);
+#pragma unroll
+        for (int k = 0; k < H; ++k) {
+            a2[k] = pack2(av[2 * k] * kLog2e, av[2 * k + 1] * kLog2e);
+            h[k] = e[k] = pack2(0.f, 0.f);
+            m[k] = pack2(1.f, 1.f);          // a_1 ... a_t
+        }
+    }
+    // staging: this thread's channels and first token
+    const int q = tid % Q, r0 = tid / Q, ds = d0 + 4 * q, dl = XV ? min(ds, p.D - 4) : min(ds, p.D - 1), last = p.D - 1 - dl;
+    const long long row = g.row0 + g.t0;
+    const T *x = static_cast<const T *>(p.x) + row * p.ld_x + dl, *delta = static_cast<const T *>(p.delta) + row * p.ld_delta + dl;
+    const T *dy = GRAD ? static_cast<const T *>(p.dy) + row * p.ld_dy + dl : x;
+    const T *z = GRAD && p.z ? static_cast<const T *>(p.z) + row * p.ld_z + dl : x;
+    const long long ldz = GRAD && p.z ? p.ld_z : p.ld_x, lddy = GRAD ? p.ld_dy : p.ld_x;
+    float bias[4], sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) bias[k] = p.delta_bias && ds + k < p.D ? p.delta_bias[ds + k] : 0.f;
+    for (int t0 = 0; t0 < g.len; t0 += TT) {
+        __syncthreads();
+        stage_rows<T, NP, TT>(sm.B, p.Bm, p.ld_B, p.N, g, t0, vec);
+        if (GRAD) stage_rows<T, NP, TT>(sm.C, p.Cm, p.ld_C, p.N, g, t0, vec);
+#pragma unroll 2
+        for (int k = 0; k < K; ++k) {
+            const int t = r0 + k * ROWS;
+            const bool in = t0 + t < g.len;
+            const long long tl = min(t0 + t, g.len - 1);
+            float xv[4], dv[4], yv[4], zv[4];
+            load_four<T, XV>(xv, x + tl * p.ld_x, last);
+            load_four<T, XV>(dv, delta + tl * p.ld_delta, last);
+            if (GRAD) {
+                load_four<T, XV>(yv, dy + tl * lddy, last);
+                load_four<T, XV>(zv, z + tl * ldz, last);
+            }
+#pragma unroll
+            for (int s = 0; s < 4; s += 2) {
+                f2 dt = pack2(dv[s] + bias[s], dv[s + 1] + bias[s + 1]);
+                if (p.softplus) dt = softplus2(dt);
+                float lo, hi;
+                unpack2(dt, lo, hi);
+                lo = in ? lo : 0.f;
+                hi = in ? hi : 0.f;
+                sum[s] += lo;
+                sum[s + 1] += hi;
+                const float ul = in ? lo * xv[s] : 0.f, uh = in ? hi * xv[s + 1] : 0.f;
+                sm.d[t][S::at(4 * q + s)] = {both(lo), both(ul)};
+                sm.d[t][S::at(4 * q + s + 1)] = {both(hi), both(uh)};
+                if (GRAD) {
+                    f2 gy = pack2(yv[s], yv[s + 1]);
+                    if (p.z) gy = mul2(gy, silu2(pack2(zv[s], zv[s + 1])));
+                    unpack2(gy, lo, hi);
+                    sm.g[t][S::at(4 * q + s)] = both(in ? lo : 0.f);
+                    sm.g[t][S::at(4 * q + s + 1)] = both(in ? hi : 0.f);
+                }
+            }
+        }
+        __syncthreads();
+#pragma unroll 4
+        for (int t = 0; t < TT; ++t) {
+            const f2x2 v = sm.d[t][S::at(c)];
+            const f2 gy = GRAD ? sm.g[t][S::at(c)] : 0;
+#pragma unroll
+            for (int k = 0; k < H; k += 2) {
+                const f2x2 b = *reinterpret_cast<const f2x2 *>(&sm.B[t][n0 + 2 * k]);
+                const f2 a0 = ex2_2(mul2(v.a, a2[k])), a1 = ex2_2(mul2(v.a, a2[k + 1]));
+                h[k] = fma2(a0, h[k], mul2(v.b, b.a));
+                h[k + 1] = fma2(a1, h[k + 1], mul2(v.b, b.b));
+                if (GRAD) {
+                    const f2x2 cq = *reinterpret_cast<const f2x2 *>(&sm.C[t][n0 + 2 * k]);
+                    m[k] = mul2(m[k], a0);
+                    m[k + 1] = mul2(m[k + 1], a1);
+                    e[k] = fma2(m[k], mul2(gy, cq.a), e[k]);
+                    e[k + 1] = fma2(m[k + 1], mul2(gy, cq.b), e[k + 1]);
+                }
+            }
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sm.sum[r0][q][k] = sum[k];
+    __syncthreads();
+    const long long at = slot * p.D + d;
+    if (tid < CH && d0 + tid < p.D) {
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) s += sm.sum[k][tid / 4][tid % 4];
+        p.seg_dt[slot * p.D + d0 + tid] = s;
+    }
+    if (!live) return;
+#pragma unroll
+    for (int k = 0; k < H; k += 2) {
+        *reinterpret_cast<f2x2 *>(p.seg_state + at * NP + n0 + 2 * k) = {h[k], h[k + 1]};
+        if (GRAD) *reinterpret_cast<f2x2 *>(p.seg_grad + at * NP + n0 + 2 * k) = {e[k], e[k + 1]};
+    }
+}
+
+// One thread per (sequence, channel, state) and direction: entry states forwards (blockIdx.y = 0), exit
+// gradients backwards (1), eight segments' values on their way at a time.
+__global__ void __launch_bounds__(128) scan_boundary_kernel(ScanParams p, int NP) {
     const long long u = (long long)blockIdx.x * 128 + threadIdx.x;
     const long long per = (long long)p.D * NP;
     const int b = (int)(u / per);
     if (b >= p.B) return;
     const int d = (int)((u - b * per) / NP), n = (int)(u % NP);
+    const bool back = blockIdx.y;
     long long s0;
     int count;
     if (!p.cu_seqlens) {
-        count = (int)((p.T + (long long)p.seg - 1) / p.seg);
+        count = (int)((p.T + (long long)p.lseg - 1) / p.lseg);
         s0 = (long long)b * count;
     } else {
         const int lo = clamped(p.cu_seqlens[b], 0, p.T), hi = clamped(p.cu_seqlens[b + 1], lo, p.T);
-        count = hi > lo ? (int)((hi - lo + (long long)p.seg - 1) / p.seg) : 1;
-        s0 = b + lo / p.seg;
+        count = hi > lo ? (int)((hi - lo + (long long)p.lseg - 1) / p.lseg) : 1;
+        s0 = b + lo / p.lseg;
     }
     const bool in = n < p.N;
     const float a2 = in ? p.A[(long long)d * p.N + n] * kLog2e : 0.f;
     const long long at = ((long long)b * p.D + d) * p.N + n;
-    float h = in && p.h0 ? p.h0[at] : 0.f;
-    for (int i = 0; i < count; ++i) {
-        const long long k = (s0 + i) * p.D + d;
-        const float local = p.seg_state[k * NP + n], a = ex2(a2 * p.seg_dt[k]);
-        p.seg_state[k * NP + n] = h;
-        h = fmaf(a, h, local);
+    const float *first = back ? p.dht : p.h0;
+    float v = in && first ? first[at] : 0.f;
+    const long long step = back ? -(long long)p.D : p.D;
+    const long long k0 = (back ? s0 + count - 1 : s0) * p.D + d;
+    float *vals = (back ? p.seg_grad : p.seg_state) + n;
+    for (int i = 0; i < count; i += 8) {
+        float local[8], dt[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const long long k = k0 + (long long)min(i + j, count - 1) * step;
+            local[j] = vals[k * NP];
+            dt[j] = p.seg_dt[k];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (i + j < count) {
+                vals[(k0 + (i + j) * step) * NP] = v;
+                v = fmaf(ex2(a2 * dt[j]), v, local[j]);
+            }
     }
-    if (!GRAD) return;
-    float e = in && p.dht ? p.dht[at] : 0.f;
-    for (int i = count - 1; i >= 0; --i) {
-        const long long k = (s0 + i) * p.D + d;
-        const float local = p.seg_grad[k * NP + n], a = ex2(a2 * p.seg_dt[k]);
-        p.seg_grad[k * NP + n] = e;
-        e = fmaf(a, e, local);
-    }
-    if (in && p.dh0) p.dh0[at] = e;
+    if (back && in && p.dh0) p.dh0[at] = v;
 }
 
 constexpr int TC = 8;                // tokens per part, recomputed into registers
-constexpr int GROUPS = 4;            // channel groups that a block walks per part
+constexpr int GROUPS = 2;            // channel groups that a block walks per part
 constexpr int PARTS = SEG / TC;
+constexpr int kGradThreads = 256;
 
-// Per-thread values in shared memory, one set per channel group.
-struct GradShared {
-    float4 entry[GROUPS][PARTS][kScanThreads];   // states before each part
-    float4 carry[GROUPS][kScanThreads];          // gradient of the state after the part at hand
-    float4 dA[GROUPS][kScanThreads];
-    float2 par[GROUPS][kScanThreads];            // dD, dbias
+template <int L> struct GradTiles {
+    static constexpr int NP = 4 * L, CW = 32 / L, CG = 8 * CW, CH = GROUPS * CG;   // channels of a warp, group, block
+    static constexpr int XS = CH + 4;
+    f2x2 entry[GROUPS][PARTS][kGradThreads];     // states before each part
+    float2 du[SEG][XS];                          // dt, dt x; after a part: dt, sum_n G B
+    float g[SEG][XS];                            // g; after a part: sum_n q A / ln 2
+    float y[SEG][XS];                            // sum_n C h
+    float B[SEG][NP], C[SEG][NP];
+    float red[8][TC * 2 * NP];
 };
 
-template <class T, int L> struct GradTiles {
-    float B[SEG][4 * L], C[SEG][4 * L];
-    float4 d[4][TC][32 / L];
-    float red[4][TC * 2 * 4 * L];
-};
-
-template <class T, int L>
-__global__ void __launch_bounds__(kScanThreads) scan_grad_kernel(ScanParams p, int chan_blocks, bool vec) {
-    constexpr int NP = 4 * L, CW = 32 / L, CH = 4 * CW, TL = TC / L;
+// A block: 64 tokens, 16 CW channels, 8 warps.  All inputs go through shared memory once, four channels
+// per access; the parts leave their sums over states there, and a last sweep over (token, channel) turns
+// them into dx, ddelta and dz, again four channels per access.
+template <class T, int L, bool XV>
+__global__ void __launch_bounds__(kGradThreads, 1) scan_grad_kernel(ScanParams p, int chan_blocks, bool vec) {
+    using S = GradTiles<L>;
+    constexpr int NP = S::NP, CW = S::CW, CH = S::CH, TL = TC / L, Q = CH / 4, ROWS = kGradThreads / Q, K = SEG / ROWS;
     extern __shared__ __align__(16) unsigned char raw[];
-    GradShared &S = *reinterpret_cast<GradShared *>(raw);
-    GradTiles<T, L> &W = *reinterpret_cast<GradTiles<T, L> *>(raw + sizeof(GradShared));
+    S &sm = *reinterpret_cast<S *>(raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane / L, i = lane % L, n0 = 4 * i;
     const long long slot = blockIdx.x / chan_blocks;
-    const int cb = (int)(blockIdx.x - slot * chan_blocks);
+    const int cb = (int)(blockIdx.x - slot * chan_blocks), d0 = cb * CH;
     Segment g;
-    if (!segment_of(p.cu_seqlens, p.B, p.T, p.seg, slot, g)) return;
-    const T *x = static_cast<const T *>(p.x), *delta = static_cast<const T *>(p.delta);
-    const T *z = static_cast<const T *>(p.z), *dy = static_cast<const T *>(p.dy);
+    if (!segment_of(p.cu_seqlens, p.B, p.T, SEG, slot, g)) return;
     const long long row = g.row0 + g.t0;
-    stage_rows<T, NP, SEG>(W.B, p.Bm, p.ld_B, p.N, g, 0, vec);
-    stage_rows<T, NP, SEG>(W.C, p.Cm, p.ld_C, p.N, g, 0, vec);
-    __syncthreads();
-    const int parts = (g.len + TC - 1) / TC;
-    // forward sweep: the state before every part
-    for (int k = 0; k < GROUPS; ++k) {
-        const int d = (cb * GROUPS + k) * CH + warp * CW + c;
-        const bool live = d < p.D;
-        float a2[4] = {0.f, 0.f, 0.f, 0.f}, h[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};
-        float dbias = 0.f;
-        if (live) {
-            load_states(a2, p.A + (long long)d * p.N, n0, p.N);
-            load_states(h, p.seg_state + (slot * p.D + d) * NP, n0, NP);
-            load_states(e, p.seg_grad + (slot * p.D + d) * NP, n0, NP);
-            if (p.delta_bias) dbias = p.delta_bias[d];
-        }
-        S.carry[k][tid] = make_float4(e[0], e[1], e[2], e[3]);
-        S.dA[k][tid] = make_float4(0.f, 0.f, 0.f, 0.f);
-        S.par[k][tid] = make_float2(0.f, 0.f);
+
+    // ---- inputs to shared memory
+    const int q = tid % Q, r0 = tid / Q, ds = d0 + 4 * q, dl = XV ? min(ds, p.D - 4) : min(ds, p.D - 1), last = p.D - 1 - dl;
+    const T *x = static_cast<const T *>(p.x) + row * p.ld_x + dl, *delta = static_cast<const T *>(p.delta) + row * p.ld_delta + dl;
+    const T *dy = static_cast<const T *>(p.dy) + row * p.ld_dy + dl;
+    const T *z = p.z ? static_cast<const T *>(p.z) + row * p.ld_z + dl : x;
+    const long long ldz = p.z ? p.ld_z : p.ld_x;
+    float bias[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) a2[q] *= kLog2e;
-        for (int part = 0; part < parts; ++part) {
-            S.entry[k][part][tid] = make_float4(h[0], h[1], h[2], h[3]);
-            if (part == parts - 1) break;          // its tokens are swept below
-            __syncwarp();
+    for (int k = 0; k < 4; ++k) bias[k] = p.delta_bias && ds + k < p.D ? p.delta_bias[ds + k] : 0.f;
+    if (g.len > 0) {
+#pragma unroll 2
+        for (int k = 0; k < K; ++k) {
+            const int t = r0 + k * ROWS;
+            const bool in = t < g.len;
+            const long long tl = min(t, g.len - 1);
+            float xv[4], dv[4], yv[4], zv[4];
+            load_four<T, XV>(xv, x + tl * p.ld_x, last);
+            load_four<T, XV>(dv, delta + tl * p.ld_delta, last);
+            load_four<T, XV>(yv, dy + tl * p.ld_dy, last);
+            load_four<T, XV>(zv, z + tl * ldz, last);
 #pragma unroll
-            for (int j = 0; j < TL; ++j) {
-                const int t = part * TC + i * TL + j;
-                float dt = 0.f, xv = 0.f;
-                if (live && t < g.len) {
-                    xv = to_f(x[(row + t) * p.ld_x + d]);
-                    dt = to_f(delta[(row + t) * p.ld_delta + d]) + dbias;
-                    if (p.softplus) dt = softplus(dt);
-                }
-                W.d[warp][i * TL + j][c] = make_float4(dt, dt * xv, 0.f, 0.f);
-            }
-            __syncwarp();
-#pragma unroll
-            for (int t = 0; t < TC; ++t) {
-                const float4 v = W.d[warp][t][c];
-                const float4 b = *reinterpret_cast<const float4 *>(&W.B[part * TC + t][n0]);
-                h[0] = fmaf(ex2(v.x * a2[0]), h[0], v.y * b.x);
-                h[1] = fmaf(ex2(v.x * a2[1]), h[1], v.y * b.y);
-                h[2] = fmaf(ex2(v.x * a2[2]), h[2], v.y * b.z);
-                h[3] = fmaf(ex2(v.x * a2[3]), h[3], v.y * b.w);
+            for (int s = 0; s < 4; s += 2) {
+                f2 dt = pack2(dv[s] + bias[s], dv[s + 1] + bias[s + 1]), gy = pack2(yv[s], yv[s + 1]);
+                if (p.softplus) dt = softplus2(dt);
+                if (p.z) gy = mul2(gy, silu2(pack2(zv[s], zv[s + 1])));
+                float lo, hi, gl, gh;
+                unpack2(dt, lo, hi);
+                unpack2(gy, gl, gh);
+                // tokens past the end leave the state as it is, channels past the end add nothing to dB and dC
+                const bool il = in && ds + s < p.D, ih = in && ds + s + 1 < p.D;
+                *reinterpret_cast<float4 *>(&sm.du[t][4 * q + s]) =
+                    make_float4(il ? lo : 0.f, il ? lo * xv[s] : 0.f, ih ? hi : 0.f, ih ? hi * xv[s + 1] : 0.f);
+                *reinterpret_cast<float2 *>(&sm.g[t][4 * q + s]) = make_float2(il ? gl : 0.f, ih ? gh : 0.f);
             }
         }
     }
-    // the parts, last to first
+    stage_rows<T, NP, SEG, kGradThreads>(sm.B, p.Bm, p.ld_B, p.N, g, 0, vec);
+    stage_rows<T, NP, SEG, kGradThreads>(sm.C, p.Cm, p.ld_C, p.N, g, 0, vec);
+    __syncthreads();
+    const int parts = (g.len + TC - 1) / TC;
+
+    f2 a2[GROUPS][2], carry[GROUPS][2], dA[GROUPS][2];   // per channel group: A log2 e, gradient of the state after the part
+#pragma unroll
+    for (int k = 0; k < GROUPS; ++k) {
+        const int d = d0 + k * S::CG + warp * CW + c;
+        float av[4] = {0.f, 0.f, 0.f, 0.f}, hv[4] = {0.f, 0.f, 0.f, 0.f}, ev[4] = {0.f, 0.f, 0.f, 0.f};
+        if (d < p.D) {
+            load_states(av, p.A + (long long)d * p.N, n0, p.N);
+            load_states(hv, p.seg_state + (slot * p.D + d) * NP, n0, NP);
+            load_states(ev, p.seg_grad + (slot * p.D + d) * NP, n0, NP);
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            a2[k][s] = pack2(av[2 * s] * kLog2e, av[2 * s + 1] * kLog2e);
+            carry[k][s] = pack2(ev[2 * s], ev[2 * s + 1]);
+            dA[k][s] = pack2(0.f, 0.f);
+        }
+        // ---- forward sweep: the state before every part (the last part's tokens are swept below)
+        f2 h0 = pack2(hv[0], hv[1]), h1 = pack2(hv[2], hv[3]);
+        const int cc = k * S::CG + warp * CW + c;
+        for (int part = 0; part < parts; ++part) {
+            sm.entry[k][part][tid] = {h0, h1};
+            if (part == parts - 1) break;
+#pragma unroll
+            for (int t = 0; t < TC; ++t) {
+                const float2 v = sm.du[part * TC + t][cc];
+                const f2x2 b = *reinterpret_cast<const f2x2 *>(&sm.B[part * TC + t][n0]);
+                const f2 dt = both(v.x), u = both(v.y);
+                h0 = fma2(ex2_2(mul2(dt, a2[k][0])), h0, mul2(u, b.a));
+                h1 = fma2(ex2_2(mul2(dt, a2[k][1])), h1, mul2(u, b.b));
+            }
+        }
+    }
+
+    // ---- the parts, last to first
     for (int part = parts - 1; part >= 0; --part) {
-        float acc[2][TC][4];         // dB, dC of this lane's states, over the channel groups
+        f2 accB[TC][2], accC[TC][2];     // dB, dC of this lane's states, over the channel groups
 #pragma unroll
-        for (int t = 0; t < TC; ++t)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) acc[0][t][q] = acc[1][t][q] = 0.f;
         for (int k = 0; k < GROUPS; ++k) {
-            const int d = (cb * GROUPS + k) * CH + warp * CW + c;
-            const bool live = d < p.D;
-            float a2[4] = {0.f, 0.f, 0.f, 0.f};
-            float dbias = 0.f, skip = 0.f;
-            if (live) {
-                load_states(a2, p.A + (long long)d * p.N, n0, p.N);
-                if (p.delta_bias) dbias = p.delta_bias[d];
-                if (p.Dskip) skip = p.Dskip[d];
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) a2[q] *= kLog2e;
-            float dts[TL], xs[TL], zs[TL], dys[TL], sg[TL], gys[TL];
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < TL; ++j) {
-                const int t = part * TC + i * TL + j;
-                dts[j] = xs[j] = zs[j] = dys[j] = sg[j] = gys[j] = 0.f;
-                if (live && t < g.len) {
-                    xs[j] = to_f(x[(row + t) * p.ld_x + d]);
-                    dts[j] = to_f(delta[(row + t) * p.ld_delta + d]) + dbias;
-                    sg[j] = 1.f;
-                    if (p.softplus) {
-                        sg[j] = sigmoid(dts[j]);
-                        dts[j] = softplus(dts[j]);
-                    }
-                    gys[j] = dys[j] = to_f(dy[(row + t) * p.ld_dy + d]);
-                    if (z) {
-                        zs[j] = to_f(z[(row + t) * p.ld_z + d]);
-                        gys[j] *= zs[j] * sigmoid(zs[j]);
-                    }
-                }
-                W.d[warp][i * TL + j][c] = make_float4(dts[j], dts[j] * xs[j], gys[j], 0.f);
-            }
-            __syncwarp();
-            float h[TC + 1][4], a[TC][4], ys[TC], us[TC], qs[TC];
+            const int cc = k * S::CG + warp * CW + c;
+            float ys[TC], us[TC], qs[TC];
+            f2 h[TC + 1][2], a[TC][2];
             {
-                const float4 v = S.entry[k][part][tid];
-                h[0][0] = v.x; h[0][1] = v.y; h[0][2] = v.z; h[0][3] = v.w;
+                const f2x2 v = sm.entry[k][part][tid];
+                h[0][0] = v.a;
+                h[0][1] = v.b;
             }
 #pragma unroll
             for (int t = 0; t < TC; ++t) {
-                const float4 v = W.d[warp][t][c];
-                const float4 b = *reinterpret_cast<const float4 *>(&W.B[part * TC + t][n0]);
-                const float4 q = *reinterpret_cast<const float4 *>(&W.C[part * TC + t][n0]);
-#pragma unroll
-                for (int s = 0; s < 4; ++s) a[t][s] = ex2(v.x * a2[s]);
-                h[t + 1][0] = fmaf(a[t][0], h[t][0], v.y * b.x);
-                h[t + 1][1] = fmaf(a[t][1], h[t][1], v.y * b.y);
-                h[t + 1][2] = fmaf(a[t][2], h[t][2], v.y * b.z);
-                h[t + 1][3] = fmaf(a[t][3], h[t][3], v.y * b.w);
-                ys[t] = fmaf(h[t + 1][0], q.x, h[t + 1][1] * q.y) + fmaf(h[t + 1][2], q.z, h[t + 1][3] * q.w);
+                const float2 v = sm.du[part * TC + t][cc];
+                const f2x2 b = *reinterpret_cast<const f2x2 *>(&sm.B[part * TC + t][n0]);
+                const f2x2 cq = *reinterpret_cast<const f2x2 *>(&sm.C[part * TC + t][n0]);
+                const f2 dt = both(v.x), u = both(v.y);
+                a[t][0] = ex2_2(mul2(dt, a2[k][0]));
+                a[t][1] = ex2_2(mul2(dt, a2[k][1]));
+                h[t + 1][0] = fma2(a[t][0], h[t][0], mul2(u, b.a));
+                h[t + 1][1] = fma2(a[t][1], h[t][1], mul2(u, b.b));
+                float lo, hi;
+                unpack2(fma2(h[t + 1][0], cq.a, mul2(h[t + 1][1], cq.b)), lo, hi);
+                ys[t] = lo + hi;
             }
-            float G[4], dA[4];
-            {
-                const float4 v = S.carry[k][tid], w = S.dA[k][tid];
-                G[0] = v.x; G[1] = v.y; G[2] = v.z; G[3] = v.w;
-                dA[0] = w.x; dA[1] = w.y; dA[2] = w.z; dA[3] = w.w;
-            }
+            f2 G0 = carry[k][0], G1 = carry[k][1];
 #pragma unroll
             for (int t = TC - 1; t >= 0; --t) {
-                const float4 v = W.d[warp][t][c];
-                const float4 b4 = *reinterpret_cast<const float4 *>(&W.B[part * TC + t][n0]);
-                const float4 c4 = *reinterpret_cast<const float4 *>(&W.C[part * TC + t][n0]);
-                const float b[4] = {b4.x, b4.y, b4.z, b4.w}, cc[4] = {c4.x, c4.y, c4.z, c4.w};
-                us[t] = qs[t] = 0.f;
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    G[s] = fmaf(cc[s], v.z, G[s]);
-                    acc[1][t][s] = fmaf(v.z, h[t + 1][s], acc[1][t][s]);
-                    acc[0][t][s] = fmaf(G[s], v.y, acc[0][t][s]);
-                    us[t] = fmaf(G[s], b[s], us[t]);
-                    G[s] *= a[t][s];
-                    const float q = G[s] * h[t][s];
-                    dA[s] = fmaf(q, v.x, dA[s]);
-                    qs[t] = fmaf(q, a2[s], qs[t]);
-                }
+                const float2 v = sm.du[part * TC + t][cc];
+                const f2 dt = both(v.x), u = both(v.y), gy = both(sm.g[part * TC + t][cc]);
+                const f2x2 b = *reinterpret_cast<const f2x2 *>(&sm.B[part * TC + t][n0]);
+                const f2x2 cq = *reinterpret_cast<const f2x2 *>(&sm.C[part * TC + t][n0]);
+                G0 = fma2(cq.a, gy, G0);
+                G1 = fma2(cq.b, gy, G1);
+                accC[t][0] = k ? fma2(gy, h[t + 1][0], accC[t][0]) : mul2(gy, h[t + 1][0]);
+                accC[t][1] = k ? fma2(gy, h[t + 1][1], accC[t][1]) : mul2(gy, h[t + 1][1]);
+                accB[t][0] = k ? fma2(u, G0, accB[t][0]) : mul2(u, G0);
+                accB[t][1] = k ? fma2(u, G1, accB[t][1]) : mul2(u, G1);
+                float lo, hi;
+                unpack2(fma2(G0, b.a, mul2(G1, b.b)), lo, hi);
+                us[t] = lo + hi;
+                G0 = mul2(G0, a[t][0]);
+                G1 = mul2(G1, a[t][1]);
+                const f2 q0 = mul2(G0, h[t][0]), q1 = mul2(G1, h[t][1]);
+                dA[k][0] = fma2(q0, dt, dA[k][0]);
+                dA[k][1] = fma2(q1, dt, dA[k][1]);
+                unpack2(fma2(q0, a2[k][0], mul2(q1, a2[k][1])), lo, hi);
+                qs[t] = lo + hi;
             }
-            S.carry[k][tid] = make_float4(G[0], G[1], G[2], G[3]);
-            S.dA[k][tid] = make_float4(dA[0], dA[1], dA[2], dA[3]);
+            carry[k][0] = G0;
+            carry[k][1] = G1;
             spread_sum<TC, L>(us, i);
             spread_sum<TC, L>(qs, i);
-            if (z) spread_sum<TC, L>(ys, i);
-            float2 par = S.par[k][tid];
+            spread_sum<TC, L>(ys, i);
+            __syncwarp();                // du and g of these tokens have been read by the channel's lanes
 #pragma unroll
             for (int j = 0; j < TL; ++j) {
                 const int t = part * TC + i * TL + j;
-                if (live && t < g.len) {
-                    const long long r = row + t;
-                    const float dd = fmaf(us[j], xs[j], qs[j] * kLn2) * sg[j];
-                    static_cast<T *>(p.dx)[r * p.ld_dx + d] = from_f<T>(fmaf(us[j], dts[j], skip * gys[j]));
-                    static_cast<T *>(p.ddelta)[r * p.ld_ddelta + d] = from_f<T>(dd);
-                    if (z) {
-                        const float s = sigmoid(zs[j]);
-                        static_cast<T *>(p.dz)[r * p.ld_dz + d] =
-                            from_f<T>(dys[j] * fmaf(skip, xs[j], ys[j]) * s * fmaf(zs[j], 1.f - s, 1.f));
-                    }
-                    par.x = fmaf(gys[j], xs[j], par.x);
-                    par.y += dd;
-                }
+                sm.du[t][cc].y = us[j];
+                sm.g[t][cc] = qs[j];
+                sm.y[t][cc] = ys[j];
             }
-            S.par[k][tid] = par;
         }
-        // dB and dC over the warp's channels, then over the four warps
+        // dB and dC over the warp's channels, then over the eight warps
         float v[2 * TC * 4];
 #pragma unroll
-        for (int w = 0; w < 2; ++w)
+        for (int t = 0; t < TC; ++t)
 #pragma unroll
-            for (int t = 0; t < TC; ++t)
-#pragma unroll
-                for (int s = 0; s < 4; ++s) v[(w * TC + t) * 4 + s] = acc[w][t][s];
+            for (int s = 0; s < 2; ++s) {
+                unpack2(accB[t][s], v[t * 4 + 2 * s], v[t * 4 + 2 * s + 1]);
+                unpack2(accC[t][s], v[(TC + t) * 4 + 2 * s], v[(TC + t) * 4 + 2 * s + 1]);
+            }
         int n = 2 * TC * 4, base = 0;
 #pragma unroll
         for (int s = 16; s >= L; s >>= 1) {
@@ -354,34 +419,80 @@ __global__ void __launch_bounds__(kScanThreads) scan_grad_kernel(ScanParams p, i
 #pragma unroll
         for (int k = 0; k < LEFT; ++k) {
             const int w = (base + k) / (TC * 4), t = (base + k) / 4 % TC, s = (base + k) % 4;
-            W.red[warp][(t * 2 + w) * NP + n0 + s] = v[k];
+            sm.red[warp][(t * 2 + w) * NP + n0 + s] = v[k];
         }
         __syncthreads();
-        for (int u = tid; u < TC * 2 * NP; u += kScanThreads) {
+        for (int u = tid; u < TC * 2 * NP; u += kGradThreads) {
             const int t = part * TC + u / (2 * NP);
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) s += sm.red[w][u];
             if (t < g.len)
-                p.part_bc[((long long)cb * ((long long)(p.cu_seqlens ? 1 : p.B) * p.T) + row + t) * (2 * NP) + u % (2 * NP)] =
-                    (W.red[0][u] + W.red[1][u]) + (W.red[2][u] + W.red[3][u]);
+                p.part_bc[((long long)cb * ((long long)(p.cu_seqlens ? 1 : p.B) * p.T) + row + t) * (2 * NP) + u % (2 * NP)] = s;
         }
         __syncthreads();
     }
-    for (int k = 0; k < GROUPS; ++k) {
-        const int d = (cb * GROUPS + k) * CH + warp * CW + c;
-        float2 par = S.par[k][tid];
+    float *out = p.part_par + slot * ((long long)p.D * (p.N + 2));
 #pragma unroll
-        for (int s = L / 2; s; s >>= 1) {
-            par.x += __shfl_xor_sync(~0u, par.x, s);
-            par.y += __shfl_xor_sync(~0u, par.y, s);
+    for (int k = 0; k < GROUPS; ++k) {
+        const int d = d0 + k * S::CG + warp * CW + c;
+        float w[4];
+        unpack2(dA[k][0], w[0], w[1]);
+        unpack2(dA[k][1], w[2], w[3]);
+        if (d < p.D) store_states(out + (long long)d * p.N, w, n0, p.N);
+    }
+
+    // ---- outputs, token by token of this thread's four channels
+    __syncthreads();
+    const int nl = p.D - ds;
+    float pd[4] = {0.f, 0.f, 0.f, 0.f}, pb[4] = {0.f, 0.f, 0.f, 0.f}, skip[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) skip[k] = p.Dskip && ds + k < p.D ? p.Dskip[ds + k] : 0.f;
+    T *dx = static_cast<T *>(p.dx) + row * p.ld_dx + ds, *dd = static_cast<T *>(p.ddelta) + row * p.ld_ddelta + ds;
+    T *dz = static_cast<T *>(p.dz) + row * p.ld_dz + ds;
+    if (g.len > 0 && nl > 0)
+#pragma unroll 2
+        for (int k = 0; k < K; ++k) {
+            const int t = r0 + k * ROWS;
+            const bool in = t < g.len;
+            const long long tl = min(t, g.len - 1);
+            float xv[4], dv[4], yv[4], zv[4], ox[4], od[4], oz[4];
+            load_four<T, XV>(xv, x + tl * p.ld_x, last);
+            load_four<T, XV>(dv, delta + tl * p.ld_delta, last);
+            load_four<T, XV>(yv, dy + tl * p.ld_dy, last);
+            load_four<T, XV>(zv, z + tl * ldz, last);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const float2 w = sm.du[t][4 * q + s];
+                const float sz = sigmoid(zv[s]), gy = p.z ? yv[s] * zv[s] * sz : yv[s];
+                const float sd = p.softplus ? sigmoid(dv[s] + bias[s]) : 1.f;
+                ox[s] = fmaf(w.y, w.x, skip[s] * gy);
+                od[s] = fmaf(w.y, xv[s], sm.g[t][4 * q + s] * kLn2) * sd;
+                oz[s] = yv[s] * fmaf(skip[s], xv[s], sm.y[t][4 * q + s]) * sz * fmaf(zv[s], 1.f - sz, 1.f);
+                pd[s] = in ? fmaf(gy, xv[s], pd[s]) : pd[s];
+                pb[s] = in ? pb[s] + od[s] : pb[s];
+            }
+            if (in) {
+                store_four<T, XV>(dx + tl * p.ld_dx, ox, nl);
+                store_four<T, XV>(dd + tl * p.ld_ddelta, od, nl);
+                if (p.z) store_four<T, XV>(dz + tl * p.ld_dz, oz, nl);
+            }
         }
-        if (d >= p.D) continue;
-        const float4 w = S.dA[k][tid];
-        const float dA[4] = {w.x, w.y, w.z, w.w};
-        float *out = p.part_par + slot * ((long long)p.D * (p.N + 2));
-        store_states(out + (long long)d * p.N, dA, n0, p.N);
-        if (i == 0) {
-            out[(long long)p.D * p.N + d] = par.x;
-            out[(long long)p.D * (p.N + 1) + d] = par.y;
-        }
+    // dD and dbias over the block's tokens
+    float *part = &sm.red[0][0];                 // [ROWS][CH][2]
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        part[(r0 * CH + 4 * q + s) * 2] = pd[s];
+        part[(r0 * CH + 4 * q + s) * 2 + 1] = pb[s];
+    }
+    __syncthreads();
+    for (int u = tid; u < 2 * CH; u += kGradThreads) {
+        const int d = d0 + u / 2;
+        float s = 0.f;
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) s += part[r * CH * 2 + u];
+        if (d < p.D) out[(long long)p.D * (p.N + (u & 1)) + d] = s;
     }
 }
 
@@ -405,59 +516,70 @@ __global__ void __launch_bounds__(256) scan_clear_kernel(ScanParams p, long long
     for (long long k = threadIdx.x; k < per; k += 256) p.part_par[blockIdx.x * per + k] = 0.f;
 }
 
-template <class T, int L> cudaError_t segments_launch(const ScanParams &p, bool grad, cudaStream_t s) {
-    constexpr int CH = 4 * (32 / L), NP = 4 * L;
-    const int cb = (p.D + CH - 1) / CH;
-    const long long blocks = scan_slots(p, p.seg) * cb;
-    const long long bblocks = ((long long)p.B * p.D * NP + 127) / 128;
+// Four channels per access where every array that is read or written allows it.
+template <class T> bool local_xv(const ScanParams &p) {
+    const size_t es = sizeof(T), n = 4 * es;
+    return p.D % 4 == 0 && rows_aligned(p.x, p.ld_x, es, n) && rows_aligned(p.delta, p.ld_delta, es, n) &&
+           rows_aligned(p.z, p.ld_z, es, n) && rows_aligned(p.dy, p.ld_dy, es, n);
+}
+template <class T> bool grad_xv(const ScanParams &p) {
+    const size_t es = sizeof(T), n = 4 * es;
+    return local_xv<T>(p) && rows_aligned(p.dx, p.ld_dx, es, n) && rows_aligned(p.ddelta, p.ld_ddelta, es, n) &&
+           rows_aligned(p.dz, p.ld_dz, es, n);
+}
+
+template <class T, int L, int NS, bool GRAD, bool XV> cudaError_t local_start(const ScanParams &p, cudaStream_t s) {
+    using S = LocalTiles<L, NS>;
+    const int cb = (p.D + S::CH - 1) / S::CH;
+    const long long blocks = scan_slots(p, p.lseg) * cb;
+    const long long bblocks = ((long long)p.B * p.D * S::NP + 127) / 128;
     if (blocks > 0x7fffffffLL || bblocks > 0x7fffffffLL) return cudaErrorNotSupported;
-    const bool vec = bc_vec_ok<T>(p, NP);
-    if (grad) scan_local_kernel<T, L, true><<<(unsigned)blocks, kScanThreads, 0, s>>>(p, cb, vec);
-    else scan_local_kernel<T, L, false><<<(unsigned)blocks, kScanThreads, 0, s>>>(p, cb, vec);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = cudaFuncSetAttribute(scan_local_kernel<T, L, NS, GRAD, XV>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(S));
     if (e != cudaSuccess) return e;
-    if (grad) scan_boundary_kernel<true><<<(unsigned)bblocks, 128, 0, s>>>(p, NP);
-    else scan_boundary_kernel<false><<<(unsigned)bblocks, 128, 0, s>>>(p, NP);
+    scan_local_kernel<T, L, NS, GRAD, XV><<<(unsigned)blocks, kScanThreads, sizeof(S), s>>>(p, cb, bc_vec_ok<T>(p, S::NP));
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    scan_boundary_kernel<<<dim3((unsigned)bblocks, GRAD ? 2 : 1), 128, 0, s>>>(p, S::NP);
     return cudaGetLastError();
 }
-
-template <class T> cudaError_t segments_type(const ScanParams &p, bool grad, cudaStream_t s) {
-    switch (lanes_for(p.N)) {
-    case 1: return segments_launch<T, 1>(p, grad, s);
-    case 2: return segments_launch<T, 2>(p, grad, s);
-    case 4: return segments_launch<T, 4>(p, grad, s);
-    default: return segments_launch<T, 8>(p, grad, s);
-    }
+template <class T, int L, int NS> cudaError_t local_launch(const ScanParams &p, bool grad, cudaStream_t s) {
+    const bool xv = local_xv<T>(p);
+    if (grad) return xv ? local_start<T, L, NS, true, true>(p, s) : local_start<T, L, NS, true, false>(p, s);
+    return xv ? local_start<T, L, NS, false, true>(p, s) : local_start<T, L, NS, false, false>(p, s);
 }
 
+// The states' layout in the workspace, [slots][D][padded states]: the forward takes its own padding, the
+// backward's two passes share theirs (16 or 32).
+template <class T> cudaError_t segments_type(const ScanParams &p, bool grad, cudaStream_t s) {
+    if (!grad && p.N <= 4) return local_launch<T, 1, 4>(p, grad, s);
+    if (!grad && p.N <= 8) return local_launch<T, 1, 8>(p, grad, s);
+    if (p.N <= 16) return local_launch<T, 2, 8>(p, grad, s);
+    return local_launch<T, 4, 8>(p, grad, s);
+}
+
+int grad_states(int N) { return N <= 16 ? 16 : 32; }
 int grad_blocks(const ScanParams &p) {
-    const int ch = GROUPS * 4 * (32 / lanes_for(p.N));
+    const int ch = p.N <= 16 ? GradTiles<4>::CH : GradTiles<8>::CH;
     return (p.D + ch - 1) / ch;
 }
 
 long long batch_rows(const ScanParams &p) { return (long long)(p.cu_seqlens ? 1 : p.B) * p.T; }
 
-template <class T, int L> cudaError_t grad_launch(const ScanParams &p, cudaStream_t s) {
+template <class T, int L, bool XV> cudaError_t grad_start(const ScanParams &p, cudaStream_t s) {
     const int cb = grad_blocks(p);
     const long long slots = scan_slots(p, SEG), blocks = slots * cb, rows = batch_rows(p);
     const long long out = (rows * 8 * L + 255) / 256;
     if (blocks > 0x7fffffffLL || out > 0x7fffffffLL) return cudaErrorNotSupported;
-    constexpr int smem = sizeof(GradShared) + sizeof(GradTiles<T, L>);
-    cudaError_t e = cudaFuncSetAttribute(scan_grad_kernel<T, L>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    constexpr int smem = sizeof(GradTiles<L>);
+    cudaError_t e = cudaFuncSetAttribute(scan_grad_kernel<T, L, XV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    scan_grad_kernel<T, L><<<(unsigned)blocks, kScanThreads, smem, s>>>(p, cb, bc_vec_ok<T>(p, 4 * L));
+    scan_grad_kernel<T, L, XV><<<(unsigned)blocks, kGradThreads, smem, s>>>(p, cb, bc_vec_ok<T>(p, 4 * L));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     scan_bc_kernel<T><<<(unsigned)out, 256, 0, s>>>(p, cb, 4 * L, rows);
     return cudaGetLastError();
 }
-
 template <class T> cudaError_t grad_type(const ScanParams &p, cudaStream_t s) {
-    switch (lanes_for(p.N)) {
-    case 1: return grad_launch<T, 1>(p, s);
-    case 2: return grad_launch<T, 2>(p, s);
-    case 4: return grad_launch<T, 4>(p, s);
-    default: return grad_launch<T, 8>(p, s);
-    }
+    if (p.N <= 16) return grad_xv<T>(p) ? grad_start<T, 4, true>(p, s) : grad_start<T, 4, false>(p, s);
+    return grad_xv<T>(p) ? grad_start<T, 8, true>(p, s) : grad_start<T, 8, false>(p, s);
 }
 
 }  // namespace
@@ -469,12 +591,12 @@ cudaError_t launch_scan_segments(const ScanParams &p, bool bf, bool grad, cudaSt
 // Workspace: [slots][D][NP] x 2, [slots][D], [slots][D (N + 2)], [channel blocks][rows][2 NP].
 // The first two and the last are read and written four floats at a time and lie first.
 size_t ssm_scan_bwd_floats(const ScanParams &p) {
-    const size_t slots = (size_t)scan_slots(p, SEG), NP = 4 * lanes_for(p.N);
+    const size_t slots = (size_t)scan_slots(p, SEG), NP = grad_states(p.N);
     return slots * p.D * (2 * NP + 1 + p.N + 2) + (size_t)grad_blocks(p) * batch_rows(p) * 2 * NP;
 }
 
 void ssm_scan_bwd_carve(ScanParams &p, float *ws) {
-    const size_t slots = (size_t)scan_slots(p, SEG), NP = 4 * lanes_for(p.N);
+    const size_t slots = (size_t)scan_slots(p, SEG), NP = grad_states(p.N);
     p.seg_state = ws;
     p.seg_grad = p.seg_state + slots * p.D * NP;
     p.part_bc = p.seg_grad + slots * p.D * NP;
@@ -484,7 +606,7 @@ void ssm_scan_bwd_carve(ScanParams &p, float *ws) {
 
 cudaError_t launch_ssm_scan_bwd(const ScanParams &q, bool bf, cudaStream_t s) {
     ScanParams p = q;
-    p.seg = SEG;
+    p.seg = p.lseg = SEG;
     cudaError_t e = launch_scan_segments(p, bf, true, s);
     if (e != cudaSuccess) return e;
     const long long slots = scan_slots(p, SEG), per = (long long)p.D * (p.N + 2);

@@ -262,7 +262,8 @@ __global__ void __launch_bounds__(16 * KT + kScanThreads) scan_fwd_kernel(ScanPa
         for (int k = 0; k < NS; ++k) av[k] = hv[k] = 0.f;
         if (live) {
             load_states(av, p.A + (long long)d * p.N, n0, p.N);
-            if (p.seg_state) load_states(hv, p.seg_state + (slot * p.D + d) * NP, n0, NP);
+            if (p.seg_state)
+                load_states(hv, p.seg_state + (slot_at(p.cu_seqlens, p.T, p.lseg, g.b, g.t0) * p.D + d) * NP, n0, NP);
             else if (p.h0) load_states(hv, p.h0 + ((long long)g.b * p.D + d) * p.N, n0, p.N);
         }
 #pragma unroll
@@ -446,18 +447,33 @@ template <class T> cudaError_t step_type(const ScanParams &p, cudaStream_t s) {
 
 }  // namespace
 
-int ssm_scan_fwd_segment(const ScanParams &p) { return p.T; }
+// Whole sequences while their blocks (of 128 / lanes channels) fill half of the SMs: at B 4, D 2048
+// (128 blocks on 152 SMs) splitting in two costs more than it gives.  Below that every sequence is cut
+// so that the blocks fill the SMs once, at segments of 256 tokens or more: the local pass over all
+// tokens and two more launches cost about half of an unsplit pass with every SM busy.  The lengths
+// of packed sequences are not known here: they are taken to be as uneven as they can be, up to four
+// blocks per SM.
+int ssm_scan_fwd_segment(const ScanParams &p) {
+    const int ch = p.N <= 8 ? 128 : p.N <= 16 ? 64 : 32, sms = sm_count();
+    const long long cb = (p.D + ch - 1) / ch, blocks = cb * p.B;
+    if (p.cu_seqlens ? blocks > 4LL * sms && p.B > 1 : 2 * blocks > sms) return p.T;
+    const long long cuts = p.cu_seqlens ? sms / cb : sms / blocks;   // segments in all, or per sequence
+    if (cuts < 2) return p.T;
+    long long seg = (p.T + cuts - 1) / cuts;
+    seg = (seg + kFwdLocal - 1) / kFwdLocal * kFwdLocal;
+    if (seg < 256) seg = 256;
+    return 2 * seg > p.T + seg / 2 ? p.T : (int)seg;
+}
 
 size_t ssm_scan_fwd_floats(const ScanParams &p) {
-    const int seg = ssm_scan_fwd_segment(p);
-    if (seg >= p.T) return 0;
-    return (size_t)scan_slots(p, seg) * p.D * (4 * lanes_for(p.N) + 1);
+    if (ssm_scan_fwd_segment(p) >= p.T) return 0;
+    return (size_t)scan_slots(p, kFwdLocal) * p.D * (padded_states(p.N) + 1);
 }
 
 void ssm_scan_fwd_carve(ScanParams &p, float *ws) {
-    const size_t slots = (size_t)scan_slots(p, p.seg);
+    p.lseg = kFwdLocal;
     p.seg_state = ws;
-    p.seg_dt = ws + slots * p.D * 4 * lanes_for(p.N);
+    p.seg_dt = ws + (size_t)scan_slots(p, kFwdLocal) * p.D * padded_states(p.N);
 }
 
 cudaError_t launch_ssm_scan_fwd(const ScanParams &p, bool bf, cudaStream_t s) {
