@@ -14,12 +14,11 @@
 namespace mixer {
 namespace {
 
-// Sum over the TPR threads of a row of two values.  TPR = 32: one warp; otherwise the whole block.
+// Sum of two values over a block of TPR threads.
 template <int TPR>
 __device__ __forceinline__ float2 row_sum2(float2 v, float2 *sm) {
     v.x = warp_sum(v.x);
     v.y = warp_sum(v.y);
-    if (TPR == 32) return v;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __syncthreads();                       // the previous sum has been read
     if (lane == 0) sm[warp] = v;
@@ -33,55 +32,175 @@ __device__ __forceinline__ float2 row_sum2(float2 v, float2 *sm) {
     return r;
 }
 
-// One row per TPR threads, the row packed in registers: thread i holds vectors i, i + TPR, ...
-template <class T, int V, int ITEMS, int TPR>
-__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) norm_fwd_kernel(NormParams p) {
-    __shared__ float2 sm[TPR / 32];
-    constexpr int ROWS = TPR == 32 ? 4 : 1;
-    const int tid = TPR == 32 ? threadIdx.x & 31 : threadIdx.x;
-    const long long row = (long long)blockIdx.x * ROWS + (TPR == 32 ? threadIdx.x >> 5 : 0);
-    if (row >= p.rows) return;             // whole warps (TPR = 32) or the whole block
+// Sums of N values (a power of two, at most 8) over a block of TPR threads: every thread ends with all of
+// them.  A warp folds the values and its lanes into each other (half as many values at each step), so
+// several rows cost hardly more than one.
+template <int N, int TPR>
+__device__ __forceinline__ void block_sums(float (&v)[N], float (*sm)[N]) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int n = N, base = 0;
+#pragma unroll
+    for (int s = 16; s; s >>= 1) {
+        if (n > 1) {
+            n /= 2;
+            const bool up = lane & s;
+            if (up) base += n;
+#pragma unroll
+            for (int k = 0; k < N / 2; ++k)
+                if (k < n) {
+                    const float send = up ? v[k] : v[k + n], keep = up ? v[k + n] : v[k];
+                    v[k] = keep + __shfl_xor_sync(~0u, send, s);
+                }
+        } else {
+            v[0] += __shfl_xor_sync(~0u, v[0], s);
+        }
+    }
+    __syncthreads();                       // the previous sums have been read
+    if ((lane & (32 / N - 1)) == 0) sm[warp][base] = v[0];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        v[k] = 0.f;
+#pragma unroll
+        for (int w = 0; w < TPR / 32; ++w) v[k] += sm[w][k];
+    }
+}
+
+// Short rows: one per warp, lane i with vectors i and i + 32.
+template <class T, int V, int ITEMS>
+__global__ void __launch_bounds__(128) norm_fwd_warp_kernel(NormParams p) {
+    constexpr int P = (V + 1) / 2;
+    const int lane = threadIdx.x & 31, nv = p.D / V;       // V divides D
+    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (row >= p.rows) return;
     const T *x = static_cast<const T *>(p.x) + row * p.ld_x;
     T *y = static_cast<T *>(p.y) + row * p.ld_y;
-    const int nv = p.D / V;                // V divides D
-    Vec<T, V> v[ITEMS];
-    float s = 0.f;
+    Lanes<T, V> in[ITEMS];
+    f2 v[ITEMS][P], acc = both(0.f);
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) in[k].load(x + (size_t)min(lane + k * 32, nv - 1) * V);
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k)
-        if (tid + k * TPR < nv) v[k] = load_vec<T, V>(x + (size_t)(tid + k * TPR) * V);
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+            v[k][e] = in[k].pair(e);
+            if (lane + k * 32 < nv) acc = add2(acc, v[k][e]);
+        }
+    const float mean = warp_sum(pair_sum<V>(acc)) / (float)p.D;
+    acc = both(0.f);
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k)
-        if (tid + k * TPR < nv)
 #pragma unroll
-            for (int e = 0; e < V; ++e) s += to_f(v[k].e[e]);
-    const float mean = row_sum2<TPR>(make_float2(s, 0.f), sm).x / (float)p.D;
-    float q = 0.f;
-#pragma unroll
-    for (int k = 0; k < ITEMS; ++k)
-        if (tid + k * TPR < nv)
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float c = to_f(v[k].e[e]) - mean;
-                q = fmaf(c, c, q);
-            }
-    const float rstd = 1.f / sqrtf(row_sum2<TPR>(make_float2(q, 0.f), sm).x / (float)p.D + p.eps);
-    if (tid == 0) {
+        for (int e = 0; e < P; ++e) {
+            v[k][e] = add2(v[k][e], both(-mean));
+            if (lane + k * 32 < nv) acc = fma2(v[k][e], v[k][e], acc);
+        }
+    const float rstd = 1.f / sqrtf(warp_sum(pair_sum<V>(acc)) / (float)p.D + p.eps);
+    if (lane == 0) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
     }
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k)
-        if (tid + k * TPR < nv) {
-            const int c0 = (tid + k * TPR) * V;
-            Vec<T, V> o;
+        if (lane + k * 32 < nv) {
+            const int c0 = (lane + k * 32) * V;
+            f2 w[P], b[P], o[P];
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float w = p.weight ? load_w(p.weight, c0 + e, p.w_bf16) : 1.f;
-                const float b = p.bias ? load_w(p.bias, c0 + e, p.w_bf16) : 0.f;
-                o.e[e] = from_f<T>(fmaf((to_f(v[k].e[e]) - mean) * rstd, w, b));
+            for (int e = 0; e < P; ++e) {
+                w[e] = both(1.f);
+                b[e] = both(0.f);
             }
-            store_vec<T, V>(y + c0, o);
+            if (p.weight) load_param_pairs<V>(w, p.weight, c0, p.w_bf16);
+            if (p.bias) load_param_pairs<V>(b, p.bias, c0, p.w_bf16);
+#pragma unroll
+            for (int e = 0; e < P; ++e) o[e] = fma2(mul2(v[k][e], both(rstd)), w[e], b[e]);
+            store_lanes<T, V>(y + c0, o);
         }
+}
+
+// Longer rows: a block owns all columns (and keeps their weights) and visits R neighbouring rows at a time,
+// their sums taken together and the next R rows on their way.  A warp per row of 2048 bfloat16 elements,
+// with the weights fetched for every row, took 33 to 56 us for 16384 rows; this takes 26.
+template <class T, int V, int ITEMS, int TPR, int R>
+__global__ void __launch_bounds__(TPR, 512 / TPR) norm_fwd_kernel(NormParams p) {
+    __shared__ float sm[TPR / 32][R];
+    constexpr int P = (V + 1) / 2;
+    const int tid = threadIdx.x, nv = p.D / V;
+    const float inv = 1.f / (float)p.D;
+    f2 w[ITEMS][P], b[ITEMS][P];
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+            w[k][e] = both(1.f);
+            b[k][e] = both(0.f);
+        }
+        const long long c = (long long)min(tid + k * TPR, nv - 1) * V;
+        if (p.weight) load_param_pairs<V>(w[k], p.weight, c, p.w_bf16);
+        if (p.bias) load_param_pairs<V>(b[k], p.bias, c, p.w_bf16);
+    }
+    Lanes<T, V> in[R][ITEMS];
+    auto fetch = [&](long long row) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {      // past the end the last row and vector again, not counted
+            const T *x = static_cast<const T *>(p.x) + (row + r < p.rows ? row + r : p.rows - 1) * p.ld_x;
+#pragma unroll
+            for (int k = 0; k < ITEMS; ++k) in[r][k].load(x + (size_t)min(tid + k * TPR, nv - 1) * V);
+        }
+    };
+    const long long step = (long long)gridDim.x * R;
+    fetch((long long)blockIdx.x * R);
+    for (long long row = (long long)blockIdx.x * R; row < p.rows; row += step) {
+        f2 v[R][ITEMS][P];
+        float s[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            f2 acc = both(0.f);
+#pragma unroll
+            for (int k = 0; k < ITEMS; ++k)
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    v[r][k][e] = in[r][k].pair(e);
+                    if (tid + k * TPR < nv) acc = add2(acc, v[r][k][e]);
+                }
+            s[r] = pair_sum<V>(acc);
+        }
+        fetch(row + step);
+        block_sums<R, TPR>(s, sm);
+        float mean[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            mean[r] = s[r] * inv;
+            f2 acc = both(0.f);
+#pragma unroll
+            for (int k = 0; k < ITEMS; ++k)
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    v[r][k][e] = add2(v[r][k][e], both(-mean[r]));
+                    if (tid + k * TPR < nv) acc = fma2(v[r][k][e], v[r][k][e], acc);
+                }
+            s[r] = pair_sum<V>(acc);
+        }
+        block_sums<R, TPR>(s, sm);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (row + r >= p.rows) break;
+            const float rstd = 1.f / sqrtf(s[r] * inv + p.eps);
+            if (tid == 0) {
+                if (p.mean) p.mean[row + r] = mean[r];
+                if (p.rstd) p.rstd[row + r] = rstd;
+            }
+            T *y = static_cast<T *>(p.y) + (row + r) * p.ld_y;
+#pragma unroll
+            for (int k = 0; k < ITEMS; ++k)
+                if (tid + k * TPR < nv) {
+                    f2 o[P];
+#pragma unroll
+                    for (int e = 0; e < P; ++e) o[e] = fma2(mul2(v[r][k][e], both(rstd)), w[k][e], b[k][e]);
+                    store_lanes<T, V>(y + (size_t)(tid + k * TPR) * V, o);
+                }
+        }
+    }
 }
 
 // Rows too long for registers: three passes over the row (the later ones from L2), 1024 threads.
@@ -111,69 +230,105 @@ __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(NormParams p) {
     }
 }
 
-// Backward: a block owns all columns and visits every gridDim.x-th row.
-template <class T, int V, int ITEMS, int TPR>
-__global__ void __launch_bounds__(TPR) norm_bwd_kernel(NormParams p) {
-    __shared__ float2 sm[TPR / 32];
+// Backward: a block owns all columns and visits R neighbouring rows at a time, their sums taken together
+// and the next R rows on their way.
+template <class T, int V, int ITEMS, int TPR, int R>
+__global__ void __launch_bounds__(TPR, 512 / TPR) norm_bwd_kernel(NormParams p) {
+    __shared__ float sm[TPR / 32][2 * R];
+    constexpr int P = (V + 1) / 2;
     const int tid = threadIdx.x, nv = p.D / V;
-    float aw[ITEMS][V], ab[ITEMS][V];
+    const float inv = 1.f / (float)p.D;
+    f2 aw[ITEMS][P], ab[ITEMS][P], w[ITEMS][P];
 #pragma unroll
-    for (int k = 0; k < ITEMS; ++k)
+    for (int k = 0; k < ITEMS; ++k) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) aw[k][e] = ab[k][e] = 0.f;
-    for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        const T *x = static_cast<const T *>(p.x) + row * p.ld_x;
-        const T *dy = static_cast<const T *>(p.dy) + row * p.ld_dy;
-        T *dx = static_cast<T *>(p.y) + row * p.ld_y;
-        const float mean = p.mean[row], rstd = p.rstd[row];
-        Vec<T, V> vx[ITEMS], vd[ITEMS];
+        for (int e = 0; e < P; ++e) {
+            aw[k][e] = ab[k][e] = both(0.f);
+            w[k][e] = both(1.f);
+        }
+        if (p.weight && tid + k * TPR < nv) load_param_pairs<V>(w[k], p.weight, (long long)(tid + k * TPR) * V, p.w_bf16);
+    }
+    Lanes<T, V> nx[R][ITEMS], nd[R][ITEMS];
+    float nm[R], nr[R];
+    auto fetch = [&](long long row) {
 #pragma unroll
-        for (int k = 0; k < ITEMS; ++k)
-            if (tid + k * TPR < nv) {
-                vx[k] = load_vec<T, V>(x + (size_t)(tid + k * TPR) * V);
-                vd[k] = load_vec<T, V>(dy + (size_t)(tid + k * TPR) * V);
+        for (int r = 0; r < R; ++r) {
+            const long long q = row + r < p.rows ? row + r : p.rows - 1;     // past the end: the last row, not counted
+            const T *x = static_cast<const T *>(p.x) + q * p.ld_x;
+            const T *dy = static_cast<const T *>(p.dy) + q * p.ld_dy;
+            nm[r] = p.mean[q];
+            nr[r] = p.rstd[q];
+#pragma unroll
+            for (int k = 0; k < ITEMS; ++k) {
+                const size_t at = (size_t)min(tid + k * TPR, nv - 1) * V;
+                nx[r][k].load(x + at);
+                nd[r][k].load(dy + at);
             }
-        float2 s = make_float2(0.f, 0.f);
+        }
+    };
+    const long long step = (long long)gridDim.x * R;
+    fetch((long long)blockIdx.x * R);
+    for (long long row = (long long)blockIdx.x * R; row < p.rows; row += step) {
+        Lanes<T, V> vx[R][ITEMS], vd[R][ITEMS];
+        float mean[R], rstd[R], s[2 * R];
 #pragma unroll
-        for (int k = 0; k < ITEMS; ++k)
-            if (tid + k * TPR < nv)
+        for (int r = 0; r < R; ++r) {
+            mean[r] = nm[r];
+            rstd[r] = nr[r];
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const int c = (tid + k * TPR) * V + e;
-                    const float d = to_f(vd[k].e[e]), xh = (to_f(vx[k].e[e]) - mean) * rstd;
-                    const float g = p.weight ? d * load_w(p.weight, c, p.w_bf16) : d;
-                    s.x += g;
-                    s.y = fmaf(g, xh, s.y);
-                    aw[k][e] = fmaf(d, xh, aw[k][e]);
-                    ab[k][e] += d;
-                }
-        s = row_sum2<TPR>(s, sm);
-        const float mg = s.x / (float)p.D, mgx = s.y / (float)p.D;
-#pragma unroll
-        for (int k = 0; k < ITEMS; ++k)
-            if (tid + k * TPR < nv) {
-                Vec<T, V> o;
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const int c = (tid + k * TPR) * V + e;
-                    const float d = to_f(vd[k].e[e]), xh = (to_f(vx[k].e[e]) - mean) * rstd;
-                    const float g = p.weight ? d * load_w(p.weight, c, p.w_bf16) : d;
-                    o.e[e] = from_f<T>(rstd * (g - mg - xh * mgx));
-                }
-                store_vec<T, V>(dx + (size_t)(tid + k * TPR) * V, o);
+            for (int k = 0; k < ITEMS; ++k) {
+                vx[r][k] = nx[r][k];
+                vd[r][k] = nd[r][k];
             }
+        }
+        fetch(row + step);
+        f2 xh[R][ITEMS][P], g[R][ITEMS][P];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            f2 s0 = both(0.f), s1 = both(0.f);
+            const f2 on = both(row + r < p.rows ? 1.f : 0.f);
+#pragma unroll
+            for (int k = 0; k < ITEMS; ++k)
+                if (tid + k * TPR < nv)
+#pragma unroll
+                    for (int e = 0; e < P; ++e) {
+                        const f2 d = mul2(vd[r][k].pair(e), on);
+                        xh[r][k][e] = mul2(add2(vx[r][k].pair(e), both(-mean[r])), both(rstd[r]));
+                        g[r][k][e] = mul2(d, w[k][e]);
+                        s0 = add2(s0, g[r][k][e]);
+                        s1 = fma2(g[r][k][e], xh[r][k][e], s1);
+                        aw[k][e] = fma2(d, xh[r][k][e], aw[k][e]);
+                        ab[k][e] = add2(ab[k][e], d);
+                    }
+            s[2 * r] = pair_sum<V>(s0);
+            s[2 * r + 1] = pair_sum<V>(s1);
+        }
+        block_sums<2 * R, TPR>(s, sm);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (row + r >= p.rows) break;
+            T *dx = static_cast<T *>(p.y) + (row + r) * p.ld_y;
+            const f2 mg = both(-s[2 * r] * inv), mgx = both(-s[2 * r + 1] * inv);
+#pragma unroll
+            for (int k = 0; k < ITEMS; ++k)
+                if (tid + k * TPR < nv) {
+                    f2 o[P];
+#pragma unroll
+                    for (int e = 0; e < P; ++e)
+                        o[e] = mul2(fma2(xh[r][k][e], mgx, add2(g[r][k][e], mg)), both(rstd[r]));
+                    store_lanes<T, V>(dx + (size_t)(tid + k * TPR) * V, o);
+                }
+        }
     }
     if (!p.part) return;
     float *part = p.part + (size_t)blockIdx.x * 2 * p.D;
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k)
-        if (tid + k * TPR < nv)
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const int c = (tid + k * TPR) * V + e;
-                part[c] = aw[k][e];
-                part[p.D + c] = ab[k][e];
-            }
+        if (tid + k * TPR < nv) {
+            const int c = (tid + k * TPR) * V;
+            store_lanes<float, V>(part + c, aw[k]);
+            store_lanes<float, V>(part + p.D + c, ab[k]);
+        }
 }
 
 // Long rows: dx in two passes over the row, and the partial sums of a block of columns over a
@@ -214,47 +369,55 @@ __global__ void __launch_bounds__(256) norm_bwd_cols_kernel(NormParams p) {
     p.part[(size_t)blockIdx.x * 2 * p.D + p.D + c] = ab;
 }
 
-constexpr int kBwdBlocks = 2 * 152;    // two blocks of 256 threads per SM visit the rows
-
-int bwd_blocks(long long rows) { return (int)(rows < kBwdBlocks ? rows : kBwdBlocks); }
+// Blocks of the backward: two of 256 threads per SM (128 registers each) visit the rows, at least four
+// each where there are that many.
+int bwd_blocks(long long rows) {
+    const long long most = 2LL * sm_count(), want = rows <= 256 ? rows : (rows + 3) / 4;
+    return (int)(want < most ? want : most);
+}
 
 template <class T> constexpr int kVec = 16 / sizeof(T);
 
 template <class T> bool vec_ok(const NormParams &p) {
     return p.D % kVec<T> == 0 && rows_aligned(p.x, p.ld_x, sizeof(T), 16) && rows_aligned(p.y, p.ld_y, sizeof(T), 16) &&
-           rows_aligned(p.dy, p.ld_dy, sizeof(T), 16);
-}
-
-template <class T, int V, int TPR>
-cudaError_t fwd_items(const NormParams &p, int items, cudaStream_t s) {
-    const unsigned grid = (unsigned)(TPR == 32 ? (p.rows + 3) / 4 : p.rows);
-    const int threads = TPR == 32 ? 128 : TPR;
-    if (items <= 1) norm_fwd_kernel<T, V, 1, TPR><<<grid, threads, 0, s>>>(p);
-    else if (items <= 2) norm_fwd_kernel<T, V, 2, TPR><<<grid, threads, 0, s>>>(p);
-    else if (items <= 4) norm_fwd_kernel<T, V, 4, TPR><<<grid, threads, 0, s>>>(p);
-    else norm_fwd_kernel<T, V, 8, TPR><<<grid, threads, 0, s>>>(p);
-    return cudaGetLastError();
+           rows_aligned(p.dy, p.ld_dy, sizeof(T), 16) &&
+           aligned_to(p.weight, 16) && aligned_to(p.bias, 16);
 }
 
 template <class T, int V> cudaError_t fwd_vec(const NormParams &p, cudaStream_t s) {
     const int nv = p.D / V;
-    if (nv <= 8 * 32) return fwd_items<T, V, 32>(p, (nv + 31) / 32, s);
-    if (nv <= 8 * 256) return fwd_items<T, V, 256>(p, (nv + 255) / 256, s);
-    norm_fwd_long_kernel<T><<<(unsigned)p.rows, 1024, 0, s>>>(p);
+    if (nv <= 64) {
+        const unsigned grid = (unsigned)((p.rows + 3) / 4);
+        if (nv <= 32) norm_fwd_warp_kernel<T, V, 1><<<grid, 128, 0, s>>>(p);
+        else norm_fwd_warp_kernel<T, V, 2><<<grid, 128, 0, s>>>(p);
+        return cudaGetLastError();
+    }
+    if (nv > (V == 1 ? 8 : 4) * 512) {
+        norm_fwd_long_kernel<T><<<(unsigned)p.rows, 1024, 0, s>>>(p);
+        return cudaGetLastError();
+    }
+    // two blocks of 256 threads (or one of 512) per SM; four rows at a time where there are rows enough
+    const long long most = (nv <= 512 ? 2LL : 1LL) * sm_count();
+    const unsigned blocks = (unsigned)(p.rows < most ? p.rows : most);
+    if (nv <= 256 && p.rows >= 4 * most) norm_fwd_kernel<T, V, 1, 256, 4><<<blocks, 256, 0, s>>>(p);
+    else if (nv <= 256) norm_fwd_kernel<T, V, 1, 256, 1><<<blocks, 256, 0, s>>>(p);
+    else if (nv <= 512) norm_fwd_kernel<T, V, 2, 256, 1><<<blocks, 256, 0, s>>>(p);
+    else if (nv <= 1024) norm_fwd_kernel<T, V, 2, 512, 1><<<blocks, 512, 0, s>>>(p);
+    else if (nv <= 2048) norm_fwd_kernel<T, V, 4, 512, 1><<<blocks, 512, 0, s>>>(p);
+    else if constexpr (V == 1) norm_fwd_kernel<T, V, 8, 512, 1><<<blocks, 512, 0, s>>>(p);
     return cudaGetLastError();
 }
 
-template <class T, int V, int TPR>
-void bwd_items(const NormParams &p, int items, int blocks, cudaStream_t s) {
-    if (items <= 1) norm_bwd_kernel<T, V, 1, TPR><<<blocks, TPR, 0, s>>>(p);
-    else if (items <= 2) norm_bwd_kernel<T, V, 2, TPR><<<blocks, TPR, 0, s>>>(p);
-    else norm_bwd_kernel<T, V, 4, TPR><<<blocks, TPR, 0, s>>>(p);
-}
-
+// Rows at a time: two while a thread has one vector of each; 512 threads where 256 would run out of
+// registers.
 template <class T, int V> cudaError_t bwd_vec(const NormParams &p, cudaStream_t s) {
     const int nv = p.D / V, blocks = bwd_blocks(p.rows);
-    if (nv <= 4 * 256) {
-        bwd_items<T, V, 256>(p, (nv + 255) / 256, blocks, s);
+    if (nv <= (V == 1 ? 8 : 2) * 512) {
+        if (nv <= 256 && p.rows > blocks) norm_bwd_kernel<T, V, 1, 256, 2><<<blocks, 256, 0, s>>>(p);
+        else if (nv <= 256) norm_bwd_kernel<T, V, 1, 256, 1><<<blocks, 256, 0, s>>>(p);
+        else if (nv <= 512) norm_bwd_kernel<T, V, 2, 256, 1><<<blocks, 256, 0, s>>>(p);
+        else if (nv <= 1024) norm_bwd_kernel<T, V, 2, 512, 1><<<blocks, 512, 0, s>>>(p);
+        else if constexpr (V == 1) norm_bwd_kernel<T, V, 8, 512, 1><<<blocks, 512, 0, s>>>(p);
     } else {
         norm_bwd_long_kernel<T><<<(unsigned)p.rows, 1024, 0, s>>>(p);
         if (p.part) norm_bwd_cols_kernel<T><<<dim3(blocks, (p.D + 255) / 256), 256, 0, s>>>(p);

@@ -3,32 +3,33 @@
 
 namespace mixer {
 
-// 32 columns x 8 groups of rows per block.  A few MB at most, from L2: latency bound, so the
+// 32 columns x 32 groups of rows per block.  A few MB at most, from L2: bound by latency, so the
 // groups run side by side and each thread keeps four loads in flight.
-__global__ void __launch_bounds__(256) sum_rows_kernel(const float *part, int rows, long long cols, SumOut o0, SumOut o1,
-                                                       SumOut o2) {
-    __shared__ float sm[8][33];
+__global__ void __launch_bounds__(1024) sum_rows_kernel(const float *part, int rows, long long cols, SumOut o0, SumOut o1,
+                                                        SumOut o2) {
+    __shared__ float sm[32][33];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const long long c = (long long)blockIdx.x * 32 + tx;
     float s = 0.f;
     if (c < cols) {
+        const float *p = part + c;
         float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
         int r = ty;
-        for (; r + 24 < rows; r += 32) {
-            a0 += part[(long long)r * cols + c];
-            a1 += part[(long long)(r + 8) * cols + c];
-            a2 += part[(long long)(r + 16) * cols + c];
-            a3 += part[(long long)(r + 24) * cols + c];
+        for (; r + 96 < rows; r += 128) {
+            a0 += p[(long long)r * cols];
+            a1 += p[(long long)(r + 32) * cols];
+            a2 += p[(long long)(r + 64) * cols];
+            a3 += p[(long long)(r + 96) * cols];
         }
-        for (; r < rows; r += 8) a0 += part[(long long)r * cols + c];
+        for (; r < rows; r += 32) a0 += p[(long long)r * cols];
         s = (a0 + a1) + (a2 + a3);
     }
     sm[ty][tx] = s;
     __syncthreads();
-    if (ty == 0 && c < cols) {
-#pragma unroll
-        for (int k = 1; k < 8; ++k) s += sm[k][tx];
-        long long i = c;
+    s = warp_sum(sm[tx][ty]);            // warp ty: column ty's 32 groups
+    const long long k = (long long)blockIdx.x * 32 + ty;
+    if (tx == 0 && k < cols) {
+        long long i = k;
         if (i < o0.cols) {
             if (o0.out) store_w(o0.out, i, o0.bf16, s);
         } else if ((i -= o0.cols) < o1.cols) {
@@ -42,7 +43,7 @@ __global__ void __launch_bounds__(256) sum_rows_kernel(const float *part, int ro
 cudaError_t launch_sum_rows(const float *part, int rows, SumOut o0, SumOut o1, SumOut o2, cudaStream_t s) {
     const long long cols = o0.cols + o1.cols + o2.cols;
     if (cols <= 0) return cudaSuccess;
-    sum_rows_kernel<<<(unsigned)((cols + 31) / 32), 256, 0, s>>>(part, rows, cols, o0, o1, o2);
+    sum_rows_kernel<<<(unsigned)((cols + 31) / 32), 1024, 0, s>>>(part, rows, cols, o0, o1, o2);
     return cudaGetLastError();
 }
 

@@ -13,187 +13,243 @@
 namespace mixer {
 namespace {
 
-template <class T, int V> __device__ __forceinline__ void load_f(float (&o)[V], const T *p) {
-    const Vec<T, V> v = load_vec<T, V>(p);
-#pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = to_f(v.e[e]);
-}
-template <class T, int V> __device__ __forceinline__ void store_f(T *p, const float (&o)[V]) {
-    Vec<T, V> v;
-#pragma unroll
-    for (int e = 0; e < V; ++e) v.e[e] = from_f<T>(o[e]);
-    store_vec<T, V>(p, v);
-}
-
-// Input at position t of a sequence: its tokens, then (t < 0) the initial state, then zeros.
+// Input at position t of a sequence as pairs: its tokens, then (t < 0) the initial state, then zeros.
 template <class T, int W, int V>
-__device__ __forceinline__ void load_input(float (&o)[V], const ConvParams &p, const Segment &g, int t, int c) {
-    if (t >= 0)
-        load_f<T, V>(o, static_cast<const T *>(p.x) + (g.row0 + t) * p.ld_x + c);
-    else if (p.h0)
-        load_f<T, V>(o, static_cast<const T *>(p.h0) + ((long long)g.b * (W - 1) + t + W - 1) * p.D + c);
-    else
+__device__ __forceinline__ void load_input(f2 (&o)[(V + 1) / 2], const ConvParams &p, const Segment &g, int t, int c) {
+    Lanes<T, V> v;
+    if (t >= 0) v.load(static_cast<const T *>(p.x) + (g.row0 + t) * p.ld_x + c);
+    else if (p.h0) v.load(static_cast<const T *>(p.h0) + ((long long)g.b * (W - 1) + t + W - 1) * p.D + c);
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = 0.f;
+    for (int e = 0; e < (V + 1) / 2; ++e) o[e] = t >= 0 || p.h0 ? v.pair(e) : both(0.f);
 }
 
+// The taps and bias of V channels as pairs: V W neighbouring parameters, in accesses of V.
 template <int W, int V>
-__device__ __forceinline__ void load_taps(float (&w)[W][V], float (&b)[V], const ConvParams &p, int c) {
+__device__ __forceinline__ void load_taps(f2 (&w)[W][(V + 1) / 2], f2 (&b)[(V + 1) / 2], const ConvParams &p, int c) {
+    float q[W][V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
+    for (int j = 0; j < W; ++j) load_params<V>(q[j], p.weight, (long long)c * W + j * V, p.w_bf16);
 #pragma unroll
-        for (int j = 0; j < W; ++j) w[j][e] = load_w(p.weight, (long long)(c + e) * W + j, p.w_bf16);
-        b[e] = p.bias ? load_w(p.bias, c + e, p.w_bf16) : 0.f;
+    for (int e = 0; e < (V + 1) / 2; ++e) {
+        const int lo = 2 * e, hi = V == 1 ? 0 : 2 * e + 1;
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[j][e] = pack2(q[(lo * W + j) / V][(lo * W + j) % V], q[(hi * W + j) / V][(hi * W + j) % V]);
+        b[e] = both(0.f);
     }
+    if (p.bias) load_param_pairs<V>(b, p.bias, c, p.w_bf16);
 }
 
 template <class T, int W, int V>
-__global__ void __launch_bounds__(128) conv_fwd_kernel(ConvParams p, long long slots) {
+__global__ void __launch_bounds__(128, 4) conv_fwd_kernel(ConvParams p, long long slots) {
+    constexpr int P = (V + 1) / 2;
     const int groups = p.D / V;
     const long long u = (long long)blockIdx.x * 128 + threadIdx.x;
     const long long slot = u / groups;
     const int c = (int)(u - slot * groups) * V;
     Segment g;
     if (slot >= slots || !segment_of(p.cu_seqlens, p.B, p.T, p.seg, slot, g)) return;
-    float w[W][V], bias[V], win[W][V];
+    f2 w[W][P], bias[P], win[W][P];
     load_taps<W, V>(w, bias, p, c);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) load_input<T, W, V>(win[j], p, g, g.t0 - (W - 1) + j, c);
     const T *x = static_cast<const T *>(p.x) + (g.row0 + g.t0) * p.ld_x + c;
     T *y = static_cast<T *>(p.y) + (g.row0 + g.t0) * p.ld_y + c;
-    for (int t0 = 0; t0 < g.len; t0 += 4) {
-        Vec<T, V> in[4];
+    // four rows at a time, the next four on their way (past the end the last row again, without a branch)
+    Lanes<T, V> in[4], next[4];
+    if (g.len > 0)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) next[k].load(x + min(k, g.len - 1) * p.ld_x);
+    for (int left = g.len; left > 0; left -= 4) {
+        x += 4 * p.ld_x;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            in[k] = next[k];
+            next[k].load(x + min(k, left - 5) * p.ld_x);       // (at or before the last row)
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (t0 + k < g.len) in[k] = load_vec<T, V>(x + (t0 + k) * p.ld_x);
+            if (k < left) {
+                f2 o[P];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (t0 + k < g.len) {
-                float o[V];
+                for (int e = 0; e < P; ++e) {
+                    win[W - 1][e] = in[k].pair(e);
+                    f2 pre = bias[e];
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    win[W - 1][e] = to_f(in[k].e[e]);
-                    float pre = bias[e];
-#pragma unroll
-                    for (int j = 0; j < W; ++j) pre = fmaf(w[j][e], win[j][e], pre);
-                    o[e] = p.silu ? pre * sigmoid(pre) : pre;
+                    for (int j = 0; j < W; ++j) pre = fma2(w[j][e], win[j][e], pre);
+                    o[e] = p.silu ? silu2(pre) : pre;
 #pragma unroll
                     for (int j = 0; j < W - 1; ++j) win[j][e] = win[j + 1][e];
                 }
-                store_f<T, V>(y + (t0 + k) * p.ld_y, o);
+                store_lanes<T, V>(y, o);
+                y += p.ld_y;
             }
     }
     if (p.ht && g.i == g.n - 1)     // the last inputs, the state's among them after a short sequence
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
-            store_f<T, V>(static_cast<T *>(p.ht) + ((long long)g.b * (W - 1) + j) * p.D + c, win[j]);
+            store_lanes<T, V>(static_cast<T *>(p.ht) + ((long long)g.b * (W - 1) + j) * p.D + c, win[j]);
 }
 
 // Backward of V channels of one segment: tokens t0 .. t0 + len + W - 2, the last W - 1 of which
 // belong to the next segment (their dpre is computed there again for dw and dbias).
-// blockDim = (32 channel groups, 4 segments); the four partial sums are joined in shared memory.
+// A block: 32 channel groups, 4 segments; the four partial sums are joined in shared memory.
 template <class T, int W, int V>
-__global__ void __launch_bounds__(128) conv_bwd_kernel(ConvParams p, long long slots) {
-    __shared__ float sm[3][(W + 1) * V][33];
+__global__ void __launch_bounds__(128, 3) conv_bwd_kernel(ConvParams p, long long slots) {
+    constexpr int P = (V + 1) / 2;
+    __shared__ f2 sm[3][(W + 1) * P][33];
     const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
     const int groups = p.D / V, gx = (groups + 31) / 32;
     const long long by = blockIdx.x / gx;
     const int grp = (int)(blockIdx.x - by * gx) * 32 + lane;
     const int c = grp * V;
     const long long slot = by * 4 + row;
-    float dw[W][V], db[V];
+    f2 dw[W][P], db[P];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        db[e] = 0.f;
+    for (int e = 0; e < P; ++e) {
+        db[e] = both(0.f);
 #pragma unroll
-        for (int j = 0; j < W; ++j) dw[j][e] = 0.f;
+        for (int j = 0; j < W; ++j) dw[j][e] = both(0.f);
     }
     Segment g;
     if (grp < groups && slot < slots && segment_of(p.cu_seqlens, p.B, p.T, p.seg, slot, g)) {
-        float w[W][V], bias[V], win[W][V], dp[W][V];     // dp[i]: dpre of token t - (W - 1) + i
+        f2 w[W][P], bias[P], win[W][P], dp[W][P];     // dp[i]: dpre of token t - (W - 1) + i
         load_taps<W, V>(w, bias, p, c);
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) load_input<T, W, V>(win[j], p, g, g.t0 - (W - 1) + j, c);
 #pragma unroll
         for (int j = 0; j < W; ++j)
 #pragma unroll
-            for (int e = 0; e < V; ++e) dp[j][e] = 0.f;
-        const int end = g.t0 + g.len + W - 1;
-        for (int t = g.t0; t < end; ++t) {
-            if (t < g.total) {
-                float dy[V];
-                load_f<T, V>(win[W - 1], static_cast<const T *>(p.x) + (g.row0 + t) * p.ld_x + c);
-                load_f<T, V>(dy, static_cast<const T *>(p.dy) + (g.row0 + t) * p.ld_dy + c);
+            for (int e = 0; e < P; ++e) dp[j][e] = both(0.f);
+        const T *x = static_cast<const T *>(p.x) + (g.row0 + g.t0) * p.ld_x + c;
+        const T *gy = static_cast<const T *>(p.dy) + (g.row0 + g.t0) * p.ld_dy + c;
+        T *dx = static_cast<T *>(p.y) + (g.row0 + g.t0) * p.ld_y + c;
+        // dpre of token t from its input and dy
+        auto dpre = [&](const Lanes<T, V> &xi, const Lanes<T, V> &di, bool mine) {
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    float d = dy[e];
-                    if (p.silu) {
-                        float pre = bias[e];
+            for (int e = 0; e < P; ++e) {
+                win[W - 1][e] = xi.pair(e);
+                f2 d = di.pair(e);
+                if (p.silu) {
+                    f2 pre = bias[e];
 #pragma unroll
-                        for (int j = 0; j < W; ++j) pre = fmaf(w[j][e], win[j][e], pre);
-                        const float sg = sigmoid(pre);
-                        d *= sg * fmaf(pre, 1.f - sg, 1.f);
-                    }
-                    dp[W - 1][e] = d;
-                    if (t < g.t0 + g.len) {
-                        db[e] += d;
-#pragma unroll
-                        for (int j = 0; j < W; ++j) dw[j][e] = fmaf(d, win[j][e], dw[j][e]);
-                    }
+                    for (int j = 0; j < W; ++j) pre = fma2(w[j][e], win[j][e], pre);
+                    const f2 sg = sigmoid2(pre);      // SiLU' = sg (1 + pre (1 - sg))
+                    d = mul2(mul2(d, sg), fma2(pre, fma2(sg, both(-1.f), both(1.f)), both(1.f)));
                 }
-            } else {
+                dp[W - 1][e] = d;
+                if (mine) {
+                    db[e] = add2(db[e], d);
 #pragma unroll
-                for (int e = 0; e < V; ++e) dp[W - 1][e] = win[W - 1][e] = 0.f;
+                    for (int j = 0; j < W; ++j) dw[j][e] = fma2(d, win[j][e], dw[j][e]);
+                }
             }
-            const int q = t - (W - 1);                   // its gradient is complete now
-            if (q >= g.t0 || (g.i == 0 && q < 0 && p.dh0)) {
-                float o[V];
+        };
+        // the gradient of position t - (W - 1), complete now
+        auto gradient = [&](f2 (&o)[P]) {
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    o[e] = 0.f;
+            for (int e = 0; e < P; ++e) {
+                o[e] = mul2(w[W - 1][e], dp[0][e]);
 #pragma unroll
-                    for (int i = 0; i < W; ++i) o[e] = fmaf(w[W - 1 - i][e], dp[i][e], o[e]);
-                }
-                const int k = q - (g.total - (W - 1));   // its place in the final state
-                if (p.dht && k >= 0) {
-                    float h[V];
-                    load_f<T, V>(h, static_cast<const T *>(p.dht) + ((long long)g.b * (W - 1) + k) * p.D + c);
-#pragma unroll
-                    for (int e = 0; e < V; ++e) o[e] += h[e];
-                }
-                if (q >= 0)
-                    store_f<T, V>(static_cast<T *>(p.y) + (g.row0 + q) * p.ld_y + c, o);
-                else
-                    store_f<T, V>(static_cast<T *>(p.dh0) + ((long long)g.b * (W - 1) + q + W - 1) * p.D + c, o);
+                for (int i = 1; i < W; ++i) o[e] = fma2(w[W - 1 - i][e], dp[i][e], o[e]);
             }
+        };
+        auto shift = [&] {
 #pragma unroll
             for (int j = 0; j < W - 1; ++j)
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
+                for (int e = 0; e < P; ++e) {
                     win[j][e] = win[j + 1][e];
                     dp[j][e] = dp[j + 1][e];
                 }
+        };
+        // where the gradient of position q goes: its row, or the initial state's (nowhere before another segment)
+        auto put = [&](int q, f2 (&o)[P]) {
+            const int h = q - (g.total - (W - 1));       // its place in the final state
+            if (p.dht && h >= 0) {
+                Lanes<T, V> v;
+                v.load(static_cast<const T *>(p.dht) + ((long long)g.b * (W - 1) + h) * p.D + c);
+#pragma unroll
+                for (int e = 0; e < P; ++e) o[e] = add2(o[e], v.pair(e));
+            }
+            if (q >= g.t0) store_lanes<T, V>(dx + (q - g.t0) * p.ld_y, o);
+            else if (q < 0 && p.dh0) store_lanes<T, V>(static_cast<T *>(p.dh0) + ((long long)g.b * (W - 1) + q + W - 1) * p.D + c, o);
+        };
+        Lanes<T, V> xi[4], di[4], xn[4], dn[4];          // four rows, and the next four on their way
+        const int last = g.total - 1 - g.t0;             // the sequence's last row from here
+        if (last >= 0)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                xn[k].load(x + min(k, last) * p.ld_x);
+                dn[k].load(gy + min(k, last) * p.ld_dy);
+            }
+        const T *px = x, *pd = gy;
+        T *out = dx - (W - 1) * p.ld_y;                  // of position t - (W - 1)
+        for (int t = 0; t < g.len; t += 4) {
+            px += 4 * p.ld_x;
+            pd += 4 * p.ld_dy;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                xi[k] = xn[k];
+                di[k] = dn[k];
+                xn[k].load(px + min(k, last - 4 - t) * p.ld_x);
+                dn[k].load(pd + min(k, last - 4 - t) * p.ld_dy);
+            }
+            // inside the segment, away from the sequence's end: nothing to ask for
+            const bool inside = t > 0 && t + 4 <= g.len && (!p.dht || g.t0 + t + 4 <= g.total);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (t + k >= g.len) break;
+                f2 o[P];
+                dpre(xi[k], di[k], true);
+                gradient(o);
+                if (inside) store_lanes<T, V>(out, o);
+                else put(g.t0 + t + k - (W - 1), o);
+                out += p.ld_y;
+                shift();
+            }
+        }
+        // the W - 1 tokens behind the segment: the next segment's, or none (dpre = 0)
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) {
+            const int t = g.len + k;
+            f2 o[P];
+            if (t <= last) {
+                Lanes<T, V> a, b;
+                a.load(x + (long long)t * p.ld_x);
+                b.load(gy + (long long)t * p.ld_dy);
+                dpre(a, b, false);
+            } else {
+#pragma unroll
+                for (int e = 0; e < P; ++e) dp[W - 1][e] = win[W - 1][e] = both(0.f);
+            }
+            gradient(o);
+            put(g.t0 + t - (W - 1), o);
+            shift();
         }
     }
     if (!p.part) return;
     if (row)
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
+        for (int e = 0; e < P; ++e) {
 #pragma unroll
             for (int j = 0; j < W; ++j) sm[row - 1][e * W + j][lane] = dw[j][e];
-            sm[row - 1][W * V + e][lane] = db[e];
+            sm[row - 1][W * P + e][lane] = db[e];
         }
     __syncthreads();
     if (row == 0 && grp < groups) {
         float *out = p.part + by * (long long)p.D * (W + 1);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
+        for (int e = 0; e < P; ++e) {
+            float lo, hi;
 #pragma unroll
-            for (int j = 0; j < W; ++j)
-                out[(long long)(c + e) * W + j] =
-                    dw[j][e] + sm[0][e * W + j][lane] + sm[1][e * W + j][lane] + sm[2][e * W + j][lane];
-            out[(long long)p.D * W + c + e] =
-                db[e] + sm[0][W * V + e][lane] + sm[1][W * V + e][lane] + sm[2][W * V + e][lane];
+            for (int j = 0; j < W; ++j) {
+                unpack2(add2(add2(dw[j][e], sm[0][e * W + j][lane]), add2(sm[1][e * W + j][lane], sm[2][e * W + j][lane])), lo, hi);
+                out[(long long)(c + 2 * e) * W + j] = lo;
+                if (V > 1) out[(long long)(c + 2 * e + 1) * W + j] = hi;
+            }
+            unpack2(add2(add2(db[e], sm[0][W * P + e][lane]), add2(sm[1][W * P + e][lane], sm[2][W * P + e][lane])), lo, hi);
+            out[(long long)p.D * W + c + 2 * e] = lo;
+            if (V > 1) out[(long long)p.D * W + c + 2 * e + 1] = hi;
         }
     }
 }
@@ -206,11 +262,12 @@ __global__ void __launch_bounds__(128) conv_step_kernel(ConvParams p) {
     if (b >= p.B) return;
     const int slot = p.slot ? p.slot[b] : b;
     T *y = static_cast<T *>(p.y) + (long long)b * p.ld_y + c;
-    float o[V];
+    constexpr int P = (V + 1) / 2;
+    f2 o[P];
     if (slot < 0 || slot >= p.slots) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = 0.f;
-        store_f<T, V>(y, o);
+        for (int e = 0; e < P; ++e) o[e] = both(0.f);
+        store_lanes<T, V>(y, o);
         return;
     }
     T *st = static_cast<T *>(p.state) + (long long)slot * (W - 1) * p.D + c;
@@ -218,47 +275,54 @@ __global__ void __launch_bounds__(128) conv_step_kernel(ConvParams p) {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) in[j] = load_vec<T, V>(st + (long long)j * p.D);
     in[W - 1] = load_vec<T, V>(static_cast<const T *>(p.x) + (long long)b * p.ld_x + c);
-    float w[W][V], bias[V];
+    f2 w[W][P], bias[P];
     load_taps<W, V>(w, bias, p, c);
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        float pre = bias[e];
+    for (int e = 0; e < P; ++e) {
+        f2 pre = bias[e];
 #pragma unroll
-        for (int j = 0; j < W; ++j) pre = fmaf(w[j][e], to_f(in[j].e[e]), pre);
-        o[e] = p.silu ? pre * sigmoid(pre) : pre;
+        for (int j = 0; j < W; ++j)
+            pre = fma2(w[j][e], pack2(to_f(in[j].e[2 * e]), V == 1 ? 0.f : to_f(in[j].e[V == 1 ? 0 : 2 * e + 1])), pre);
+        o[e] = p.silu ? silu2(pre) : pre;
     }
-    store_f<T, V>(y, o);
+    store_lanes<T, V>(y, o);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) store_vec<T, V>(st + (long long)j * p.D, in[j + 1]);
 }
 
 template <class T, int V> bool conv_vec_ok(const ConvParams &p) {
     const size_t es = sizeof(T), n = V * es;
-    return p.D % V == 0 && rows_aligned(p.x, p.ld_x, es, n) && rows_aligned(p.y, p.ld_y, es, n) &&
+    return p.D % V == 0 && aligned_to(p.weight, 16) && aligned_to(p.bias, 16) && rows_aligned(p.x, p.ld_x, es, n) && rows_aligned(p.y, p.ld_y, es, n) &&
            rows_aligned(p.dy, p.ld_dy, es, n) && rows_aligned(p.h0, p.D, es, n) && rows_aligned(p.ht, p.D, es, n) &&
            rows_aligned(p.dht, p.D, es, n) && rows_aligned(p.dh0, p.D, es, n) && rows_aligned(p.state, p.D, es, n);
 }
 
 enum Way { kFwd, kBwd, kStep };
 
-template <class T, int W, int V> cudaError_t conv_launch(const ConvParams &p, Way way, cudaStream_t s) {
-    const int groups = p.D / V;
-    if (way == kStep) {
-        const long long blocks = ((long long)p.B * groups + 127) / 128;
-        if (blocks > 0x7fffffffLL) return cudaErrorNotSupported;
-        conv_step_kernel<T, W, V><<<(unsigned)blocks, 128, 0, s>>>(p);
-        return cudaGetLastError();
-    }
-    const long long slots = segment_slots(p.B, p.T, p.seg, p.cu_seqlens != nullptr);
-    const long long blocks = way == kFwd ? (slots * groups + 127) / 128 : (slots + 3) / 4 * ((groups + 31) / 32);
+template <class T, int W, int V> cudaError_t fwd_start(const ConvParams &p, cudaStream_t s) {
+    const long long slots = segment_slots(p.B, p.T, p.seg, p.cu_seqlens != nullptr), blocks = (slots * (p.D / V) + 127) / 128;
     if (blocks > 0x7fffffffLL) return cudaErrorNotSupported;
-    if (way == kFwd) conv_fwd_kernel<T, W, V><<<(unsigned)blocks, 128, 0, s>>>(p, slots);
+    conv_fwd_kernel<T, W, V><<<(unsigned)blocks, 128, 0, s>>>(p, slots);
+    return cudaGetLastError();
+}
+template <class T, int W, int V> cudaError_t other_start(const ConvParams &p, Way way, cudaStream_t s) {
+    const int groups = p.D / V;
+    const long long slots = segment_slots(p.B, p.T, p.seg, p.cu_seqlens != nullptr);
+    const long long blocks = way == kStep ? ((long long)p.B * groups + 127) / 128 : (slots + 3) / 4 * ((groups + 31) / 32);
+    if (blocks > 0x7fffffffLL) return cudaErrorNotSupported;
+    if (way == kStep) conv_step_kernel<T, W, V><<<(unsigned)blocks, 128, 0, s>>>(p);
     else conv_bwd_kernel<T, W, V><<<(unsigned)blocks, 128, 0, s>>>(p, slots);
     return cudaGetLastError();
 }
 
+// Channels per access: 16 bytes in the forward, four channels in the backward (whose taps, window and
+// sums are four times V values per tap) and for single tokens (whose threads are few); else one.
 template <class T, int W> cudaError_t conv_width(const ConvParams &p, Way way, cudaStream_t s) {
-    return conv_vec_ok<T, 4>(p) ? conv_launch<T, W, 4>(p, way, s) : conv_launch<T, W, 1>(p, way, s);
+    constexpr int F = 16 / sizeof(T);
+    const bool four = conv_vec_ok<T, 4>(p);
+    if (way != kFwd) return four ? other_start<T, W, 4>(p, way, s) : other_start<T, W, 1>(p, way, s);
+    if (conv_vec_ok<T, F>(p)) return fwd_start<T, W, F>(p, s);
+    return fwd_start<T, W, 1>(p, s);
 }
 
 template <class T> cudaError_t conv_type(const ConvParams &p, int W, Way way, cudaStream_t s) {
@@ -271,30 +335,51 @@ template <class T> cudaError_t conv_type(const ConvParams &p, int W, Way way, cu
 
 }  // namespace
 
+namespace {
+// Tokens per thread.  Each segment costs its tokens plus about eight for the taps and the rows before
+// it, and the last wave of blocks should be full: the length with the smallest number of waves times
+// cost, `resident` blocks of 128 threads to an SM.
+int segment_length(const ConvParams &p, int V, int resident) {
+    const long long tokens = (long long)(p.cu_seqlens ? 1 : p.B) * p.T, groups = (p.D + V - 1) / V;
+    const long long room = 128LL * resident * sm_count();
+    long long best = 0;
+    int seg = 4;
+    for (int s = 4; s <= 64; s += 4) {
+        const long long threads = (tokens + s - 1) / s * groups, cost = (threads + room - 1) / room * (s + 8);
+        if (!best || cost <= best) {
+            best = cost;
+            seg = s;
+        }
+    }
+    return seg;
+}
+int bwd_segment(const ConvParams &p) { return segment_length(p, 4, 3); }
+}  // namespace
+
 cudaError_t launch_short_conv_fwd(const ConvParams &q, int W, bool bf, cudaStream_t s) {
     ConvParams p = q;
-    p.seg = 16;
+    p.seg = segment_length(p, bf ? 8 : 4, 4);
     return bf ? conv_type<bf16>(p, W, kFwd, s) : conv_type<float>(p, W, kFwd, s);
 }
 
-constexpr int kBwdSeg = 32;
-
 size_t short_conv_part_floats(const ConvParams &p, int W) {
-    const long long slots = segment_slots(p.B, p.T, kBwdSeg, p.cu_seqlens != nullptr);
+    const long long slots = segment_slots(p.B, p.T, bwd_segment(p), p.cu_seqlens != nullptr);
     return (size_t)((slots + 3) / 4) * p.D * (W + 1);
 }
 
 cudaError_t launch_short_conv_bwd(const ConvParams &q, int W, bool bf, cudaStream_t s) {
     ConvParams p = q;
-    p.seg = kBwdSeg;
+    p.seg = bwd_segment(p);
     const cudaError_t e = bf ? conv_type<bf16>(p, W, kBwd, s) : conv_type<float>(p, W, kBwd, s);
     if (e != cudaSuccess || !p.part) return e;
-    const long long slots = segment_slots(p.B, p.T, kBwdSeg, p.cu_seqlens != nullptr);
+    const long long slots = segment_slots(p.B, p.T, p.seg, p.cu_seqlens != nullptr);
     return launch_sum_rows(p.part, (int)((slots + 3) / 4), {p.dweight, (long long)p.D * W, p.w_bf16},
                            {p.dbias, p.D, p.w_bf16}, {nullptr, 0, false}, s);
 }
 
-cudaError_t launch_short_conv_step(const ConvParams &p, int W, bool bf, cudaStream_t s) {
+cudaError_t launch_short_conv_step(const ConvParams &q, int W, bool bf, cudaStream_t s) {
+    ConvParams p = q;
+    p.seg = 1;
     return bf ? conv_type<bf16>(p, W, kStep, s) : conv_type<float>(p, W, kStep, s);
 }
 

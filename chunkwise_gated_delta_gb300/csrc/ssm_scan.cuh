@@ -26,35 +26,6 @@ __device__ __forceinline__ float log1p_unit(float u) {
 // softplus(v) = max(v, 0) + log(1 + exp(-|v|)).
 __device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1p_unit(ex2(-kLog2e * fabsf(v))); }
 
-// Two float32 values in one 64-bit register: the packed forms of the FMA pipe do both in one issue
-// slot (the same arithmetic rate, half the instructions, and issue slots are what runs short).
-using f2 = unsigned long long;
-__device__ __forceinline__ f2 pack2(float lo, float hi) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack2(f2 v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f2 ex2_2(f2 v) {
-    float a, b;
-    unpack2(v, a, b);
-    return pack2(ex2(a), ex2(b));
-}
 // The same, kept in the order in which they are written.
 __device__ __forceinline__ f2 mul2v(f2 a, f2 b) {
     f2 r;
@@ -77,8 +48,6 @@ struct alignas(16) f2x2 {
     f2 a, b;
 };
 
-__device__ __forceinline__ f2 both(float v) { return pack2(v, v); }
-
 // softplus of two values at once.
 __device__ __forceinline__ f2 softplus2(f2 v) {
     float a, b, lo, hi;
@@ -90,14 +59,6 @@ __device__ __forceinline__ f2 softplus2(f2 v) {
     const f2 r = fma2(fma2(fma2(both(kAtanh[3]), q, both(kAtanh[2])), q, both(kAtanh[1])), q, both(kAtanh[0]));
     return fma2(fma2(mul2(s, q), r, s), both(2.f), pack2(fmaxf(a, 0.f), fmaxf(b, 0.f)));
 }
-// v sigmoid(v) of two values at once.
-__device__ __forceinline__ f2 silu2(f2 v) {
-    float lo, hi;
-    unpack2(mul2(v, both(-kLog2e)), lo, hi);
-    unpack2(add2(pack2(ex2(lo), ex2(hi)), both(1.f)), lo, hi);
-    return mul2(v, pack2(rcp(lo), rcp(hi)));
-}
-
 // Sums v[k] over the L lanes of a channel; lane i ends with the sums of k = i K / L ... in v[0 ..].
 // K is a multiple of L.
 template <int K, int L> __device__ __forceinline__ void spread_sum(float (&v)[K], int i) {
@@ -115,20 +76,6 @@ template <int K, int L> __device__ __forceinline__ void spread_sum(float (&v)[K]
     }
 }
 
-// Four neighbouring elements as they lie in memory.
-template <class T> struct RawQuad;
-template <> struct RawQuad<float> {
-    using type = float4;
-    static __device__ __forceinline__ float4 floats(float4 v) { return v; }
-};
-template <> struct RawQuad<bf16> {
-    using type = uint2;
-    static __device__ __forceinline__ float4 floats(uint2 v) {
-        return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
-                           __uint_as_float(v.y & 0xffff0000u));
-    }
-};
-
 // Rows t0 .. t0 + TT - 1 of Bm or Cm into shared memory as float32 [TT][NP], zero behind the
 // segment's end and past N.  One thread per group of four states.
 template <class T, int NP, int TT, int THREADS = kScanThreads>
@@ -141,7 +88,7 @@ __device__ __forceinline__ void stage_rows(float (*dst)[NP], const void *src, lo
         if (t0 + t < g.len) {
             const T *r = static_cast<const T *>(src) + (g.row0 + g.t0 + t0 + t) * ld + n;
             if (vec) {       // N = NP and rows aligned to four elements
-                const Vec<T, 4> q = load_vec<T, 4>(r);
+                const Vec<T, 4> q = load_const<T, 4>(r);
                 v = make_float4(to_f(q.e[0]), to_f(q.e[1]), to_f(q.e[2]), to_f(q.e[3]));
             } else {
                 if (n < N) v.x = to_f(r[0]);

@@ -27,7 +27,7 @@ constexpr int SEG = kBwdSegment;
 // ones (last: the last offset that exists).
 template <class T, bool XV> __device__ __forceinline__ void load_four(float (&o)[4], const T *p, int last) {
     if (XV) {
-        const float4 v = RawQuad<T>::floats(*reinterpret_cast<const typename RawQuad<T>::type *>(p));
+        const float4 v = RawQuad<T>::floats(__ldg(reinterpret_cast<const typename RawQuad<T>::type *>(p)));
         o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
     } else {
         uint32_t v[4];
@@ -204,19 +204,30 @@ __global__ void __launch_bounds__(128) scan_boundary_kernel(ScanParams p, int NP
     const long long step = back ? -(long long)p.D : p.D;
     const long long k0 = (back ? s0 + count - 1 : s0) * p.D + d;
     float *vals = (back ? p.seg_grad : p.seg_state) + n;
-    for (int i = 0; i < count; i += 8) {
-        float local[8], dt[8];
+    constexpr int K = 8;
+    float local[K], dt[K];
+    auto fetch = [&](int i) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < K; ++j) {
             const long long k = k0 + (long long)min(i + j, count - 1) * step;
             local[j] = vals[k * NP];
             dt[j] = p.seg_dt[k];
         }
+    };
+    fetch(0);
+    for (int i = 0; i < count; i += K) {
+        float now[K], a[K];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < K; ++j) {
+            now[j] = local[j];
+            a[j] = ex2(a2 * dt[j]);
+        }
+        if (i + K < count) fetch(i + K);       // before this batch is stored: nothing of it is read again
+#pragma unroll
+        for (int j = 0; j < K; ++j)
             if (i + j < count) {
                 vals[(k0 + (i + j) * step) * NP] = v;
-                v = fmaf(ex2(a2 * dt[j]), v, local[j]);
+                v = fmaf(a[j], v, now[j]);
             }
     }
     if (back && in && p.dh0) p.dh0[at] = v;

@@ -447,22 +447,21 @@ template <class T> cudaError_t step_type(const ScanParams &p, cudaStream_t s) {
 
 }  // namespace
 
-// Whole sequences while their blocks (of 128 / lanes channels) fill half of the SMs: at B 4, D 2048
-// (128 blocks on 152 SMs) splitting in two costs more than it gives.  Below that every sequence is cut
-// so that the blocks fill the SMs once, at segments of 256 tokens or more: the local pass over all
-// tokens and two more launches cost about half of an unsplit pass with every SM busy.  The lengths
-// of packed sequences are not known here: they are taken to be as uneven as they can be, up to four
-// blocks per SM.
+// Whole sequences unless their blocks (of 128 / lanes channels) fill less than a third of the SMs; then
+// every sequence is cut so that the blocks fill the SMs once, at segments of 256 tokens or more.  The
+// local pass over all tokens and two more launches cost about what an unsplit pass over half the tokens
+// does, so two segments gain nothing (T 2048, 64 blocks: 97 us whole, 108 in two), and nine of T 16384
+// with 16 blocks take 190 us for 750.  The lengths of packed sequences are not known here: they are
+// taken to be as uneven as they can be, one of them with nearly all tokens.
 int ssm_scan_fwd_segment(const ScanParams &p) {
     const int ch = p.N <= 8 ? 128 : p.N <= 16 ? 64 : 32, sms = sm_count();
-    const long long cb = (p.D + ch - 1) / ch, blocks = cb * p.B;
-    if (p.cu_seqlens ? blocks > 4LL * sms && p.B > 1 : 2 * blocks > sms) return p.T;
-    const long long cuts = p.cu_seqlens ? sms / cb : sms / blocks;   // segments in all, or per sequence
-    if (cuts < 2) return p.T;
+    const long long cb = (p.D + ch - 1) / ch, blocks = p.cu_seqlens ? cb : cb * p.B;
+    const long long cuts = sms / blocks;
+    if (cuts < 3) return p.T;
     long long seg = (p.T + cuts - 1) / cuts;
     seg = (seg + kFwdLocal - 1) / kFwdLocal * kFwdLocal;
     if (seg < 256) seg = 256;
-    return 2 * seg > p.T + seg / 2 ? p.T : (int)seg;
+    return 3 * seg > p.T + seg ? p.T : (int)seg;
 }
 
 size_t ssm_scan_fwd_floats(const ScanParams &p) {

@@ -23,23 +23,48 @@ from . import _lib
 from ._lib import KdaError
 
 _CODES = {torch.bfloat16: _lib.KDA_BF16, torch.float32: _lib.KDA_F32}
+_F32 = torch.float32
+
+# The current stream's handle and the current device without building Python objects for them (a
+# decoding step's calls are short); the public functions where a build lacks these.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_device_index = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+_functions: dict = {}
+
+
+def _function(name):
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(_lib.load(), name)
+    return fn
 
 
 def _code(t, name):
-    try:
-        return _CODES[t.dtype]
-    except KeyError:
-        raise TypeError(f"{name}: unsupported dtype {t.dtype}") from None
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    return code
+
+
+def _check(t, name, shape, dtype, device):
+    """Shape, dtype and device (a CUDA index; -1 is the CPU).  An axis of None may have any size."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on device cuda:{device}, not {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
 def _tensor(t, name, shape, dtype, device):
-    """A contiguous tensor of this shape and dtype (an axis of None may have any size)."""
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
-        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    """Pointer of a contiguous tensor of this shape and dtype."""
+    if type(t) is not torch.Tensor or t.dtype != dtype or t.get_device() != device or t.shape != shape:
+        _check(t, name, shape, dtype, device)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
@@ -47,13 +72,12 @@ def _tensor(t, name, shape, dtype, device):
 
 def _rows(t, name, shape, dtype, device):
     """Pointer and row stride of a tensor whose rows (last axis) may lie apart."""
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    width, st = shape[-1], t.stride()
+    if type(t) is not torch.Tensor or t.dtype != dtype or t.get_device() != device or t.shape != shape:
+        _check(t, name, shape, dtype, device)
+    width = shape[-1]
+    if t.is_contiguous():
+        return t.data_ptr(), width
+    st = t.stride()
     if width > 1 and st[-1] != 1:
         raise ValueError(f"{name} must be contiguous in its last axis")
     rows = [k for k in range(len(shape) - 1) if shape[k] > 1]
@@ -68,11 +92,12 @@ def _rows(t, name, shape, dtype, device):
 
 
 def _cuda(t, name):
+    """The index of the tensor's CUDA device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+    return t.get_device()
 
 
 def _sequences(cu_seqlens, B, device):
@@ -83,40 +108,44 @@ def _sequences(cu_seqlens, B, device):
         raise TypeError("cu_seqlens must be int32")
     if B != 1 or cu_seqlens.numel() < 2:
         raise ValueError("with cu_seqlens (at least two offsets) the tensors are [1, T, C]")
-    return _tensor(cu_seqlens, "cu_seqlens", (None,), torch.int32, device), cu_seqlens.numel() - 1
+    return _tensor(cu_seqlens, "cu_seqlens", (cu_seqlens.numel(),), torch.int32, device), cu_seqlens.numel() - 1
 
 
 class _On:
-    """The device and stream of a call: allocations inside go to that stream."""
+    """The stream of a call: allocations inside go to it, launches too."""
+
+    __slots__ = ("device", "handle", "ctx")
 
     def __init__(self, device, stream, inputs):
         self.device = device
-        current = torch.cuda.current_stream(device)
-        self.stream = current if stream is None else stream
-        self._ctx = None
-        if self.stream != current or torch.cuda.current_device() != device.index:
-            self._ctx = torch.cuda.stream(self.stream)
-            for t in inputs:
-                if t is not None and self.stream != current:
-                    t.record_stream(self.stream)
+        self.handle = _raw_stream(device)
+        self.ctx = None
+        if stream is not None and stream.cuda_stream != self.handle:
+            self.ctx = torch.cuda.stream(stream)
+            self.handle = stream.cuda_stream
+            for t in inputs:             # the allocator must not hand them out while that stream uses them
+                if t is not None:
+                    t.record_stream(stream)
+        elif _device_index() != device:
+            self.ctx = torch.cuda.device(device)
 
     def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
+        if self.ctx is not None:
+            self.ctx.__enter__()
         return self
 
     def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
 
     def launch(self, name, args):
-        rc = getattr(_lib.load(), name)(ctypes.byref(args), self.stream.cuda_stream)
-        if rc != _lib.KDA_OK:
+        rc = _function(name)(ctypes.byref(args), self.handle)
+        if rc:
             raise KdaError(rc, name)
 
     def workspace(self, name, args):
         """Points args at a workspace of the size that the library asks for."""
-        need = getattr(_lib.load(), name)(ctypes.byref(args))
+        need = _function(name)(ctypes.byref(args))
         if need:
             ws = torch.empty(need, dtype=torch.uint8, device=self.device)
             args.workspace, args.workspace_bytes = ws.data_ptr(), need
@@ -128,12 +157,14 @@ def _out(given, name, shape, dtype, device):
     """An output tensor (rows may lie apart): the caller's, or a new one."""
     if given is None:
         given = torch.empty(shape, dtype=dtype, device=device)
+        return given, given.data_ptr(), shape[-1]
     return (given, *_rows(given, name, shape, dtype, device))
 
 
 def _dense_out(given, name, shape, dtype, device):
     if given is None:
         given = torch.empty(shape, dtype=dtype, device=device)
+        return given, given.data_ptr()
     return given, _tensor(given, name, shape, dtype, device)
 
 
@@ -148,6 +179,8 @@ def _known(grads, names):
 def _weights(weight, bias, wname, shape, D, device, default):
     """Pointers of weight and bias, and their dtype's code."""
     dt = weight.dtype if weight is not None else bias.dtype if bias is not None else default
+    if weight is not None and len(shape) == 2 and weight.dim() == 2:
+        shape = (D, weight.shape[1])     # [D, W], any W
     w = None if weight is None else _tensor(weight, wname, shape, dt, device)
     b = None if bias is None else _tensor(bias, "bias", (D,), dt, device)
     if dt not in _CODES:
@@ -293,7 +326,7 @@ def short_conv_step(x, weight, bias, state, *, activation="silu", slots=None, y=
     xp, ldx = _rows(x, "x", x.shape, x.dtype, dev)
     wp, bp, wdt = _weights(weight, bias, "weight", (D, None), D, dev, x.dtype)
     W = weight.shape[1]
-    sp = _tensor(state, "state", (None, W - 1, D), x.dtype, dev)
+    sp = _tensor(state, "state", (state.shape[0], W - 1, D), x.dtype, dev)
     ip = None if slots is None else _tensor(slots, "slots", (B,), torch.int32, dev)
     with _On(dev, stream, (x, weight, bias, state, slots)) as on:
         y, yp, ldy = _out(y, "y", x.shape, x.dtype, dev)
@@ -396,7 +429,7 @@ def ssm_scan_step(x, delta, A, B, C, state, D=None, z=None, delta_bias=None, *, 
     """
     dev, code, ch, n, ptrs = _scan_inputs(x, delta, A, B, C, D, z, delta_bias, 2)
     bt = x.shape[0]
-    sp = _tensor(state, "state", (None, ch, n), torch.float32, dev)
+    sp = _tensor(state, "state", (state.shape[0], ch, n) if state.dim() == 3 else (None, ch, n), _F32, dev)
     ip = None if slots is None else _tensor(slots, "slots", (bt,), torch.int32, dev)
     with _On(dev, stream, (x, delta, A, B, C, state, D, z, delta_bias, slots)) as on:
         y, yp, ldy = _out(y, "y", x.shape, x.dtype, dev)

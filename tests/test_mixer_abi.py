@@ -154,7 +154,7 @@ def test_segment_arithmetic(tmp_path):
 
 
 # ------------------------------------------------------------------------------ Python binding
-CPU = torch.device("cpu")
+CPU = -1                                     # the index of tensors that are on no GPU
 
 
 def test_rows_takes_what_one_stride_serves():
