@@ -88,7 +88,7 @@ __device__ __forceinline__ void stage_rows(float (*dst)[NP], const void *src, lo
         if (t0 + t < g.len) {
             const T *r = static_cast<const T *>(src) + (g.row0 + g.t0 + t0 + t) * ld + n;
             if (vec) {       // N = NP and rows aligned to four elements
-                const Vec<T, 4> q = load_const<T, 4>(r);
+                const Vec<T, 4> q = load_vec<T, 4>(r);
                 v = make_float4(to_f(q.e[0]), to_f(q.e[1]), to_f(q.e[2]), to_f(q.e[3]));
             } else {
                 if (n < N) v.x = to_f(r[0]);

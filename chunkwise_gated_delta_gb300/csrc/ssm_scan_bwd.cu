@@ -23,20 +23,29 @@ namespace {
 
 constexpr int SEG = kBwdSegment;
 
-// Four neighbouring channels of one token (XV: in one access).  Channels past the end repeat the last
-// ones (last: the last offset that exists).
-template <class T, bool XV> __device__ __forceinline__ void load_four(float (&o)[4], const T *p, int last) {
-    if (XV) {
-        const float4 v = RawQuad<T>::floats(__ldg(reinterpret_cast<const typename RawQuad<T>::type *>(p)));
-        o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
-    } else {
-        uint32_t v[4];
+// Four neighbouring channels of one token (XV: in one access), as they lie in memory.  Channels past the
+// end repeat the last ones (last: the last offset that exists).
+template <class T, bool XV> struct Four {
+    typename RawQuad<T>::type v;
+    uint32_t e[XV ? 1 : 4];
+    __device__ __forceinline__ void load(const T *p, int last) {
+        if (XV) {
+            v = *reinterpret_cast<const typename RawQuad<T>::type *>(p);
+        } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = load_bits(p + min(k, last));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = bits_f<T>(v[k]);
+            for (int k = 0; k < 4; ++k) e[k] = load_bits(p + min(k, last));
+        }
     }
-}
+    __device__ __forceinline__ void get(float (&o)[4]) const {
+        if (XV) {
+            const float4 q = RawQuad<T>::floats(v);
+            o[0] = q.x; o[1] = q.y; o[2] = q.z; o[3] = q.w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] = bits_f<T>(e[k]);
+        }
+    }
+};
 template <class T, bool XV> __device__ __forceinline__ void store_four(T *p, const float (&v)[4], int n) {
     if (XV) {
         Vec<T, 4> q;
@@ -101,19 +110,34 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_local_kernel(ScanParams 
     for (int k = 0; k < 4; ++k) bias[k] = p.delta_bias && ds + k < p.D ? p.delta_bias[ds + k] : 0.f;
     for (int t0 = 0; t0 < g.len; t0 += TT) {
         __syncthreads();
-        stage_rows<T, NP, TT>(sm.B, p.Bm, p.ld_B, p.N, g, t0, vec);
-        if (GRAD) stage_rows<T, NP, TT>(sm.C, p.Cm, p.ld_C, p.N, g, t0, vec);
-#pragma unroll 2
-        for (int k = 0; k < K; ++k) {
-            const int t = r0 + k * ROWS;
-            const bool in = t0 + t < g.len;
-            const long long tl = min(t0 + t, g.len - 1);
-            float xv[4], dv[4], yv[4], zv[4];
-            load_four<T, XV>(xv, x + tl * p.ld_x, last);
-            load_four<T, XV>(dv, delta + tl * p.ld_delta, last);
+        // KB tokens' loads in flight together, as many as the registers hold
+        constexpr int KB = K < 2 ? K : XV && sizeof(T) == 2 && K >= 4 ? 4 : 2;
+        Four<T, XV> rx[KB], rd[KB], ry[GRAD ? KB : 1], rz[GRAD ? KB : 1];
+        for (int k0 = 0; k0 < K; k0 += KB) {
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+            const long long tl = min(t0 + r0 + (k0 + k) * ROWS, g.len - 1);
+            rx[k].load(x + tl * p.ld_x, last);
+            rd[k].load(delta + tl * p.ld_delta, last);
             if (GRAD) {
-                load_four<T, XV>(yv, dy + tl * lddy, last);
-                load_four<T, XV>(zv, z + tl * ldz, last);
+                ry[k].load(dy + tl * lddy, last);
+                rz[k].load(z + tl * ldz, last);
+            }
+        }
+        if (k0 == 0) {
+            stage_rows<T, NP, TT>(sm.B, p.Bm, p.ld_B, p.N, g, t0, vec);
+            if (GRAD) stage_rows<T, NP, TT>(sm.C, p.Cm, p.ld_C, p.N, g, t0, vec);
+        }
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+            const int t = r0 + (k0 + k) * ROWS;
+            const bool in = t0 + t < g.len;
+            float xv[4], dv[4], yv[4], zv[4];
+            rx[k].get(xv);
+            rd[k].get(dv);
+            if (GRAD) {
+                ry[k].get(yv);
+                rz[k].get(zv);
             }
 #pragma unroll
             for (int s = 0; s < 4; s += 2) {
@@ -136,6 +160,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_local_kernel(ScanParams 
                     sm.g[t][S::at(4 * q + s + 1)] = both(in ? hi : 0.f);
                 }
             }
+        }
         }
         __syncthreads();
 #pragma unroll 4
@@ -274,17 +299,33 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grad_kernel(ScanParams p
     float bias[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) bias[k] = p.delta_bias && ds + k < p.D ? p.delta_bias[ds + k] : 0.f;
-    if (g.len > 0) {
-#pragma unroll 2
-        for (int k = 0; k < K; ++k) {
-            const int t = r0 + k * ROWS;
+    constexpr int KB = K < 4 ? K : 4;            // tokens per thread whose loads are in flight together
+    Four<T, XV> rx[KB], rd[KB], ry[KB], rz[KB];
+    auto fetch = [&](int k0) {
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+            const long long tl = min(r0 + (k0 + k) * ROWS, g.len - 1);
+            rx[k].load(x + tl * p.ld_x, last);
+            rd[k].load(delta + tl * p.ld_delta, last);
+            ry[k].load(dy + tl * p.ld_dy, last);
+            rz[k].load(z + tl * ldz, last);
+        }
+    };
+    for (int k0 = 0; k0 < K && g.len > 0; k0 += KB) {
+        fetch(k0);
+        if (k0 == 0) {
+            stage_rows<T, NP, SEG, kGradThreads>(sm.B, p.Bm, p.ld_B, p.N, g, 0, vec);
+            stage_rows<T, NP, SEG, kGradThreads>(sm.C, p.Cm, p.ld_C, p.N, g, 0, vec);
+        }
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+            const int t = r0 + (k0 + k) * ROWS;
             const bool in = t < g.len;
-            const long long tl = min(t, g.len - 1);
             float xv[4], dv[4], yv[4], zv[4];
-            load_four<T, XV>(xv, x + tl * p.ld_x, last);
-            load_four<T, XV>(dv, delta + tl * p.ld_delta, last);
-            load_four<T, XV>(yv, dy + tl * p.ld_dy, last);
-            load_four<T, XV>(zv, z + tl * ldz, last);
+            rx[k].get(xv);
+            rd[k].get(dv);
+            ry[k].get(yv);
+            rz[k].get(zv);
 #pragma unroll
             for (int s = 0; s < 4; s += 2) {
                 f2 dt = pack2(dv[s] + bias[s], dv[s + 1] + bias[s + 1]), gy = pack2(yv[s], yv[s + 1]);
@@ -301,8 +342,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grad_kernel(ScanParams p
             }
         }
     }
-    stage_rows<T, NP, SEG, kGradThreads>(sm.B, p.Bm, p.ld_B, p.N, g, 0, vec);
-    stage_rows<T, NP, SEG, kGradThreads>(sm.C, p.Cm, p.ld_C, p.N, g, 0, vec);
     __syncthreads();
     const int parts = (g.len + TC - 1) / TC;
 
@@ -461,17 +500,18 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grad_kernel(ScanParams p
     for (int k = 0; k < 4; ++k) skip[k] = p.Dskip && ds + k < p.D ? p.Dskip[ds + k] : 0.f;
     T *dx = static_cast<T *>(p.dx) + row * p.ld_dx + ds, *dd = static_cast<T *>(p.ddelta) + row * p.ld_ddelta + ds;
     T *dz = static_cast<T *>(p.dz) + row * p.ld_dz + ds;
-    if (g.len > 0 && nl > 0)
-#pragma unroll 2
-        for (int k = 0; k < K; ++k) {
-            const int t = r0 + k * ROWS;
+    for (int k0 = 0; k0 < K && g.len > 0 && nl > 0; k0 += KB) {
+        fetch(k0);                               // (from L2)
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+            const int t = r0 + (k0 + k) * ROWS;
             const bool in = t < g.len;
-            const long long tl = min(t, g.len - 1);
+            const long long tl = t;
             float xv[4], dv[4], yv[4], zv[4], ox[4], od[4], oz[4];
-            load_four<T, XV>(xv, x + tl * p.ld_x, last);
-            load_four<T, XV>(dv, delta + tl * p.ld_delta, last);
-            load_four<T, XV>(yv, dy + tl * p.ld_dy, last);
-            load_four<T, XV>(zv, z + tl * ldz, last);
+            rx[k].get(xv);
+            rd[k].get(dv);
+            ry[k].get(yv);
+            rz[k].get(zv);
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 const float2 w = sm.du[t][4 * q + s];
@@ -489,6 +529,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grad_kernel(ScanParams p
                 if (p.z) store_four<T, XV>(dz + tl * p.ld_dz, oz, nl);
             }
         }
+    }
     // dD and dbias over the block's tokens
     float *part = &sm.red[0][0];                 // [ROWS][CH][2]
     __syncthreads();

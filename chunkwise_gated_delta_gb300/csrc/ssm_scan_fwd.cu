@@ -356,7 +356,8 @@ __global__ void __launch_bounds__(16 * KT + kScanThreads) scan_fwd_kernel(ScanPa
 }
 
 // The same for one token of each request; the state is read, updated and written once: bound by HBM.
-template <class T, int L>
+// VEC: N = 4 L, state, A, Bm and Cm in accesses of four.
+template <class T, int L, bool VEC>
 __global__ void __launch_bounds__(kScanThreads) scan_step_kernel(ScanParams p, int chan_blocks) {
     constexpr int CH = kScanThreads / L;
     const int c = threadIdx.x / L, i = threadIdx.x % L, n0 = 4 * i;
@@ -364,41 +365,50 @@ __global__ void __launch_bounds__(kScanThreads) scan_step_kernel(ScanParams p, i
     const int d = (blockIdx.x - b * chan_blocks) * CH + c;
     const int slot = p.slot ? p.slot[b] : b;
     const bool pad = slot < 0 || slot >= p.slots, live = d < p.D && !pad;
-    float y[1] = {0.f};
-    float xv = 0.f;
+    float y = 0.f, xv = 0.f, zv = 0.f, skip = 0.f;
     if (live) {
         float h[4], a[4], bv[4], cv[4];
         float *st = p.state + ((long long)slot * p.D + d) * p.N;
-        load_states(h, st, n0, p.N);
-        load_states(a, p.A + (long long)d * p.N, n0, p.N);
+        const float *ar = p.A + (long long)d * p.N;
         const T *br = static_cast<const T *>(p.Bm) + b * p.ld_B, *cr = static_cast<const T *>(p.Cm) + b * p.ld_C;
+        if (VEC) {
+            const float4 hq = *reinterpret_cast<const float4 *>(st + n0), aq = __ldg(reinterpret_cast<const float4 *>(ar + n0));
+            const float4 bq = RawQuad<T>::floats(__ldg(reinterpret_cast<const typename RawQuad<T>::type *>(br + n0)));
+            const float4 cq = RawQuad<T>::floats(__ldg(reinterpret_cast<const typename RawQuad<T>::type *>(cr + n0)));
+            h[0] = hq.x; h[1] = hq.y; h[2] = hq.z; h[3] = hq.w;
+            a[0] = aq.x; a[1] = aq.y; a[2] = aq.z; a[3] = aq.w;
+            bv[0] = bq.x; bv[1] = bq.y; bv[2] = bq.z; bv[3] = bq.w;
+            cv[0] = cq.x; cv[1] = cq.y; cv[2] = cq.z; cv[3] = cq.w;
+        } else {
+            load_states(h, st, n0, p.N);
+            load_states(a, ar, n0, p.N);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            bv[k] = n0 + k < p.N ? to_f(br[n0 + k]) : 0.f;
-            cv[k] = n0 + k < p.N ? to_f(cr[n0 + k]) : 0.f;
-        }
-        xv = to_f(static_cast<const T *>(p.x)[b * p.ld_x + d]);
-        float dt = to_f(static_cast<const T *>(p.delta)[b * p.ld_delta + d]) + (p.delta_bias ? p.delta_bias[d] : 0.f);
-        if (p.softplus) dt = softplus(dt);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            h[k] = fmaf(ex2(dt * a[k] * kLog2e), h[k], dt * xv * bv[k]);
-            y[0] = fmaf(cv[k], h[k], y[0]);
-        }
-        store_states(st, h, n0, p.N);
-    }
-#pragma unroll
-    for (int s = L / 2; s; s >>= 1) y[0] += __shfl_xor_sync(~0u, y[0], s);
-    if (d < p.D && i == 0) {
-        float o = 0.f;
-        if (!pad) {
-            o = fmaf(p.Dskip ? p.Dskip[d] : 0.f, xv, y[0]);
-            if (p.z) {
-                const float zv = to_f(static_cast<const T *>(p.z)[b * p.ld_z + d]);
-                o *= zv * sigmoid(zv);
+            for (int k = 0; k < 4; ++k) {
+                bv[k] = n0 + k < p.N ? to_f(br[n0 + k]) : 0.f;
+                cv[k] = n0 + k < p.N ? to_f(cr[n0 + k]) : 0.f;
             }
         }
-        static_cast<T *>(p.y)[b * p.ld_y + d] = from_f<T>(o);
+        xv = bits_f<T>(load_bits(static_cast<const T *>(p.x) + b * p.ld_x + d));
+        if (p.z) zv = bits_f<T>(load_bits(static_cast<const T *>(p.z) + b * p.ld_z + d));
+        if (p.Dskip) skip = __ldg(p.Dskip + d);
+        float dt = bits_f<T>(load_bits(static_cast<const T *>(p.delta) + b * p.ld_delta + d));
+        if (p.delta_bias) dt += __ldg(p.delta_bias + d);
+        if (p.softplus) dt = softplus(dt);
+        const float e = dt * kLog2e, u = dt * xv;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            h[k] = fmaf(ex2(e * a[k]), h[k], u * bv[k]);
+            y = fmaf(cv[k], h[k], y);
+        }
+        if (VEC) *reinterpret_cast<float4 *>(st + n0) = make_float4(h[0], h[1], h[2], h[3]);
+        else store_states(st, h, n0, p.N);
+    }
+#pragma unroll
+    for (int s = L / 2; s; s >>= 1) y += __shfl_xor_sync(~0u, y, s);
+    if (d < p.D && i == 0) {
+        y = fmaf(skip, xv, y);
+        if (p.z) y *= zv * sigmoid(zv);
+        static_cast<T *>(p.y)[b * p.ld_y + d] = from_f<T>(pad ? 0.f : y);
     }
 }
 
@@ -426,7 +436,10 @@ template <class T, int L> cudaError_t step_launch(const ScanParams &p, cudaStrea
     constexpr int CH = kScanThreads / L;
     const int cb = (p.D + CH - 1) / CH;
     if ((long long)p.B * cb > 0x7fffffffLL) return cudaErrorNotSupported;
-    scan_step_kernel<T, L><<<(unsigned)(p.B * cb), kScanThreads, 0, s>>>(p, cb);
+    if (bc_vec_ok<T>(p, 4 * L) && aligned_to(p.state, 16) && aligned_to(p.A, 16))
+        scan_step_kernel<T, L, true><<<(unsigned)(p.B * cb), kScanThreads, 0, s>>>(p, cb);
+    else
+        scan_step_kernel<T, L, false><<<(unsigned)(p.B * cb), kScanThreads, 0, s>>>(p, cb);
     return cudaGetLastError();
 }
 
