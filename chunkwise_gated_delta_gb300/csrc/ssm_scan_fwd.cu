@@ -23,11 +23,11 @@ namespace {
 // own shared-memory loads and exponentials two cycles of three, and one block of 32 channels per
 // 1.7 warps and scheduler is all that B 4, D 2048 has: the feeders fill those slots.
 
-// L lanes of NS states per channel; a tile has KT tokens per lane.
-template <int L, int NS, int KT> struct FwdTiles {
-    static constexpr int kFeeders = 16 * KT, kThreads = kScanThreads + kFeeders;   // one feeder per 8 channels of a token
+// L lanes of NS states per channel, WN carrier warps; a tile has KT tokens per lane.
+template <int L, int NS, int KT, int WN> struct FwdTiles {
+    static constexpr int kFeeders = 4 * WN * KT, kCarriers = 32 * WN, kThreads = kCarriers + kFeeders;   // one feeder per 8 channels of a token
     static_assert(NS % 4 == 0 && 32 % L == 0, "16-byte shared-memory accesses take four states");
-    static constexpr int NP = NS * L, CW = 32 / L, CH = 4 * CW, TT = KT * L, YS = CH + CW;
+    static constexpr int NP = NS * L, CW = 32 / L, CH = WN * CW, TT = KT * L, YS = CH + CW;
     f2x2 d[2][TT * CH];                    // {dt, dt}, {dt x, dt x}; 16-byte words swizzled, see at()
     float B[2][TT][NP], C[2][TT][NP];
     float y[2][TT][YS];                    // row stride: the tokens of a channel's lanes in different banks
@@ -65,9 +65,9 @@ template <class T, bool XV> struct Eight {
     }
 };
 
-template <class T, int L, int NS, int KT, bool XV>
-__global__ void __launch_bounds__(16 * KT + kScanThreads) scan_fwd_kernel(ScanParams p, int chan_blocks) {
-    using S = FwdTiles<L, NS, KT>;
+template <class T, int L, int NS, int KT, int WN, bool XV>
+__global__ void __launch_bounds__(4 * WN * KT + 32 * WN) scan_fwd_kernel(ScanParams p, int chan_blocks) {
+    using S = FwdTiles<L, NS, KT, WN>;
     constexpr int kFeeders = S::kFeeders;
     auto meet = [] { meet_all<S::kThreads>(); };
     constexpr int NP = S::NP, CW = S::CW, CH = S::CH, TT = S::TT;
@@ -80,9 +80,9 @@ __global__ void __launch_bounds__(16 * KT + kScanThreads) scan_fwd_kernel(ScanPa
     const int tiles = (g.len + TT - 1) / TT;
     const long long row0 = g.row0 + g.t0;
 
-    if (threadIdx.x >= kScanThreads) {
+    if (threadIdx.x >= S::kCarriers) {
         // ------------------------------------------------------------------ feeders
-        const int tid = threadIdx.x - kScanThreads;
+        const int tid = threadIdx.x - S::kCarriers;
         const int t = tid / (CH / 8), c0 = tid % (CH / 8) * 8;       // this thread's token and channels
         const int d = d0 + c0, n = p.D - d;                          // n <= 0: none of them exist
         const bool some = n > 0;
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(16 * KT + kScanThreads) scan_fwd_kernel(ScanPa
         }
     }
     // the swizzle's period in tokens: at() sees t CH / 8 modulo 8
-    constexpr int P = L <= 2 ? 1 : L / 2;
+    constexpr int P = CH >= 64 ? 1 : 64 / CH;
     int off[P];
 #pragma unroll
     for (int k = 0; k < P; ++k) off[k] = S::at(k * CH + warp * CW + c) - k * CH;
@@ -412,24 +412,30 @@ __global__ void __launch_bounds__(kScanThreads) scan_step_kernel(ScanParams p, i
     }
 }
 
-template <class T, int L, int NS, int KT, bool XV> cudaError_t fwd_start(const ScanParams &p, cudaStream_t s) {
-    using S = FwdTiles<L, NS, KT>;
+template <class T, int L, int NS, int KT, int WN, bool XV> cudaError_t fwd_start(const ScanParams &p, cudaStream_t s) {
+    using S = FwdTiles<L, NS, KT, WN>;
     const int cb = (p.D + S::CH - 1) / S::CH;
     const long long blocks = scan_slots(p, p.seg) * cb;
     if (blocks > 0x7fffffffLL) return cudaErrorNotSupported;
     constexpr int smem = sizeof(S) + (XV ? 3 * 3 * Eight<T, XV>::W * 16 * S::kFeeders : 0);
     const cudaError_t e =
-        cudaFuncSetAttribute(scan_fwd_kernel<T, L, NS, KT, XV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaFuncSetAttribute(scan_fwd_kernel<T, L, NS, KT, WN, XV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    scan_fwd_kernel<T, L, NS, KT, XV><<<(unsigned)blocks, S::kThreads, smem, s>>>(p, cb);
+    scan_fwd_kernel<T, L, NS, KT, WN, XV><<<(unsigned)blocks, S::kThreads, smem, s>>>(p, cb);
     return cudaGetLastError();
 }
 
 // 16-byte accesses to x, delta, z and y where all of them allow it.
-template <class T, int L, int NS, int KT> cudaError_t fwd_launch(const ScanParams &p, cudaStream_t s) {
+template <class T, int L, int NS, int KT, int WN> cudaError_t fwd_warps(const ScanParams &p, cudaStream_t s) {
     const bool xv = p.D % 8 == 0 && rows_aligned(p.x, p.ld_x, sizeof(T), 16) && rows_aligned(p.delta, p.ld_delta, sizeof(T), 16) &&
                     rows_aligned(p.z, p.ld_z, sizeof(T), 16) && rows_aligned(p.y, p.ld_y, sizeof(T), 16);
-    return xv ? fwd_start<T, L, NS, KT, true>(p, s) : fwd_start<T, L, NS, KT, false>(p, s);
+    return xv ? fwd_start<T, L, NS, KT, WN, true>(p, s) : fwd_start<T, L, NS, KT, WN, false>(p, s);
+}
+// Two carrier warps to a block where blocks of four would leave half of the SMs without one: the same work
+// on twice the SMs (T 2048, 64 blocks of four: 99 us, 128 of two: ).
+template <class T, int L, int NS, int KT> cudaError_t fwd_launch(const ScanParams &p, cudaStream_t s) {
+    const long long four = scan_slots(p, p.seg) * ((p.D + 128 / L - 1) / (128 / L));
+    return 2 * four <= sm_count() ? fwd_warps<T, L, NS, KT, 2>(p, s) : fwd_warps<T, L, NS, KT, 4>(p, s);
 }
 
 template <class T, int L> cudaError_t step_launch(const ScanParams &p, cudaStream_t s) {

@@ -8,10 +8,12 @@ dt |A| >= 0.01 for all but a few states and T <= 300, so a state is off by at mo
 m (4 u) + 8 u with m <= 100: 2.5e-5, and each gradient, a product of two such
 recurrences, by twice that plus its sums' rounding: 1e-4.
 """
+import ctypes
+
 import pytest
 import torch
 
-from chunkwise_gated_delta_gb300 import ssm_scan_bwd, ssm_scan_fwd, ssm_scan_step
+from chunkwise_gated_delta_gb300 import _lib, ssm_scan_bwd, ssm_scan_fwd, ssm_scan_step
 
 from mixer_ref import half_step, rel, spans_of, ssm_scan
 
@@ -94,6 +96,34 @@ def test_packed(dtype, lens):
     d, dy, dht = _inputs(T, len(lens), 50, 16, dtype, seed=T)
     cu = torch.tensor([0] + [b for _, b in spans_of(lens)], dtype=torch.int32, device=DEV)
     _check(d, dy, dht, lens, _call(d, dy, dht, 1, T, cu))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N,D,lens", [(16, 70, [1500]), (5, 24, [1030, 0, 300, 257, 1]), (32, 100, [900]), (3, 36, [2050]),
+                                      (16, 64, [0, 1100]), (16, 48, [769])])
+def test_long_sequences_on_few_channels(dtype, N, D, lens):
+    """Few blocks, long sequences: the forward cuts them into segments (256 tokens and more) that
+    run side by side; against the definition and against the unsplit form of the same call.
+    The tolerance of the module holds for T <= 300; the states' memory, not T, bounds the error, and
+    dt |A| >= 0.01 keeps it at 100 tokens here too."""
+    T = sum(lens)
+    d, dy, dht = _inputs(T, len(lens), D, N, dtype, seed=T + N)
+    cu = torch.tensor([0] + [b for _, b in spans_of(lens)], dtype=torch.int32, device=DEV) if len(lens) > 1 else None
+    v = [d[k] if k in ("A", "D", "delta_bias", "h0") else d[k][None] for k in NAMES]
+    y, ht = ssm_scan_fwd(*v, cu_seqlens=cu)
+    ry, rht = ssm_scan(*(d[k].double() for k in NAMES), spans_of(lens), True)
+    assert rel(y[0], ry) <= half_step(dtype) + F_TOL and rel(ht, rht) <= F_TOL
+    # the unsplit form: no workspace
+    code = _lib.KDA_BF16 if dtype == torch.bfloat16 else _lib.KDA_F32
+    y1, ht1 = torch.empty_like(y), torch.empty_like(ht)
+    p = lambda t: t.data_ptr()  # noqa: E731
+    args = _lib.SsmScanFwdArgs(len(lens), T, D, N, code, 1, p(v[0]), 0, p(v[1]), 0, p(v[3]), 0, p(v[4]), 0, p(v[6]), 0, p(v[2]),
+                               p(v[5]), p(v[7]), p(v[8]), p(y1), 0, p(ht1), None, 0, None if cu is None else p(cu))
+    lib = _lib.load()
+    assert lib.ssm_scan_fwd_workspace(ctypes.byref(args)) > 0
+    assert lib.ssm_scan_fwd(ctypes.byref(args), torch.cuda.current_stream().cuda_stream) == _lib.KDA_OK
+    torch.cuda.synchronize()
+    assert rel(y1[0], ry) <= half_step(dtype) + F_TOL and rel(ht1, rht) <= F_TOL
 
 
 def test_empty_batch_of_sequences_passes_the_states():
