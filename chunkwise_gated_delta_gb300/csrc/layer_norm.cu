@@ -58,12 +58,22 @@ __device__ __forceinline__ void block_sums(float (&v)[N], float (*sm)[N]) {
     __syncthreads();                       // the previous sums have been read
     if ((lane & (32 / N - 1)) == 0) sm[warp][base] = v[0];
     __syncthreads();
+    // N times warps values, one per lane (the lanes beyond repeat them): over the warps, then to everyone
+    constexpr int M = TPR / 32 * N;
+    static_assert(M <= 32, "one value per lane");
+    float t = (&sm[0][0])[lane % M];
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-        v[k] = 0.f;
+    for (int s = N; s < M; s <<= 1) t += __shfl_xor_sync(~0u, t, s);
 #pragma unroll
-        for (int w = 0; w < TPR / 32; ++w) v[k] += sm[w][k];
-    }
+    for (int k = 0; k < N; ++k) v[k] = __shfl_sync(~0u, t, k);
+}
+
+// 1 / sqrt(v): the approximate function and one step of Newton's method, off by about one unit in the last
+// place; a division after a square root takes thirty instructions per row and thread.
+__device__ __forceinline__ float inv_sqrt(float v) {
+    const float r = rsqrtf(v);
+    const float n = fmaf(-0.5f * v * r, r, 0.5f);
+    return v > 0.f && r > 0.f ? fmaf(r, n, r) : r;      // (0 and infinity: the function's own infinity and 0)
 }
 
 // Short rows: one per warp, lane i with vectors i and i + 32.
@@ -95,7 +105,7 @@ __global__ void __launch_bounds__(128) norm_fwd_warp_kernel(NormParams p) {
             v[k][e] = add2(v[k][e], both(-mean));
             if (lane + k * 32 < nv) acc = fma2(v[k][e], v[k][e], acc);
         }
-    const float rstd = 1.f / sqrtf(warp_sum(pair_sum<V>(acc)) / (float)p.D + p.eps);
+    const float rstd = inv_sqrt(warp_sum(pair_sum<V>(acc)) / (float)p.D + p.eps);
     if (lane == 0) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
@@ -185,7 +195,7 @@ __global__ void __launch_bounds__(TPR, 512 / TPR) norm_fwd_kernel(NormParams p) 
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (row + r >= p.rows) break;
-            const float rstd = 1.f / sqrtf(s[r] * inv + p.eps);
+            const float rstd = inv_sqrt(s[r] * inv + p.eps);
             if (tid == 0) {
                 if (p.mean) p.mean[row + r] = mean[r];
                 if (p.rstd) p.rstd[row + r] = rstd;
@@ -218,7 +228,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(NormParams p) {
         const float d = to_f(x[c]) - mean;
         q = fmaf(d, d, q);
     }
-    const float rstd = 1.f / sqrtf(row_sum2<1024>(make_float2(q, 0.f), sm).x / (float)p.D + p.eps);
+    const float rstd = inv_sqrt(row_sum2<1024>(make_float2(q, 0.f), sm).x / (float)p.D + p.eps);
     if (threadIdx.x == 0) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;

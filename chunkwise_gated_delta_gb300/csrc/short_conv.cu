@@ -56,34 +56,38 @@ __global__ void __launch_bounds__(128, 4) conv_fwd_kernel(ConvParams p, long lon
     T *y = static_cast<T *>(p.y) + (g.row0 + g.t0) * p.ld_y + c;
     // four rows at a time, the next four on their way (past the end the last row again, without a branch)
     Lanes<T, V> in[4], next[4];
-    if (g.len > 0)
+    auto fetch = [&](int last) {               // rows 0 .. 3 from x, at most up to row `last`
 #pragma unroll
-        for (int k = 0; k < 4; ++k) next[k].load(x + min(k, g.len - 1) * p.ld_x);
-    for (int left = g.len; left > 0; left -= 4) {
+        for (int k = 0; k < 4; ++k) next[k].load(x + min(k, last) * p.ld_x);
         x += 4 * p.ld_x;
+    };
+    auto token = [&](const Lanes<T, V> &v) {
+        f2 o[P];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            in[k] = next[k];
-            next[k].load(x + min(k, left - 5) * p.ld_x);       // (at or before the last row)
+        for (int e = 0; e < P; ++e) {
+            win[W - 1][e] = v.pair(e);
+            f2 pre = bias[e];
+#pragma unroll
+            for (int j = 0; j < W; ++j) pre = fma2(w[j][e], win[j][e], pre);
+            o[e] = p.silu ? silu2(pre) : pre;
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) win[j][e] = win[j + 1][e];
         }
+        store_lanes<T, V>(y, o);
+        y += p.ld_y;
+    };
+    int left = g.len;
+    if (left > 0) fetch(left - 1);
+    for (; left >= 4; left -= 4) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (k < left) {
-                f2 o[P];
+        for (int k = 0; k < 4; ++k) in[k] = next[k];
+        fetch(left - 5);                       // (at or before the last row)
 #pragma unroll
-                for (int e = 0; e < P; ++e) {
-                    win[W - 1][e] = in[k].pair(e);
-                    f2 pre = bias[e];
-#pragma unroll
-                    for (int j = 0; j < W; ++j) pre = fma2(w[j][e], win[j][e], pre);
-                    o[e] = p.silu ? silu2(pre) : pre;
-#pragma unroll
-                    for (int j = 0; j < W - 1; ++j) win[j][e] = win[j + 1][e];
-                }
-                store_lanes<T, V>(y, o);
-                y += p.ld_y;
-            }
+        for (int k = 0; k < 4; ++k) token(in[k]);
     }
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+        if (k < left) token(next[k]);
     if (p.ht && g.i == g.n - 1)     // the last inputs, the state's among them after a short sequence
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
@@ -184,7 +188,7 @@ __global__ void __launch_bounds__(128, 3) conv_bwd_kernel(ConvParams p, long lon
             }
         const T *px = x, *pd = gy;
         T *out = dx - (W - 1) * p.ld_y;                  // of position t - (W - 1)
-        for (int t = 0; t < g.len; t += 4) {
+        auto four = [&](int t) {                         // rows t .. t + 3 to work on, the next four on their way
             px += 4 * p.ld_x;
             pd += 4 * p.ld_dy;
 #pragma unroll
@@ -194,20 +198,36 @@ __global__ void __launch_bounds__(128, 3) conv_bwd_kernel(ConvParams p, long lon
                 xn[k].load(px + min(k, last - 4 - t) * p.ld_x);
                 dn[k].load(pd + min(k, last - 4 - t) * p.ld_dy);
             }
-            // inside the segment, away from the sequence's end: nothing to ask for
-            const bool inside = t > 0 && t + 4 <= g.len && (!p.dht || g.t0 + t + 4 <= g.total);
+        };
+        auto edge = [&](int t) {                         // near the ends of the segment or of the sequence
+            four(t);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (t + k < g.len) {
+                    f2 o[P];
+                    dpre(xi[k], di[k], true);
+                    gradient(o);
+                    put(g.t0 + t + k - (W - 1), o);
+                    shift();
+                }
+            out += 4 * p.ld_y;
+        };
+        int t = 0;
+        if (g.len > 0) edge(0);
+        // inside, with nothing to ask for: positions t - (W - 1) .. are this segment's, and before the final state's
+        for (t = 4; t + 4 <= g.len && g.t0 + t + 4 <= g.total; t += 4) {
+            four(t);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                if (t + k >= g.len) break;
                 f2 o[P];
                 dpre(xi[k], di[k], true);
                 gradient(o);
-                if (inside) store_lanes<T, V>(out, o);
-                else put(g.t0 + t + k - (W - 1), o);
+                store_lanes<T, V>(out, o);
                 out += p.ld_y;
                 shift();
             }
         }
+        for (; t < g.len; t += 4) edge(t);
         // the W - 1 tokens behind the segment: the next segment's, or none (dpre = 0)
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) {
@@ -345,7 +365,7 @@ int segment_length(const ConvParams &p, int V, int resident) {
     long long best = 0;
     int seg = 4;
     for (int s = 4; s <= 64; s += 4) {
-        const long long threads = (tokens + s - 1) / s * groups, cost = (threads + room - 1) / room * (s + 8);
+        const long long threads = ((tokens + s - 1) / s + (p.cu_seqlens ? p.B : 0)) * groups, cost = (threads + room - 1) / room * (s + 8);
         if (!best || cost <= best) {
             best = cost;
             seg = s;

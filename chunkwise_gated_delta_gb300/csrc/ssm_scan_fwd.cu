@@ -6,6 +6,8 @@
 // elements of HBM traffic.  With N = 16 the exponentials (32 per clock and SM) take 1.4 times
 // as long as the traffic, so the kernel is bound by the special-function and FMA pipes, and the
 // states stay in registers from the first token to the last.
+#include <type_traits>
+
 #include "ssm_scan.cuh"
 
 namespace mixer {
@@ -38,6 +40,9 @@ template <int L, int NS, int KT, int WN> struct FwdTiles {
 
 template <int N> __device__ __forceinline__ void meet_all() { asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory"); }
 
+__device__ __forceinline__ void store_pairs(uint32_t to, f2 a, f2 b) {
+    asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(to), "l"(a), "l"(b) : "memory");
+}
 __device__ __forceinline__ void copy16(void *to, const void *from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
 }
@@ -71,7 +76,7 @@ __global__ void __launch_bounds__(4 * WN * KT + 32 * WN) scan_fwd_kernel(ScanPar
     constexpr int kFeeders = S::kFeeders;
     auto meet = [] { meet_all<S::kThreads>(); };
     constexpr int NP = S::NP, CW = S::CW, CH = S::CH, TT = S::TT;
-    extern __shared__ __align__(16) unsigned char raw[];
+    extern __shared__ __align__(128) unsigned char raw[];
     S &sm = *reinterpret_cast<S *>(raw);
     const long long slot = blockIdx.x / chan_blocks;
     const int d0 = (int)(blockIdx.x - slot * chan_blocks) * CH;
@@ -100,14 +105,15 @@ __global__ void __launch_bounds__(4 * WN * KT + 32 * WN) scan_fwd_kernel(ScanPar
             dbias[k] = pack2(e < n && p.delta_bias ? p.delta_bias[d + e] : 0.f, e + 1 < n && p.delta_bias ? p.delta_bias[d + e + 1] : 0.f);
             skip[k] = pack2(e < n && p.Dskip ? p.Dskip[d + e] : 0.f, e + 1 < n && p.Dskip ? p.Dskip[d + e + 1] : 0.f);
         }
-        // Bm and Cm of a tile: elements tid, tid + 256, ...
+        // Bm and Cm of a tile: four neighbouring states per access (XV), or elements tid, tid + feeders, ...
+        constexpr int EV = (2 * TT * NP / 4 + kFeeders - 1) / kFeeders;
         constexpr int E = TT * NP < kFeeders ? 1 : TT * NP / kFeeders;
         const int bt = tid / NP, bn = tid % NP;                      // NP divides the feeders
         const bool bs = TT * NP >= kFeeders || bt < TT;              // (N <= 8: more threads than elements)
         const int bl = min(bn, p.N - 1);
-        const T *Bp = static_cast<const T *>(p.Bm) + row0 * p.ld_B + bl;
-        const T *Cp = static_cast<const T *>(p.Cm) + row0 * p.ld_C + bl;
+        const T *const Bp = static_cast<const T *>(p.Bm) + row0 * p.ld_B, *const Cp = static_cast<const T *>(p.Cm) + row0 * p.ld_C;
         constexpr int BT = kFeeders / NP;                            // tokens between a thread's elements
+        using Quad = RawQuad<T>;
         // x, delta and z on their way.  XV: asynchronous copies of three tiles, each thread its own
         // eight channels into words of its own, so nobody else waits for them.  Otherwise one tile in registers.
         using Data = Eight<T, XV>;
@@ -115,7 +121,8 @@ __global__ void __launch_bounds__(4 * WN * KT + 32 * WN) scan_fwd_kernel(ScanPar
         uint4 *const ring = reinterpret_cast<uint4 *>(raw + sizeof(S)) + tid;      // [RING][3][W][feeders]
         Data f[XV ? 1 : 3] = {};
         Data xc{}, zc{}, xo{}, zo{};                                 // x and z of the current and the last tile
-        uint32_t be[E], ce[E];                                       // the next tile's Bm and Cm
+        uint32_t be[XV ? 1 : E], ce[XV ? 1 : E];                     // the next tile's Bm and Cm
+        typename Quad::type bq[XV ? EV : 1];
         const T *const pz = z ? z : x;                               // (no gate: loaded all the same, not used)
         const long long ldz = z ? p.ld_z : p.ld_x, sy = TT * p.ld_y;
         int row = t, slot3 = 0;                                      // of the next fetch; its place in the ring
@@ -141,32 +148,57 @@ __global__ void __launch_bounds__(4 * WN * KT + 32 * WN) scan_fwd_kernel(ScanPar
             }
             row += TT;
         };
-        int rowb = bt;
+        int rowb = 0;
         auto fetch_bc = [&] {
+            if constexpr (XV) {
 #pragma unroll
-            for (int k = 0; k < E; ++k) {
-                const long long r = min(rowb + k * BT, g.len - 1);
-                be[k] = load_bits(Bp + r * p.ld_B);
-                ce[k] = load_bits(Cp + r * p.ld_C);
+                for (int k = 0; k < EV; ++k) {
+                    constexpr int PER = TT * NP / 4;                 // quads of Bm, then as many of Cm
+                    const int u = min(tid + k * kFeeders, 2 * PER - 1), w = u % PER;
+                    const long long r = min(rowb + w / (NP / 4), g.len - 1);
+                    const int n = min(w % (NP / 4) * 4, p.N - 4);
+                    bq[k] = *reinterpret_cast<const typename Quad::type *>((u < PER ? Bp + r * p.ld_B : Cp + r * p.ld_C) + n);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < E; ++k) {
+                    const long long r = min(rowb + bt + k * BT, g.len - 1);
+                    be[k] = load_bits(Bp + r * p.ld_B + bl);
+                    ce[k] = load_bits(Cp + r * p.ld_C + bl);
+                }
             }
             rowb += TT;
         };
         auto stage_bc = [&](int tile) {
             const int b = tile & 1;
+            if constexpr (XV) {
 #pragma unroll
-            for (int k = 0; k < E; ++k) {
-                if (!bs) break;
-                sm.B[b][bt + k * BT][bn] = bn < p.N ? bits_f<T>(be[k]) : 0.f;
-                sm.C[b][bt + k * BT][bn] = bn < p.N ? bits_f<T>(ce[k]) : 0.f;
+                for (int k = 0; k < EV; ++k) {
+                    constexpr int PER = TT * NP / 4;
+                    const int u = tid + k * kFeeders, w = u % PER, n = w % (NP / 4) * 4;
+                    float4 v = Quad::floats(bq[k]);
+                    if (n >= p.N) v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (u < 2 * PER) *reinterpret_cast<float4 *>(&(u < PER ? sm.B : sm.C)[b][w / (NP / 4)][n]) = v;
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < E; ++k) {
+                    if (!bs) break;
+                    sm.B[b][bt + k * BT][bn] = bn < p.N ? bits_f<T>(be[k]) : 0.f;
+                    sm.C[b][bt + k * BT][bn] = bn < p.N ? bits_f<T>(ce[k]) : 0.f;
+                }
             }
         };
-        f2x2 *const sd0 = &sm.d[0][tid * 8], *const sd1 = &sm.d[1][tid * 8];
-        const int sw = tid & 7;                                      // at(tid 8 + k) = tid 8 + (k ^ sw)
+        // word at(tid 8 + k) = tid 8 + (k ^ (tid & 7)): the address is that of k = 0, exclusive or 16 k
+        const uint32_t sd0 = (uint32_t)__cvta_generic_to_shared(&sm.d[0][tid * 8 + (tid & 7)]);
+        const uint32_t sd1 = (uint32_t)__cvta_generic_to_shared(&sm.d[1][tid * 8 + (tid & 7)]);
         int from = 0;
         // Stage one tile and finish another.  The two have nothing to do with each other, and there is no
         // branch in either, so their long dependent chains (exponential, sum, reciprocal, ...) overlap.
-        auto work = [&](int staged, int finished, bool store) {
-            f2x2 *const sd = staged & 1 ? sd1 : sd0;
+        // PLAIN: a gate, a softplus and a whole tile, which take no selections.
+        auto work_on = [&](auto plain, int staged, int finished, bool store) {
+            constexpr bool PLAIN = decltype(plain)::value;
+            const uint32_t sd = staged & 1 ? sd1 : sd0;
             Data dc{}, xn{}, zn{};
             if (XV) {
                 asm volatile("cp.async.wait_group 2;" ::: "memory");
@@ -189,21 +221,23 @@ __global__ void __launch_bounds__(4 * WN * KT + 32 * WN) scan_fwd_kernel(ScanPar
             const bool in = staged * TT + t < g.len;                 // behind the end the state stays as it is
 #pragma unroll
             for (int k = 0; k < 8; k += 2) {
-                const f2 raw_dt = add2(dc.pair(k), dbias[k / 2]);
-                const f2 sp = softplus2(raw_dt);
-                const f2 dt = p.softplus ? sp : raw_dt;
+                f2 dt = add2(dc.pair(k), dbias[k / 2]);
+                const f2 sp = softplus2(dt);
+                dt = PLAIN || p.softplus ? sp : dt;
                 o[k / 2] = fma2(skip[k / 2], xo.pair(k), o[k / 2]);
                 const f2 gated = mul2(o[k / 2], silu2(zo.pair(k)));
-                o[k / 2] = z ? gated : o[k / 2];
+                o[k / 2] = PLAIN || z ? gated : o[k / 2];
                 float lo, hi, ul, uh;
                 unpack2(dt, lo, hi);
                 unpack2(mul2(dt, xn.pair(k)), ul, uh);
-                lo = in ? lo : 0.f;
-                hi = in ? hi : 0.f;
-                ul = in ? ul : 0.f;
-                uh = in ? uh : 0.f;
-                sd[k ^ sw] = {both(lo), both(ul)};
-                sd[(k + 1) ^ sw] = {both(hi), both(uh)};
+                if (!PLAIN) {
+                    lo = in ? lo : 0.f;
+                    hi = in ? hi : 0.f;
+                    ul = in ? ul : 0.f;
+                    uh = in ? uh : 0.f;
+                }
+                store_pairs(sd ^ 16 * k, both(lo), both(ul));
+                store_pairs(sd ^ 16 * (k + 1), both(hi), both(uh));
             }
             float v[8];
 #pragma unroll
@@ -225,6 +259,10 @@ __global__ void __launch_bounds__(4 * WN * KT + 32 * WN) scan_fwd_kernel(ScanPar
             zo = zc;
             xc = xn;
             zc = zn;
+        };
+        auto work = [&](int staged, int finished, bool store) {
+            if (z && p.softplus && (staged + 1) * TT <= g.len) work_on(std::true_type{}, staged, finished, store);
+            else work_on(std::false_type{}, staged, finished, store);
         };
         if (tiles > 0) {
             fetch_bc();
@@ -425,10 +463,12 @@ template <class T, int L, int NS, int KT, int WN, bool XV> cudaError_t fwd_start
     return cudaGetLastError();
 }
 
-// 16-byte accesses to x, delta, z and y where all of them allow it.
+// 16-byte accesses to x, delta, z and y, and four states of Bm and Cm at a time, where all of them allow it.
 template <class T, int L, int NS, int KT, int WN> cudaError_t fwd_warps(const ScanParams &p, cudaStream_t s) {
-    const bool xv = p.D % 8 == 0 && rows_aligned(p.x, p.ld_x, sizeof(T), 16) && rows_aligned(p.delta, p.ld_delta, sizeof(T), 16) &&
-                    rows_aligned(p.z, p.ld_z, sizeof(T), 16) && rows_aligned(p.y, p.ld_y, sizeof(T), 16);
+    const size_t es = sizeof(T);
+    const bool xv = p.D % 8 == 0 && rows_aligned(p.x, p.ld_x, es, 16) && rows_aligned(p.delta, p.ld_delta, es, 16) &&
+                    rows_aligned(p.z, p.ld_z, es, 16) && rows_aligned(p.y, p.ld_y, es, 16) && p.N % 4 == 0 &&
+                    rows_aligned(p.Bm, p.ld_B, es, 4 * es) && rows_aligned(p.Cm, p.ld_C, es, 4 * es);
     return xv ? fwd_start<T, L, NS, KT, WN, true>(p, s) : fwd_start<T, L, NS, KT, WN, false>(p, s);
 }
 // Two carrier warps to a block where blocks of four would leave half of the SMs without one: the same work
