@@ -63,7 +63,7 @@ template <class T, bool XV> __device__ __forceinline__ void store_four(T *p, con
 // and g of all channels into shared memory (four channels per access), then the recurrences.  Four
 // blocks to an SM cover each other's phases.
 template <int L, int NS> struct LocalTiles {
-    static constexpr int TT = 32, CH = kScanThreads / L, NP = NS * L;
+    static constexpr int TT = 16, CH = kScanThreads / L, NP = NS * L;
     f2x2 d[TT][CH];                  // {dt, dt}, {dt x, dt x}; columns swizzled, see at()
     f2 g[TT][CH];
     float B[TT][NP], C[TT][NP];
@@ -74,7 +74,7 @@ template <int L, int NS> struct LocalTiles {
 };
 
 template <class T, int L, int NS, bool GRAD, bool XV>
-__global__ void __launch_bounds__(kScanThreads, 4) scan_local_kernel(ScanParams p, int chan_blocks, bool vec) {
+__global__ void __launch_bounds__(kScanThreads, XV && sizeof(T) == 2 ? 6 : 4) scan_local_kernel(ScanParams p, int chan_blocks, bool vec) {
     using S = LocalTiles<L, NS>;
     constexpr int TT = S::TT, CH = S::CH, NP = S::NP, H = NS / 2, Q = CH / 4, ROWS = kScanThreads / Q, K = TT / ROWS;
     extern __shared__ __align__(16) unsigned char raw[];
@@ -261,24 +261,25 @@ __global__ void __launch_bounds__(128) scan_boundary_kernel(ScanParams p, int NP
 constexpr int TC = 8;                // tokens per part, recomputed into registers
 constexpr int GROUPS = 2;            // channel groups that a block walks per part
 constexpr int PARTS = SEG / TC;
-constexpr int kGradThreads = 256;
+constexpr int kGradThreads = 128;   // two blocks to an SM: one loads or stores while the other computes
+constexpr int kGradWarps = kGradThreads / 32;
 
 template <int L> struct GradTiles {
-    static constexpr int NP = 4 * L, CW = 32 / L, CG = 8 * CW, CH = GROUPS * CG;   // channels of a warp, group, block
+    static constexpr int NP = 4 * L, CW = 32 / L, CG = kGradWarps * CW, CH = GROUPS * CG;   // channels of a warp, group, block
     static constexpr int XS = CH + 4;
     f2x2 entry[GROUPS][PARTS][kGradThreads];     // states before each part
     float2 du[SEG][XS];                          // dt, dt x; after a part: dt, sum_n G B
     float g[SEG][XS];                            // g; after a part: sum_n q A / ln 2
     float y[SEG][XS];                            // sum_n C h
     float B[SEG][NP], C[SEG][NP];
-    float red[8][TC * 2 * NP];
+    float red[kGradWarps][TC * 2 * NP];
 };
 
-// A block: 64 tokens, 16 CW channels, 8 warps.  All inputs go through shared memory once, four channels
+// A block: 64 tokens, 8 CW channels, 4 warps.  All inputs go through shared memory once, four channels
 // per access; the parts leave their sums over states there, and a last sweep over (token, channel) turns
 // them into dx, ddelta and dz, again four channels per access.
 template <class T, int L, bool XV>
-__global__ void __launch_bounds__(kGradThreads, 1) scan_grad_kernel(ScanParams p, int chan_blocks, bool vec) {
+__global__ void __launch_bounds__(kGradThreads, 2) scan_grad_kernel(ScanParams p, int chan_blocks, bool vec) {
     using S = GradTiles<L>;
     constexpr int NP = S::NP, CW = S::CW, CH = S::CH, TL = TC / L, Q = CH / 4, ROWS = kGradThreads / Q, K = SEG / ROWS;
     extern __shared__ __align__(16) unsigned char raw[];
@@ -443,7 +444,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grad_kernel(ScanParams p
                 sm.y[t][cc] = ys[j];
             }
         }
-        // dB and dC over the warp's channels, then over the eight warps
+        // dB and dC over the warp's channels, then over the warps
         float v[2 * TC * 4];
 #pragma unroll
         for (int t = 0; t < TC; ++t)
@@ -476,7 +477,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grad_kernel(ScanParams p
             const int t = part * TC + u / (2 * NP);
             float s = 0.f;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) s += sm.red[w][u];
+            for (int w = 0; w < kGradWarps; ++w) s += sm.red[w][u];
             if (t < g.len)
                 p.part_bc[((long long)cb * ((long long)(p.cu_seqlens ? 1 : p.B) * p.T) + row + t) * (2 * NP) + u % (2 * NP)] = s;
         }

@@ -471,11 +471,12 @@ template <class T, int L, int NS, int KT, int WN> cudaError_t fwd_warps(const Sc
                     rows_aligned(p.Bm, p.ld_B, es, 4 * es) && rows_aligned(p.Cm, p.ld_C, es, 4 * es);
     return xv ? fwd_start<T, L, NS, KT, WN, true>(p, s) : fwd_start<T, L, NS, KT, WN, false>(p, s);
 }
-// Two carrier warps to a block where blocks of four would leave half of the SMs without one: the same work
-// on twice the SMs (T 2048, 64 blocks of four: 99 us, 128 of two: ).
-template <class T, int L, int NS, int KT> cudaError_t fwd_launch(const ScanParams &p, cudaStream_t s) {
-    const long long four = scan_slots(p, p.seg) * ((p.D + 128 / L - 1) / (128 / L));
-    return 2 * four <= sm_count() ? fwd_warps<T, L, NS, KT, 2>(p, s) : fwd_warps<T, L, NS, KT, 4>(p, s);
+// Half as many carrier warps to a block where full blocks would leave half of the SMs without one: the same
+// work on twice the SMs (training step B 2, T 2048, D 2048: 382 -> 368 us).
+template <class T, int L, int NS, int KT, int WN> cudaError_t fwd_launch(const ScanParams &p, cudaStream_t s) {
+    constexpr int CH = WN * 32 / L;
+    const long long full = scan_slots(p, p.seg) * ((p.D + CH - 1) / CH);
+    return 2 * full <= sm_count() ? fwd_warps<T, L, NS, KT, WN / 2>(p, s) : fwd_warps<T, L, NS, KT, WN>(p, s);
 }
 
 template <class T, int L> cudaError_t step_launch(const ScanParams &p, cudaStream_t s) {
@@ -490,10 +491,10 @@ template <class T, int L> cudaError_t step_launch(const ScanParams &p, cudaStrea
 }
 
 template <class T> cudaError_t fwd_type(const ScanParams &p, cudaStream_t s) {
-    if (p.N <= 4) return fwd_launch<T, 1, 4, 16>(p, s);
-    if (p.N <= 8) return fwd_launch<T, 1, 8, 16>(p, s);
-    if (p.N <= 16) return fwd_launch<T, 2, 8, 16>(p, s);
-    return fwd_launch<T, 4, 8, 16>(p, s);
+    if (p.N <= 4) return fwd_launch<T, 1, 4, 16, 4>(p, s);
+    if (p.N <= 8) return fwd_launch<T, 1, 8, 16, 4>(p, s);
+    if (p.N <= 16) return fwd_launch<T, 2, 8, 16, 4>(p, s);
+    return fwd_launch<T, 4, 8, 16, 4>(p, s);
 }
 template <class T> cudaError_t step_type(const ScanParams &p, cudaStream_t s) {
     switch (lanes_for(p.N)) {
