@@ -386,6 +386,62 @@ int bwd_blocks(long long rows) {
     return (int)(want < most ? want : most);
 }
 
+// Few rows: dx by one block per row and dweight, dbias by blocks of 32 columns that read all rows once more
+// (from L2), in one launch and without partial sums.
+template <class T>
+__global__ void __launch_bounds__(256) norm_bwd_few_kernel(NormParams p, int col_blocks) {
+    __shared__ float2 sm[8][33];
+    const int tid = threadIdx.x;
+    if ((int)blockIdx.x < col_blocks) {
+        const int tx = tid & 31, ty = tid >> 5, c = blockIdx.x * 32 + tx;
+        float aw = 0.f, ab = 0.f;
+        if (c < p.D)
+#pragma unroll 4
+            for (int row = ty; row < (int)p.rows; row += 8) {
+                const float d = bits_f<T>(load_bits(static_cast<const T *>(p.dy) + row * p.ld_dy + c));
+                const float x = bits_f<T>(load_bits(static_cast<const T *>(p.x) + row * p.ld_x + c));
+                aw = fmaf(d, (x - __ldg(p.mean + row)) * __ldg(p.rstd + row), aw);
+                ab += d;
+            }
+        sm[ty][tx] = make_float2(aw, ab);
+        __syncthreads();
+        if (ty == 0 && c < p.D) {
+#pragma unroll
+            for (int k = 1; k < 8; ++k) {
+                aw += sm[k][tx].x;
+                ab += sm[k][tx].y;
+            }
+            if (p.dweight) store_w(p.dweight, c, p.w_bf16, aw);
+            if (p.dbias) store_w(p.dbias, c, p.w_bf16, ab);
+        }
+        return;
+    }
+    const long long row = blockIdx.x - col_blocks;
+    const T *x = static_cast<const T *>(p.x) + row * p.ld_x, *dy = static_cast<const T *>(p.dy) + row * p.ld_dy;
+    T *dx = static_cast<T *>(p.y) + row * p.ld_y;
+    const float mean = p.mean[row], rstd = p.rstd[row];
+    constexpr int K = 16;                        // D <= 256 K
+    float g[K], xh[K];
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = tid + 256 * k, cl = min(c, p.D - 1);
+        g[k] = bits_f<T>(load_bits(dy + cl)) * (p.weight ? load_w(p.weight, cl, p.w_bf16) : 1.f);
+        xh[k] = (bits_f<T>(load_bits(x + cl)) - mean) * rstd;
+        if (c < p.D) {
+            s.x += g[k];
+            s.y = fmaf(g[k], xh[k], s.y);
+        }
+    }
+    s = row_sum2<256>(s, &sm[0][0]);
+    const float mg = s.x / (float)p.D, mgx = s.y / (float)p.D;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (tid + 256 * k < p.D) dx[tid + 256 * k] = from_f<T>(rstd * (g[k] - mg - xh[k] * mgx));
+}
+// where the second reading costs less than a second launch
+bool few_rows(const NormParams &p) { return p.rows <= 256 && p.D <= 4096; }
+
 template <class T> constexpr int kVec = 16 / sizeof(T);
 
 template <class T> bool vec_ok(const NormParams &p) {
@@ -445,10 +501,19 @@ cudaError_t launch_layer_norm_fwd(const NormParams &p, bool bf, cudaStream_t s) 
 }
 
 cudaError_t launch_layer_norm_bwd(const NormParams &p, bool bf, cudaStream_t s) {
+    if (few_rows(p)) {
+        const int cols = p.dweight || p.dbias ? (p.D + 31) / 32 : 0;
+        const unsigned grid = (unsigned)(cols + p.rows);
+        if (bf) norm_bwd_few_kernel<bf16><<<grid, 256, 0, s>>>(p, cols);
+        else norm_bwd_few_kernel<float><<<grid, 256, 0, s>>>(p, cols);
+        return cudaGetLastError();
+    }
     if (bf) return vec_ok<bf16>(p) ? bwd_vec<bf16, 8>(p, s) : bwd_vec<bf16, 1>(p, s);
     return vec_ok<float>(p) ? bwd_vec<float, 4>(p, s) : bwd_vec<float, 1>(p, s);
 }
 
-size_t layer_norm_part_floats(const NormParams &p, bool) { return (size_t)bwd_blocks(p.rows) * 2 * p.D; }
+size_t layer_norm_part_floats(const NormParams &p, bool) {
+    return few_rows(p) ? 0 : (size_t)bwd_blocks(p.rows) * 2 * p.D;
+}
 
 }  // namespace mixer

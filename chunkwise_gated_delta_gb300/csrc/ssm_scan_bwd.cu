@@ -288,7 +288,15 @@ __global__ void __launch_bounds__(kGradThreads, 2) scan_grad_kernel(ScanParams p
     const long long slot = blockIdx.x / chan_blocks;
     const int cb = (int)(blockIdx.x - slot * chan_blocks), d0 = cb * CH;
     Segment g;
-    if (!segment_of(p.cu_seqlens, p.B, p.T, SEG, slot, g)) return;
+    if (!segment_of(p.cu_seqlens, p.B, p.T, SEG, slot, g)) {
+        // a slot that no sequence uses: its partial sums are zeros, so that the sums may take all slots
+        float *out = p.part_par + slot * ((long long)p.D * (p.N + 2));
+        const int end = min(d0 + CH, p.D);
+        for (int u = d0 * p.N + tid; u < end * p.N; u += kGradThreads) out[u] = 0.f;
+        for (int d = d0 + tid; d < end; d += kGradThreads)
+            out[(long long)p.D * p.N + d] = out[(long long)p.D * (p.N + 1) + d] = 0.f;
+        return;
+    }
     const long long row = g.row0 + g.t0;
 
     // ---- inputs to shared memory
@@ -549,24 +557,53 @@ __global__ void __launch_bounds__(kGradThreads, 2) scan_grad_kernel(ScanParams p
     }
 }
 
-// Sums dB and dC over the channel blocks and rounds them; rows outside every sequence are left alone.
-template <class T> __global__ void __launch_bounds__(256) scan_bc_kernel(ScanParams p, int blocks, int NP, long long rows) {
-    const long long u = (long long)blockIdx.x * 256 + threadIdx.x;
-    const long long row = u / (2 * NP);
-    const int j = (int)(u - row * (2 * NP)), n = j % NP;
-    if (row >= rows || n >= p.N) return;
-    if (p.cu_seqlens && (row < clamped(p.cu_seqlens[0], 0, p.T) || row >= clamped(p.cu_seqlens[p.B], 0, p.T))) return;
+// The sums, in a fixed order: blocks 0 .. bc_blocks - 1 add dB and dC over the channel blocks and round them
+// (rows outside every sequence are left alone), the others dA, dD and dbias over the segments, 32
+// columns of [D N + 2 D] each.
+template <class T>
+__global__ void __launch_bounds__(256) scan_sums_kernel(ScanParams p, int blocks, int NP, long long rows, unsigned bc_blocks, int slots) {
+    if (blockIdx.x < bc_blocks) {
+        const long long u = (long long)blockIdx.x * 256 + threadIdx.x;
+        const long long row = u / (2 * NP);
+        const int j = (int)(u - row * (2 * NP)), n = j % NP;
+        if (row >= rows || n >= p.N) return;
+        if (p.cu_seqlens && (row < clamped(p.cu_seqlens[0], 0, p.T) || row >= clamped(p.cu_seqlens[p.B], 0, p.T))) return;
+        float s = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < blocks; ++k) s += p.part_bc[(k * rows + row) * (2 * NP) + j];
+        if (j < NP) static_cast<T *>(p.dBm)[row * p.ld_dB + n] = from_f<T>(s);
+        else static_cast<T *>(p.dCm)[row * p.ld_dC + n] = from_f<T>(s);
+        return;
+    }
+    __shared__ float sm[8][33];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const long long par = (long long)p.D * p.N, cols = par + 2LL * p.D;
+    const long long c = (long long)(blockIdx.x - bc_blocks) * 32 + tx;
     float s = 0.f;
-    for (int k = 0; k < blocks; ++k) s += p.part_bc[(k * rows + row) * (2 * NP) + j];
-    if (j < NP) static_cast<T *>(p.dBm)[row * p.ld_dB + n] = from_f<T>(s);
-    else static_cast<T *>(p.dCm)[row * p.ld_dC + n] = from_f<T>(s);
-}
-
-// Slots that no sequence uses hold no partial sums: cleared, so that the sums may take all rows.
-__global__ void __launch_bounds__(256) scan_clear_kernel(ScanParams p, long long per) {
-    Segment g;
-    if (segment_of(p.cu_seqlens, p.B, p.T, p.seg, blockIdx.x, g) && g.len > 0) return;
-    for (long long k = threadIdx.x; k < per; k += 256) p.part_par[blockIdx.x * per + k] = 0.f;
+    if (c < cols) {
+        const float *q = p.part_par + c;
+        float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+        int r = ty;
+        for (; r + 24 < slots; r += 32) {
+            a0 += q[(long long)r * cols];
+            a1 += q[(long long)(r + 8) * cols];
+            a2 += q[(long long)(r + 16) * cols];
+            a3 += q[(long long)(r + 24) * cols];
+        }
+        for (; r < slots; r += 8) a0 += q[(long long)r * cols];
+        s = (a0 + a1) + (a2 + a3);
+    }
+    sm[ty][tx] = s;
+    __syncthreads();
+    if (ty || c >= cols) return;
+#pragma unroll
+    for (int k = 1; k < 8; ++k) s += sm[k][tx];
+    if (c < par) p.dA[c] = s;
+    else if (c < par + p.D) {
+        if (p.dDskip) p.dDskip[c - par] = s;
+    } else if (p.ddelta_bias) {
+        p.ddelta_bias[c - par - p.D] = s;
+    }
 }
 
 // Four channels per access where every array that is read or written allows it.
@@ -620,14 +657,14 @@ long long batch_rows(const ScanParams &p) { return (long long)(p.cu_seqlens ? 1 
 template <class T, int L, bool XV> cudaError_t grad_start(const ScanParams &p, cudaStream_t s) {
     const int cb = grad_blocks(p);
     const long long slots = scan_slots(p, SEG), blocks = slots * cb, rows = batch_rows(p);
-    const long long out = (rows * 8 * L + 255) / 256;
-    if (blocks > 0x7fffffffLL || out > 0x7fffffffLL) return cudaErrorNotSupported;
+    const long long bc = (rows * 8 * L + 255) / 256, par = ((long long)p.D * (p.N + 2) + 31) / 32;
+    if (blocks > 0x7fffffffLL || bc + par > 0x7fffffffLL) return cudaErrorNotSupported;
     constexpr int smem = sizeof(GradTiles<L>);
     cudaError_t e = cudaFuncSetAttribute(scan_grad_kernel<T, L, XV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     scan_grad_kernel<T, L, XV><<<(unsigned)blocks, kGradThreads, smem, s>>>(p, cb, bc_vec_ok<T>(p, 4 * L));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    scan_bc_kernel<T><<<(unsigned)out, 256, 0, s>>>(p, cb, 4 * L, rows);
+    scan_sums_kernel<T><<<(unsigned)(bc + par), 256, 0, s>>>(p, cb, 4 * L, rows, (unsigned)bc, (int)slots);
     return cudaGetLastError();
 }
 template <class T> cudaError_t grad_type(const ScanParams &p, cudaStream_t s) {
@@ -660,17 +697,9 @@ void ssm_scan_bwd_carve(ScanParams &p, float *ws) {
 cudaError_t launch_ssm_scan_bwd(const ScanParams &q, bool bf, cudaStream_t s) {
     ScanParams p = q;
     p.seg = p.lseg = SEG;
-    cudaError_t e = launch_scan_segments(p, bf, true, s);
+    const cudaError_t e = launch_scan_segments(p, bf, true, s);
     if (e != cudaSuccess) return e;
-    const long long slots = scan_slots(p, SEG), per = (long long)p.D * (p.N + 2);
-    if (p.cu_seqlens) {
-        scan_clear_kernel<<<(unsigned)slots, 256, 0, s>>>(p, per);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    e = bf ? grad_type<bf16>(p, s) : grad_type<float>(p, s);
-    if (e != cudaSuccess) return e;
-    return launch_sum_rows(p.part_par, (int)slots, {p.dA, (long long)p.D * p.N, false}, {p.dDskip, p.D, false},
-                           {p.ddelta_bias, p.D, false}, s);
+    return bf ? grad_type<bf16>(p, s) : grad_type<float>(p, s);
 }
 
 }  // namespace mixer

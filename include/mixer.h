@@ -78,7 +78,8 @@ typedef struct {
     size_t workspace_bytes;
 } layer_norm_bwd_args;
 
-/* Bytes of workspace (0 on bad args): per-block partial sums of dweight and dbias. */
+/* Bytes of workspace: per-block partial sums of dweight and dbias (0 on bad args, and where few rows
+   take none; layer_norm_bwd tells which). */
 size_t layer_norm_bwd_workspace(const layer_norm_bwd_args *args);
 
 /*

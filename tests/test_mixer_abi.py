@@ -99,8 +99,9 @@ for _n in _SIZES:
         _CASES += [(_n, dict(slots=0), BAD), (_n, dict(slot=None, slots=3), BAD), (_n, dict(state=None), BAD)]
 _CASES += [("layer_norm_fwd", dict(rows=0), BAD), ("layer_norm_fwd", dict(eps=-1.0), BAD),
            ("layer_norm_fwd", dict(eps=float("nan")), BAD), ("layer_norm_fwd", dict(y=None), BAD),
-           ("layer_norm_bwd", dict(mean=None), BAD), ("layer_norm_bwd", dict(workspace=None), SPACE),
-           ("layer_norm_bwd", dict(workspace_bytes=64), SPACE), ("layer_norm_bwd", dict(workspace=BASE + (1 << 45) + 4), BAD),
+           ("layer_norm_bwd", dict(mean=None), BAD), ("layer_norm_bwd", dict(rows=5000, workspace=None), SPACE),
+           ("layer_norm_bwd", dict(rows=5000, workspace_bytes=64), SPACE),
+           ("layer_norm_bwd", dict(rows=5000, workspace=BASE + (1 << 45) + 4), BAD),
            ("short_conv_bwd", dict(workspace=None), SPACE), ("short_conv_bwd", dict(dx=None), BAD),
            ("ssm_scan_bwd", dict(workspace_bytes=1024), SPACE), ("ssm_scan_bwd", dict(dz=None), BAD),
            ("ssm_scan_bwd", dict(z=None), BAD), ("ssm_scan_bwd", dict(dA=None), BAD),
@@ -132,7 +133,7 @@ def test_null_argument_block(lib, name):
 
 def test_workspace_sizes(lib):
     size = lambda n, **o: getattr(lib, n + "_workspace")(ctypes.byref(_args(n, **o)))  # noqa: E731
-    assert size("layer_norm_bwd") >= 8 * 2 * 64 * 4 and size("layer_norm_bwd", dweight=None, dbias=None) == 0
+    assert size("layer_norm_bwd", rows=5000) >= 8 * 2 * 64 * 4 and size("layer_norm_bwd", dweight=None, dbias=None) == 0
     assert size("short_conv_bwd") >= 64 * 5 * 4 and size("short_conv_bwd", dweight=None, dbias=None) == 0
     dense, packed = size("ssm_scan_bwd", T=640), size("ssm_scan_bwd", B=2, T=1280, cu_seqlens=BASE)
     assert 0 < dense < packed                # a packed batch has a slot more per sequence
