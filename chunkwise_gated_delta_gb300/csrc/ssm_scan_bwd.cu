@@ -66,7 +66,7 @@ template <int L, int NS> struct LocalTiles {
     static constexpr int TT = 16, CH = kScanThreads / L, NP = NS * L;
     f2x2 d[TT][CH];                  // {dt, dt}, {dt x, dt x}; columns swizzled, see at()
     f2 g[TT][CH];
-    float B[TT][NP], C[TT][NP];
+    float bc[128][NP];               // Bm of the segment; in the backward Bm of 64 tokens, then Cm
     float sum[TT][CH / 4][4];        // dt over a thread's tokens
     // Column of channel c: threads that write every fourth channel and threads that read neighbouring
     // ones both meet eight different 16-byte words.
@@ -74,7 +74,7 @@ template <int L, int NS> struct LocalTiles {
 };
 
 template <class T, int L, int NS, bool GRAD, bool XV>
-__global__ void __launch_bounds__(kScanThreads, XV && sizeof(T) == 2 ? 6 : 4) scan_local_kernel(ScanParams p, int chan_blocks, bool vec) {
+__global__ void __launch_bounds__(kScanThreads, XV && sizeof(T) == 2 ? 5 : 4) scan_local_kernel(ScanParams p, int chan_blocks, bool vec) {
     using S = LocalTiles<L, NS>;
     constexpr int TT = S::TT, CH = S::CH, NP = S::NP, H = NS / 2, Q = CH / 4, ROWS = kScanThreads / Q, K = TT / ROWS;
     extern __shared__ __align__(16) unsigned char raw[];
@@ -108,15 +108,14 @@ __global__ void __launch_bounds__(kScanThreads, XV && sizeof(T) == 2 ? 6 : 4) sc
     float bias[4], sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < 4; ++k) bias[k] = p.delta_bias && ds + k < p.D ? p.delta_bias[ds + k] : 0.f;
-    for (int t0 = 0; t0 < g.len; t0 += TT) {
-        __syncthreads();
-        // KB tokens' loads in flight together, as many as the registers hold
-        constexpr int KB = K < 2 ? K : XV && sizeof(T) == 2 && K >= 4 ? 4 : 2;
-        Four<T, XV> rx[KB], rd[KB], ry[GRAD ? KB : 1], rz[GRAD ? KB : 1];
-        for (int k0 = 0; k0 < K; k0 += KB) {
+    static_assert(kBwdSegment <= 64 && kFwdLocal <= 128, "rows of bc");
+    stage_rows<T, NP, GRAD ? 64 : 128>(sm.bc, p.Bm, p.ld_B, p.N, g, 0, vec);
+    if (GRAD) stage_rows<T, NP, 64>(sm.bc + 64, p.Cm, p.ld_C, p.N, g, 0, vec);
+    Four<T, XV> rx[K], rd[K], ry[GRAD ? K : 1], rz[GRAD ? K : 1];     // the next tile, on its way
+    auto fetch = [&](int t0) {
 #pragma unroll
-        for (int k = 0; k < KB; ++k) {
-            const long long tl = min(t0 + r0 + (k0 + k) * ROWS, g.len - 1);
+        for (int k = 0; k < K; ++k) {
+            const long long tl = min(t0 + r0 + k * ROWS, g.len - 1);
             rx[k].load(x + tl * p.ld_x, last);
             rd[k].load(delta + tl * p.ld_delta, last);
             if (GRAD) {
@@ -124,13 +123,13 @@ __global__ void __launch_bounds__(kScanThreads, XV && sizeof(T) == 2 ? 6 : 4) sc
                 rz[k].load(z + tl * ldz, last);
             }
         }
-        if (k0 == 0) {
-            stage_rows<T, NP, TT>(sm.B, p.Bm, p.ld_B, p.N, g, t0, vec);
-            if (GRAD) stage_rows<T, NP, TT>(sm.C, p.Cm, p.ld_C, p.N, g, t0, vec);
-        }
+    };
+    if (g.len > 0) fetch(0);
+    for (int t0 = 0; t0 < g.len; t0 += TT) {
+        __syncthreads();
 #pragma unroll
-        for (int k = 0; k < KB; ++k) {
-            const int t = r0 + (k0 + k) * ROWS;
+        for (int k = 0; k < K; ++k) {
+            const int t = r0 + k * ROWS;
             const bool in = t0 + t < g.len;
             float xv[4], dv[4], yv[4], zv[4];
             rx[k].get(xv);
@@ -161,7 +160,7 @@ __global__ void __launch_bounds__(kScanThreads, XV && sizeof(T) == 2 ? 6 : 4) sc
                 }
             }
         }
-        }
+        fetch(t0 + TT);                  // (past the end the last row again)
         __syncthreads();
 #pragma unroll 4
         for (int t = 0; t < TT; ++t) {
@@ -169,12 +168,12 @@ __global__ void __launch_bounds__(kScanThreads, XV && sizeof(T) == 2 ? 6 : 4) sc
             const f2 gy = GRAD ? sm.g[t][S::at(c)] : 0;
 #pragma unroll
             for (int k = 0; k < H; k += 2) {
-                const f2x2 b = *reinterpret_cast<const f2x2 *>(&sm.B[t][n0 + 2 * k]);
+                const f2x2 b = *reinterpret_cast<const f2x2 *>(&sm.bc[t0 + t][n0 + 2 * k]);
                 const f2 a0 = ex2_2(mul2(v.a, a2[k])), a1 = ex2_2(mul2(v.a, a2[k + 1]));
                 h[k] = fma2(a0, h[k], mul2(v.b, b.a));
                 h[k + 1] = fma2(a1, h[k + 1], mul2(v.b, b.b));
                 if (GRAD) {
-                    const f2x2 cq = *reinterpret_cast<const f2x2 *>(&sm.C[t][n0 + 2 * k]);
+                    const f2x2 cq = *reinterpret_cast<const f2x2 *>(&sm.bc[64 + t0 + t][n0 + 2 * k]);
                     m[k] = mul2(m[k], a0);
                     m[k + 1] = mul2(m[k + 1], a1);
                     e[k] = fma2(m[k], mul2(gy, cq.a), e[k]);

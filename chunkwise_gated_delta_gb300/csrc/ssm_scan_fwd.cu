@@ -507,21 +507,22 @@ template <class T> cudaError_t step_type(const ScanParams &p, cudaStream_t s) {
 
 }  // namespace
 
-// Whole sequences unless their blocks (of 128 / lanes channels) fill less than a third of the SMs; then
-// every sequence is cut so that the blocks fill the SMs once, at segments of 256 tokens or more.  The
-// local pass over all tokens and two more launches cost about what an unsplit pass over half the tokens
-// does, so two segments gain nothing (T 2048, 64 blocks: 97 us whole, 108 in two), and nine of T 16384
-// with 16 blocks take 190 us for 750.  The lengths of packed sequences are not known here: they are
-// taken to be as uneven as they can be, one of them with nearly all tokens.
+// Whole sequences, or segments of them side by side where that is expected to be sooner done.  A block takes
+// about 47 ns a token, alone or with the others.  Segments take a local pass over all tokens (0.235 ps per
+// token, channel and state with every SM busy) and two more launches (25 us with the latencies of both).
+// T 16384 with 16 blocks: 750 us whole, 166 in nine; T 2048 with 64 blocks: 97 us whole, 108 in two.
+// The lengths of packed sequences are not known here: one of them may have nearly all tokens.
 int ssm_scan_fwd_segment(const ScanParams &p) {
-    const int ch = p.N <= 8 ? 128 : p.N <= 16 ? 64 : 32, sms = sm_count();
-    const long long cb = (p.D + ch - 1) / ch, blocks = p.cu_seqlens ? cb : cb * p.B;
-    const long long cuts = sms / blocks;
-    if (cuts < 3) return p.T;
+    const int ch = p.N <= 8 ? 128 : p.N <= 16 ? 64 : 32;
+    const long long cb = (p.D + ch - 1) / ch, batch = p.cu_seqlens ? 1 : p.B;
+    const long long cuts = sm_count() / (cb * batch);
+    if (cuts < 2) return p.T;
     long long seg = (p.T + cuts - 1) / cuts;
     seg = (seg + kFwdLocal - 1) / kFwdLocal * kFwdLocal;
     if (seg < 256) seg = 256;
-    return 3 * seg > p.T + seg ? p.T : (int)seg;
+    const double gain = 47.0 * (double)(p.T - seg);
+    const double cost = 25000.0 + 0.235e-3 * (double)batch * p.T * p.D * padded_states(p.N);
+    return gain > cost ? (int)seg : p.T;
 }
 
 size_t ssm_scan_fwd_floats(const ScanParams &p) {
