@@ -1,7 +1,9 @@
 """Chunkwise gated delta rule (KDA, GDN, DeltaNet, GLA) on GB300 / sm_103a.
 
 The computation lives in the CUDA library ``_build/libkda.so`` (C ABI in
-``include/kda.h``); :mod:`.api` is its Python binding.  Build the library with
+``include/kda.h``); :mod:`.api` is its Python binding.  The operators around the
+mixer (layer norm, short causal convolution, selective scan; ``include/mixer.h``)
+are bound by :mod:`.mixer`.  Build the library with
 :func:`.build.build`.
 """
 from .api import (HostRunner, KdaError, deltanet_fwd, dplr_chunk_bwd, dplr_chunk_fwd, dplr_factor_norms,  # noqa: F401

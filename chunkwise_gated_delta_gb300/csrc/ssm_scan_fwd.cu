@@ -2,10 +2,11 @@
 //
 //   dt = softplus(delta + bias), h = exp(dt A) h + dt x B, y = (C . h + D x) SiLU(z)
 //
-// Per (token, channel, state): one exponential and four multiply-adds; per (token, channel) four
-// elements of HBM traffic.  With N = 16 the exponentials (32 per clock and SM) take 1.4 times
-// as long as the traffic, so the kernel is bound by the special-function and FMA pipes, and the
-// states stay in registers from the first token to the last.
+// Per (token, channel, state): one exponential and four multiply-adds; per (token, channel) four more
+// special functions (softplus, gate) and four elements of HBM traffic.  With N = 16 the special functions
+// (32 per clock and SM) take 1.8 times as long as the traffic, so the states stay in registers from
+// the first token to the last and everything else is arranged around that pipe and the FMA pipe.
+// B 4, T 4096, D 2048, N 16, bfloat16: 184 us (special functions 73, traffic 40).
 #include <type_traits>
 
 #include "ssm_scan.cuh"
@@ -13,18 +14,19 @@
 namespace mixer {
 namespace {
 
-// A block: 128 / L channels, four warps that carry the states (32 / L channels each) and four that
-// feed them.  Per tile of 8 L tokens
-//   the feeders   bring x, delta, z (8 neighbouring channels of one token per thread) and Bm, Cm of
-//                 the tile after the next into registers, turn the next tile's delta into dt and
-//                 leave {dt, dt, dt x, dt x} and float32 Bm, Cm in shared memory, and finish the
-//                 last tile's outputs: + D x, gate, rounding, store;
-//   the carriers  run the recurrence over the tile, four states of a channel per lane, and leave
-//                 sum_n C h in shared memory.
-// Both sides work on double buffers and meet once per tile.  Alone, a carrier warp waits for its
-// own shared-memory loads and exponentials two cycles of three, and one block of 32 channels per
-// 1.7 warps and scheduler is all that B 4, D 2048 has: the feeders fill those slots.
-
+// A block: WN warps that carry the states (32 / L channels each, NS states of a channel per lane) and
+// twice as many that feed them.  Per tile of KT L tokens
+//   the feeders   bring x, delta, z (8 neighbouring channels of one token per thread, three tiles ahead) and
+//                 Bm, Cm into shared memory or registers, turn the next tile's delta into dt and leave
+//                 {dt, dt, dt x, dt x} and float32 Bm, Cm in shared memory, and finish the last tile's
+//                 outputs: + D x, gate, rounding, store;
+//   the carriers  run the recurrence over the tile and leave sum_n C h in shared memory.
+// Both sides work on double buffers and meet once per tile.  With one kind of warp doing both, 8 warps to
+// an SM at B 4, D 2048 waited for their own loads and chains two cycles of three (382 us against 248
+// with four states per lane).  Eight states per lane amortise the loads and the sum over lanes: one
+// carrier warp per scheduler then issues near what the half-rate packed and quarter-rate exponential
+// instructions of one warp allow, 70 cycles a token, 85 with the feeders in the other slots.  Two carrier
+// warps of four states per scheduler take 242 us, 512 feeders of four channels 217.
 // L lanes of NS states per channel, WN carrier warps; a tile has KT tokens per lane.
 template <int L, int NS, int KT, int WN> struct FwdTiles {
     static constexpr int kFeeders = 4 * WN * KT, kCarriers = 32 * WN, kThreads = kCarriers + kFeeders;   // one feeder per 8 channels of a token
@@ -396,11 +398,10 @@ __global__ void __launch_bounds__(4 * WN * KT + 32 * WN) scan_fwd_kernel(ScanPar
 // The same for one token of each request; the state is read, updated and written once: bound by HBM.
 // VEC: N = 4 L, state, A, Bm and Cm in accesses of four.
 template <class T, int L, bool VEC>
-__global__ void __launch_bounds__(kScanThreads) scan_step_kernel(ScanParams p, int chan_blocks) {
+__global__ void __launch_bounds__(kScanThreads) scan_step_kernel(ScanParams p) {
     constexpr int CH = kScanThreads / L;
     const int c = threadIdx.x / L, i = threadIdx.x % L, n0 = 4 * i;
-    const int b = blockIdx.x / chan_blocks;
-    const int d = (blockIdx.x - b * chan_blocks) * CH + c;
+    const int b = blockIdx.x, d = blockIdx.y * CH + c;
     const int slot = p.slot ? p.slot[b] : b;
     const bool pad = slot < 0 || slot >= p.slots, live = d < p.D && !pad;
     float y = 0.f, xv = 0.f, zv = 0.f, skip = 0.f;
@@ -482,11 +483,12 @@ template <class T, int L, int NS, int KT, int WN> cudaError_t fwd_launch(const S
 template <class T, int L> cudaError_t step_launch(const ScanParams &p, cudaStream_t s) {
     constexpr int CH = kScanThreads / L;
     const int cb = (p.D + CH - 1) / CH;
-    if ((long long)p.B * cb > 0x7fffffffLL) return cudaErrorNotSupported;
+    if (cb > 65535) return cudaErrorNotSupported;
+    const dim3 grid(p.B, cb);
     if (bc_vec_ok<T>(p, 4 * L) && aligned_to(p.state, 16) && aligned_to(p.A, 16))
-        scan_step_kernel<T, L, true><<<(unsigned)(p.B * cb), kScanThreads, 0, s>>>(p, cb);
+        scan_step_kernel<T, L, true><<<grid, kScanThreads, 0, s>>>(p);
     else
-        scan_step_kernel<T, L, false><<<(unsigned)(p.B * cb), kScanThreads, 0, s>>>(p, cb);
+        scan_step_kernel<T, L, false><<<grid, kScanThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 
