@@ -175,6 +175,11 @@ template <class T, int V> struct Lanes {
             for (int k = 0; k < WORDS; ++k) w[k] = v.e[k];
         }
     }
+    __device__ __forceinline__ void load_shared(const void *p) {      // (V sizeof(T) >= 4)
+        const Vec<uint32_t, WORDS> v = load_vec<uint32_t, WORDS>(static_cast<const uint32_t *>(p));
+#pragma unroll
+        for (int k = 0; k < WORDS; ++k) w[k] = v.e[k];
+    }
     __device__ __forceinline__ f2 pair(int k) const {
         if constexpr (V == 1) return pack2(bits_f<T>(w[0]), 0.f);
         else if constexpr (sizeof(T) == 4) return pack2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
@@ -198,6 +203,16 @@ template <class T, int V> __device__ __forceinline__ void store_lanes(T *p, cons
         store_vec<T, V>(p, o);
     }
 }
+// N bytes (4, 8 or 16) from global to shared memory, asynchronously.
+template <int N> __device__ __forceinline__ void copy_async(void *to, const void *from) {
+    const uint32_t s = (uint32_t)__cvta_generic_to_shared(to);
+    if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(from) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(s), "l"(from), "n"(N) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last N groups of this thread's copies have arrived.
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 template <int V> __device__ __forceinline__ float pair_sum(f2 v) {
     float lo, hi;
     unpack2(v, lo, hi);

@@ -99,9 +99,16 @@ __global__ void __launch_bounds__(128, 4) conv_fwd_kernel(ConvParams p, long lon
 // Backward of V channels of one segment: tokens t0 .. t0 + len + W - 2, the last W - 1 of which
 // belong to the next segment (their dpre is computed there again for dw and dbias).
 // A block: 32 channel groups, 4 segments; the four partial sums are joined in shared memory.
+constexpr int kBwdBlocks = 4;        // to an SM
 template <class T, int W, int V>
-__global__ void __launch_bounds__(128, 3) conv_bwd_kernel(ConvParams p, long long slots) {
-    constexpr int P = (V + 1) / 2;
+__global__ void __launch_bounds__(128, kBwdBlocks) conv_bwd_kernel(ConvParams p, long long slots) {
+    constexpr int P = (V + 1) / 2, BYTES = V * sizeof(T);
+    // Rows on their way: groups of four, asynchronous copies into words of the thread's own (a register
+    // ring of one group leaves too few bytes in flight); single bfloat16 elements, which are too small
+    // for that, one group ahead in registers.
+    constexpr bool RING = BYTES >= 4;
+    constexpr int GROUPS = BYTES == 16 ? 2 : 3;
+    __shared__ __align__(16) unsigned char ring[RING ? GROUPS * 8 * 128 * BYTES : 16];
     __shared__ f2 sm[3][(W + 1) * P][33];
     const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
     const int groups = p.D / V, gx = (groups + 31) / 32;
@@ -180,29 +187,59 @@ __global__ void __launch_bounds__(128, 3) conv_bwd_kernel(ConvParams p, long lon
             if (q >= g.t0) store_lanes<T, V>(dx + (q - g.t0) * p.ld_y, o);
             else if (q < 0 && p.dh0) store_lanes<T, V>(static_cast<T *>(p.dh0) + ((long long)g.b * (W - 1) + q + W - 1) * p.D + c, o);
         };
-        Lanes<T, V> xi[4], di[4], xn[4], dn[4];          // four rows, and the next four on their way
+        Lanes<T, V> xi[4], di[4], xn[RING ? 1 : 4], dn[RING ? 1 : 4];
         const int last = g.total - 1 - g.t0;             // the sequence's last row from here
-        if (last >= 0)
+        int ahead = 0, at = 0;                           // first row of the next copy; the ring's next group
+        auto word = [&](int group, int k) { return ring + (((group * 4 + k) * 2) * 128 + threadIdx.x) * BYTES; };
+        auto copy = [&](int group) {                     // past the sequence's end its last row again
+            if (last >= 0)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                xn[k].load(x + min(k, last) * p.ld_x);
-                dn[k].load(gy + min(k, last) * p.ld_dy);
-            }
-        const T *px = x, *pd = gy;
+                for (int k = 0; k < 4; ++k) {
+                    const long long r = min(ahead + k, last);
+                    copy_async<RING ? BYTES : 4>(word(group, k), x + r * p.ld_x);
+                    copy_async<RING ? BYTES : 4>(word(group, k) + 128 * BYTES, gy + r * p.ld_dy);
+                }
+            copies_end();
+            ahead += 4;
+        };
+        auto next = [&] {
+            if (last >= 0)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const long long r = min(ahead + k, last);
+                    xn[RING ? 0 : k].load(x + r * p.ld_x);
+                    dn[RING ? 0 : k].load(gy + r * p.ld_dy);
+                }
+            ahead += 4;
+        };
+        if constexpr (RING) {
+#pragma unroll
+            for (int k = 0; k < GROUPS; ++k) copy(k);
+        } else {
+            next();
+        }
         T *out = dx - (W - 1) * p.ld_y;                  // of position t - (W - 1)
-        auto four = [&](int t) {                         // rows t .. t + 3 to work on, the next four on their way
-            px += 4 * p.ld_x;
-            pd += 4 * p.ld_dy;
+        auto four = [&] {                                // the next four rows to work on
+            if constexpr (RING) {
+                copies_wait<GROUPS - 1>();
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                xi[k] = xn[k];
-                di[k] = dn[k];
-                xn[k].load(px + min(k, last - 4 - t) * p.ld_x);
-                dn[k].load(pd + min(k, last - 4 - t) * p.ld_dy);
+                for (int k = 0; k < 4; ++k) {
+                    xi[k].load_shared(word(at, k));
+                    di[k].load_shared(word(at, k) + 128 * BYTES);
+                }
+                copy(at);
+                at = at == GROUPS - 1 ? 0 : at + 1;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    xi[k] = xn[RING ? 0 : k];
+                    di[k] = dn[RING ? 0 : k];
+                }
+                next();
             }
         };
         auto edge = [&](int t) {                         // near the ends of the segment or of the sequence
-            four(t);
+            four();
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 if (t + k < g.len) {
@@ -218,7 +255,7 @@ __global__ void __launch_bounds__(128, 3) conv_bwd_kernel(ConvParams p, long lon
         if (g.len > 0) edge(0);
         // inside, with nothing to ask for: positions t - (W - 1) .. are this segment's, and before the final state's
         for (t = 4; t + 4 <= g.len && g.t0 + t + 4 <= g.total; t += 4) {
-            four(t);
+            four();
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 f2 o[P];
@@ -230,6 +267,7 @@ __global__ void __launch_bounds__(128, 3) conv_bwd_kernel(ConvParams p, long lon
             }
         }
         for (; t < g.len; t += 4) edge(t);
+        if constexpr (RING) copies_wait<0>();
         // the W - 1 tokens behind the segment: the next segment's, or none (dpre = 0)
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) {
@@ -375,7 +413,7 @@ int segment_length(const ConvParams &p, int V, int resident) {
     }
     return seg;
 }
-int bwd_segment(const ConvParams &p) { return segment_length(p, 4, 3); }
+int bwd_segment(const ConvParams &p) { return segment_length(p, 4, kBwdBlocks); }
 }  // namespace
 
 cudaError_t launch_short_conv_fwd(const ConvParams &q, int W, bool bf, cudaStream_t s) {

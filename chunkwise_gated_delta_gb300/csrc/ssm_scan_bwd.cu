@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) scan_grad_kernel(ScanParams p
         // a slot that no sequence uses: its partial sums are zeros, so that the sums may take all slots
         float *out = p.part_par + slot * ((long long)p.D * (p.N + 2));
         const int end = min(d0 + CH, p.D);
-        for (int u = d0 * p.N + tid; u < end * p.N; u += kGradThreads) out[u] = 0.f;
+        for (long long u = (long long)d0 * p.N + tid; u < (long long)end * p.N; u += kGradThreads) out[u] = 0.f;
         for (int d = d0 + tid; d < end; d += kGradThreads)
             out[(long long)p.D * p.N + d] = out[(long long)p.D * (p.N + 1) + d] = 0.f;
         return;

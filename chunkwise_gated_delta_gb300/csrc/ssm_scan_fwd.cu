@@ -45,10 +45,6 @@ template <int N> __device__ __forceinline__ void meet_all() { asm volatile("bar.
 __device__ __forceinline__ void store_pairs(uint32_t to, f2 a, f2 b) {
     asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(to), "l"(a), "l"(b) : "memory");
 }
-__device__ __forceinline__ void copy16(void *to, const void *from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
-}
-
 // Eight neighbouring channels of one token, as they lie in memory (XV: two or one 16-byte accesses).
 template <class T, bool XV> struct Eight {
     static constexpr int W = 8 * sizeof(T) / 16;
@@ -136,12 +132,12 @@ __global__ void __launch_bounds__(4 * WN * KT + 32 * WN) scan_fwd_kernel(ScanPar
                     uint4 *to = ring + slot3 * (3 * Data::W * kFeeders);
 #pragma unroll
                     for (int k = 0; k < Data::W; ++k) {
-                        copy16(to + k * kFeeders, px + k * (16 / sizeof(T)));
-                        copy16(to + (Data::W + k) * kFeeders, pd + k * (16 / sizeof(T)));
-                        if (z) copy16(to + (2 * Data::W + k) * kFeeders, pg + k * (16 / sizeof(T)));
+                        copy_async<16>(to + k * kFeeders, px + k * (16 / sizeof(T)));
+                        copy_async<16>(to + (Data::W + k) * kFeeders, pd + k * (16 / sizeof(T)));
+                        if (z) copy_async<16>(to + (2 * Data::W + k) * kFeeders, pg + k * (16 / sizeof(T)));
                     }
                 }
-                asm volatile("cp.async.commit_group;" ::: "memory");
+                copies_end();
                 slot3 = slot3 == RING - 1 ? 0 : slot3 + 1;
             } else {
                 f[0].load(px, last);
@@ -203,7 +199,7 @@ __global__ void __launch_bounds__(4 * WN * KT + 32 * WN) scan_fwd_kernel(ScanPar
             const uint32_t sd = staged & 1 ? sd1 : sd0;
             Data dc{}, xn{}, zn{};
             if (XV) {
-                asm volatile("cp.async.wait_group 2;" ::: "memory");
+                copies_wait<2>();
                 const uint4 *src = ring + from * (3 * Data::W * kFeeders);
 #pragma unroll
                 for (int k = 0; k < Data::W; ++k) {
@@ -288,6 +284,7 @@ __global__ void __launch_bounds__(4 * WN * KT + 32 * WN) scan_fwd_kernel(ScanPar
         }
         meet();
         if (tiles > 0) work(tiles + 1, tiles - 1, some && (tiles - 1) * TT + t < g.len);
+        if (XV) copies_wait<0>();
         return;
     }
     // ---------------------------------------------------------------------- carriers
