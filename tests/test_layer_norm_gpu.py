@@ -39,6 +39,7 @@ def _check(x, w, b, dy, eps=1e-5, **outs):
                      torch.autograd.grad((ry * dy.double()).sum(), used)))
     h = half_step(x.dtype)
     assert rel(y, ry) <= h + 2e-5
+    rm = rm.detach()
     assert float((mean.double() - rm).abs().max()) <= 2e-5 * max(1.0, float(rm.abs().max()))
     assert rel(rstd, rr) <= 2e-5
     assert set(got) == set(grads)
@@ -50,7 +51,7 @@ def _check(x, w, b, dy, eps=1e-5, **outs):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("rows,D", [(1, 8), (3, 1), (5, 7), (37, 64), (700, 96), (2, 2051), (129, 1000), (1300, 2048), (9, 4096),
-                                    (5, 8200), (3, 16384), (2, 20001), (1, 40000)])
+                                    (5, 8200), (3, 16384), (2, 20001), (1, 40000), (2000, 1000), (1301, 3080), (900, 8000), (400, 16390)])
 def test_against_the_definition(dtype, rows, D):
     _check(*_inputs(rows, D, dtype, seed=rows + D), eps=1e-5 if D > 1 else 1e-3)
 

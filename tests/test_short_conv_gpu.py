@@ -77,6 +77,17 @@ def test_packed(dtype, W, lens):
     _check(d, lens, True, y, ht, got)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("W,D,lens", [(4, 1024, [2000, 2000]), (3, 1032, [1999, 3, 0, 1500, 498]), (2, 1025, [3001, 700]),
+                                      (4, 1028, [1, 2500, 2, 1100])])
+def test_long_segments(dtype, W, D, lens):
+    """Enough rows and channels that a thread walks many tokens of one segment."""
+    T = sum(lens)
+    d = _inputs(T, len(lens), D, W, dtype, seed=T + W)
+    cu = torch.tensor([0] + [b for _, b in spans_of(lens)], dtype=torch.int32, device=DEV)
+    _check(d, lens, True, *_run(d, 1, T, cu, True))
+
+
 def test_rows_outside_every_sequence_are_left_alone():
     """Rows past the last offset hold NaN on input and a sentinel on output."""
     d = _inputs(20, 2, 16, 4, torch.float32, seed=1)

@@ -126,6 +126,14 @@ def test_long_sequences_on_few_channels(dtype, N, D, lens):
     assert rel(y1[0], ry) <= half_step(dtype) + F_TOL and rel(ht1, rht) <= F_TOL
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,D,N", [(3, 1704, 16), (3, 1699, 16), (6, 1704, 8), (2, 1312, 32), (8, 1304, 4), (3, 1704, 12)])
+def test_many_channels(dtype, B, D, N):
+    """Enough blocks to fill the SMs: full blocks, whole sequences, several tiles and a ragged last one."""
+    d, dy, dht = _inputs(B * 75, B, D, N, dtype, seed=B + D + N)
+    _check(d, dy, dht, [75] * B, _call(d, dy, dht, B, 75))
+
+
 def test_empty_batch_of_sequences_passes_the_states():
     d, dy, dht = _inputs(1, 2, 20, 16, torch.float32, seed=12)
     cu = torch.zeros(3, dtype=torch.int32, device=DEV)
