@@ -13,6 +13,12 @@ constexpr int kScanThreads = 128;
 constexpr int kBwdSegment = 64;      // tokens between boundary states in the backward
 constexpr int kFwdLocal = 128;       // and in the split forward
 
+// Added to the exponent of a decay, 2^(dt A log2 e): the special-function unit's results lie 0.5e-8 to 2.6e-8
+// (relative) below the exact ones on average for exponents between -1 and 0 (measured), and a state
+// multiplies as many of them as it remembers tokens.  With this the averages are within 1.2e-8 of 0 on
+// all of that range, like expf's; at dt = 0 the decay is exactly 1.
+constexpr float kDecayBias = 2.5e-8f;
+
 // log(1 + u) for u in [0, 1]: 2 atanh(s) with s = u / (2 + u) <= 1/3, atanh(s) = s + s^3 P(s^2) with P
 // fitted for the smallest relative error of atanh on that interval (Lawson's reweighted least
 // squares): 5.4e-9 with these four coefficients, below the rounding of one operation.  Relative
@@ -59,6 +65,9 @@ __device__ __forceinline__ f2 softplus2(f2 v) {
     const f2 r = fma2(fma2(fma2(both(kAtanh[3]), q, both(kAtanh[2])), q, both(kAtanh[1])), q, both(kAtanh[0]));
     return fma2(fma2(mul2(s, q), r, s), both(2.f), pack2(fmaxf(a, 0.f), fmaxf(b, 0.f)));
 }
+// The decays of two states.
+__device__ __forceinline__ f2 decay2(f2 dt, f2 a2) { return ex2_2(fma2(dt, a2, both(kDecayBias))); }
+
 // Sums v[k] over the L lanes of a channel; lane i ends with the sums of k = i K / L ... in v[0 ..].
 // K is a multiple of L.
 template <int K, int L> __device__ __forceinline__ void spread_sum(float (&v)[K], int i) {

@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kScanThreads, XV && sizeof(T) == 2 ? 5 : 4) sc
 #pragma unroll
             for (int k = 0; k < H; k += 2) {
                 const f2x2 b = *reinterpret_cast<const f2x2 *>(&sm.bc[t0 + t][n0 + 2 * k]);
-                const f2 a0 = ex2_2(mul2(v.a, a2[k])), a1 = ex2_2(mul2(v.a, a2[k + 1]));
+                const f2 a0 = decay2(v.a, a2[k]), a1 = decay2(v.a, a2[k + 1]);
                 h[k] = fma2(a0, h[k], mul2(v.b, b.a));
                 h[k + 1] = fma2(a1, h[k + 1], mul2(v.b, b.b));
                 if (GRAD) {
@@ -384,8 +384,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) scan_grad_kernel(ScanParams p
                 const float2 v = sm.du[part * TC + t][cc];
                 const f2x2 b = *reinterpret_cast<const f2x2 *>(&sm.B[part * TC + t][n0]);
                 const f2 dt = both(v.x), u = both(v.y);
-                h0 = fma2(ex2_2(mul2(dt, a2[k][0])), h0, mul2(u, b.a));
-                h1 = fma2(ex2_2(mul2(dt, a2[k][1])), h1, mul2(u, b.b));
+                h0 = fma2(decay2(dt, a2[k][0]), h0, mul2(u, b.a));
+                h1 = fma2(decay2(dt, a2[k][1]), h1, mul2(u, b.b));
             }
         }
     }
@@ -409,8 +409,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) scan_grad_kernel(ScanParams p
                 const f2x2 b = *reinterpret_cast<const f2x2 *>(&sm.B[part * TC + t][n0]);
                 const f2x2 cq = *reinterpret_cast<const f2x2 *>(&sm.C[part * TC + t][n0]);
                 const f2 dt = both(v.x), u = both(v.y);
-                a[t][0] = ex2_2(mul2(dt, a2[k][0]));
-                a[t][1] = ex2_2(mul2(dt, a2[k][1]));
+                a[t][0] = decay2(dt, a2[k][0]);
+                a[t][1] = decay2(dt, a2[k][1]);
                 h[t + 1][0] = fma2(a[t][0], h[t][0], mul2(u, b.a));
                 h[t + 1][1] = fma2(a[t][1], h[t][1], mul2(u, b.b));
                 float lo, hi;

@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(4 * WN * KT + 32 * WN) scan_fwd_kernel(ScanPar
         for (int k = 0; k < L; ++k)
 #pragma unroll
             for (int q = 0; q < H; ++q) {
-                e[0][k][q] = ex2_2(mul2(sv[k].a, a2[q]));
+                e[0][k][q] = decay2(sv[k].a, a2[q]);
                 u[0][k][q] = mul2(sv[k].b, half(bv[k][q / 2], q));
             }
         load(1);
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(4 * WN * KT + 32 * WN) scan_fwd_kernel(ScanPar
                 for (int k = 0; k < L; ++k)
 #pragma unroll
                     for (int q = 0; q < H; ++q) {
-                        e[y][k][q] = mul2v(sv[k].a, a2[q]);
+                        e[y][k][q] = fma2v(sv[k].a, a2[q], both(kDecayBias));
                         u[y][k][q] = mul2v(sv[k].b, half(bv[k][q / 2], q));
                     }
             float ys[L];
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_step_kernel(ScanParams p) {
         const float e = dt * kLog2e, u = dt * xv;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            h[k] = fmaf(ex2(e * a[k]), h[k], u * bv[k]);
+            h[k] = fmaf(ex2(fmaf(e, a[k], kDecayBias)), h[k], u * bv[k]);
             y = fmaf(cv[k], h[k], y);
         }
         if (VEC) *reinterpret_cast<float4 *>(st + n0) = make_float4(h[0], h[1], h[2], h[3]);
