@@ -470,7 +470,7 @@ template <class T, int L, int NS, int KT, int WN> cudaError_t fwd_warps(const Sc
     return xv ? fwd_start<T, L, NS, KT, WN, true>(p, s) : fwd_start<T, L, NS, KT, WN, false>(p, s);
 }
 // Half as many carrier warps to a block where full blocks would leave half of the SMs without one: the same
-// work on twice the SMs (training step B 2, T 2048, D 2048: 382 -> 368 us).
+// work on twice the SMs (training step B 2, T 2048, D 2048, both with eight states per lane: 382 -> 368 us).
 template <class T, int L, int NS, int KT, int WN> cudaError_t fwd_launch(const ScanParams &p, cudaStream_t s) {
     constexpr int CH = WN * 32 / L;
     const long long full = scan_slots(p, p.seg) * ((p.D + CH - 1) / CH);
