@@ -634,19 +634,17 @@ template <class T, int L, int NS, bool GRAD, bool XV> cudaError_t local_start(co
     scan_boundary_kernel<<<dim3((unsigned)bblocks, GRAD ? 2 : 1), 128, 0, s>>>(p, S::NP);
     return cudaGetLastError();
 }
-template <class T, int L, int NS> cudaError_t local_launch(const ScanParams &p, bool grad, cudaStream_t s) {
-    const bool xv = local_xv<T>(p);
-    if (grad) return xv ? local_start<T, L, NS, true, true>(p, s) : local_start<T, L, NS, true, false>(p, s);
-    return xv ? local_start<T, L, NS, false, true>(p, s) : local_start<T, L, NS, false, false>(p, s);
+template <class T, int L, int NS, bool GRAD> cudaError_t local_launch(const ScanParams &p, cudaStream_t s) {
+    return local_xv<T>(p) ? local_start<T, L, NS, GRAD, true>(p, s) : local_start<T, L, NS, GRAD, false>(p, s);
 }
 
 // The states' layout in the workspace, [slots][D][padded states]: the forward takes its own padding, the
 // backward's two passes share theirs (16 or 32).
 template <class T> cudaError_t segments_type(const ScanParams &p, bool grad, cudaStream_t s) {
-    if (!grad && p.N <= 4) return local_launch<T, 1, 4>(p, grad, s);
-    if (!grad && p.N <= 8) return local_launch<T, 1, 8>(p, grad, s);
-    if (p.N <= 16) return local_launch<T, 2, 8>(p, grad, s);
-    return local_launch<T, 4, 8>(p, grad, s);
+    if (grad) return p.N <= 16 ? local_launch<T, 2, 8, true>(p, s) : local_launch<T, 4, 8, true>(p, s);
+    if (p.N <= 4) return local_launch<T, 1, 4, false>(p, s);
+    if (p.N <= 8) return local_launch<T, 1, 8, false>(p, s);
+    return p.N <= 16 ? local_launch<T, 2, 8, false>(p, s) : local_launch<T, 4, 8, false>(p, s);
 }
 
 int grad_states(int N) { return N <= 16 ? 16 : 32; }
