@@ -193,6 +193,26 @@ def test_extreme_steps():
     _check(d, dy, dht, [40], _call(d, dy, dht, 1, 40))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_decays_of_a_long_memory_have_no_drift(dtype):
+    """x = 0, h0 = 1: ht is the product of T decays.  A decay's error may be 1.2e-8 in the mean; the
+    products' and arguments' roundings have mean zero, but for log2 e's own, at most 2^-25 of an exponent
+    of about 8 in all."""
+    T, D, N = 512, 64, 16
+    g = torch.Generator(device=DEV).manual_seed(24)
+    rand = lambda *s: torch.rand(*s, generator=g, device=DEV)  # noqa: E731
+    delta, A = (0.01 * (0.5 + rand(1, T, D))).to(dtype), -(1 + rand(D, N))
+    x, bc, h0 = delta.new_zeros(1, T, D), delta.new_ones(1, T, N), torch.ones(1, D, N, device=DEV)
+    exact = (delta[0].double().sum(0)[:, None] * A.double()).exp()
+    tol = T * 1.2e-8 + 8 * 2.0 ** -25
+    _, ht = ssm_scan_fwd(x, delta, A, bc, bc, h0=h0, delta_softplus=False)
+    assert abs(float((ht[0].double() / exact - 1).mean())) <= tol
+    state = h0.clone()
+    for t in range(T):
+        ssm_scan_step(x[:, t], delta[:, t], A, bc[:, t], bc[:, t], state, delta_softplus=False)
+    assert abs(float((state[0].double() / exact - 1).mean())) <= tol
+
+
 def test_non_finite_values_stay_in_their_channel():
     d, dy, dht = _inputs(50, 1, 40, 16, torch.float32, seed=17)
     y0, ht0, _ = _call(d, dy, dht, 1, 50)
