@@ -38,8 +38,10 @@ __device__ __forceinline__ void store_w(void *p, long long i, bool is_bf16, floa
 // V neighbouring parameters from element i (a multiple of V; V elements of a 16-byte aligned vector).
 template <int V> __device__ __forceinline__ void load_params(float (&o)[V], const void *p, long long i, bool is_bf16);
 
-// V neighbouring elements in one access of V sizeof(T) bytes, kept packed.
+// V neighbouring elements in one access of V sizeof(T) bytes, kept packed.  At most 16 bytes: no pointer is
+// known to be aligned to more, neither the caller's tensors nor the workspaces.
 template <class T, int V> struct alignas(V * sizeof(T)) Vec {
+    static_assert(V * sizeof(T) <= 16, "an access takes at most 16 bytes");
     T e[V];
 };
 template <class T, int V> __device__ __forceinline__ Vec<T, V> load_vec(const T *p) {
@@ -192,15 +194,19 @@ template <class T, int V> __device__ __forceinline__ void store_lanes(T *p, cons
         unpack2(v[0], lo, hi);
         *p = from_f<T>(lo);
     } else {
-        Vec<T, V> o;
+        constexpr int E = V * sizeof(T) <= 16 ? V : 16 / (int)sizeof(T);      // elements per access
 #pragma unroll
-        for (int k = 0; k < V / 2; ++k) {
-            float lo, hi;
-            unpack2(v[k], lo, hi);
-            o.e[2 * k] = from_f<T>(lo);
-            o.e[2 * k + 1] = from_f<T>(hi);
+        for (int a = 0; a < V; a += E) {
+            Vec<T, E> o;
+#pragma unroll
+            for (int k = 0; k < E / 2; ++k) {
+                float lo, hi;
+                unpack2(v[a / 2 + k], lo, hi);
+                o.e[2 * k] = from_f<T>(lo);
+                o.e[2 * k + 1] = from_f<T>(hi);
+            }
+            store_vec<T, E>(p + a, o);
         }
-        store_vec<T, V>(p, o);
     }
 }
 // N bytes (4, 8 or 16) from global to shared memory, asynchronously.

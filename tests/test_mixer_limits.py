@@ -1,0 +1,31 @@
+"""Limits of the operators of include/mixer.h that need no GPU: what the types of the kernels' accesses
+assume, counters near 2^31, sizes that are taken or refused, and the Python binding's refusals."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+from chunkwise_gated_delta_gb300 import build as kbuild
+
+
+def _nvcc():
+    nvcc = kbuild._nvcc()
+    if not (os.path.exists(nvcc) or shutil.which(nvcc)):
+        pytest.skip("nvcc not found")
+    return nvcc
+
+
+def _compile(tmp_path, src, *flags):
+    f = tmp_path / "check.cu"
+    f.write_text(src)
+    return subprocess.run([_nvcc(), "-O1", "-std=c++17", *flags, "-I", kbuild.CSRC, str(f), "-o", str(tmp_path / "check")],
+                          capture_output=True, text=True, timeout=600)
+
+
+@pytest.mark.parametrize("kind,count,ok", [("float", 4, True), ("mixer::bf16", 8, True), ("float", 8, False), ("mixer::bf16", 16, False)])
+def test_no_access_is_wider_than_the_workspaces_alignment(tmp_path, kind, count, ok):
+    """Workspaces are promised 16-byte alignment, so a type whose alignment is more must not exist."""
+    r = _compile(tmp_path, f'#include "mixer_common.cuh"\nsize_t n = alignof(mixer::Vec<{kind}, {count}>);\n', *kbuild.ARCH, "-c")
+    assert (r.returncode == 0) is ok, r.stderr[-2000:]
+    assert ok or "at most 16 bytes" in r.stderr

@@ -1,0 +1,67 @@
+"""The operators of include/mixer.h at the limits of what they take: workspaces at the promised alignment
+and no more, non-finite values, supplied outputs on other streams, gradients that nothing asks for."""
+import ctypes
+
+import pytest
+import torch
+
+from chunkwise_gated_delta_gb300 import _lib, layer_norm_bwd, layer_norm_fwd, mixer, short_conv_bwd, ssm_scan_bwd, ssm_scan_fwd
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def _rand(seed, dtype):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    rn = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    return rn, lambda *s: rn(*s).to(dtype)  # noqa: E731
+
+
+# ------------------------------------------------------------------------------------ workspaces
+class _Shifted(mixer._On):
+    """Workspaces at 16 bytes past a multiple of 512, and no longer than asked for."""
+
+    seen = 0
+
+    def workspace(self, name, args):
+        need = getattr(_lib.load(), name)(ctypes.byref(args))
+        if not need:
+            return None
+        buf = torch.full((need + 32,), 0x5A, dtype=torch.uint8, device=DEV)
+        assert buf.data_ptr() % 512 == 0
+        args.workspace, args.workspace_bytes = buf.data_ptr() + 16, need
+        type(self).seen += 1
+        self.buf = buf
+        return buf
+
+    def launch(self, name, args):
+        super().launch(name, args)
+        if getattr(self, "buf", None) is not None:
+            assert bool((self.buf[:16] == 0x5A).all()) and bool((self.buf[-16:] == 0x5A).all()), "written outside"
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_workspaces_of_sixteen_byte_alignment(dtype, monkeypatch):
+    rn, t = _rand(1, dtype)
+    x, w, dy = t(700, 96), t(96), t(700, 96)
+    _, mean, rstd = layer_norm_fwd(x, w)
+    cx, cw, cdy = t(1, 300, 64), t(64, 4), t(1, 300, 64)
+    sx = [t(1, 1500, 64), t(1, 1500, 64), -torch.rand(64, 16, device=DEV) - 0.5, t(1, 1500, 16), t(1, 1500, 16), rn(64), t(1, 1500, 64), rn(64), None]
+    sdy = t(1, 1500, 64)
+
+    def run():
+        y, ht = ssm_scan_fwd(*sx)
+        out = {"y": y, "ht": ht}
+        for name, grads in (("norm", layer_norm_bwd(dy, x, w, mean, rstd)), ("conv", short_conv_bwd(cx, cw, None, None, cdy)),
+                            ("scan", ssm_scan_bwd(*sx, sdy))):
+            out.update({f"{name}.{k}": v for k, v in grads.items()})
+        return out
+
+    ref = run()
+    monkeypatch.setattr(mixer, "_On", _Shifted)
+    got = run()
+    torch.cuda.synchronize()
+    assert _Shifted.seen >= 4
+    _Shifted.seen = 0
+    for k in ref:
+        assert torch.equal(got[k], ref[k]), k
