@@ -67,4 +67,12 @@ __host__ __device__ inline long long slot_at(const int32_t *cu, int T, int seg, 
     return (cu ? first_slot(cu, T, seg, b) : b * ((T + (long long)seg - 1) / seg)) + t0 / seg;
 }
 
+// A kernel that walks `len` tokens in tiles counts tokens past the end too: the last tile's, and those of the
+// tiles that it looks ahead.  Lengths reach 2^31 - 1, so these positions have no sign.
+__host__ __device__ inline int tiles_of(int len, int tile) { return (int)(((unsigned)len + tile - 1) / tile); }
+__host__ __device__ inline unsigned tile_token(int k, int tile, int t) { return (unsigned)k * tile + t; }
+__host__ __device__ inline bool inside(unsigned pos, int len) { return pos < (unsigned)len; }
+// Row at a position, the last one past the end (len > 0).
+__host__ __device__ inline long long row_or_last(unsigned pos, int len) { return inside(pos, len) ? pos : (unsigned)len - 1; }
+
 }  // namespace mixer

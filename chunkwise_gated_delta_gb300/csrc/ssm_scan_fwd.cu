@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(4 * WN * KT + 32 * WN) scan_fwd_kernel(ScanPar
     const int d0 = (int)(blockIdx.x - slot * chan_blocks) * CH;
     Segment g;
     if (!segment_of(p.cu_seqlens, p.B, p.T, p.seg, slot, g)) return;
-    const int tiles = (g.len + TT - 1) / TT;
+    const int tiles = tiles_of(g.len, TT);
     const long long row0 = g.row0 + g.t0;
 
     if (threadIdx.x >= S::kCarriers) {
@@ -123,12 +123,13 @@ __global__ void __launch_bounds__(4 * WN * KT + 32 * WN) scan_fwd_kernel(ScanPar
         typename Quad::type bq[XV ? EV : 1];
         const T *const pz = z ? z : x;                               // (no gate: loaded all the same, not used)
         const long long ldz = z ? p.ld_z : p.ld_x, sy = TT * p.ld_y;
-        int row = t, slot3 = 0;                                      // of the next fetch; its place in the ring
+        unsigned row = t;                                            // of the next fetch
+        int slot3 = 0;                                               // its place in the ring
         auto fetch = [&] {                                           // tile by tile; past the end the last row again
-            const long long r = min(row, g.len - 1);
+            const long long r = row_or_last(row, g.len);
             const T *px = x + r * p.ld_x, *pd = delta + r * p.ld_delta, *pg = pz + r * ldz;
             if (XV) {
-                if (row - t < g.len) {
+                if (inside(row - t, g.len)) {
                     uint4 *to = ring + slot3 * (3 * Data::W * kFeeders);
 #pragma unroll
                     for (int k = 0; k < Data::W; ++k) {
@@ -146,21 +147,21 @@ __global__ void __launch_bounds__(4 * WN * KT + 32 * WN) scan_fwd_kernel(ScanPar
             }
             row += TT;
         };
-        int rowb = 0;
+        unsigned rowb = 0;
         auto fetch_bc = [&] {
             if constexpr (XV) {
 #pragma unroll
                 for (int k = 0; k < EV; ++k) {
                     constexpr int PER = TT * NP / 4;                 // quads of Bm, then as many of Cm
                     const int u = min(tid + k * kFeeders, 2 * PER - 1), w = u % PER;
-                    const long long r = min(rowb + w / (NP / 4), g.len - 1);
+                    const long long r = row_or_last(rowb + w / (NP / 4), g.len);
                     const int n = min(w % (NP / 4) * 4, p.N - 4);
                     bq[k] = *reinterpret_cast<const typename Quad::type *>((u < PER ? Bp + r * p.ld_B : Cp + r * p.ld_C) + n);
                 }
             } else {
 #pragma unroll
                 for (int k = 0; k < E; ++k) {
-                    const long long r = min(rowb + bt + k * BT, g.len - 1);
+                    const long long r = row_or_last(rowb + bt + k * BT, g.len);
                     be[k] = load_bits(Bp + r * p.ld_B + bl);
                     ce[k] = load_bits(Cp + r * p.ld_C + bl);
                 }
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(4 * WN * KT + 32 * WN) scan_fwd_kernel(ScanPar
             const f2x2 *src = reinterpret_cast<const f2x2 *>(&sm.y[finished & 1][t][c0]);
             const f2x2 ya = src[0], yb = src[1];
             f2 o[4] = {ya.a, ya.b, yb.a, yb.b};
-            const bool in = staged * TT + t < g.len;                 // behind the end the state stays as it is
+            const bool in = inside(tile_token(staged, TT, t), g.len);                 // behind the end the state stays as it is
 #pragma unroll
             for (int k = 0; k < 8; k += 2) {
                 f2 dt = add2(dc.pair(k), dbias[k / 2]);
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(4 * WN * KT + 32 * WN) scan_fwd_kernel(ScanPar
             zc = zn;
         };
         auto work = [&](int staged, int finished, bool store) {
-            if (z && p.softplus && (staged + 1) * TT <= g.len) work_on(std::true_type{}, staged, finished, store);
+            if (z && p.softplus && inside(tile_token(staged, TT, TT - 1), g.len)) work_on(std::true_type{}, staged, finished, store);
             else work_on(std::false_type{}, staged, finished, store);
         };
         if (tiles > 0) {
@@ -278,12 +279,12 @@ __global__ void __launch_bounds__(4 * WN * KT + 32 * WN) scan_fwd_kernel(ScanPar
             meet();                              // tile staged; tile - 1 carried
             stage_bc(tile + 1);                  // (of the last tile's data again past the end: read by nobody)
             fetch_bc();
-            work(tile + 1, tile - 1, tile > 0 && some && (tile - 1) * TT + t < g.len);
+            work(tile + 1, tile - 1, tile > 0 && some && inside(tile_token(tile - 1, TT, t), g.len));
             fetch();
             if (tile > 0) y += sy;
         }
         meet();
-        if (tiles > 0) work(tiles + 1, tiles - 1, some && (tiles - 1) * TT + t < g.len);
+        if (tiles > 0) work(tiles + 1, tiles - 1, some && inside(tile_token(tiles - 1, TT, t), g.len));
         if (XV) copies_wait<0>();
         return;
     }

@@ -29,3 +29,13 @@ def test_no_access_is_wider_than_the_workspaces_alignment(tmp_path, kind, count,
     r = _compile(tmp_path, f'#include "mixer_common.cuh"\nsize_t n = alignof(mixer::Vec<{kind}, {count}>);\n', *kbuild.ARCH, "-c")
     assert (r.returncode == 0) is ok, r.stderr[-2000:]
     assert ok or "at most 16 bytes" in r.stderr
+
+
+def test_positions_past_the_longest_length(tmp_path):
+    """The scan's forward walks whole sequences of up to 2^31 - 1 tokens and looks some tiles ahead."""
+    exe = tmp_path / "mixer_limits_check"
+    r = subprocess.run([_nvcc(), "-O1", "-std=c++17", "-I", kbuild.CSRC, os.path.join(kbuild.ROOT, "tests", "host", "mixer_limits_check.cu"),
+                        "-o", str(exe)], capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stderr[-2000:]
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
