@@ -213,7 +213,8 @@ __global__ void __launch_bounds__(TPR, 512 / TPR) norm_fwd_kernel(NormParams p) 
     }
 }
 
-// Rows too long for registers: three passes over the row (the later ones from L2), 1024 threads.
+// Rows too long for registers: three passes over the row (the later ones from L2), 1024 threads.  Columns
+// are counted without a sign: a step past a width near 2^31 does not wrap below 0.
 template <class T>
 __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(NormParams p) {
     __shared__ float2 sm[32];
@@ -221,10 +222,10 @@ __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(NormParams p) {
     const T *x = static_cast<const T *>(p.x) + row * p.ld_x;
     T *y = static_cast<T *>(p.y) + row * p.ld_y;
     float s = 0.f;
-    for (int c = threadIdx.x; c < p.D; c += 1024) s += to_f(x[c]);
+    for (unsigned c = threadIdx.x; c < (unsigned)p.D; c += 1024) s += to_f(x[c]);
     const float mean = row_sum2<1024>(make_float2(s, 0.f), sm).x / (float)p.D;
     float q = 0.f;
-    for (int c = threadIdx.x; c < p.D; c += 1024) {
+    for (unsigned c = threadIdx.x; c < (unsigned)p.D; c += 1024) {
         const float d = to_f(x[c]) - mean;
         q = fmaf(d, d, q);
     }
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(NormParams p) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
     }
-    for (int c = threadIdx.x; c < p.D; c += 1024) {
+    for (unsigned c = threadIdx.x; c < (unsigned)p.D; c += 1024) {
         const float w = p.weight ? load_w(p.weight, c, p.w_bf16) : 1.f;
         const float b = p.bias ? load_w(p.bias, c, p.w_bf16) : 0.f;
         y[c] = from_f<T>(fmaf((to_f(x[c]) - mean) * rstd, w, b));
@@ -352,14 +353,14 @@ __global__ void __launch_bounds__(1024) norm_bwd_long_kernel(NormParams p) {
     T *dx = static_cast<T *>(p.y) + row * p.ld_y;
     const float mean = p.mean[row], rstd = p.rstd[row];
     float2 s = make_float2(0.f, 0.f);
-    for (int c = threadIdx.x; c < p.D; c += 1024) {
+    for (unsigned c = threadIdx.x; c < (unsigned)p.D; c += 1024) {
         const float g = to_f(dy[c]) * (p.weight ? load_w(p.weight, c, p.w_bf16) : 1.f);
         s.x += g;
         s.y = fmaf(g, (to_f(x[c]) - mean) * rstd, s.y);
     }
     s = row_sum2<1024>(s, sm);
     const float mg = s.x / (float)p.D, mgx = s.y / (float)p.D;
-    for (int c = threadIdx.x; c < p.D; c += 1024) {
+    for (unsigned c = threadIdx.x; c < (unsigned)p.D; c += 1024) {
         const float g = to_f(dy[c]) * (p.weight ? load_w(p.weight, c, p.w_bf16) : 1.f);
         dx[c] = from_f<T>(rstd * (g - mg - (to_f(x[c]) - mean) * rstd * mgx));
     }

@@ -5,7 +5,8 @@ import ctypes
 import pytest
 import torch
 
-from chunkwise_gated_delta_gb300 import _lib, layer_norm_bwd, layer_norm_fwd, mixer, short_conv_bwd, ssm_scan_bwd, ssm_scan_fwd
+from chunkwise_gated_delta_gb300 import (_lib, layer_norm_bwd, layer_norm_fwd, mixer, short_conv_bwd, ssm_scan_bwd,
+                                         ssm_scan_fwd)
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -65,3 +66,21 @@ def test_workspaces_of_sixteen_byte_alignment(dtype, monkeypatch):
     _Shifted.seen = 0
     for k in ref:
         assert torch.equal(got[k], ref[k]), k
+
+
+# ------------------------------------------------------------------------------------ sizes near 2^31
+def test_rows_of_more_columns_than_a_signed_step_reaches():
+    """One row of 2^31 - 1 values, half of them 1, half -1 and a last 0: every sum is a whole number that
+    float32 holds, so the mean is 0 and a normalised value is 1 / sqrt(1 + eps) up to a few units of
+    float32, which bfloat16 rounds to 1.  The same row as dy: mean(g xh) = rstd (D - 1) / D, so dx =
+    x rstd (1 - xh rstd) < 2 eps, and 0 at the end."""
+    D = (1 << 31) - 1
+    x = torch.ones(1, D, dtype=torch.bfloat16, device=DEV)
+    x[0, 1::2] = -1
+    x[0, -1] = 0
+    y, mean, rstd = layer_norm_fwd(x, eps=1e-5)
+    assert float(mean[0]) == 0.0 and abs(float(rstd[0]) - (1 + 1e-5) ** -0.5) <= 1e-6
+    assert torch.equal(y, x)
+    got = layer_norm_bwd(x, x, None, mean, rstd, bias=False, grads=dict(dx=y))
+    assert set(got) == {"dx"} and float(y[0, -1]) == 0.0
+    assert float(y.max()) <= 2e-5 and float(y.min()) >= -2e-5
