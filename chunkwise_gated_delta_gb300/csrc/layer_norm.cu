@@ -367,17 +367,17 @@ __global__ void __launch_bounds__(1024) norm_bwd_long_kernel(NormParams p) {
 }
 template <class T>
 __global__ void __launch_bounds__(256) norm_bwd_cols_kernel(NormParams p) {
-    const int c = blockIdx.y * 256 + threadIdx.x;
-    if (c >= p.D) return;
+    const unsigned c = blockIdx.x * 256 + threadIdx.x;      // (columns in x: y ends at 65535 blocks)
+    if (c >= (unsigned)p.D) return;
     float aw = 0.f, ab = 0.f;
-    for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    for (long long row = blockIdx.y; row < p.rows; row += gridDim.y) {
         const float d = to_f(static_cast<const T *>(p.dy)[row * p.ld_dy + c]);
         const float xh = (to_f(static_cast<const T *>(p.x)[row * p.ld_x + c]) - p.mean[row]) * p.rstd[row];
         aw = fmaf(d, xh, aw);
         ab += d;
     }
-    p.part[(size_t)blockIdx.x * 2 * p.D + c] = aw;
-    p.part[(size_t)blockIdx.x * 2 * p.D + p.D + c] = ab;
+    p.part[(size_t)blockIdx.y * 2 * p.D + c] = aw;
+    p.part[(size_t)blockIdx.y * 2 * p.D + p.D + c] = ab;
 }
 
 // Blocks of the backward: two of 256 threads per SM (128 registers each) visit the rows, at least four
@@ -487,7 +487,7 @@ template <class T, int V> cudaError_t bwd_vec(const NormParams &p, cudaStream_t 
         else if constexpr (V == 1) norm_bwd_kernel<T, V, 8, 512, 1><<<blocks, 512, 0, s>>>(p);
     } else {
         norm_bwd_long_kernel<T><<<(unsigned)p.rows, 1024, 0, s>>>(p);
-        if (p.part) norm_bwd_cols_kernel<T><<<dim3(blocks, (p.D + 255) / 256), 256, 0, s>>>(p);
+        if (p.part) norm_bwd_cols_kernel<T><<<dim3(((unsigned)p.D + 255) / 256, blocks), 256, 0, s>>>(p);
     }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !p.part) return e;

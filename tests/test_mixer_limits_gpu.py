@@ -84,3 +84,21 @@ def test_rows_of_more_columns_than_a_signed_step_reaches():
     got = layer_norm_bwd(x, x, None, mean, rstd, bias=False, grads=dict(dx=y))
     assert set(got) == {"dx"} and float(y[0, -1]) == 0.0
     assert float(y.max()) <= 2e-5 and float(y.min()) >= -2e-5
+
+
+def test_parameter_sums_of_more_column_blocks_than_a_grid_has_in_y():
+    """65536 blocks of 256 columns and five more.  x of ones and minus ones (mean 0, whole sums), dy of small
+    whole numbers: dbias is exact, dweight = rstd sum(dy x) off by two roundings of each of three
+    products and of their sums, 5 u of at most 6."""
+    D, rows = 65536 * 256 + 5, 3
+    x = torch.ones(rows, D, device=DEV)
+    x[:, 1::2] = -1
+    x[:, -1] = 0
+    g = torch.Generator(device=DEV).manual_seed(2)
+    dy = torch.randint(-2, 3, (rows, D), generator=g, device=DEV).float()
+    w = torch.ones(D, device=DEV)
+    _, mean, rstd = layer_norm_fwd(x, w)
+    got = layer_norm_bwd(dy, x, w, mean, rstd)
+    assert torch.equal(got["dbias"], dy.sum(0))
+    ref = (dy.double() * x.double() * rstd.double()[:, None]).sum(0)
+    assert float((got["dweight"].double() - ref).abs().max()) <= 5 * 2.0 ** -24 * 6
