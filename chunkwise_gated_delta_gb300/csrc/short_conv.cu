@@ -318,10 +318,11 @@ template <class T, int W, int V>
 __global__ void __launch_bounds__(128) conv_step_kernel(ConvParams p) {
     const int groups = p.D / V;
     const long long u = (long long)blockIdx.x * 128 + threadIdx.x;
-    const int b = (int)(u / groups), c = (int)(u - (long long)b * groups) * V;
+    const long long b = u / groups;                // (the last block's threads may pass 2^31 requests)
+    const int c = (int)(u - b * groups) * V;
     if (b >= p.B) return;
-    const int slot = p.slot ? p.slot[b] : b;
-    T *y = static_cast<T *>(p.y) + (long long)b * p.ld_y + c;
+    const int slot = p.slot ? p.slot[b] : (int)b;
+    T *y = static_cast<T *>(p.y) + b * p.ld_y + c;
     constexpr int P = (V + 1) / 2;
     f2 o[P];
     if (slot < 0 || slot >= p.slots) {
@@ -334,7 +335,7 @@ __global__ void __launch_bounds__(128) conv_step_kernel(ConvParams p) {
     Vec<T, V> in[W];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) in[j] = load_vec<T, V>(st + (long long)j * p.D);
-    in[W - 1] = load_vec<T, V>(static_cast<const T *>(p.x) + (long long)b * p.ld_x + c);
+    in[W - 1] = load_vec<T, V>(static_cast<const T *>(p.x) + b * p.ld_x + c);
     f2 w[W][P], bias[P];
     load_taps<W, V>(w, bias, p, c);
 #pragma unroll

@@ -5,7 +5,7 @@ import ctypes
 import pytest
 import torch
 
-from chunkwise_gated_delta_gb300 import (_lib, layer_norm_bwd, layer_norm_fwd, mixer, short_conv_bwd, ssm_scan_bwd,
+from chunkwise_gated_delta_gb300 import (_lib, layer_norm_bwd, layer_norm_fwd, mixer, short_conv_bwd, short_conv_step, ssm_scan_bwd,
                                          ssm_scan_fwd)
 
 pytestmark = pytest.mark.gpu
@@ -102,3 +102,16 @@ def test_parameter_sums_of_more_column_blocks_than_a_grid_has_in_y():
     assert torch.equal(got["dbias"], dy.sum(0))
     ref = (dy.double() * x.double() * rstd.double()[:, None]).sum(0)
     assert float((got["dweight"].double() - ref).abs().max()) <= 5 * 2.0 ** -24 * 6
+
+
+def test_single_tokens_of_more_requests_than_blocks_end_at():
+    """2^31 - 1 requests of one channel: the last block has a thread past them."""
+    B = (1 << 31) - 1
+    x = torch.full((B, 1), 2.0, dtype=torch.bfloat16, device=DEV)
+    x[-1] = 3
+    state = torch.full((B, 1, 1), 5.0, dtype=torch.bfloat16, device=DEV)
+    state[-1] = 7
+    w = torch.tensor([[1.0, 10.0]], dtype=torch.bfloat16, device=DEV)
+    y = short_conv_step(x, w, None, state, activation=None)
+    assert float(y[0]) == 25.0 and float(y[-2]) == 25.0 and float(y[-1]) == 37.0 and bool((y[:-1] == 25).all())
+    assert torch.equal(state[:, 0], x)
