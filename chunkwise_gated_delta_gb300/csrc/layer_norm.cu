@@ -284,12 +284,15 @@ __global__ void __launch_bounds__(TPR, 512 / TPR) norm_bwd_kernel(NormParams p) 
         float mean[R], rstd[R], s[2 * R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
+            // The dy of a row past the end becomes zeros by its bits: times 0 an infinity of the last row, which
+            // stands in for it, would turn the sums into NaN.
+            const bool on = r == 0 || row + r < p.rows;
             mean[r] = nm[r];
             rstd[r] = nr[r];
 #pragma unroll
             for (int k = 0; k < ITEMS; ++k) {
                 vx[r][k] = nx[r][k];
-                vd[r][k] = nd[r][k];
+                vd[r][k] = nd[r][k].kept(on);
             }
         }
         fetch(row + step);
@@ -297,13 +300,12 @@ __global__ void __launch_bounds__(TPR, 512 / TPR) norm_bwd_kernel(NormParams p) 
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             f2 s0 = both(0.f), s1 = both(0.f);
-            const f2 on = both(row + r < p.rows ? 1.f : 0.f);
 #pragma unroll
             for (int k = 0; k < ITEMS; ++k)
                 if (tid + k * TPR < nv)
 #pragma unroll
                     for (int e = 0; e < P; ++e) {
-                        const f2 d = mul2(vd[r][k].pair(e), on);
+                        const f2 d = vd[r][k].pair(e);
                         xh[r][k][e] = mul2(add2(vx[r][k].pair(e), both(-mean[r])), both(rstd[r]));
                         g[r][k][e] = mul2(d, w[k][e]);
                         s0 = add2(s0, g[r][k][e]);

@@ -182,6 +182,13 @@ template <class T, int V> struct Lanes {
 #pragma unroll
         for (int k = 0; k < WORDS; ++k) w[k] = v.e[k];
     }
+    // These elements, or zeros.
+    __device__ __forceinline__ Lanes kept(bool on) const {
+        Lanes r;
+#pragma unroll
+        for (int k = 0; k < WORDS; ++k) r.w[k] = w[k] & (on ? ~0u : 0u);
+        return r;
+    }
     __device__ __forceinline__ f2 pair(int k) const {
         if constexpr (V == 1) return pack2(bits_f<T>(w[0]), 0.f);
         else if constexpr (sizeof(T) == 4) return pack2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
