@@ -168,6 +168,8 @@ __global__ void __launch_bounds__(4 * WN * KT + 32 * WN) scan_fwd_kernel(ScanPar
             }
             rowb += TT;
         };
+        // Tokens past the end are staged as zeros: their dt x is 0, and an infinity of the last row times 0
+        // would turn the final state into NaN.
         auto stage_bc = [&](int tile) {
             const int b = tile & 1;
             if constexpr (XV) {
@@ -176,15 +178,16 @@ __global__ void __launch_bounds__(4 * WN * KT + 32 * WN) scan_fwd_kernel(ScanPar
                     constexpr int PER = TT * NP / 4;
                     const int u = tid + k * kFeeders, w = u % PER, n = w % (NP / 4) * 4;
                     float4 v = Quad::floats(bq[k]);
-                    if (n >= p.N) v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (n >= p.N || !inside(tile_token(tile, TT, w / (NP / 4)), g.len)) v = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (u < 2 * PER) *reinterpret_cast<float4 *>(&(u < PER ? sm.B : sm.C)[b][w / (NP / 4)][n]) = v;
                 }
             } else {
 #pragma unroll
                 for (int k = 0; k < E; ++k) {
                     if (!bs) break;
-                    sm.B[b][bt + k * BT][bn] = bn < p.N ? bits_f<T>(be[k]) : 0.f;
-                    sm.C[b][bt + k * BT][bn] = bn < p.N ? bits_f<T>(ce[k]) : 0.f;
+                    const bool real = bn < p.N && inside(tile_token(tile, TT, bt + k * BT), g.len);
+                    sm.B[b][bt + k * BT][bn] = real ? bits_f<T>(be[k]) : 0.f;
+                    sm.C[b][bt + k * BT][bn] = real ? bits_f<T>(ce[k]) : 0.f;
                 }
             }
         };
@@ -277,7 +280,7 @@ __global__ void __launch_bounds__(4 * WN * KT + 32 * WN) scan_fwd_kernel(ScanPar
         }
         for (int tile = 0; tile < tiles; ++tile) {
             meet();                              // tile staged; tile - 1 carried
-            stage_bc(tile + 1);                  // (of the last tile's data again past the end: read by nobody)
+            stage_bc(tile + 1);                  // (past the last tile: read by nobody)
             fetch_bc();
             work(tile + 1, tile - 1, tile > 0 && some && inside(tile_token(tile - 1, TT, t), g.len));
             fetch();

@@ -8,9 +8,9 @@ operators' own tests, the output's rounding half_step(dtype) and 1e-4 for the lo
 import pytest
 import torch
 
-from chunkwise_gated_delta_gb300 import layer_norm_bwd, layer_norm_fwd, short_conv_bwd, short_conv_fwd
+from chunkwise_gated_delta_gb300 import layer_norm_bwd, layer_norm_fwd, short_conv_bwd, short_conv_fwd, ssm_scan_bwd, ssm_scan_fwd
 
-from mixer_ref import half_step, layer_norm, short_conv, spans_of
+from mixer_ref import half_step, layer_norm, short_conv, spans_of, ssm_scan
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -83,3 +83,46 @@ def test_conv(dtype, D, which, value, at):
     _alike(ht, rht, "ht")
     for k, r in zip(names, grads):
         _alike(got["d" + k], r, "d" + k)
+
+
+# ------------------------------------------------------------------------------------ scan
+NAMES = ("x", "delta", "A", "B", "C", "D", "z", "delta_bias", "h0")
+
+
+def _scan_inputs(lens, D, N, dtype, seed):
+    rn, t = _rand(seed, dtype)
+    T, n = sum(lens), len(lens)
+    g = torch.Generator(device=DEV).manual_seed(seed + 1)
+    d = dict(x=t(T, D), delta=t(T, D), A=-(0.5 + torch.arange(N, device=DEV) + torch.rand(D, N, generator=g, device=DEV)), B=t(T, N),
+             C=t(T, N), D=rn(D), z=t(T, D), delta_bias=rn(D) - 2.0, h0=rn(n, D, N))
+    return d, t(T, D), rn(n, D, N)
+
+
+def _scan_check(d, dy, dht, lens, grads=True):
+    cu = torch.tensor([0] + [b for _, b in spans_of(lens)], dtype=torch.int32, device=DEV) if len(lens) > 1 else None
+    v = [d[k] if k in ("A", "D", "delta_bias", "h0") else d[k][None] for k in NAMES]
+    y, ht = ssm_scan_fwd(*v, cu_seqlens=cu)
+    leaf = {k: d[k].double() for k in NAMES}
+    if grads:
+        for k in NAMES:
+            leaf[k].requires_grad_()
+    ry, rht = ssm_scan(*(leaf[k] for k in NAMES), spans_of(lens), True)
+    _alike(y, ry, "y")
+    _alike(ht, rht, "ht")
+    if grads:
+        got = ssm_scan_bwd(*v, dy[None], dht, cu_seqlens=cu)
+        for k, r in zip(NAMES, torch.autograd.grad((ry, rht), [leaf[k] for k in NAMES], (dy.double(), dht.double()))):
+            _alike(got["d" + k], r, "d" + k)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,N,T", [(64, 16, 33), (64, 16, 64), (37, 5, 50), (64, 8, 1100), (1704, 16, 45)])
+def test_scan_ends_with_an_infinite_input(dtype, D, N, T):
+    """B of the last token: one state of every channel ends infinite, not NaN."""
+    d, dy, dht = _scan_inputs([T], D, N, dtype, 6)
+    d["B"][-1, 2] = INF
+    v = [d[k] if k in ("A", "D", "delta_bias", "h0") else d[k][None] for k in NAMES]
+    _, ht = ssm_scan_fwd(*v)
+    assert bool(torch.isinf(ht[0, :, 2]).all())
+    assert torch.equal(torch.sign(ht[0, :, 2]), torch.sign(d["x"][-1].float()))
+    _scan_check(d, dy, dht, [T], grads=False)
