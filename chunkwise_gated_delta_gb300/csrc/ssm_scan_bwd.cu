@@ -393,6 +393,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) scan_grad_kernel(ScanParams p
     // ---- the parts, last to first
     for (int part = parts - 1; part >= 0; --part) {
         f2 accB[TC][2], accC[TC][2];     // dB, dC of this lane's states, over the channel groups
+        const int real = g.len - part * TC;
 #pragma unroll
         for (int k = 0; k < GROUPS; ++k) {
             const int cc = k * S::CG + warp * CW + c;
@@ -436,8 +437,10 @@ __global__ void __launch_bounds__(kGradThreads, 2) scan_grad_kernel(ScanParams p
                 G0 = mul2(G0, a[t][0]);
                 G1 = mul2(G1, a[t][1]);
                 const f2 q0 = mul2(G0, h[t][0]), q1 = mul2(G1, h[t][1]);
-                dA[k][0] = fma2(q0, dt, dA[k][0]);
-                dA[k][1] = fma2(q1, dt, dA[k][1]);
+                if (t < real) {          // past the end q may be infinite, and dt is 0
+                    dA[k][0] = fma2(q0, dt, dA[k][0]);
+                    dA[k][1] = fma2(q1, dt, dA[k][1]);
+                }
                 unpack2(fma2(q0, a2[k][0], mul2(q1, a2[k][1])), lo, hi);
                 qs[t] = lo + hi;
             }

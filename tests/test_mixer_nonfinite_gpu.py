@@ -116,6 +116,20 @@ def _scan_check(d, dy, dht, lens, grads=True):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,N", [(64, 16), (37, 5), (32, 32)])
+@pytest.mark.parametrize("which,value", [("x", INF), ("x", NAN), ("B", INF), ("B", NAN), ("C", INF), ("delta", NAN), ("z", NAN), ("dy", INF),
+                                         ("dy", NAN)])
+@pytest.mark.parametrize("at", ["last", "inside"])
+def test_scan_of_packed_sequences(dtype, D, N, which, value, at):
+    lens = [9, 0, 70, 1, 33]
+    d, dy, dht = _scan_inputs(lens, D, N, dtype, 5)
+    lo, hi = spans_of(lens)[2]
+    row = hi - 1 if at == "last" else lo + 40
+    (dy if which == "dy" else d[which])[row, 3] = value
+    _scan_check(d, dy, dht, lens)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("D,N,T", [(64, 16, 33), (64, 16, 64), (37, 5, 50), (64, 8, 1100), (1704, 16, 45)])
 def test_scan_ends_with_an_infinite_input(dtype, D, N, T):
     """B of the last token: one state of every channel ends infinite, not NaN."""
