@@ -19,6 +19,13 @@ constexpr int kFwdLocal = 128;       // and in the split forward
 // all of that range, like expf's; at dt = 0 the decay is exactly 1.
 constexpr float kDecayBias = 2.5e-8f;
 
+// A log2 e.  An infinity (minus infinity: a state without memory) becomes the largest value of its sign: the
+// tokens that fill the end of a tile have dt = 0 and leave the state as it is, but 0 times infinity is NaN.
+__device__ __forceinline__ float decay_rate(float a) {
+    const float v = a * kLog2e;
+    return isinf(v) ? copysignf(3.402823466e38f, v) : v;
+}
+
 // log(1 + u) for u in [0, 1]: 2 atanh(s) with s = u / (2 + u) <= 1/3, atanh(s) = s + s^3 P(s^2) with P
 // fitted for the smallest relative error of atanh on that interval (Lawson's reweighted least
 // squares): 5.4e-9 with these four coefficients, below the rounding of one operation.  Relative

@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kScanThreads, XV && sizeof(T) == 2 ? 5 : 4) sc
         if (live) load_states(av, p.A + (long long)d * p.N, n0, p.N);
 #pragma unroll
         for (int k = 0; k < H; ++k) {
-            a2[k] = pack2(av[2 * k] * kLog2e, av[2 * k + 1] * kLog2e);
+            a2[k] = pack2(decay_rate(av[2 * k]), decay_rate(av[2 * k + 1]));
             h[k] = e[k] = pack2(0.f, 0.f);
             m[k] = pack2(1.f, 1.f);          // a_1 ... a_t
         }
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(128) scan_boundary_kernel(ScanParams p, int NP
         s0 = b + lo / p.lseg;
     }
     const bool in = n < p.N;
-    const float a2 = in ? p.A[(long long)d * p.N + n] * kLog2e : 0.f;
+    const float a2 = in ? decay_rate(p.A[(long long)d * p.N + n]) : 0.f;
     const long long at = ((long long)b * p.D + d) * p.N + n;
     const float *first = back ? p.dht : p.h0;
     float v = in && first ? first[at] : 0.f;
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) scan_grad_kernel(ScanParams p
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            a2[k][s] = pack2(av[2 * s] * kLog2e, av[2 * s + 1] * kLog2e);
+            a2[k][s] = pack2(decay_rate(av[2 * s]), decay_rate(av[2 * s + 1]));
             carry[k][s] = pack2(ev[2 * s], ev[2 * s + 1]);
             dA[k][s] = pack2(0.f, 0.f);
         }

@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(4 * WN * KT + 32 * WN) scan_fwd_kernel(ScanPar
         }
 #pragma unroll
         for (int k = 0; k < H; ++k) {
-            a2[k] = pack2(av[2 * k] * kLog2e, av[2 * k + 1] * kLog2e);
+            a2[k] = pack2(decay_rate(av[2 * k]), decay_rate(av[2 * k + 1]));
             h[k] = pack2(hv[2 * k], hv[2 * k + 1]);
         }
     }

@@ -140,3 +140,24 @@ def test_scan_ends_with_an_infinite_input(dtype, D, N, T):
     assert bool(torch.isinf(ht[0, :, 2]).all())
     assert torch.equal(torch.sign(ht[0, :, 2]), torch.sign(d["x"][-1].float()))
     _scan_check(d, dy, dht, [T], grads=False)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,N,lens", [(64, 16, [33]), (64, 16, [64]), (37, 5, [9, 0, 50]), (64, 8, [1100]), (64, 16, [1030, 0, 300]), (8, 4, [7])])
+def test_states_without_memory(dtype, D, N, lens):
+    """A of minus infinity: the state is its last input alone, also where a tile's or a batch of segments'
+    end is filled up."""
+    d, dy, dht = _scan_inputs(lens, D, N, dtype, 7)
+    d["A"][:, 1] = -INF
+    _scan_check(d, dy, dht, lens, grads=False)
+    # the gradients that do not go through A itself: ddelta and dA have the definition's infinity times 0
+    v = [d[k] if k in ("A", "D", "delta_bias", "h0") else d[k][None] for k in NAMES]
+    cu = torch.tensor([0] + [b for _, b in spans_of(lens)], dtype=torch.int32, device=DEV) if len(lens) > 1 else None
+    got = ssm_scan_bwd(*v, dy[None], dht, cu_seqlens=cu)
+    leaf = {k: d[k].double() for k in NAMES}
+    names = ("x", "B", "C", "D", "z", "h0")
+    for k in names:
+        leaf[k].requires_grad_()
+    ry, rht = ssm_scan(*(leaf[k] for k in NAMES), spans_of(lens), True)
+    for k, r in zip(names, torch.autograd.grad((ry, rht), [leaf[k] for k in names], (dy.double(), dht.double()))):
+        _alike(got["d" + k], r, "d" + k)
