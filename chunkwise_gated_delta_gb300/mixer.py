@@ -114,18 +114,20 @@ def _sequences(cu_seqlens, B, device):
 class _On:
     """The stream of a call: allocations inside go to it, launches too."""
 
-    __slots__ = ("device", "handle", "ctx")
+    __slots__ = ("device", "handle", "ctx", "side")
 
     def __init__(self, device, stream, inputs):
         self.device = device
         self.handle = _raw_stream(device)
         self.ctx = None
+        self.side = None                 # a stream other than the current one
         if stream is not None and stream.cuda_stream != self.handle:
             self.ctx = torch.cuda.stream(stream)
             self.handle = stream.cuda_stream
-            for t in inputs:             # the allocator must not hand them out while that stream uses them
+            self.side = stream
+            for t in inputs:
                 if t is not None:
-                    t.record_stream(stream)
+                    self.uses(t)
         elif _device_index() != device:
             self.ctx = torch.cuda.device(device)
 
@@ -137,6 +139,11 @@ class _On:
     def __exit__(self, *exc):
         if self.ctx is not None:
             self.ctx.__exit__(*exc)
+
+    def uses(self, t):
+        """The allocator must not hand out a caller's tensor while another stream reads or writes it."""
+        if self.side is not None:
+            t.record_stream(self.side)
 
     def launch(self, name, args):
         rc = _function(name)(ctypes.byref(args), self.handle)
@@ -153,19 +160,23 @@ class _On:
         return None
 
 
-def _out(given, name, shape, dtype, device):
-    """An output tensor (rows may lie apart): the caller's, or a new one."""
+def _out(on, given, name, shape, dtype):
+    """An output tensor of a call (rows may lie apart): the caller's, or a new one."""
     if given is None:
-        given = torch.empty(shape, dtype=dtype, device=device)
+        given = torch.empty(shape, dtype=dtype, device=on.device)
         return given, given.data_ptr(), shape[-1]
-    return (given, *_rows(given, name, shape, dtype, device))
+    rows = _rows(given, name, shape, dtype, on.device)
+    on.uses(given)
+    return (given, *rows)
 
 
-def _dense_out(given, name, shape, dtype, device):
+def _dense_out(on, given, name, shape, dtype):
     if given is None:
-        given = torch.empty(shape, dtype=dtype, device=device)
+        given = torch.empty(shape, dtype=dtype, device=on.device)
         return given, given.data_ptr()
-    return given, _tensor(given, name, shape, dtype, device)
+    ptr = _tensor(given, name, shape, dtype, on.device)
+    on.uses(given)
+    return given, ptr
 
 
 def _known(grads, names):
@@ -203,7 +214,7 @@ def layer_norm_fwd(x, weight=None, bias=None, *, eps=1e-5, y=None, stream=None):
     xp, ldx = _rows(x, "x", x.shape, x.dtype, dev)
     wp, bp, wdt = _weights(weight, bias, "weight", (D,), D, dev, x.dtype)
     with _On(dev, stream, (x, weight, bias)) as on:
-        y, yp, ldy = _out(y, "y", x.shape, x.dtype, dev)
+        y, yp, ldy = _out(on, y, "y", x.shape, x.dtype)
         mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
         rstd = torch.empty_like(mean)
         on.launch("layer_norm_fwd", _lib.LayerNormFwdArgs(
@@ -227,12 +238,12 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, *, bias=True, grads=None, stream=N
     rp = _tensor(rstd, "rstd", tuple(x.shape[:-1]), torch.float32, dev)
     out = _known(grads, ("dx", "dweight", "dbias"))
     with _On(dev, stream, (x, dy, weight, mean, rstd)) as on:
-        out["dx"], dxp, lddx = _out(out.get("dx"), "dx", x.shape, x.dtype, dev)
+        out["dx"], dxp, lddx = _out(on, out.get("dx"), "dx", x.shape, x.dtype)
         dwp = dbp = None
         if weight is not None:
-            out["dweight"], dwp = _dense_out(out.get("dweight"), "dweight", (D,), wdt, dev)
+            out["dweight"], dwp = _dense_out(on, out.get("dweight"), "dweight", (D,), wdt)
         if bias:
-            out["dbias"], dbp = _dense_out(out.get("dbias"), "dbias", (D,), wdt, dev)
+            out["dbias"], dbp = _dense_out(on, out.get("dbias"), "dbias", (D,), wdt)
         args = _lib.LayerNormBwdArgs(x.numel() // D, D, code, _CODES[wdt], dyp, lddy, xp, ldx, wp, mp, rp, dxp, lddx,
                                      dwp, dbp, None, 0)
         ws = on.workspace("layer_norm_bwd_workspace", args)
@@ -270,10 +281,10 @@ def short_conv_fwd(x, weight, bias=None, h0=None, *, activation="silu", output_f
     W = weight.shape[1]
     hp = None if h0 is None else _tensor(h0, "h0", (n, W - 1, D), x.dtype, dev)
     with _On(dev, stream, (x, weight, bias, h0, cu_seqlens)) as on:
-        y, yp, ldy = _out(y, "y", x.shape, x.dtype, dev)
+        y, yp, ldy = _out(on, y, "y", x.shape, x.dtype)
         htp = None
         if output_final_state or ht is not None:
-            ht, htp = _dense_out(ht, "ht", (n, W - 1, D), x.dtype, dev)
+            ht, htp = _dense_out(on, ht, "ht", (n, W - 1, D), x.dtype)
         on.launch("short_conv_fwd", _lib.ShortConvFwdArgs(n, T, D, W, code, _CODES[wdt], flags, xp, ldx, wp, bp, hp, yp,
                                                           ldy, htp, cu))
     return y, ht
@@ -297,13 +308,13 @@ def short_conv_bwd(x, weight, bias, h0, dy, dht=None, *, activation="silu", grad
     dhp = None if dht is None else _tensor(dht, "dht", (n, W - 1, D), x.dtype, dev)
     out = _known(grads, ("dx", "dweight", "dbias", "dh0"))
     with _On(dev, stream, (x, weight, bias, h0, dy, dht, cu_seqlens)) as on:
-        out["dx"], dxp, lddx = _out(out.get("dx"), "dx", x.shape, x.dtype, dev)
-        out["dweight"], dwp = _dense_out(out.get("dweight"), "dweight", (D, W), wdt, dev)
+        out["dx"], dxp, lddx = _out(on, out.get("dx"), "dx", x.shape, x.dtype)
+        out["dweight"], dwp = _dense_out(on, out.get("dweight"), "dweight", (D, W), wdt)
         dbp = dh0p = None
         if bias is not None:
-            out["dbias"], dbp = _dense_out(out.get("dbias"), "dbias", (D,), wdt, dev)
+            out["dbias"], dbp = _dense_out(on, out.get("dbias"), "dbias", (D,), wdt)
         if h0 is not None:
-            out["dh0"], dh0p = _dense_out(out.get("dh0"), "dh0", (n, W - 1, D), x.dtype, dev)
+            out["dh0"], dh0p = _dense_out(on, out.get("dh0"), "dh0", (n, W - 1, D), x.dtype)
         args = _lib.ShortConvBwdArgs(n, T, D, W, code, _CODES[wdt], flags, xp, ldx, wp, bp, hp, dyp, lddy, dhp, dxp, lddx,
                                      dh0p, dwp, dbp, None, 0, cu)
         ws = on.workspace("short_conv_bwd_workspace", args)
@@ -329,7 +340,7 @@ def short_conv_step(x, weight, bias, state, *, activation="silu", slots=None, y=
     sp = _tensor(state, "state", (state.shape[0], W - 1, D), x.dtype, dev)
     ip = None if slots is None else _tensor(slots, "slots", (B,), torch.int32, dev)
     with _On(dev, stream, (x, weight, bias, state, slots)) as on:
-        y, yp, ldy = _out(y, "y", x.shape, x.dtype, dev)
+        y, yp, ldy = _out(on, y, "y", x.shape, x.dtype)
         on.launch("short_conv_step", _lib.ShortConvStepArgs(B, D, W, state.shape[0], code, _CODES[wdt], flags, xp, ldx,
                                                             wp, bp, sp, ip, yp, ldy))
     return y
@@ -370,10 +381,10 @@ def ssm_scan_fwd(x, delta, A, B, C, D=None, z=None, delta_bias=None, h0=None, *,
     cu, seqs = _sequences(cu_seqlens, bt, dev)
     hp = None if h0 is None else _tensor(h0, "h0", (seqs, ch, n), torch.float32, dev)
     with _On(dev, stream, (x, delta, A, B, C, D, z, delta_bias, h0, cu_seqlens)) as on:
-        y, yp, ldy = _out(y, "y", x.shape, x.dtype, dev)
+        y, yp, ldy = _out(on, y, "y", x.shape, x.dtype)
         htp = None
         if output_final_state or ht is not None:
-            ht, htp = _dense_out(ht, "ht", (seqs, ch, n), torch.float32, dev)
+            ht, htp = _dense_out(on, ht, "ht", (seqs, ch, n), torch.float32)
         args = _lib.SsmScanFwdArgs(seqs, T, ch, n, code, int(delta_softplus), *ptrs, hp, yp, ldy, htp, None, 0, cu)
         ws = on.workspace("ssm_scan_fwd_workspace", args)
         on.launch("ssm_scan_fwd", args)
@@ -398,10 +409,10 @@ def ssm_scan_bwd(x, delta, A, B, C, D, z, delta_bias, h0, dy, dht=None, *, delta
     with _On(dev, stream, (x, delta, A, B, C, D, z, delta_bias, h0, dy, dht, cu_seqlens)) as on:
         seq = []
         for name, shape in (("dx", x.shape), ("ddelta", x.shape), ("dB", B.shape), ("dC", C.shape)):
-            out[name], p, ld = _out(out.get(name), name, shape, x.dtype, dev)
+            out[name], p, ld = _out(on, out.get(name), name, shape, x.dtype)
             seq += [p, ld]
         if z is not None:
-            out["dz"], p, ld = _out(out.get("dz"), "dz", x.shape, x.dtype, dev)
+            out["dz"], p, ld = _out(on, out.get("dz"), "dz", x.shape, x.dtype)
             seq += [p, ld]
         else:
             seq += [None, 0]
@@ -410,7 +421,7 @@ def ssm_scan_bwd(x, delta, A, B, C, D, z, delta_bias, h0, dy, dht=None, *, delta
                                  ("dh0", h0, (seqs, ch, n))):
             p = None
             if src is not None:
-                out[name], p = _dense_out(out.get(name), name, shape, f32, dev)
+                out[name], p = _dense_out(on, out.get(name), name, shape, f32)
             par.append(p)
         args = _lib.SsmScanBwdArgs(seqs, T, ch, n, code, int(delta_softplus), *ptrs, hp, *dyp, dhp, *seq, *par, None, 0,
                                    cu)
@@ -432,7 +443,7 @@ def ssm_scan_step(x, delta, A, B, C, state, D=None, z=None, delta_bias=None, *, 
     sp = _tensor(state, "state", (state.shape[0], ch, n) if state.dim() == 3 else (None, ch, n), _F32, dev)
     ip = None if slots is None else _tensor(slots, "slots", (bt,), torch.int32, dev)
     with _On(dev, stream, (x, delta, A, B, C, state, D, z, delta_bias, slots)) as on:
-        y, yp, ldy = _out(y, "y", x.shape, x.dtype, dev)
+        y, yp, ldy = _out(on, y, "y", x.shape, x.dtype)
         on.launch("ssm_scan_step", _lib.SsmScanStepArgs(bt, ch, n, state.shape[0], code, int(delta_softplus), *ptrs, sp, ip,
                                                         yp, ldy))
     return y

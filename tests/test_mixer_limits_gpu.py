@@ -115,3 +115,49 @@ def test_single_tokens_of_more_requests_than_blocks_end_at():
     y = short_conv_step(x, w, None, state, activation=None)
     assert float(y[0]) == 25.0 and float(y[-2]) == 25.0 and float(y[-1]) == 37.0 and bool((y[:-1] == 25).all())
     assert torch.equal(state[:, 0], x)
+
+
+# ------------------------------------------------------------------------------------ outputs on other streams
+def _calls(T=2000, D=1024, N=16):
+    """Every operator with all of its outputs supplied: (name, names and shapes of the outputs, call)."""
+    rn, t = _rand(4, torch.float32)
+    x, w, b, cw, h, bc = t(1, T, D), t(D), t(D), t(D, 4), t(1, 3, D), t(1, T, N)
+    A, sh = -torch.rand(D, N, device=DEV) - 0.5, rn(1, D, N)
+    _, mean, rstd = layer_norm_fwd(x, w, b)
+    seq, vec = (1, T, D), (D,)
+    yield "layer_norm_fwd", dict(y=seq), lambda o, s: layer_norm_fwd(x, w, b, y=o["y"], stream=s)
+    yield ("layer_norm_bwd", dict(dx=seq, dweight=vec, dbias=vec),
+           lambda o, s: layer_norm_bwd(x, x, w, mean, rstd, grads=o, stream=s))
+    yield "short_conv_fwd", dict(y=seq, ht=(1, 3, D)), lambda o, s: mixer.short_conv_fwd(x, cw, b, h, y=o["y"], ht=o["ht"], stream=s)
+    yield ("short_conv_bwd", dict(dx=seq, dweight=(D, 4), dbias=vec, dh0=(1, 3, D)),
+           lambda o, s: short_conv_bwd(x, cw, b, h, x, grads=o, stream=s))
+    state = t(T, 3, D)
+    yield "short_conv_step", dict(y=(T, D)), lambda o, s: short_conv_step(x[0], cw, b, state, y=o["y"], stream=s)
+    args = (x, x, A, bc, bc, w, x, b, sh)
+    yield "ssm_scan_fwd", dict(y=seq, ht=(1, D, N)), lambda o, s: ssm_scan_fwd(*args, y=o["y"], ht=o["ht"], stream=s)
+    yield ("ssm_scan_bwd", dict(dx=seq, ddelta=seq, dz=seq, dB=(1, T, N), dC=(1, T, N), dA=(D, N), dD=vec, ddelta_bias=vec, dh0=(1, D, N)),
+           lambda o, s: ssm_scan_bwd(*args, x, grads=o, stream=s))
+    st = t(T, D, N)
+    yield ("ssm_scan_step", dict(y=(T, D)),
+           lambda o, s: mixer.ssm_scan_step(x[0], x[0], A, bc[0], bc[0], st, w, x[0], b, y=o["y"], stream=s))
+
+
+def test_supplied_outputs_are_not_handed_out_while_the_call_runs():
+    """The call waits on its stream behind 50 ms of other work; the outputs' memory, given up by the caller
+    meanwhile, must not come back from the allocator."""
+    side = torch.cuda.Stream()
+    for name, shapes, call in _calls():
+        call({k: torch.empty(v, device=DEV) for k, v in shapes.items()}, None)        # (compiled modules loaded, pools warm)
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        out = {k: torch.empty(v, device=DEV) for k, v in shapes.items()}
+        at = {t.data_ptr() for t in out.values()}
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)
+        res = call(dict(out), side)
+        busy = not side.query()
+        del out, res
+        new = [torch.empty(v, device=DEV) for v in shapes.values()]
+        assert busy and not at & {t.data_ptr() for t in new}, name
+        torch.cuda.synchronize()
