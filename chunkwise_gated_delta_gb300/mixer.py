@@ -121,6 +121,8 @@ class _On:
         self.handle = _raw_stream(device)
         self.ctx = None
         self.side = None                 # a stream other than the current one
+        if stream is not None and stream.device.index != device:
+            raise ValueError(f"stream must be on device cuda:{device}, not {stream.device}")
         if stream is not None and stream.cuda_stream != self.handle:
             self.ctx = torch.cuda.stream(stream)
             self.handle = stream.cuda_stream

@@ -5,8 +5,10 @@ import shutil
 import subprocess
 
 import pytest
+import torch
 
 from chunkwise_gated_delta_gb300 import build as kbuild
+from chunkwise_gated_delta_gb300 import mixer
 
 
 def _nvcc():
@@ -39,3 +41,22 @@ def test_positions_past_the_longest_length(tmp_path):
     assert r.returncode == 0, r.stderr[-2000:]
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
+# ------------------------------------------------------------------------------------ Python binding
+class _Stream:
+    """Stands in for a CUDA stream."""
+
+    def __init__(self, index, handle):
+        self.device, self.cuda_stream = torch.device("cuda", index), handle
+
+
+@pytest.mark.parametrize("handle", [0, 7])
+def test_streams_of_other_devices_are_refused(monkeypatch, handle):
+    """Their kernels would run where the tensors are not; the handle may even be the current stream's (both 0)."""
+    monkeypatch.setattr(mixer, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(mixer, "_device_index", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: s)
+    assert mixer._On(0, _Stream(0, handle), ()).handle == handle
+    with pytest.raises(ValueError, match="stream must be on device cuda:0, not cuda:1"):
+        mixer._On(0, _Stream(1, handle), ())
