@@ -181,11 +181,16 @@ def _dense_out(on, given, name, shape, dtype):
     return given, ptr
 
 
-def _known(grads, names):
-    grads = dict(grads or {})
+def _known(grads, names, **inputs):
+    """The caller's gradient tensors by name.  ``inputs``: for names that depend on it, whether the call has the
+    input (or asks for the gradient): a tensor for another would come back unwritten."""
+    grads = {k: v for k, v in (grads or {}).items() if v is not None or k not in names}
     extra = set(grads) - set(names)
     if extra:
         raise ValueError(f"unknown gradients: {sorted(extra)}")
+    idle = sorted(k for k in grads if not inputs.get(k, True))
+    if idle:
+        raise ValueError(f"gradients that this call does not compute: {idle}")
     return grads
 
 
@@ -227,7 +232,7 @@ def layer_norm_fwd(x, weight=None, bias=None, *, eps=1e-5, y=None, stream=None):
 def layer_norm_bwd(dy, x, weight, mean, rstd, *, bias=True, grads=None, stream=None):
     """Backward of :func:`layer_norm_fwd`: a dict with dx (dtype of x), dweight when weight is
     given, and dbias when ``bias`` is set (both in weight's dtype; x's without a weight).
-    ``grads`` may supply output tensors by those names."""
+    ``grads`` may supply output tensors by the names of those that the call returns."""
     dev = _cuda(x, "x")
     D = x.shape[-1] if x.dim() else 0
     if x.dim() < 1 or x.numel() == 0:
@@ -238,7 +243,7 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, *, bias=True, grads=None, stream=N
     wp, _, wdt = _weights(weight, None, "weight", (D,), D, dev, x.dtype)
     mp = _tensor(mean, "mean", tuple(x.shape[:-1]), torch.float32, dev)
     rp = _tensor(rstd, "rstd", tuple(x.shape[:-1]), torch.float32, dev)
-    out = _known(grads, ("dx", "dweight", "dbias"))
+    out = _known(grads, ("dx", "dweight", "dbias"), dweight=weight is not None, dbias=bias)
     with _On(dev, stream, (x, dy, weight, mean, rstd)) as on:
         out["dx"], dxp, lddx = _out(on, out.get("dx"), "dx", x.shape, x.dtype)
         dwp = dbp = None
@@ -295,7 +300,7 @@ def short_conv_fwd(x, weight, bias=None, h0=None, *, activation="silu", output_f
 def short_conv_bwd(x, weight, bias, h0, dy, dht=None, *, activation="silu", grads=None, cu_seqlens=None, stream=None):
     """Backward of :func:`short_conv_fwd`: a dict with dx, dweight (weight's dtype), dbias when bias is
     given and dh0 when h0 is given.  dht: gradient of ht, or None.  ``grads`` may supply output
-    tensors by those names."""
+    tensors by the names of those that the call returns."""
     dev = _cuda(x, "x")
     if x.dim() != 3:
         raise ValueError("x must be [B, T, D]")
@@ -308,7 +313,7 @@ def short_conv_bwd(x, weight, bias, h0, dy, dht=None, *, activation="silu", grad
     W = weight.shape[1]
     hp = None if h0 is None else _tensor(h0, "h0", (n, W - 1, D), x.dtype, dev)
     dhp = None if dht is None else _tensor(dht, "dht", (n, W - 1, D), x.dtype, dev)
-    out = _known(grads, ("dx", "dweight", "dbias", "dh0"))
+    out = _known(grads, ("dx", "dweight", "dbias", "dh0"), dbias=bias is not None, dh0=h0 is not None)
     with _On(dev, stream, (x, weight, bias, h0, dy, dht, cu_seqlens)) as on:
         out["dx"], dxp, lddx = _out(on, out.get("dx"), "dx", x.shape, x.dtype)
         out["dweight"], dwp = _dense_out(on, out.get("dweight"), "dweight", (D, W), wdt)
@@ -399,7 +404,7 @@ def ssm_scan_bwd(x, delta, A, B, C, D, z, delta_bias, h0, dy, dht=None, *, delta
     """Backward of :func:`ssm_scan_fwd`, whose inputs it takes again: a dict with dx, ddelta, dB, dC
     (dtype of x) and dA (fp32), and dz, dD, ddelta_bias, dh0 for the inputs that are given.
     dy: [B, T, D]; dht: gradient of ht, fp32 [B, D, N] or None.  ``grads`` may supply output tensors by
-    those names."""
+    the names of those that the call returns."""
     dev, code, ch, n, ptrs = _scan_inputs(x, delta, A, B, C, D, z, delta_bias, 3)
     bt, T = x.shape[:2]
     cu, seqs = _sequences(cu_seqlens, bt, dev)
@@ -407,7 +412,8 @@ def ssm_scan_bwd(x, delta, A, B, C, D, z, delta_bias, h0, dy, dht=None, *, delta
     hp = None if h0 is None else _tensor(h0, "h0", (seqs, ch, n), f32, dev)
     dyp = _rows(dy, "dy", x.shape, x.dtype, dev)
     dhp = None if dht is None else _tensor(dht, "dht", (seqs, ch, n), f32, dev)
-    out = _known(grads, ("dx", "ddelta", "dA", "dB", "dC", "dD", "dz", "ddelta_bias", "dh0"))
+    out = _known(grads, ("dx", "ddelta", "dA", "dB", "dC", "dD", "dz", "ddelta_bias", "dh0"), dD=D is not None, dz=z is not None,
+                 ddelta_bias=delta_bias is not None, dh0=h0 is not None)
     with _On(dev, stream, (x, delta, A, B, C, D, z, delta_bias, h0, dy, dht, cu_seqlens)) as on:
         seq = []
         for name, shape in (("dx", x.shape), ("ddelta", x.shape), ("dB", B.shape), ("dC", C.shape)):

@@ -60,3 +60,12 @@ def test_streams_of_other_devices_are_refused(monkeypatch, handle):
     assert mixer._On(0, _Stream(0, handle), ()).handle == handle
     with pytest.raises(ValueError, match="stream must be on device cuda:0, not cuda:1"):
         mixer._On(0, _Stream(1, handle), ())
+
+
+def test_gradients_that_a_call_does_not_compute_are_refused():
+    t = torch.zeros(3)
+    names = ("dx", "dweight", "dbias")
+    assert mixer._known(dict(dx=t, dbias=None), names, dweight=False, dbias=False) == dict(dx=t)
+    assert mixer._known(dict(dx=t, dweight=t), names, dweight=True, dbias=False) == dict(dx=t, dweight=t)
+    with pytest.raises(ValueError, match="does not compute.*dbias"):
+        mixer._known(dict(dx=t, dbias=t), names, dweight=True, dbias=False)

@@ -161,3 +161,23 @@ def test_supplied_outputs_are_not_handed_out_while_the_call_runs():
         new = [torch.empty(v, device=DEV) for v in shapes.values()]
         assert busy and not at & {t.data_ptr() for t in new}, name
         torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------------------------ refusals
+def test_gradient_buffers_without_their_inputs_are_refused():
+    """They would come back in the result as they were."""
+    rn, t = _rand(5, torch.float32)
+    x, w, h, A, bc = t(1, 20, 8), t(8), t(1, 3, 8), -torch.rand(8, 4, device=DEV), t(1, 20, 4)
+    _, mean, rstd = layer_norm_fwd(x, w)
+    norm = lambda **g: layer_norm_bwd(x, x, g.pop("weight", None), mean, rstd, bias=g.pop("bias", False), grads=g)  # noqa: E731
+    conv = lambda **g: short_conv_bwd(x, t(8, 4), None, None, x, grads=g)  # noqa: E731
+    scan = lambda **g: ssm_scan_bwd(x, x, A, bc, bc, None, None, None, None, x, grads=g)  # noqa: E731
+    for call, buffers in ((norm, dict(dweight=w, dbias=w)), (conv, dict(dbias=w, dh0=h)),
+                          (scan, dict(dD=w, ddelta_bias=w, dz=torch.empty_like(x), dh0=t(1, 8, 4)))):
+        given = set(call())
+        for k, v in buffers.items():
+            assert k not in given
+            with pytest.raises(ValueError, match=f"does not compute.*{k}"):
+                call(**{k: v})
+            assert set(call(**{k: None})) == given
+    assert set(norm(weight=w, bias=True, dweight=torch.empty_like(w), dbias=torch.empty_like(w))) == {"dx", "dweight", "dbias"}
