@@ -104,6 +104,8 @@ def _sequences(cu_seqlens, B, device):
     """Pointer to the offsets and the number of sequences."""
     if cu_seqlens is None:
         return None, B
+    if not isinstance(cu_seqlens, torch.Tensor):
+        raise TypeError("cu_seqlens must be a tensor")
     if cu_seqlens.dtype != torch.int32:
         raise TypeError("cu_seqlens must be int32")
     if B != 1 or cu_seqlens.numel() < 2:
@@ -195,7 +197,11 @@ def _known(grads, names, **inputs):
 
 
 def _weights(weight, bias, wname, shape, D, device, default):
-    """Pointers of weight and bias, and their dtype's code."""
+    """Pointers of weight and bias, and their dtype's code.  A weight of two axes (the convolution's) is needed."""
+    if not isinstance(weight, torch.Tensor) and (weight is not None or len(shape) == 2):
+        raise TypeError(f"{wname} must be a tensor")
+    if bias is not None and not isinstance(bias, torch.Tensor):
+        raise TypeError("bias must be a tensor")
     dt = weight.dtype if weight is not None else bias.dtype if bias is not None else default
     if weight is not None and len(shape) == 2 and weight.dim() == 2:
         shape = (D, weight.shape[1])     # [D, W], any W
@@ -337,6 +343,8 @@ def short_conv_step(x, weight, bias, state, *, activation="silu", slots=None, y=
     state b).  A request whose slot lies outside [0, S) is padding: its y is 0, no state changes.
     """
     dev = _cuda(x, "x")
+    if not isinstance(state, torch.Tensor):
+        raise TypeError("state must be a tensor")
     if x.dim() != 2 or state.dim() != 3:
         raise ValueError("x must be [B, D] and state [S, W-1, D]")
     B, D = x.shape
@@ -359,6 +367,8 @@ def _scan_inputs(x, delta, A, B, C, D, z, delta_bias, dims):
     dev = _cuda(x, "x")
     if x.dim() != dims:
         raise ValueError("x must be [B, T, D]" if dims == 3 else "x must be [B, D]")
+    if not isinstance(A, torch.Tensor):
+        raise TypeError("A must be a tensor")
     if A.dim() != 2:
         raise ValueError("A must be [D, N]")
     ch, n = x.shape[-1], A.shape[1]
@@ -448,6 +458,8 @@ def ssm_scan_step(x, delta, A, B, C, state, D=None, z=None, delta_bias=None, *, 
     """
     dev, code, ch, n, ptrs = _scan_inputs(x, delta, A, B, C, D, z, delta_bias, 2)
     bt = x.shape[0]
+    if not isinstance(state, torch.Tensor):
+        raise TypeError("state must be a tensor")
     sp = _tensor(state, "state", (state.shape[0], ch, n) if state.dim() == 3 else (None, ch, n), _F32, dev)
     ip = None if slots is None else _tensor(slots, "slots", (bt,), torch.int32, dev)
     with _On(dev, stream, (x, delta, A, B, C, state, D, z, delta_bias, slots)) as on:

@@ -69,3 +69,15 @@ def test_gradients_that_a_call_does_not_compute_are_refused():
     assert mixer._known(dict(dx=t, dweight=t), names, dweight=True, dbias=False) == dict(dx=t, dweight=t)
     with pytest.raises(ValueError, match="does not compute.*dbias"):
         mixer._known(dict(dx=t, dbias=t), names, dweight=True, dbias=False)
+
+
+def test_arguments_that_are_no_tensors_are_refused_by_name():
+    w = torch.zeros(8, 4)
+    assert mixer._weights(w, None, "weight", (8, None), 8, -1, w.dtype) == (w.data_ptr(), None, w.dtype)
+    assert mixer._weights(None, None, "weight", (8,), 8, -1, w.dtype) == (None, None, w.dtype)
+    for call, name in ((lambda: mixer._weights(None, None, "weight", (8, None), 8, -1, w.dtype), "weight"),
+                       (lambda: mixer._weights([1.0], None, "weight", (1,), 1, -1, w.dtype), "weight"),
+                       (lambda: mixer._weights(w, [1.0], "weight", (8, None), 8, -1, w.dtype), "bias"),
+                       (lambda: mixer._sequences([0, 3], 1, -1), "cu_seqlens"), (lambda: mixer._cuda(None, "x"), "x")):
+        with pytest.raises(TypeError, match=f"{name} must be a tensor"):
+            call()

@@ -181,3 +181,19 @@ def test_gradient_buffers_without_their_inputs_are_refused():
                 call(**{k: v})
             assert set(call(**{k: None})) == given
     assert set(norm(weight=w, bias=True, dweight=torch.empty_like(w), dbias=torch.empty_like(w))) == {"dx", "dweight", "dbias"}
+
+
+def test_arguments_that_are_no_tensors_are_refused_by_name():
+    rn, t = _rand(6, torch.float32)
+    x, w, A, bc = t(1, 20, 8), t(8, 4), -torch.rand(8, 4, device=DEV), t(1, 20, 4)
+    state, scan_state = t(20, 3, 8), t(20, 8, 4)
+    for call, name in ((lambda: mixer.short_conv_fwd(x, None), "weight"), (lambda: short_conv_bwd(x, None, None, None, x), "weight"),
+                       (lambda: short_conv_step(x[0], None, None, state), "weight"), (lambda: short_conv_step(x[0], w, None, None), "state"),
+                       (lambda: mixer.short_conv_fwd(x, w, cu_seqlens=[0, 20]), "cu_seqlens"),
+                       (lambda: ssm_scan_fwd(x, x, None, bc, bc), "A"), (lambda: ssm_scan_fwd(x, x, A, None, bc), "B"),
+                       (lambda: ssm_scan_fwd(x, None, A, bc, bc), "delta"), (lambda: ssm_scan_bwd(x, x, A, bc, bc, None, None, None, None, None), "dy"),
+                       (lambda: mixer.ssm_scan_step(x[0], x[0], A, bc[0], bc[0], None), "state"),
+                       (lambda: layer_norm_fwd(x, [1.0]), "weight"), (lambda: layer_norm_bwd(x, x, None, None, None), "mean")):
+        with pytest.raises(TypeError, match=f"{name} must be a tensor"):
+            call()
+    assert mixer.ssm_scan_step(x[0], x[0], A, bc[0], bc[0], scan_state).shape == (20, 8)
