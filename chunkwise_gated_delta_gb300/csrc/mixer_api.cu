@@ -50,8 +50,9 @@ template <size_t NI, size_t NO> bool blocks_ok(const Block (&in)[NI], const Bloc
     return true;
 }
 
-bool sizes_ok(int B, int T, int D) {
-    return B >= 1 && T >= 1 && D >= 1 && (long long)B * T <= 0x7fffffffLL && (long long)B * D <= (1LL << 40);
+// A packed batch has T rows whatever B is.
+bool sizes_ok(int B, int T, int D, bool packed = false) {
+    return B >= 1 && T >= 1 && D >= 1 && (packed || (long long)B * T <= 0x7fffffffLL) && (long long)B * D <= (1LL << 40);
 }
 
 Block dense(const void *p, long long rows, long long cols, size_t es) { return {p, rows, cols, cols, es}; }
@@ -119,7 +120,7 @@ template <class A> void conv_fill(const A *a, mixer::ConvParams &p) {
 }
 
 kda_status conv_fwd(const short_conv_fwd_args *a, mixer::ConvParams &p) {
-    if (!a || !sizes_ok(a->B, a->T, a->D) || !a->y) return KDA_ERR_INVALID_ARG;
+    if (!a || !sizes_ok(a->B, a->T, a->D, a->cu_seqlens) || !a->y) return KDA_ERR_INVALID_ARG;
     const kda_status st = conv_common(a);
     if (st != KDA_OK) return st;
     conv_fill(a, p);
@@ -134,7 +135,7 @@ kda_status conv_fwd(const short_conv_fwd_args *a, mixer::ConvParams &p) {
 }
 
 kda_status conv_bwd(const short_conv_bwd_args *a, mixer::ConvParams &p, size_t &need) {
-    if (!a || !sizes_ok(a->B, a->T, a->D) || !a->dy || !a->dx) return KDA_ERR_INVALID_ARG;
+    if (!a || !sizes_ok(a->B, a->T, a->D, a->cu_seqlens) || !a->dy || !a->dx) return KDA_ERR_INVALID_ARG;
     const kda_status st = conv_common(a);
     if (st != KDA_OK) return st;
     conv_fill(a, p);
@@ -169,7 +170,7 @@ template <class A> void scan_fill(const A *a, mixer::ScanParams &p) {
 }
 
 kda_status scan_fwd(const ssm_scan_fwd_args *a, mixer::ScanParams &p, size_t &need) {
-    if (!a || !sizes_ok(a->B, a->T, a->D) || !a->y) return KDA_ERR_INVALID_ARG;
+    if (!a || !sizes_ok(a->B, a->T, a->D, a->cu_seqlens) || !a->y) return KDA_ERR_INVALID_ARG;
     const kda_status st = scan_common(a);
     if (st != KDA_OK) return st;
     scan_fill(a, p);
@@ -188,7 +189,7 @@ kda_status scan_fwd(const ssm_scan_fwd_args *a, mixer::ScanParams &p, size_t &ne
 }
 
 kda_status scan_bwd(const ssm_scan_bwd_args *a, mixer::ScanParams &p, size_t &need) {
-    if (!a || !sizes_ok(a->B, a->T, a->D) || !a->dy || !a->dx || !a->ddelta || !a->dBm || !a->dCm || !a->dA)
+    if (!a || !sizes_ok(a->B, a->T, a->D, a->cu_seqlens) || !a->dy || !a->dx || !a->ddelta || !a->dBm || !a->dCm || !a->dA)
         return KDA_ERR_INVALID_ARG;
     if ((a->z == nullptr) != (a->dz == nullptr)) return KDA_ERR_INVALID_ARG;
     const kda_status st = scan_common(a);

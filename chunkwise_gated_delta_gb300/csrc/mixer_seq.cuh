@@ -29,7 +29,7 @@ __host__ __device__ inline long long segment_slots(int B, int T, int seg, bool p
 __host__ __device__ inline int clamped(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
 
 __host__ __device__ inline long long first_slot(const int32_t *cu, int T, int seg, int b) {
-    return b + clamped(cu[b], 0, T) / seg;
+    return (long long)b + clamped(cu[b], 0, T) / seg;
 }
 
 // The segment in slot s.  False for a slot that no sequence uses.

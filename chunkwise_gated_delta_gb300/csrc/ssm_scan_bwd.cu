@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kScanThreads, XV && sizeof(T) == 2 ? 5 : 4) sc
 __global__ void __launch_bounds__(128) scan_boundary_kernel(ScanParams p, int NP) {
     const long long u = (long long)blockIdx.x * 128 + threadIdx.x;
     const long long per = (long long)p.D * NP;
-    const int b = (int)(u / per);
+    const long long b = u / per;
     if (b >= p.B) return;
     const int d = (int)((u - b * per) / NP), n = (int)(u % NP);
     const bool back = blockIdx.y;
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(128) scan_boundary_kernel(ScanParams p, int NP
     int count;
     if (!p.cu_seqlens) {
         count = (int)((p.T + (long long)p.lseg - 1) / p.lseg);
-        s0 = (long long)b * count;
+        s0 = b * count;
     } else {
         const int lo = clamped(p.cu_seqlens[b], 0, p.T), hi = clamped(p.cu_seqlens[b + 1], lo, p.T);
         count = hi > lo ? (int)((hi - lo + (long long)p.lseg - 1) / p.lseg) : 1;
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(128) scan_boundary_kernel(ScanParams p, int NP
     }
     const bool in = n < p.N;
     const float a2 = in ? decay_rate(p.A[(long long)d * p.N + n]) : 0.f;
-    const long long at = ((long long)b * p.D + d) * p.N + n;
+    const long long at = (b * p.D + d) * p.N + n;
     const float *first = back ? p.dht : p.h0;
     float v = in && first ? first[at] : 0.f;
     const long long step = back ? -(long long)p.D : p.D;

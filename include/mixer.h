@@ -22,7 +22,8 @@
  *   - cu_seqlens as in kda_fwd_args: B sequences back to back in [1, T, C] tensors, B + 1
  *     int32 offsets on the device, clamped into [0, T]; empty sequences are allowed (their
  *     final state is their initial one).  Rows that no sequence covers are not written.
- *   - T >= 1, B >= 1 and B T at most 2^31 - 1; KDA_ERR_INVALID_ARG otherwise.
+ *   - T >= 1, B >= 1 and rows (B T, in a packed batch T) at most 2^31 - 1;
+ *     KDA_ERR_INVALID_ARG otherwise.
  *   - Arithmetic is float32 for both dtypes; results are rounded once on output.  Sums
  *     over tokens and channels are added in a fixed order: equal calls give equal bits.
  *   - Nothing waits on the device, so there is no status block; workspaces need no

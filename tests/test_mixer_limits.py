@@ -1,5 +1,6 @@
 """Limits of the operators of include/mixer.h that need no GPU: what the types of the kernels' accesses
 assume, counters near 2^31, sizes that are taken or refused, and the Python binding's refusals."""
+import ctypes
 import os
 import shutil
 import subprocess
@@ -8,7 +9,7 @@ import pytest
 import torch
 
 from chunkwise_gated_delta_gb300 import build as kbuild
-from chunkwise_gated_delta_gb300 import mixer
+from chunkwise_gated_delta_gb300 import _lib, mixer
 
 
 def _nvcc():
@@ -81,3 +82,24 @@ def test_arguments_that_are_no_tensors_are_refused_by_name():
                        (lambda: mixer._sequences([0, 3], 1, -1), "cu_seqlens"), (lambda: mixer._cuda(None, "x"), "x")):
         with pytest.raises(TypeError, match=f"{name} must be a tensor"):
             call()
+
+
+# ------------------------------------------------------------------------------------ sizes
+@pytest.mark.parametrize("name", ["short_conv_bwd", "ssm_scan_bwd"])
+def test_a_packed_batch_has_as_many_rows_as_tokens(name):
+    """2048 sequences in 2^20 packed tokens are 2^20 rows; dense they would be 2^31, one too many.  (Workspace
+    queries, which check the arguments and launch nothing; the addresses are made up.)"""
+    kbuild.build()
+
+    def size(**over):
+        a = _lib.MIXER_EXPORTS[name][0]()
+        for i, (f, t) in enumerate(a._fields_):
+            if t is ctypes.c_void_p and f != "cu_seqlens":
+                setattr(a, f, (i + 1) << 40)
+        for k, v in {**dict(B=2048, T=1 << 20, D=8, W=4, N=16, workspace_bytes=1 << 33), **over}.items():
+            if any(f == k for f, _ in a._fields_):
+                setattr(a, k, v)
+        return getattr(_lib.load(), name + "_workspace")(ctypes.byref(a))
+
+    assert size(cu_seqlens=1 << 30) > 0
+    assert size() == 0 and size(T=(1 << 20) - 1) > 0

@@ -117,6 +117,33 @@ def test_single_tokens_of_more_requests_than_blocks_end_at():
     assert torch.equal(state[:, 0], x)
 
 
+def test_many_sequences_of_many_packed_tokens():
+    """4096 sequences of 256 tokens each, packed: more than 2^31 as a product, 2^20 rows in memory.  Against
+    the same sequences as a dense batch: bit for bit where a sequence is walked alone, in another order of sums
+    over the sequences (relative 1e-4 as in the operators' own tests) for the parameters' gradients."""
+    n, T, D, N = 4096, 256, 8, 4
+    rn, t = _rand(7, torch.float32)
+    x, w, b, dy = t(n, T, D), t(D, 4), t(D), t(n, T, D)
+    delta, A, bc, z = t(n, T, D), -torch.rand(D, N, device=DEV) - 0.5, t(n, T, N), t(n, T, D)
+    cu = torch.arange(n + 1, dtype=torch.int32, device=DEV) * T
+    flat = lambda v: v.reshape(1, n * T, -1)  # noqa: E731
+
+    def run(f, cu):
+        y, ht = mixer.short_conv_fwd(f(x), w, b, cu_seqlens=cu)
+        out = dict(y=y, ht=ht, **short_conv_bwd(f(x), w, b, None, f(dy), cu_seqlens=cu))
+        args = (f(x), f(delta), A, f(bc), f(bc), b, f(z), b, None)
+        out["scan"], out["state"] = ssm_scan_fwd(*args, cu_seqlens=cu)
+        out.update({"scan." + k: v for k, v in ssm_scan_bwd(*args, f(dy), cu_seqlens=cu).items()})
+        return out
+
+    one, two = run(lambda v: v, None), run(flat, cu)
+    for k, v in one.items():
+        if k in ("y", "ht", "dx", "scan", "state", "scan.dx", "scan.ddelta", "scan.dB", "scan.dC", "scan.dz"):
+            assert torch.equal(v.reshape(-1), two[k].reshape(-1)), k
+        else:
+            assert float((v.double() - two[k].double()).norm()) <= 1e-4 * float(v.double().norm()), k
+
+
 # ------------------------------------------------------------------------------------ outputs on other streams
 def _calls(T=2000, D=1024, N=16):
     """Every operator with all of its outputs supplied: (name, names and shapes of the outputs, call)."""
