@@ -176,7 +176,7 @@ kda_status scan_fwd(const ssm_scan_fwd_args *a, mixer::ScanParams &p, size_t &ne
     scan_fill(a, p);
     p.T = a->T; p.h0 = a->h0; p.y = a->y; p.ht = a->ht; p.cu_seqlens = a->cu_seqlens;
     p.ld_y = stride_or(a->ld_y, a->D);
-    need = mixer::ssm_scan_fwd_floats(p) * 4;
+    need = mixer::ssm_scan_fwd_floats(p, a->dtype == KDA_BF16) * 4;
     const long long rows = (long long)(a->cu_seqlens ? 1 : a->B) * a->T, hrows = (long long)a->B * a->D;
     const size_t es = es_of(a->dtype);
     const Block in[] = {{a->x, rows, a->D, p.ld_x, es}, {a->delta, rows, a->D, p.ld_delta, es},
@@ -302,7 +302,7 @@ kda_status ssm_scan_fwd(const ssm_scan_fwd_args *a, kda_stream_t stream) {
     p.seg = a->T;
     if (need && a->workspace && a->workspace_bytes >= need) {
         if (!mixer::aligned_to(a->workspace, 16)) return KDA_ERR_INVALID_ARG;
-        p.seg = mixer::ssm_scan_fwd_segment(p);
+        p.seg = mixer::ssm_scan_fwd_segment(p, a->dtype == KDA_BF16);
         mixer::ssm_scan_fwd_carve(p, static_cast<float *>(a->workspace));
     }
     return from(mixer::launch_ssm_scan_fwd(p, a->dtype == KDA_BF16, stream_of(stream)));

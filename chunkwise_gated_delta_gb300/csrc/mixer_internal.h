@@ -70,10 +70,10 @@ size_t short_conv_part_floats(const ConvParams &p, int W);
 
 cudaError_t launch_ssm_scan_fwd(const ScanParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_ssm_scan_step(const ScanParams &p, bool bf16, cudaStream_t s);
-int ssm_scan_fwd_segment(const ScanParams &p);          // tokens per segment (T: unsplit)
+int ssm_scan_fwd_segment(const ScanParams &p, bool bf16);   // tokens per segment (T: unsplit)
 cudaError_t launch_ssm_scan_bwd(const ScanParams &p, bool bf16, cudaStream_t s);
 // Workspace floats; carve() points the parameter block into a workspace of that size.
-size_t ssm_scan_fwd_floats(const ScanParams &p);
+size_t ssm_scan_fwd_floats(const ScanParams &p, bool bf16);
 size_t ssm_scan_bwd_floats(const ScanParams &p);
 void ssm_scan_fwd_carve(ScanParams &p, float *ws);
 void ssm_scan_bwd_carve(ScanParams &p, float *ws);

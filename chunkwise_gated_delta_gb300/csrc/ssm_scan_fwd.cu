@@ -517,26 +517,43 @@ template <class T> cudaError_t step_type(const ScanParams &p, cudaStream_t s) {
 
 }  // namespace
 
-// Whole sequences, or segments of them side by side where that is expected to be sooner done.  A block takes
-// about 47 ns a token, alone or with the others.  Segments take a local pass over all tokens (0.235 ps per
-// token, channel and state with every SM busy) and two more launches (25 us with the latencies of both).
-// T 16384 with 16 blocks: 750 us whole, 166 in nine; T 2048 with 64 blocks: 97 us whole, 108 in two.
-// The lengths of packed sequences are not known here: one of them may have nearly all tokens.
-int ssm_scan_fwd_segment(const ScanParams &p) {
+// Whole sequences, or segments of them side by side where that is sooner done.  Measured, by type and states of a
+// channel (up to 4, 8, 16, 32): ns that a token takes a block where half-sized (or four-state) blocks are taken and
+// where full ones are (fwd_launch, fwd_type), and ps that the local pass over all tokens takes per token and channel
+// with every SM busy.  Two more launches and the latencies of the local and boundary passes come to 18 us, 4 of
+// which a whole sequence has too.  Both forms, us, at the sizes where two or four segments fit:
+//                     bfloat16                              float32
+//   N 8    B 2 D 2048 T 4096    whole 179, split 127    whole 185, split 158
+//          B 4 D 2048 T 16384   whole 698, split 896    whole 732, split 1100
+//   N 16   B 1 D 2048 T 4096    whole 135, split  88    whole 158, split 111
+//          B 2 D 2048 T 4096    whole 136, split 162    whole 160, split 205
+//   N 32   B 1 D 1024 T 2048    whole 101, split  60    whole 102, split  64
+//          B 1 D 2048 T 16384   whole 866, split 672    whole 851, split 756
+// Over 168 such sizes of each type the choice takes 0.2 % more than the better form of each on average and at
+// most 14 % (of 30 us).  The lengths of packed sequences are not known here: one of them may have nearly all tokens.
+struct ScanCost {
+    double half, full, local;
+};
+constexpr ScanCost kScanCost[2][4] = {{{42.5, 67, 1.9}, {43, 69, 2.35}, {32.5, 44.5, 3.35}, {55, 52, 6.7}},
+                                      {{68, 95, 2.1}, {44.5, 93.5, 2.4}, {38, 61, 3.5}, {55, 63, 6.9}}};
+
+int ssm_scan_fwd_segment(const ScanParams &p, bool bf) {
     const int ch = p.N <= 8 ? 128 : p.N <= 16 ? 64 : 32;
-    const long long cb = (p.D + ch - 1) / ch, batch = p.cu_seqlens ? 1 : p.B;
-    const long long cuts = sm_count() / (cb * batch);
+    const long long cb = (p.D + ch - 1) / ch, batch = p.cu_seqlens ? 1 : p.B, sms = sm_count();
+    const long long cuts = sms / (cb * batch);
     if (cuts < 2) return p.T;
     long long seg = (p.T + cuts - 1) / cuts;
     seg = (seg + kFwdLocal - 1) / kFwdLocal * kFwdLocal;
     if (seg < 256) seg = 256;
-    const double gain = 47.0 * (double)(p.T - seg);
-    const double cost = 25000.0 + 0.235e-3 * (double)batch * p.T * p.D * padded_states(p.N);
-    return gain > cost ? (int)seg : p.T;
+    if (seg >= p.T) return p.T;
+    const ScanCost &c = kScanCost[bf ? 0 : 1][p.N <= 4 ? 0 : p.N <= 8 ? 1 : p.N <= 16 ? 2 : 3];
+    auto walk = [&](int tokens) { return (2 * scan_slots(p, tokens) * cb <= sms ? c.half : c.full) * tokens; };
+    const double whole = 4000.0 + walk(p.T), split = 18000.0 + walk((int)seg) + 1e-3 * c.local * (double)batch * p.T * p.D;
+    return split < whole ? (int)seg : p.T;
 }
 
-size_t ssm_scan_fwd_floats(const ScanParams &p) {
-    if (ssm_scan_fwd_segment(p) >= p.T) return 0;
+size_t ssm_scan_fwd_floats(const ScanParams &p, bool bf) {
+    if (ssm_scan_fwd_segment(p, bf) >= p.T) return 0;
     return (size_t)scan_slots(p, kFwdLocal) * p.D * (padded_states(p.N) + 1);
 }
 

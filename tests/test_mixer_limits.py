@@ -85,21 +85,39 @@ def test_arguments_that_are_no_tensors_are_refused_by_name():
 
 
 # ------------------------------------------------------------------------------------ sizes
+def _workspace(name, **sizes):
+    """The workspace that the library asks for: checks of the arguments and no launch (the addresses are made up)."""
+    kbuild.build()
+    a = _lib.MIXER_EXPORTS[name][0]()
+    for i, (f, t) in enumerate(a._fields_):
+        if t is ctypes.c_void_p and f != "cu_seqlens":
+            setattr(a, f, (i + 1) << 40)
+    for k, v in {**dict(workspace_bytes=1 << 33), **sizes}.items():
+        if any(f == k for f, _ in a._fields_):
+            setattr(a, k, v)
+    return getattr(_lib.load(), name + "_workspace")(ctypes.byref(a))
+
+
 @pytest.mark.parametrize("name", ["short_conv_bwd", "ssm_scan_bwd"])
 def test_a_packed_batch_has_as_many_rows_as_tokens(name):
     """2048 sequences in 2^20 packed tokens are 2^20 rows; dense they would be 2^31, one too many.  (Workspace
     queries, which check the arguments and launch nothing; the addresses are made up.)"""
-    kbuild.build()
-
-    def size(**over):
-        a = _lib.MIXER_EXPORTS[name][0]()
-        for i, (f, t) in enumerate(a._fields_):
-            if t is ctypes.c_void_p and f != "cu_seqlens":
-                setattr(a, f, (i + 1) << 40)
-        for k, v in {**dict(B=2048, T=1 << 20, D=8, W=4, N=16, workspace_bytes=1 << 33), **over}.items():
-            if any(f == k for f, _ in a._fields_):
-                setattr(a, k, v)
-        return getattr(_lib.load(), name + "_workspace")(ctypes.byref(a))
-
+    size = lambda **over: _workspace(name, **{**dict(B=2048, T=1 << 20, D=8, W=4, N=16), **over})  # noqa: E731
     assert size(cu_seqlens=1 << 30) > 0
     assert size() == 0 and size(T=(1 << 20) - 1) > 0
+
+
+_WHOLE_SPLIT = [  # dtype, N, B, D, T and the two forms' times in us on one GB300 (152 SMs)
+    ("bf16", 4, 2, 2048, 4096, 176, 119), ("bf16", 4, 4, 2048, 4096, 179, 219), ("bf16", 8, 1, 2048, 2048, 90, 43), ("bf16", 8, 4, 2048, 16384, 698, 896),
+    ("bf16", 16, 1, 1024, 16384, 527, 161), ("bf16", 16, 1, 2048, 4096, 135, 88), ("bf16", 16, 2, 2048, 2048, 70, 88),
+    ("bf16", 16, 2, 2048, 4096, 136, 162), ("bf16", 16, 2, 2048, 16384, 527, 590), ("bf16", 12, 4, 1216, 8192, 267, 324),
+    ("bf16", 16, 1, 256, 512, 21, 27), ("bf16", 32, 1, 2048, 4096, 221, 181), ("bf16", 32, 2, 1216, 8192, 478, 373),
+    ("f32", 4, 2, 2048, 2048, 144, 90), ("f32", 8, 2, 2048, 4096, 185, 158), ("f32", 8, 4, 2048, 8192, 370, 560), ("f32", 16, 1, 1024, 2048, 82, 43),
+    ("f32", 16, 2, 2048, 16384, 616, 754), ("f32", 16, 4, 1216, 16384, 620, 796), ("f32", 32, 1, 2048, 16384, 851, 756),
+    ("f32", 32, 1, 1024, 1024, 54, 41)]
+
+
+@pytest.mark.parametrize("dtype,N,B,D,T,whole,split", _WHOLE_SPLIT)
+def test_the_scan_is_split_where_that_was_measured_faster(dtype, N, B, D, T, whole, split):
+    code = _lib.KDA_BF16 if dtype == "bf16" else _lib.KDA_F32
+    assert (_workspace("ssm_scan_fwd", B=B, T=T, D=D, N=N, dtype=code) > 0) == (split < whole)
