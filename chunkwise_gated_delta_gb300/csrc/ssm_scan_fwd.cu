@@ -466,12 +466,13 @@ template <class T, int L, int NS, int KT, int WN, bool XV> cudaError_t fwd_start
 }
 
 // 16-byte accesses to x, delta, z and y, and four states of Bm and Cm at a time, where all of them allow it.
+bool fwd_xv(const ScanParams &p, size_t es) {
+    return p.D % 8 == 0 && rows_aligned(p.x, p.ld_x, es, 16) && rows_aligned(p.delta, p.ld_delta, es, 16) &&
+           rows_aligned(p.z, p.ld_z, es, 16) && rows_aligned(p.y, p.ld_y, es, 16) && p.N % 4 == 0 &&
+           rows_aligned(p.Bm, p.ld_B, es, 4 * es) && rows_aligned(p.Cm, p.ld_C, es, 4 * es);
+}
 template <class T, int L, int NS, int KT, int WN> cudaError_t fwd_warps(const ScanParams &p, cudaStream_t s) {
-    const size_t es = sizeof(T);
-    const bool xv = p.D % 8 == 0 && rows_aligned(p.x, p.ld_x, es, 16) && rows_aligned(p.delta, p.ld_delta, es, 16) &&
-                    rows_aligned(p.z, p.ld_z, es, 16) && rows_aligned(p.y, p.ld_y, es, 16) && p.N % 4 == 0 &&
-                    rows_aligned(p.Bm, p.ld_B, es, 4 * es) && rows_aligned(p.Cm, p.ld_C, es, 4 * es);
-    return xv ? fwd_start<T, L, NS, KT, WN, true>(p, s) : fwd_start<T, L, NS, KT, WN, false>(p, s);
+    return fwd_xv(p, sizeof(T)) ? fwd_start<T, L, NS, KT, WN, true>(p, s) : fwd_start<T, L, NS, KT, WN, false>(p, s);
 }
 // Half as many carrier warps to a block where full blocks would leave half of the SMs without one: the same
 // work on twice the SMs (training step B 2, T 2048, D 2048, both with eight states per lane: 382 -> 368 us).
@@ -497,11 +498,13 @@ template <class T> cudaError_t fwd_type(const ScanParams &p, cudaStream_t s) {
     if (p.N <= 4) return fwd_launch<T, 1, 4, 16, 4>(p, s);
     if (p.N <= 8) return fwd_launch<T, 1, 8, 16, 4>(p, s);
     if (p.N <= 16) {
-        // where half-sized blocks are taken (fwd_launch), four states per lane in twice as many carrier warps
-        // are shorter per token: B 2, T 2048, D 2048, bfloat16: 71 us for 81.  (float32: 27 for 24, not taken.)
+        // Where half-sized blocks are taken (fwd_launch), four states per lane in twice as many carrier warps are
+        // shorter per token in bfloat16 with vector accesses: 12.6 us for 14.6 at T 256, 70 for 82 at T 2048, 528 for 619 at
+        // T 16384, from D 64 to B 4, D 1216.  Single elements (N 9: 109 for 99 at T 2048, 1037 for 877 at T 16384) and
+        // float32 (14.6 for 15.5 at T 256, 81 for 82, 616 for 615; D 1000: 86 for 84) are not, and do not take them.
         const long long full = scan_slots(p, p.seg) * ((p.D + 63) / 64);
         if constexpr (sizeof(T) == 2)
-            if (2 * full <= sm_count()) return fwd_warps<T, 4, 4, 8, 4>(p, s);
+            if (2 * full <= sm_count() && fwd_xv(p, sizeof(T))) return fwd_start<T, 4, 4, 8, 4, true>(p, s);
         return fwd_launch<T, 2, 8, 16, 4>(p, s);
     }
     return fwd_launch<T, 4, 8, 16, 4>(p, s);
@@ -530,7 +533,7 @@ template <class T> cudaError_t step_type(const ScanParams &p, cudaStream_t s) {
 //   N 32   B 1 D 1024 T 2048    whole 101, split  60    whole 102, split  64
 //          B 1 D 2048 T 16384   whole 866, split 672    whole 851, split 756
 // Over 168 such sizes of each type the choice takes 0.2 % more than the better form of each on average and at
-// most 14 % (of 30 us).  The lengths of packed sequences are not known here: one of them may have nearly all tokens.
+// most 14 % (of 30 us); over 108 of each with accesses of single elements 0.7 % and at most 13 %.  The lengths of packed sequences are not known here: one of them may have nearly all tokens.
 struct ScanCost {
     double half, full, local;
 };
