@@ -493,7 +493,7 @@ template <class T, int V> cudaError_t bwd_vec(const NormParams &p, cudaStream_t 
     }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !p.part) return e;
-    return launch_sum_rows(p.part, blocks, {p.dweight, p.D, p.w_bf16}, {p.dbias, p.D, p.w_bf16}, {nullptr, 0, false}, s);
+    return launch_sum_rows(p.part, blocks, {p.dweight, p.D, p.w_bf16}, {p.dbias, p.D, p.w_bf16}, s);
 }
 
 }  // namespace
@@ -515,7 +515,7 @@ cudaError_t launch_layer_norm_bwd(const NormParams &p, bool bf, cudaStream_t s) 
     return vec_ok<float>(p) ? bwd_vec<float, 4>(p, s) : bwd_vec<float, 1>(p, s);
 }
 
-size_t layer_norm_part_floats(const NormParams &p, bool) {
+size_t layer_norm_part_floats(const NormParams &p) {
     return few_rows(p) ? 0 : (size_t)bwd_blocks(p.rows) * 2 * p.D;
 }
 

@@ -97,7 +97,7 @@ kda_status norm_bwd(const layer_norm_bwd_args *a, mixer::NormParams &p, size_t &
     p.x = a->x; p.dy = a->dy; p.weight = a->weight; p.y = a->dx;
     p.mean = const_cast<float *>(a->mean); p.rstd = const_cast<float *>(a->rstd);
     p.dweight = a->dweight; p.dbias = a->dbias; p.w_bf16 = a->w_dtype == KDA_BF16;
-    need = a->dweight || a->dbias ? mixer::layer_norm_part_floats(p, a->dtype == KDA_BF16) * 4 : 0;
+    need = a->dweight || a->dbias ? mixer::layer_norm_part_floats(p) * 4 : 0;
     const Block in[] = {{a->x, a->rows, a->D, p.ld_x, es}, {a->dy, a->rows, a->D, p.ld_dy, es},
                         dense(a->weight, 1, a->D, ws), dense(a->mean, 1, a->rows, 4), dense(a->rstd, 1, a->rows, 4)};
     const Block out[] = {{a->dx, a->rows, a->D, p.ld_y, es}, dense(a->dweight, 1, a->D, ws), dense(a->dbias, 1, a->D, ws),

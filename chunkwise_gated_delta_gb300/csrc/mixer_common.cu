@@ -5,8 +5,7 @@ namespace mixer {
 
 // 32 columns x 32 groups of rows per block.  A few MB at most, from L2: bound by latency, so the
 // groups run side by side and each thread keeps four loads in flight.
-__global__ void __launch_bounds__(1024) sum_rows_kernel(const float *part, int rows, long long cols, SumOut o0, SumOut o1,
-                                                        SumOut o2) {
+__global__ void __launch_bounds__(1024) sum_rows_kernel(const float *part, int rows, long long cols, SumOut o0, SumOut o1) {
     __shared__ float sm[32][33];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const long long c = (long long)blockIdx.x * 32 + tx;
@@ -29,21 +28,17 @@ __global__ void __launch_bounds__(1024) sum_rows_kernel(const float *part, int r
     s = warp_sum(sm[tx][ty]);            // warp ty: column ty's 32 groups
     const long long k = (long long)blockIdx.x * 32 + ty;
     if (tx == 0 && k < cols) {
-        long long i = k;
-        if (i < o0.cols) {
-            if (o0.out) store_w(o0.out, i, o0.bf16, s);
-        } else if ((i -= o0.cols) < o1.cols) {
-            if (o1.out) store_w(o1.out, i, o1.bf16, s);
-        } else if (o2.out) {
-            store_w(o2.out, i - o1.cols, o2.bf16, s);
+        if (k < o0.cols) {
+            if (o0.out) store_w(o0.out, k, o0.bf16, s);
+        } else if (o1.out) {
+            store_w(o1.out, k - o0.cols, o1.bf16, s);
         }
     }
 }
 
-cudaError_t launch_sum_rows(const float *part, int rows, SumOut o0, SumOut o1, SumOut o2, cudaStream_t s) {
-    const long long cols = o0.cols + o1.cols + o2.cols;
-    if (cols <= 0) return cudaSuccess;
-    sum_rows_kernel<<<(unsigned)((cols + 31) / 32), 1024, 0, s>>>(part, rows, cols, o0, o1, o2);
+cudaError_t launch_sum_rows(const float *part, int rows, SumOut o0, SumOut o1, cudaStream_t s) {
+    const long long cols = o0.cols + o1.cols;
+    sum_rows_kernel<<<(unsigned)((cols + 31) / 32), 1024, 0, s>>>(part, rows, cols, o0, o1);
     return cudaGetLastError();
 }
 

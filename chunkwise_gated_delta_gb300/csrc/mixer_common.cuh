@@ -249,15 +249,14 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // Sums `rows` rows of partial sums [rows][cols], in row order within each of 32 strided groups,
-// into up to three vectors that lie side by side in a row.
+// into two vectors that lie side by side in a row.
 struct SumOut {
     void *out;          // NULL: not written
     long long cols;
     bool bf16;
 };
-__global__ void __launch_bounds__(1024) sum_rows_kernel(const float *part, int rows, long long cols, SumOut o0, SumOut o1,
-                                                       SumOut o2);
-cudaError_t launch_sum_rows(const float *part, int rows, SumOut o0, SumOut o1, SumOut o2, cudaStream_t s);
+__global__ void __launch_bounds__(1024) sum_rows_kernel(const float *part, int rows, long long cols, SumOut o0, SumOut o1);
+cudaError_t launch_sum_rows(const float *part, int rows, SumOut o0, SumOut o1, cudaStream_t s);
 
 // Streaming multiprocessors of the current device (152 if the query fails: sizes only).
 int sm_count();

@@ -61,7 +61,7 @@ struct ScanParams {
 
 cudaError_t launch_layer_norm_fwd(const NormParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_layer_norm_bwd(const NormParams &p, bool bf16, cudaStream_t s);
-size_t layer_norm_part_floats(const NormParams &p, bool bf16);
+size_t layer_norm_part_floats(const NormParams &p);
 
 cudaError_t launch_short_conv_fwd(const ConvParams &p, int W, bool bf16, cudaStream_t s);
 cudaError_t launch_short_conv_bwd(const ConvParams &p, int W, bool bf16, cudaStream_t s);

@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(128, kBwdBlocks) conv_bwd_kernel(ConvParams p,
         int t = 0;
         if (g.len > 0) edge(0);
         // inside, with nothing to ask for: positions t - (W - 1) .. are this segment's, and before the final state's
-        for (t = 4; t + 4 <= g.len && g.t0 + t + 4 <= g.total; t += 4) {
+        for (t = 4; t + 4 <= g.len; t += 4) {
             four();
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -435,7 +435,7 @@ cudaError_t launch_short_conv_bwd(const ConvParams &q, int W, bool bf, cudaStrea
     if (e != cudaSuccess || !p.part) return e;
     const long long slots = segment_slots(p.B, p.T, p.seg, p.cu_seqlens != nullptr);
     return launch_sum_rows(p.part, (int)((slots + 3) / 4), {p.dweight, (long long)p.D * W, p.w_bf16},
-                           {p.dbias, p.D, p.w_bf16}, {nullptr, 0, false}, s);
+                           {p.dbias, p.D, p.w_bf16}, s);
 }
 
 cudaError_t launch_short_conv_step(const ConvParams &q, int W, bool bf, cudaStream_t s) {
