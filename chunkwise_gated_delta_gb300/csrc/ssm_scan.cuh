@@ -1,7 +1,9 @@
 // Pieces shared by the scan's forward, backward and single-token kernels.
 //
-// A channel's N states are spread over L lanes, four states each (L = 1, 2, 4 or 8 for N up to
-// 4, 8, 16 or 32; absent states have A = B = C = 0 and stay 0).  A warp holds 32 / L channels.
+// A channel's N states are spread over L lanes, a warp holds 32 / L channels; absent states have A = B = C = 0 and
+// stay 0.  Single tokens and the gradient pass have four states per lane (L = 1, 2, 4 or 8 for N up to
+// 4, 8, 16 or 32; the gradient pass 4 or 8), the forward and the local pass eight (four for N up to 4, and
+// in the forward of few bfloat16 blocks).
 #pragma once
 
 #include "mixer_common.cuh"

@@ -63,9 +63,9 @@ template <class T, bool XV> __device__ __forceinline__ void store_four(T *p, con
     }
 }
 
-// Local pass.  A block: 128 / L channels, a lane NS states of one of them.  Per 32 tokens, first dt, dt x
-// and g of all channels into shared memory (four channels per access), then the recurrences.  Four
-// blocks to an SM cover each other's phases.
+// Local pass.  A block: 128 / L channels, a lane NS states of one of them.  Per 16 tokens, first dt, dt x
+// and g of all channels into shared memory (four channels per access), then the recurrences.  Five
+// blocks to an SM (four in float32 and with single elements) cover each other's phases.
 template <int L, int NS> struct LocalTiles {
     static constexpr int TT = 16, CH = kScanThreads / L, NP = NS * L;
     f2x2 d[TT][CH];                  // {dt, dt}, {dt x, dt x}; columns swizzled, see at()

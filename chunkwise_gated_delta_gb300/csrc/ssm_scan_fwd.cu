@@ -15,7 +15,7 @@ namespace mixer {
 namespace {
 
 // A block: WN warps that carry the states (32 / L channels each, NS states of a channel per lane) and
-// twice as many that feed them.  Per tile of KT L tokens
+// KT / 8 times as many that feed them (twice, with four of 16 states per lane as many).  Per tile of KT L tokens
 //   the feeders   bring x, delta, z (8 neighbouring channels of one token per thread, three tiles ahead) and
 //                 Bm, Cm into shared memory or registers, turn the next tile's delta into dt and leave
 //                 {dt, dt, dt x, dt x} and float32 Bm, Cm in shared memory, and finish the last tile's

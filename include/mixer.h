@@ -16,9 +16,12 @@
  *   - Sequence tensors are [B, T, C] with C fastest and a row stride in elements of their
  *     own, ld_* (0: contiguous; otherwise at least C): row t of sequence b begins at
  *     element (b T + t) ld, so the parts of a wider projection's output are used where
- *     they lie.  Every pointer is aligned to its element; data aligned to 16 bytes (base
- *     and row stride, C a multiple of 8) moves in 16-byte accesses, other data in
- *     narrower ones.  The workspaces are 16-byte aligned.
+ *     they lie.  Every pointer is aligned to its element.  Where the base and row stride of
+ *     every tensor of a call are multiples of 16 bytes and C is one of 8 elements, data moves
+ *     in accesses of 8 or 16 bytes, otherwise in single elements or, where it is aligned to
+ *     four of them, in fours (convolution's and scan's backward, single tokens).  The
+ *     scan's forward asks for N, base and stride of Bm and Cm in multiples of four elements
+ *     too, and moves everything by single elements without.  Workspaces are 16-byte aligned.
  *   - cu_seqlens as in kda_fwd_args: B sequences back to back in [1, T, C] tensors, B + 1
  *     int32 offsets on the device, clamped into [0, T]; empty sequences are allowed (their
  *     final state is their initial one).  Rows that no sequence covers are not written.
