@@ -8,7 +8,7 @@
 // tokens with the last W - 1 inputs in registers, so every row is read once (and the W - 1 rows
 // before a segment once more).  The forward is bound by HBM (B 8, T 2048, D 4096, four taps, bfloat16:
 // 47 us, 5.7 TB/s), the backward by instructions and the loads' latency: its taps, window and sums leave
-// 16 warps to an SM, their rows on the way in shared memory (8191 x 2048: 28 us, 3.6 TB/s).
+// 16 warps to an SM, their rows on the way in shared memory (8191 x 2048: 29 us, 3.5 TB/s).
 #include "mixer_common.cuh"
 #include "mixer_internal.h"
 

@@ -17,7 +17,7 @@
 // The gradient pass walks two groups of channels per 8-token part, so the sums of dB and dC over
 // channels gather in registers and cross lanes once per part.
 //
-// B 2, T 2048, D 2048, N 16, bfloat16: local pass 56 us, boundary 11, gradients 180, sums 12.  The gradient
+// B 2, T 2048, D 2048, N 16, bfloat16: local pass 56 us, boundary 11, gradients 181, sums 12.  The gradient
 // pass is bound by instructions: 26 per (token, channel, state) in half of the issue slots, 8 warps to
 // an SM by registers (255) and shared memory (108 KB a block).
 #include "ssm_scan.cuh"

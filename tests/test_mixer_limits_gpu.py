@@ -170,7 +170,7 @@ def _calls(T=2000, D=1024, N=16):
 
 
 def test_supplied_outputs_are_not_handed_out_while_the_call_runs():
-    """The call waits on its stream behind 50 ms of other work; the outputs' memory, given up by the caller
+    """The call waits on its stream behind a quarter of a second of other work; the outputs' memory, given up by the caller
     meanwhile, must not come back from the allocator."""
     side = torch.cuda.Stream()
     for name, shapes, call in _calls():
@@ -181,7 +181,7 @@ def test_supplied_outputs_are_not_handed_out_while_the_call_runs():
         at = {t.data_ptr() for t in out.values()}
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):
-            torch.cuda._sleep(100_000_000)
+            torch.cuda._sleep(500_000_000)
         res = call(dict(out), side)
         busy = not side.query()
         del out, res
