@@ -154,6 +154,58 @@ class SsmScanStepArgs(ctypes.Structure):
                 ("y", _P), ("ld_y", _L)]
 
 
+GATED_SCAN_STATE_ROWS = 32
+GROUP_NORM_FLAG_CENTER = 1
+GROUP_NORM_FLAG_SHARED = 2
+GLU_FLAG_GELU = 1
+
+
+class GatedScanFwdArgs(ctypes.Structure):
+    _fields_ = [("B", _I), ("T", _I), ("D", _I), ("dtype", _I), ("scale", _F), ("x", _P), ("ld_x", _L), ("decay", _P),
+                ("ld_decay", _L), ("gate", _P), ("ld_gate", _L), ("rate", _P), ("h0", _P), ("y", _P), ("ld_y", _L),
+                ("ht", _P), ("states", _P), ("cu_seqlens", _P)]
+
+
+class GatedScanBwdArgs(ctypes.Structure):
+    _fields_ = [("B", _I), ("T", _I), ("D", _I), ("dtype", _I), ("scale", _F), ("x", _P), ("ld_x", _L), ("decay", _P),
+                ("ld_decay", _L), ("gate", _P), ("ld_gate", _L), ("rate", _P), ("h0", _P), ("dy", _P), ("ld_dy", _L),
+                ("dht", _P), ("states", _P), ("dx", _P), ("ld_dx", _L), ("ddecay", _P), ("ld_ddecay", _L),
+                ("dgate", _P), ("ld_dgate", _L), ("drate", _P), ("dh0", _P), ("workspace", _P),
+                ("workspace_bytes", _Z), ("cu_seqlens", _P)]
+
+
+class GatedScanStepArgs(ctypes.Structure):
+    _fields_ = [("B", _I), ("D", _I), ("slots", _I), ("dtype", _I), ("scale", _F), ("x", _P), ("ld_x", _L),
+                ("decay", _P), ("ld_decay", _L), ("gate", _P), ("ld_gate", _L), ("rate", _P), ("state", _P),
+                ("slot", _P), ("y", _P), ("ld_y", _L)]
+
+
+class GroupNormFwdArgs(ctypes.Structure):
+    _fields_ = [("rows", _L), ("groups", _I), ("C", _I), ("dtype", _I), ("w_dtype", _I), ("flags", _U), ("eps", _F),
+                ("x", _P), ("ld_x", _L), ("gate", _P), ("ld_gate", _L), ("weight", _P), ("bias", _P), ("y", _P),
+                ("ld_y", _L), ("mean", _P), ("rstd", _P)]
+
+
+class GroupNormBwdArgs(ctypes.Structure):
+    _fields_ = [("rows", _L), ("groups", _I), ("C", _I), ("dtype", _I), ("w_dtype", _I), ("flags", _U), ("dy", _P),
+                ("ld_dy", _L), ("x", _P), ("ld_x", _L), ("gate", _P), ("ld_gate", _L), ("weight", _P), ("bias", _P),
+                ("mean", _P), ("rstd", _P), ("dx", _P), ("ld_dx", _L), ("dgate", _P), ("ld_dgate", _L),
+                ("dweight", _P), ("dbias", _P), ("workspace", _P), ("workspace_bytes", _Z)]
+
+
+class GluFwdArgs(ctypes.Structure):
+    _fields_ = [("rows", _L), ("D", _I), ("F", _I), ("dtype", _I), ("flags", _U), ("x", _P), ("ld_x", _L),
+                ("w_gate", _P), ("ld_w_gate", _L), ("w_up", _P), ("ld_w_up", _L), ("h", _P), ("ld_h", _L), ("g", _P),
+                ("u", _P)]
+
+
+class GluBwdArgs(ctypes.Structure):
+    _fields_ = [("rows", _L), ("D", _I), ("F", _I), ("dtype", _I), ("flags", _U), ("x", _P), ("ld_x", _L),
+                ("w_gate", _P), ("ld_w_gate", _L), ("w_up", _P), ("ld_w_up", _L), ("dh", _P), ("ld_dh", _L),
+                ("g", _P), ("u", _P), ("dx", _P), ("ld_dx", _L), ("dw_gate", _P), ("ld_dw_gate", _L), ("dw_up", _P),
+                ("ld_dw_up", _L), ("workspace", _P), ("workspace_bytes", _Z)]
+
+
 # Every symbol include/mixer.h declares, with its argument block and whether it takes a stream
 # (launches) or answers a size (workspace queries).
 MIXER_EXPORTS = {
@@ -169,6 +221,16 @@ MIXER_EXPORTS = {
     "ssm_scan_bwd_workspace": (SsmScanBwdArgs, False),
     "ssm_scan_bwd": (SsmScanBwdArgs, True),
     "ssm_scan_step": (SsmScanStepArgs, True),
+    "gated_scan_fwd": (GatedScanFwdArgs, True),
+    "gated_scan_bwd_workspace": (GatedScanBwdArgs, False),
+    "gated_scan_bwd": (GatedScanBwdArgs, True),
+    "gated_scan_step": (GatedScanStepArgs, True),
+    "group_norm_fwd": (GroupNormFwdArgs, True),
+    "group_norm_bwd_workspace": (GroupNormBwdArgs, False),
+    "group_norm_bwd": (GroupNormBwdArgs, True),
+    "glu_fwd": (GluFwdArgs, True),
+    "glu_bwd_workspace": (GluBwdArgs, False),
+    "glu_bwd": (GluBwdArgs, True),
 }
 
 

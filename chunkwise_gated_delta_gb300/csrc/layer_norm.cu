@@ -69,14 +69,6 @@ __device__ __forceinline__ void block_sums(float (&v)[N], float (*sm)[N]) {
     for (int k = 0; k < N; ++k) v[k] = __shfl_sync(~0u, t, k);
 }
 
-// 1 / sqrt(v): the approximate function and one step of Newton's method, off by about one unit in the last
-// place; a division after a square root takes thirty instructions per row and thread.
-__device__ __forceinline__ float inv_sqrt(float v) {
-    const float r = rsqrtf(v);
-    const float n = fmaf(-0.5f * v * r, r, 0.5f);
-    return v > 0.f && r > 0.f ? fmaf(r, n, r) : r;      // (0 and infinity: the function's own infinity and 0)
-}
-
 // Short rows: one per warp, lane i with vectors i and i + 32.
 template <class T, int V, int ITEMS>
 __global__ void __launch_bounds__(128) norm_fwd_warp_kernel(NormParams p) {

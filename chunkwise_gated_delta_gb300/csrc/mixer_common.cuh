@@ -248,6 +248,14 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+// 1 / sqrt(v): the approximate function and one step of Newton's method, off by about one unit in the last
+// place; a division after a square root takes thirty instructions per row and thread.
+__device__ __forceinline__ float inv_sqrt(float v) {
+    const float r = rsqrtf(v);
+    const float n = fmaf(-0.5f * v * r, r, 0.5f);
+    return v > 0.f && r > 0.f ? fmaf(r, n, r) : r;      // (0 and infinity: the function's own infinity and 0)
+}
+
 // Sums `rows` rows of partial sums [rows][cols], in row order within each of 32 strided groups,
 // into two vectors that lie side by side in a row.
 struct SumOut {

@@ -59,6 +59,48 @@ struct ScanParams {
     const int32_t *slot;
 };
 
+struct GatedScanParams {
+    int B, T, D;
+    int chains, cluster;              // grid: chains of sequences side by side, blocks that share a chain
+    float scale;
+    const void *x, *decay, *gate, *dy;
+    long long ld_x, ld_decay, ld_gate, ld_y, ld_dy, ld_dx, ld_ddecay, ld_dgate;
+    const float *rate, *h0, *dht;
+    void *y, *dx, *ddecay, *dgate;
+    float *ht, *states;               // states: [ceil(rows / 32)][D], the state that enters each 32nd row
+    float *drate, *dh0, *part;        // part: [chains cluster][D]
+    const int32_t *cu_seqlens;
+    // single tokens
+    int slots;
+    float *state;
+    const int32_t *slot;
+};
+
+struct GroupNormParams {
+    long long rows;
+    int G, C;                         // groups of a row, columns of a group
+    float eps;
+    bool center, shared, w_bf16;      // shared: one weight [C] for all groups, else [G C]
+    const void *x, *gate, *dy, *weight, *bias;
+    long long ld_x, ld_gate, ld_dy, ld_y, ld_dgate;   // ld_y: of y, or of dx in the backward
+    void *y, *dgate;                  // y: y or dx
+    float *mean, *rstd;
+    void *dweight, *dbias;
+    float *part;
+};
+
+struct GluParams {
+    long long M;
+    int D, F;
+    bool gelu;
+    const void *x, *wg, *wu, *dh;
+    long long ld_x, ld_wg, ld_wu, ld_dh, ld_h, ld_dx, ld_dwg, ld_dwu;
+    void *h, *dx, *dwg, *dwu;
+    float *g, *u;                     // [M][F] the two products, or NULL
+    void *dg, *du;                    // workspace [M][ld_d]: their gradients
+    long long ld_d;
+};
+
 cudaError_t launch_layer_norm_fwd(const NormParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_layer_norm_bwd(const NormParams &p, bool bf16, cudaStream_t s);
 size_t layer_norm_part_floats(const NormParams &p);
@@ -77,5 +119,19 @@ size_t ssm_scan_fwd_floats(const ScanParams &p, bool bf16);
 size_t ssm_scan_bwd_floats(const ScanParams &p);
 void ssm_scan_fwd_carve(ScanParams &p, float *ws);
 void ssm_scan_bwd_carve(ScanParams &p, float *ws);
+
+cudaError_t launch_gated_scan_fwd(const GatedScanParams &p, bool bf16, cudaStream_t s);
+cudaError_t launch_gated_scan_bwd(const GatedScanParams &p, bool bf16, cudaStream_t s);
+cudaError_t launch_gated_scan_step(const GatedScanParams &p, bool bf16, cudaStream_t s);
+size_t gated_scan_saved_rows(const GatedScanParams &p);
+size_t gated_scan_part_floats(const GatedScanParams &p);
+
+cudaError_t launch_group_norm_fwd(const GroupNormParams &p, bool bf16, cudaStream_t s);
+cudaError_t launch_group_norm_bwd(const GroupNormParams &p, bool bf16, cudaStream_t s);
+size_t group_norm_part_floats(const GroupNormParams &p, bool bf16);
+
+cudaError_t launch_glu_fwd(const GluParams &p, bool bf16, cudaStream_t s);
+cudaError_t launch_glu_bwd(const GluParams &p, bool bf16, cudaStream_t s);
+long long glu_grad_stride(const GluParams &p, bool bf16);
 
 }  // namespace mixer

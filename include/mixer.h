@@ -1,13 +1,21 @@
 /*
  * mixer.h -- C ABI of the operators that stand around a recurrent token mixer
- * (GB300, sm_103a): layer norm, the short causal convolution, and the selective
- * state-space scan.  The pages behind kda.h do not treat them; the definitions are:
+ * (GB300, sm_103a): layer norm, the short causal convolution, the selective
+ * state-space scan, the gated recurrence, the gated norm over a mixer's heads, and
+ * the gated feed-forward product.  The pages behind kda.h do not treat them; the
+ * definitions are:
  *
  *   layer norm   y = (x - mean) rstd weight + bias,  rstd = 1 / sqrt(var + eps), per row
  *   convolution  y_t[d] = act(bias[d] + sum_j weight[d][j] x_{t-W+1+j}[d]),  act: none or SiLU
  *   scan         dt_t[d] = softplus(delta_t[d] + delta_bias[d])   (or delta + bias itself)
  *                h_t[d][n] = exp(dt_t[d] A[d][n]) h_{t-1}[d][n] + dt_t[d] x_t[d] Bm_t[n]
  *                y_t[d] = (sum_n Cm_t[n] h_t[d][n] + D[d] x_t[d]) SiLU(z_t[d])
+ *
+ *   recurrence   q_t = scale softplus(rate) sigmoid(decay_t),  a_t = exp(-q_t),
+ *                h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(gate_t) x_t,  y_t = h_t, per channel
+ *   group norm   n = (x - mean) rstd weight + bias over each group of C neighbouring columns of a row
+ *                (uncentred: x / sqrt(mean(x^2) + eps) weight + bias),  y = n SiLU(gate)
+ *   feed-forward h = act(x w_gate^T) (x w_up^T),  act: SiLU or GELU (with the normal distribution itself)
  *
  * The scan's decay depends on channel and state together, so it has no chunkwise matrix
  * form like the one kda_chunk_fwd evaluates.
@@ -275,6 +283,210 @@ typedef struct {
 
 /* One token of each request. */
 kda_status ssm_scan_step(const ssm_scan_step_args *args, kda_stream_t stream);
+
+/* ------------------------------------------------------------ gated recurrence */
+
+#define GATED_SCAN_STATE_ROWS 32
+
+typedef struct {
+    int B, T, D;           /* sequences, tokens, channels */
+    kda_dtype dtype;       /* of x, decay, gate, y */
+    float scale;           /* > 0, finite */
+    const void *x;         /* [B, T, D] */
+    long long ld_x;
+    const void *decay;     /* [B, T, D], before the sigmoid */
+    long long ld_decay;
+    const void *gate;      /* [B, T, D], before the sigmoid */
+    long long ld_gate;
+    const float *rate;     /* [D], before the softplus */
+    const float *h0;       /* [B, D], or NULL (0) */
+    void *y;               /* [B, T, D] out */
+    long long ld_y;
+    float *ht;             /* [B, D] out, or NULL */
+    float *states;         /* [ceil(rows / GATED_SCAN_STATE_ROWS), D] out, rows as they lie (B T, packed: T): the state that
+                              enters every 32nd row, for gated_scan_bwd; or NULL (not kept) */
+    const int32_t *cu_seqlens;
+} gated_scan_fwd_args;
+
+kda_status gated_scan_fwd(const gated_scan_fwd_args *args, kda_stream_t stream);
+
+typedef struct {
+    int B, T, D;
+    kda_dtype dtype;       /* of the sequence tensors and their gradients */
+    float scale;
+    const void *x;
+    long long ld_x;
+    const void *decay;
+    long long ld_decay;
+    const void *gate;
+    long long ld_gate;
+    const float *rate, *h0;    /* as the forward's */
+    const void *dy;        /* [B, T, D] gradient of y */
+    long long ld_dy;
+    const float *dht;      /* [B, D] gradient of the final state, or NULL (zero) */
+    const float *states;   /* the forward's, or NULL (computed again) */
+    void *dx;              /* [B, T, D] out */
+    long long ld_dx;
+    void *ddecay;          /* [B, T, D] out */
+    long long ld_ddecay;
+    void *dgate;           /* [B, T, D] out */
+    long long ld_dgate;
+    float *drate;          /* [D] out */
+    float *dh0;            /* [B, D] out, or NULL */
+    void *workspace;       /* gated_scan_bwd_workspace bytes */
+    size_t workspace_bytes;
+    const int32_t *cu_seqlens;
+} gated_scan_bwd_args;
+
+/* Bytes of workspace (0 on bad args): partial sums of drate, and the states where the caller has none. */
+size_t gated_scan_bwd_workspace(const gated_scan_bwd_args *args);
+
+/*
+ * Gradients of sum(y dy) + sum(ht dht).  With G_t the gradient of h_t, m = sqrt(1 - a^2), s = sigmoid(decay),
+ * u = sigmoid(gate):
+ *     G_t = dy_t + a_{t+1} G_{t+1},  dq = G (u x a^2 / m - a h_{t-1}),
+ *     ddecay = dq q (1 - s),  drate = scale sigmoid(rate) sum_t dq s,
+ *     dx = G m u,  dgate = G m x u (1 - u),  dh0 = a G of the first token.
+ * Where a rounds to exactly 1 (q = 0), a^2 / m counts as a finite number and ddecay is 0.
+ */
+kda_status gated_scan_bwd(const gated_scan_bwd_args *args, kda_stream_t stream);
+
+typedef struct {
+    int B, D;              /* requests (one token each), channels */
+    int slots;             /* states in `state` */
+    kda_dtype dtype;
+    float scale;
+    const void *x;         /* [B, D] */
+    long long ld_x;
+    const void *decay;     /* [B, D] */
+    long long ld_decay;
+    const void *gate;      /* [B, D] */
+    long long ld_gate;
+    const float *rate;
+    float *state;          /* [slots, D], updated in place */
+    const int32_t *slot;   /* [B] device or NULL: as short_conv_step_args */
+    void *y;               /* [B, D] out */
+    long long ld_y;
+} gated_scan_step_args;
+
+/* One token of each request. */
+kda_status gated_scan_step(const gated_scan_step_args *args, kda_stream_t stream);
+
+/* ------------------------------------------------------------ norm over groups */
+
+#define GROUP_NORM_FLAG_CENTER 1u    /* subtract the group's mean */
+#define GROUP_NORM_FLAG_SHARED 2u    /* weight and bias are [C], the same for every group; cleared: [groups C] */
+
+typedef struct {
+    long long rows;        /* >= 1; rows groups at most 2^31 - 1 */
+    int groups, C;         /* groups of a row, columns of a group; groups C at most 2^31 - 1 */
+    kda_dtype dtype;       /* of x, gate and y */
+    kda_dtype w_dtype;     /* of weight and bias */
+    unsigned flags;        /* GROUP_NORM_FLAG_* */
+    float eps;             /* >= 0 */
+    const void *x;         /* [rows, groups C] */
+    long long ld_x;
+    const void *gate;      /* [rows, groups C], or NULL (no gate) */
+    long long ld_gate;
+    const void *weight;    /* or NULL (1) */
+    const void *bias;      /* or NULL (0) */
+    void *y;               /* [rows, groups C] out */
+    long long ld_y;
+    float *mean;           /* [rows, groups] out, or NULL (not written; NULL without a centre) */
+    float *rstd;           /* [rows, groups] out, or NULL (not written) */
+} group_norm_fwd_args;
+
+kda_status group_norm_fwd(const group_norm_fwd_args *args, kda_stream_t stream);
+
+typedef struct {
+    long long rows;
+    int groups, C;
+    kda_dtype dtype;       /* of dy, x, gate, dx and dgate */
+    kda_dtype w_dtype;     /* of weight, bias, dweight and dbias */
+    unsigned flags;
+    const void *dy;        /* [rows, groups C] */
+    long long ld_dy;
+    const void *x;
+    long long ld_x;
+    const void *gate;      /* or NULL */
+    long long ld_gate;
+    const void *weight, *bias;   /* as the forward's */
+    const float *mean;     /* [rows, groups], from group_norm_fwd; NULL iff the flag of the centre is cleared */
+    const float *rstd;     /* [rows, groups], from group_norm_fwd */
+    void *dx;              /* [rows, groups C] out */
+    long long ld_dx;
+    void *dgate;           /* [rows, groups C] out; NULL iff gate is NULL */
+    long long ld_dgate;
+    void *dweight, *dbias; /* as weight and bias, out, or NULL (not written) */
+    void *workspace;       /* group_norm_bwd_workspace bytes */
+    size_t workspace_bytes;
+} group_norm_bwd_args;
+
+/* Bytes of workspace: partial sums of dweight and dbias (0 on bad args and where neither is asked for). */
+size_t group_norm_bwd_workspace(const group_norm_bwd_args *args);
+
+/*
+ * With xh = (x - mean) rstd, d = dy SiLU(gate) and e = d weight:
+ *     dx = rstd (e - mean_group(e) - xh mean_group(e xh))  (uncentred: without mean_group(e)),
+ *     dweight = sum d xh,  dbias = sum d  (over rows; shared: over groups too),  dgate = dy n SiLU'(gate).
+ */
+kda_status group_norm_bwd(const group_norm_bwd_args *args, kda_stream_t stream);
+
+/* ------------------------------------------------- gated feed-forward product */
+
+#define GLU_FLAG_GELU 1u    /* act(g) = g Phi(g); cleared: g sigmoid(g) */
+
+typedef struct {
+    long long rows;        /* >= 1 */
+    int D, F;              /* columns of x, rows of the weights */
+    kda_dtype dtype;       /* of x, w_gate, w_up and h */
+    unsigned flags;        /* GLU_FLAG_* */
+    const void *x;         /* [rows, D] */
+    long long ld_x;
+    const void *w_gate;    /* [F, D] */
+    long long ld_w_gate;
+    const void *w_up;      /* [F, D] */
+    long long ld_w_up;
+    void *h;               /* [rows, F] out */
+    long long ld_h;
+    float *g, *u;          /* [rows, F] out, the two products for glu_bwd; or both NULL (not kept) */
+} glu_fwd_args;
+
+kda_status glu_fwd(const glu_fwd_args *args, kda_stream_t stream);
+
+typedef struct {
+    long long rows;
+    int D, F;
+    kda_dtype dtype;       /* of x, the weights, dh and the gradients */
+    unsigned flags;
+    const void *x;
+    long long ld_x;
+    const void *w_gate;
+    long long ld_w_gate;
+    const void *w_up;
+    long long ld_w_up;
+    const void *dh;        /* [rows, F] gradient of h */
+    long long ld_dh;
+    const float *g, *u;    /* the forward's, or both NULL (computed again) */
+    void *dx;              /* [rows, D] out */
+    long long ld_dx;
+    void *dw_gate;         /* [F, D] out */
+    long long ld_dw_gate;
+    void *dw_up;           /* [F, D] out */
+    long long ld_dw_up;
+    void *workspace;       /* glu_bwd_workspace bytes */
+    size_t workspace_bytes;
+} glu_bwd_args;
+
+/* Bytes of workspace (0 on bad args): the gradients of the two products. */
+size_t glu_bwd_workspace(const glu_bwd_args *args);
+
+/*
+ *     dg = dh u act'(g),  du = dh act(g);  dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x.
+ * dg and du are rounded to the call's dtype once (they are operands of the products that follow); g and u are
+ * float32 here for that reason: rounded too, they would add as much error again.
+ */
+kda_status glu_bwd(const glu_bwd_args *args, kda_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,252 @@
+"""Gated recurrence on the GPU against its definition in float64: forward, gradients, single tokens, packed batches,
+sequences cut anywhere in a tile, strides, infinities, streams and graphs."""
+import pytest
+import torch
+
+import chunkwise_gated_delta_gb300 as lib
+import layer_ref as ref
+from mixer_ref import half_step, rel, spans_of
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+SCALE = 8.0
+
+# A state carries a product of up to n = 1 / (1 - a) decays, here a <= 0.9995 where its gate is half open or more, so n of at
+# most 2000; each decay is off by its rounding (2^-24) and by the exponent's relative error (sigmoid's exponential,
+# sum, reciprocal, two products: 6 roundings) times -log a, which over n decays adds up to 6 roundings in all.  The
+# roundings of a add up as sqrt(n) of independent ones, 45, and at most 2^-24 * 2000 = 1.2e-4 should all of them point one way; the
+# bound here takes 8 times the independent sum.
+STATE = (8 * 45 + 6) * 2.0 ** -24
+
+
+def tol(dtype):
+    return STATE if dtype == torch.float32 else half_step(dtype) + STATE
+
+
+def make(rows, n, D, dtype, seed=0, slow=False, h0=True):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    rn = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    s = dict(x=rn(rows, D).to(dtype), decay=rn(rows, D).to(dtype), gate=rn(rows, D).to(dtype), rate=rn(D) - (6 if slow else 1),
+             h0=rn(n, D) if h0 else None, dy=rn(rows, D).to(dtype), dht=rn(n, D))
+    return s
+
+
+def definition(s, spans, grads=False):
+    f = {k: v.double().requires_grad_(grads and k not in ("dy", "dht")) for k, v in s.items() if v is not None}
+    y, ht = ref.gated_scan(f["x"], f["decay"], f["gate"], f["rate"], f.get("h0"), spans, SCALE)
+    out = {"y": y, "ht": ht}
+    if grads:
+        names = [k for k in ("x", "decay", "gate", "rate", "h0") if k in f]
+        loss = sum((y[lo:hi] * f["dy"][lo:hi]).sum() for lo, hi in spans) + (ht * f["dht"]).sum()
+        got = torch.autograd.grad(loss, [f[k] for k in names], allow_unused=True)
+        out.update({"d" + k: torch.zeros_like(f[k]) if v is None else v for k, v in zip(names, got)})
+    return {k: v.detach() for k, v in out.items()}
+
+
+def call(s, shape, cu=None, states=True):
+    """Forward and backward; sequence tensors viewed as `shape` [B, T, D]."""
+    v = {k: t.view(shape) if k in ("x", "decay", "gate", "dy") else t for k, t in s.items() if t is not None}
+    args = (v["x"], v["decay"], v["gate"], v["rate"], v.get("h0"))
+    y, ht, st = lib.gated_scan_fwd(*args, scale=SCALE, save_states=True, cu_seqlens=cu)
+    g = lib.gated_scan_bwd(*args, v["dy"], v["dht"], states=st if states else None, scale=SCALE, cu_seqlens=cu)
+    return {"y": y, "ht": ht, **g}
+
+
+def compare(got, want, dtype, rows=None):
+    for k, w in want.items():
+        v = got[k].reshape(w.shape)
+        if rows is not None and k not in ("ht", "dh0", "drate"):
+            v, w = v[:rows], w[:rows]
+        assert rel(v, w) <= tol(v.dtype if k in ("ht", "drate", "dh0") else dtype), k
+
+
+DENSE = [(1, 1, 1), (1, 1, 64), (3, 1, 130), (2, 2, 2), (1, 31, 63), (2, 32, 64), (1, 33, 65), (2, 63, 66), (1, 64, 128), (3, 65, 8),
+         (2, 200, 514), (9, 17, 37)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("B,T,D", DENSE)
+def test_dense(B, T, D, dtype):
+    s = make(B * T, B, D, dtype, seed=T)
+    got = call(s, (B, T, D))
+    compare(got, definition(s, spans_of([T] * B), True), dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("lens,D,h0", [([5, 1, 0, 64, 3, 31, 1, 1, 40], 70, True), ([0, 0, 7], 64, True), ([129, 1, 300, 0, 62], 33, True),
+                                       ([1] * 77, 12, True), ([64, 64, 32, 32], 128, False), ([333], 2, False), ([0], 3, True)])
+def test_packed(lens, D, h0, dtype):
+    n, rows = len(lens), max(1, sum(lens))
+    s = make(rows, n, D, dtype, seed=D, h0=h0)
+    cu = torch.tensor([0] + list(torch.tensor(lens).cumsum(0)), dtype=torch.int32, device=DEV)
+    got = call(s, (1, rows, D), cu)
+    compare(got, definition(s, spans_of(lens), True), dtype, sum(lens))
+
+
+@pytest.mark.parametrize("B,T,D", [(1, 5000, 64), (1, 3000, 130), (2, 2100, 40)])
+def test_long_memories_and_clusters(B, T, D):
+    """Few channels: a chain's tiles go round a cluster of blocks.  Rates of a long memory."""
+    s = make(B * T, B, D, torch.float32, seed=3, slow=True)
+    compare(call(s, (B, T, D)), definition(s, spans_of([T] * B), True), torch.float32)
+
+
+def test_one_long_sequence_among_short_ones():
+    lens = [3, 0, 2500, 1, 40]
+    s = make(sum(lens), len(lens), 66, torch.float32, seed=8, slow=True)
+    cu = torch.tensor([0, 3, 3, 2503, 2504, 2544], dtype=torch.int32, device=DEV)
+    compare(call(s, (1, sum(lens), 66), cu), definition(s, spans_of(lens), True), torch.float32)
+
+
+def test_without_saved_states_the_same_bits():
+    s = make(2 * 150, 2, 96, torch.bfloat16)
+    a, b = call(s, (2, 150, 96)), call(s, (2, 150, 96), states=False)
+    for k in a:
+        assert torch.equal(a[k], b[k]), k
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_strided_rows_and_supplied_outputs(dtype):
+    B, T, D = 2, 70, 64
+    s = make(B * T, B, D, dtype)
+    want = call(s, (B, T, D))
+    wide = torch.zeros(B, T, 4 * D + 1, device=DEV, dtype=dtype)       # odd stride: single elements
+    parts = [wide[..., 1 + k * D:1 + (k + 1) * D] for k in range(3)]
+    for p, k in zip(parts, ("x", "decay", "gate")):
+        p.copy_(s[k].view(B, T, D))
+    out = torch.full((B, T, 2 * D), 7.0, device=DEV, dtype=dtype)
+    y, ht = lib.gated_scan_fwd(*parts, s["rate"], s["h0"], scale=SCALE, y=out[..., D:])
+    assert rel(y, want["y"].double()) <= half_step(dtype) * 2 and bool((out[..., :D] == 7).all())
+    grads = torch.full((B, T, 3 * D), 7.0, device=DEV, dtype=dtype)
+    g = lib.gated_scan_bwd(*parts, s["rate"], s["h0"], s["dy"].view(B, T, D), s["dht"], scale=SCALE,
+                           grads=dict(dx=grads[..., :D], ddecay=grads[..., D:2 * D], dgate=grads[..., 2 * D:]))
+    for k in ("dx", "ddecay", "dgate", "drate", "dh0"):
+        assert rel(g[k], want[k].double()) <= half_step(dtype) * 2, k
+
+
+def test_rows_behind_the_last_sequence_stay():
+    D, cu = 40, torch.tensor([0, 20, 50], dtype=torch.int32, device=DEV)
+    s = make(80, 2, D, torch.float32)
+    for k in ("x", "decay", "gate", "dy"):
+        s[k][50:] = float("nan")
+    v = {k: t.view(1, 80, D) if k in ("x", "decay", "gate", "dy") else t for k, t in s.items()}
+    buf = {k: torch.full((1, 80, D), 7.0, device=DEV) for k in ("y", "dx", "ddecay", "dgate")}
+    args = (v["x"], v["decay"], v["gate"], v["rate"], v["h0"])
+    _, ht = lib.gated_scan_fwd(*args, scale=SCALE, y=buf["y"], cu_seqlens=cu)
+    g = lib.gated_scan_bwd(*args, v["dy"], v["dht"], scale=SCALE, cu_seqlens=cu, grads={k: buf[k] for k in ("dx", "ddecay", "dgate")})
+    for t in buf.values():
+        assert bool((t[0, 50:] == 7).all()) and bool(torch.isfinite(t).all())
+    want = definition({k: t[:50] if k in ("x", "decay", "gate", "dy") else t for k, t in s.items()}, [(0, 20), (20, 50)], True)
+    compare({"y": buf["y"][0, :50], "ht": ht, **{k: t[0, :50] if t.dim() == 3 else t for k, t in g.items()}}, want, torch.float32)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_infinities_stay_in_their_sequence(bad):
+    lens, D = [10, 90, 3, 70], 48
+    s = make(sum(lens), 4, D, torch.float32)
+    cu = torch.tensor([0, 10, 100, 103, 173], dtype=torch.int32, device=DEV)
+    clean = call(s, (1, 173, D), cu)
+    s["x"][60, 5] = bad
+    s["dy"][120, 7] = bad
+    got = call(s, (1, 173, D), cu)
+    y = got["y"][0]
+    assert not bool(torch.isfinite(y[60:100, 5]).any()) and not bool(torch.isfinite(got["ht"][1, 5]))
+    keep = torch.ones(173, D, dtype=torch.bool, device=DEV)
+    keep[60:100, 5] = False
+    assert torch.equal(y[keep], clean["y"][0][keep])
+    for k in ("dx", "ddecay", "dgate"):
+        keep = torch.ones(173, D, dtype=torch.bool, device=DEV)
+        keep[10:100, 5] = False
+        keep[103:121, 7] = False
+        assert torch.equal(got[k][0][keep], clean[k][0][keep]), k
+        assert not bool(torch.isfinite(got["dx"][0, 103:121, 7]).any())
+    assert torch.equal(got["drate"][torch.arange(D, device=DEV) > 7], clean["drate"][torch.arange(D, device=DEV) > 7])
+
+
+def test_gates_that_are_shut():
+    """A gate of minus infinity lets nothing in, a decay of minus infinity keeps the state as it is: exactly, and with finite
+    gradients."""
+    T, D = 80, 34
+    s = make(T, 1, D, torch.float32)
+    s["decay"][:] = -float("inf")
+    got = call(s, (1, T, D))
+    assert torch.equal(got["y"][0], s["h0"].expand(T, D)) and torch.equal(got["ht"], s["h0"])
+    assert all(bool(torch.isfinite(t).all()) for t in got.values()) and not bool(got["ddecay"].any())
+    s = make(T, 1, D, torch.float32)
+    s["gate"][:] = -float("inf")
+    s["h0"] = None
+    got = call(s, (1, T, D))
+    assert not bool(got["y"].any()) and not bool(got["dx"].any()) and all(bool(torch.isfinite(t).all()) for t in got.values())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("D", [1, 63, 64, 200])
+def test_step(D, dtype):
+    B, S = 5, 9
+    s = make(B, B, D, dtype)
+    slots = torch.tensor([7, 0, -1, 3, 9], dtype=torch.int32, device=DEV)
+    state = torch.randn(S, D, device=DEV)
+    before = state.clone()
+    y = lib.gated_scan_step(s["x"], s["decay"], s["gate"], s["rate"], state, scale=SCALE, slots=slots)
+    live, at = [0, 1, 3], [7, 0, 3]
+    h0 = torch.zeros(B, D, device=DEV)
+    h0[live] = before[at]
+    want = definition({**s, "h0": h0}, [(b, b + 1) for b in range(B)])
+    assert rel(y[live], want["y"][live]) <= tol(dtype) and rel(state[at], want["ht"][live]) <= STATE
+    assert not bool(y[[2, 4]].any())
+    rest = [k for k in range(S) if k not in at]
+    assert torch.equal(state[rest], before[rest])
+    whole = before[:B].clone()
+    y2 = lib.gated_scan_step(s["x"], s["decay"], s["gate"], s["rate"], whole, scale=SCALE)
+    want = definition({**s, "h0": before[:B]}, [(b, b + 1) for b in range(B)])
+    assert rel(y2, want["y"]) <= tol(dtype)
+
+
+def test_prompt_in_parts_then_single_tokens():
+    B, T, D = 2, 100, 66
+    s = make(B * T, B, D, torch.float32)
+    v = {k: s[k].view(B, T, D) for k in ("x", "decay", "gate")}
+    whole, ht = lib.gated_scan_fwd(*v.values(), s["rate"], s["h0"], scale=SCALE)
+    part = lambda lo, hi: [t[:, lo:hi].contiguous() for t in v.values()]  # noqa: E731
+    a, h = lib.gated_scan_fwd(*part(0, 37), s["rate"], s["h0"], scale=SCALE)
+    b, h = lib.gated_scan_fwd(*part(37, 95), s["rate"], h, scale=SCALE)
+    tail = torch.stack([lib.gated_scan_step(*(t[:, k].contiguous() for t in v.values()), s["rate"], h, scale=SCALE) for k in range(95, T)], 1)
+    assert rel(torch.cat([a, b, tail], 1), whole.double()) <= STATE and rel(h, ht.double()) <= STATE
+
+
+def test_gradients_against_differences():
+    lens, D = [6, 0, 4], 3
+    s = make(10, 3, D, torch.float32, seed=5)
+    cu = torch.tensor([0, 6, 6, 10], dtype=torch.int32, device=DEV)
+    got = call(s, (1, 10, D), cu)
+
+    def loss(k, e):
+        t = {n: v.double() if v is not None else None for n, v in s.items()}
+        t[k] = t[k] + e
+        y, ht = ref.gated_scan(t["x"], t["decay"], t["gate"], t["rate"], t["h0"], spans_of(lens), SCALE)
+        return float((y * t["dy"]).sum() + (ht * t["dht"]).sum())
+    for k in ("x", "decay", "gate", "rate", "h0"):
+        d = torch.randn(s[k].shape, device=DEV, dtype=torch.float64)
+        diff = (loss(k, 1e-5 * d) - loss(k, -1e-5 * d)) / 2e-5
+        size = float((got["d" + k].double().reshape(d.shape) * d).abs().sum())
+        assert abs(float((got["d" + k].double().reshape(d.shape) * d).sum()) - diff) <= STATE * size + 1e-7 * size, k
+
+
+def test_equal_calls_other_streams_and_graphs():
+    s = make(2 * 300, 2, 192, torch.bfloat16)
+    want = call(s, (2, 300, 192))
+    again = call(s, (2, 300, 192))
+    assert all(torch.equal(want[k], again[k]) for k in want)
+    side = torch.cuda.Stream()
+    v = {k: s[k].view(2, 300, 192) for k in ("x", "decay", "gate")}
+    side.wait_stream(torch.cuda.current_stream())
+    y, ht = lib.gated_scan_fwd(*v.values(), s["rate"], s["h0"], scale=SCALE, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(y, want["y"]) and torch.equal(ht, want["ht"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call(s, (2, 300, 192))
+    s["x"].mul_(-1)
+    graph.replay()
+    torch.cuda.synchronize()
+    fresh = call(s, (2, 300, 192))
+    assert all(torch.equal(got[k], fresh[k]) for k in got) and not torch.equal(got["y"], want["y"])
