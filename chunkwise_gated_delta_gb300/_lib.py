@@ -196,14 +196,14 @@ class GroupNormBwdArgs(ctypes.Structure):
 class GluFwdArgs(ctypes.Structure):
     _fields_ = [("rows", _L), ("D", _I), ("F", _I), ("dtype", _I), ("flags", _U), ("x", _P), ("ld_x", _L),
                 ("w_gate", _P), ("ld_w_gate", _L), ("w_up", _P), ("ld_w_up", _L), ("h", _P), ("ld_h", _L), ("g", _P),
-                ("u", _P)]
+                ("u", _P), ("status", _P)]
 
 
 class GluBwdArgs(ctypes.Structure):
     _fields_ = [("rows", _L), ("D", _I), ("F", _I), ("dtype", _I), ("flags", _U), ("x", _P), ("ld_x", _L),
                 ("w_gate", _P), ("ld_w_gate", _L), ("w_up", _P), ("ld_w_up", _L), ("dh", _P), ("ld_dh", _L),
                 ("g", _P), ("u", _P), ("dx", _P), ("ld_dx", _L), ("dw_gate", _P), ("ld_dw_gate", _L), ("dw_up", _P),
-                ("ld_dw_up", _L), ("workspace", _P), ("workspace_bytes", _Z)]
+                ("ld_dw_up", _L), ("workspace", _P), ("workspace_bytes", _Z), ("status", _P)]
 
 
 # Every symbol include/mixer.h declares, with its argument block and whether it takes a stream

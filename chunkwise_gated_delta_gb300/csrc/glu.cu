@@ -175,8 +175,8 @@ template <class T> cudaError_t slopes(const GluParams &p, cudaStream_t s) {
 
 template <class T> cudaError_t bwd(const GluParams &p, cudaStream_t s) {
     cudaError_t e = p.g ? slopes<T>(p, s) : run_simt<T, RECOMPUTE>(p, s);
-    if (e == cudaSuccess && p.dx) e = run_simt<T, DX>(p, s);
-    if (e == cudaSuccess && p.dwg) e = run_simt<T, DW>(p, s);
+    if (e == cudaSuccess) e = run_simt<T, DX>(p, s);
+    if (e == cudaSuccess) e = run_simt<T, DW>(p, s);
     return e;
 }
 
@@ -188,10 +188,16 @@ long long glu_grad_stride(const GluParams &p, bool bf16_) {
 }
 
 cudaError_t launch_glu_fwd(const GluParams &p, bool bf16_, cudaStream_t s) {
-    return bf16_ ? run_simt<bf16, FWD>(p, s) : run_simt<float, FWD>(p, s);
+    if (!bf16_) return run_simt<float, FWD>(p, s);
+    if (glu_rows_takes(p)) return launch_glu_rows(p, s);
+    return glu_tc_takes(p) ? launch_glu_tc_fwd(p, s) : run_simt<bf16, FWD>(p, s);
 }
 cudaError_t launch_glu_bwd(const GluParams &p, bool bf16_, cudaStream_t s) {
-    return bf16_ ? bwd<bf16>(p, s) : bwd<float>(p, s);
+    if (!bf16_ || !glu_tc_takes(p)) return bf16_ ? bwd<bf16>(p, s) : bwd<float>(p, s);
+    cudaError_t e = p.g ? slopes<bf16>(p, s) : launch_glu_tc_grads(p, s);
+    if (e == cudaSuccess) e = launch_glu_tc_dx(p, s);
+    if (e == cudaSuccess) e = launch_glu_tc_dw(p, s);
+    return e;
 }
 
 }  // namespace mixer

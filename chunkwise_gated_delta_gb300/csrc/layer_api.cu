@@ -121,6 +121,8 @@ template <class A> kda_status glu_common(const A *a, mixer::GluParams &p) {
     p.M = a->rows; p.D = a->D; p.F = a->F; p.gelu = a->flags & GLU_FLAG_GELU;
     p.x = a->x; p.wg = a->w_gate; p.wu = a->w_up;
     p.ld_x = stride_or(a->ld_x, a->D); p.ld_wg = stride_or(a->ld_w_gate, a->D); p.ld_wu = stride_or(a->ld_w_up, a->D);
+    if (!mixer::aligned_to(a->status, 16)) return KDA_ERR_INVALID_ARG;
+    p.status = static_cast<int *>(a->status);
     return KDA_OK;
 }
 
@@ -131,7 +133,8 @@ kda_status glu_fwd_params(const glu_fwd_args *a, mixer::GluParams &p) {
     p.h = a->h; p.ld_h = stride_or(a->ld_h, a->F); p.g = a->g; p.u = a->u;
     const size_t es = es_of(a->dtype);
     const Block in[] = {{a->x, a->rows, a->D, p.ld_x, es}, {a->w_gate, a->F, a->D, p.ld_wg, es}, {a->w_up, a->F, a->D, p.ld_wu, es}};
-    const Block out[] = {{a->h, a->rows, a->F, p.ld_h, es}, dense(a->g, a->rows, a->F, 4), dense(a->u, a->rows, a->F, 4)};
+    const Block out[] = {{a->h, a->rows, a->F, p.ld_h, es}, dense(a->g, a->rows, a->F, 4), dense(a->u, a->rows, a->F, 4),
+                         dense(a->status, 1, 256, 1)};
     return blocks_ok(in, out) ? KDA_OK : KDA_ERR_INVALID_ARG;
 }
 
@@ -149,7 +152,8 @@ kda_status glu_bwd_params(const glu_bwd_args *a, mixer::GluParams &p, size_t &ne
     const Block in[] = {{a->x, a->rows, a->D, p.ld_x, es}, {a->w_gate, a->F, a->D, p.ld_wg, es}, {a->w_up, a->F, a->D, p.ld_wu, es},
                         {a->dh, a->rows, a->F, p.ld_dh, es}, dense(a->g, a->rows, a->F, 4), dense(a->u, a->rows, a->F, 4)};
     const Block out[] = {{a->dx, a->rows, a->D, p.ld_dx, es}, {a->dw_gate, a->F, a->D, p.ld_dwg, es},
-                         {a->dw_up, a->F, a->D, p.ld_dwu, es}, dense(a->workspace, 1, (long long)a->workspace_bytes, 1)};
+                         {a->dw_up, a->F, a->D, p.ld_dwu, es}, dense(a->workspace, 1, (long long)a->workspace_bytes, 1),
+                         dense(a->status, 1, 256, 1)};
     return blocks_ok(in, out) ? KDA_OK : KDA_ERR_INVALID_ARG;
 }
 

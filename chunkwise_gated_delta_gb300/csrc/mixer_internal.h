@@ -99,6 +99,7 @@ struct GluParams {
     float *g, *u;                     // [M][F] the two products, or NULL
     void *dg, *du;                    // workspace [M][ld_d]: their gradients
     long long ld_d;
+    int *status;                      // status block, or NULL
 };
 
 cudaError_t launch_layer_norm_fwd(const NormParams &p, bool bf16, cudaStream_t s);
@@ -133,5 +134,13 @@ size_t group_norm_part_floats(const GroupNormParams &p, bool bf16);
 cudaError_t launch_glu_fwd(const GluParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_glu_bwd(const GluParams &p, bool bf16, cudaStream_t s);
 long long glu_grad_stride(const GluParams &p, bool bf16);
+// Forms of bfloat16 calls: the tensor cores' products, and a few rows past the weights.
+bool glu_tc_takes(const GluParams &p);
+cudaError_t launch_glu_tc_fwd(const GluParams &p, cudaStream_t s);
+cudaError_t launch_glu_tc_grads(const GluParams &p, cudaStream_t s);
+cudaError_t launch_glu_tc_dx(const GluParams &p, cudaStream_t s);
+cudaError_t launch_glu_tc_dw(const GluParams &p, cudaStream_t s);
+bool glu_rows_takes(const GluParams &p);
+cudaError_t launch_glu_rows(const GluParams &p, cudaStream_t s);
 
 }  // namespace mixer

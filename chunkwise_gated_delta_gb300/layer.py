@@ -212,30 +212,41 @@ def _glu_inputs(x, w_gate, w_up):
     return dev, code, D, F, x.numel() // D, ptrs
 
 
-def glu_fwd(x, w_gate, w_up, *, activation="silu", save=False, y=None, stream=None):
+def _glu_status(status, dev):
+    if status is None:
+        return None
+    p = _tensor(status, "status", (status.shape[0],) if isinstance(status, torch.Tensor) and status.dim() == 1 else (None,),
+                torch.uint8, dev)
+    if status.shape[0] < 256:
+        raise ValueError("status must have 256 bytes")
+    return p
+
+
+def glu_fwd(x, w_gate, w_up, *, activation="silu", save=False, y=None, status=None, stream=None):
     """First half of a gated feed-forward block in one kernel: h, with ``save`` (h, g, u).
 
         g = x w_gate^T;  u = x w_up^T;  h = act(g) u
 
     x: [..., D]; w_gate, w_up: [F, D] (one dtype, bf16 or fp32); activation: "silu" or "gelu" (g Phi(g)).  h is [..., F]
-    of x's dtype.  g and u are fp32 [..., F], what :func:`glu_bwd` would otherwise compute again.
+    of x's dtype.  g and u are fp32 [..., F], what :func:`glu_bwd` would otherwise compute again.  status: uint8 [256],
+    zero at first, for :func:`.api.status_read`: whether a wait of the bf16 kernels ran out.
     """
     dev, code, D, F, rows, ptrs = _glu_inputs(x, w_gate, w_up)
     flags = _glu_activation(activation)
-    shape = (*x.shape[:-1], F)
-    with _On(dev, stream, (x, w_gate, w_up)) as on:
+    shape, stp = (*x.shape[:-1], F), _glu_status(status, dev)
+    with _On(dev, stream, (x, w_gate, w_up, status)) as on:
         y, yp, ldy = _out(on, y, "y", shape, x.dtype)
         g = u = gp = up = None
         if save:
             g, gp = _dense_out(on, None, "g", shape, _F32)
             u, up = _dense_out(on, None, "u", shape, _F32)
-        on.launch("glu_fwd", _lib.GluFwdArgs(rows, D, F, code, flags, *ptrs, yp, ldy, gp, up))
+        on.launch("glu_fwd", _lib.GluFwdArgs(rows, D, F, code, flags, *ptrs, yp, ldy, gp, up, stp))
     return (y, g, u) if save else y
 
 
-def glu_bwd(x, w_gate, w_up, dh, g=None, u=None, *, activation="silu", grads=None, stream=None):
+def glu_bwd(x, w_gate, w_up, dh, g=None, u=None, *, activation="silu", grads=None, status=None, stream=None):
     """Backward of :func:`glu_fwd`, whose inputs it takes again: a dict with dx, dw_gate and dw_up (dtype of x).
-    dh: [..., F]; g, u: the forward's, or None (computed again).  ``grads`` may supply output tensors by name."""
+    dh: [..., F]; g, u: the forward's, or None (computed again); status as there.  ``grads`` may supply output tensors by name."""
     dev, code, D, F, rows, ptrs = _glu_inputs(x, w_gate, w_up)
     flags = _glu_activation(activation)
     shape = (*x.shape[:-1], F)
@@ -244,12 +255,12 @@ def glu_bwd(x, w_gate, w_up, dh, g=None, u=None, *, activation="silu", grads=Non
         raise ValueError("g and u come together")
     gp = None if g is None else _tensor(g, "g", shape, _F32, dev)
     up = None if u is None else _tensor(u, "u", shape, _F32, dev)
-    out = _known(grads, ("dx", "dw_gate", "dw_up"))
-    with _On(dev, stream, (x, w_gate, w_up, dh, g, u)) as on:
+    out, stp = _known(grads, ("dx", "dw_gate", "dw_up")), _glu_status(status, dev)
+    with _On(dev, stream, (x, w_gate, w_up, dh, g, u, status)) as on:
         out["dx"], *dxp = _out(on, out.get("dx"), "dx", x.shape, x.dtype)
         out["dw_gate"], *dgp = _out(on, out.get("dw_gate"), "dw_gate", (F, D), x.dtype)
         out["dw_up"], *dup = _out(on, out.get("dw_up"), "dw_up", (F, D), x.dtype)
-        args = _lib.GluBwdArgs(rows, D, F, code, flags, *ptrs, *dhp, gp, up, *dxp, *dgp, *dup, None, 0)
+        args = _lib.GluBwdArgs(rows, D, F, code, flags, *ptrs, *dhp, gp, up, *dxp, *dgp, *dup, None, 0, stp)
         ws = on.workspace("glu_bwd_workspace", args)
         on.launch("glu_bwd", args)
         del ws

@@ -37,8 +37,8 @@
  *     KDA_ERR_INVALID_ARG otherwise.
  *   - Arithmetic is float32 for both dtypes; results are rounded once on output.  Sums
  *     over tokens and channels are added in a fixed order: equal calls give equal bits.
- *   - Nothing waits on the device, so there is no status block; workspaces need no
- *     initial contents.
+ *   - Nothing waits on the device but the gated feed-forward product's bfloat16 form, so only its
+ *     calls have a status block; workspaces need no initial contents.
  *   - Outputs must not overlap inputs or each other.  Parts of one row-strided buffer do
  *     not overlap when their columns are disjoint and their strides are equal.
  */
@@ -436,6 +436,13 @@ kda_status group_norm_bwd(const group_norm_bwd_args *args, kda_stream_t stream);
 
 #define GLU_FLAG_GELU 1u    /* act(g) = g Phi(g); cleared: g sigmoid(g) */
 
+/*
+ * bfloat16 products run on the tensor cores where bases and rows of x and of the weights are 16-byte aligned (a
+ * few rows aside); everything else runs on the CUDA cores.  The former's waits are bounded: where one
+ * runs out, the call leaves NaN in what it did not finish.  With a status block (the head of kda.h's workspaces:
+ * 256 bytes, 16-byte aligned, zero at first, word 7 the wait budget) kda_status_read then answers KDA_ERR_TIMEOUT.
+ */
+
 typedef struct {
     long long rows;        /* >= 1 */
     int D, F;              /* columns of x, rows of the weights */
@@ -450,6 +457,7 @@ typedef struct {
     void *h;               /* [rows, F] out */
     long long ld_h;
     float *g, *u;          /* [rows, F] out, the two products for glu_bwd; or both NULL (not kept) */
+    void *status;          /* 256-byte status block (below), or NULL */
 } glu_fwd_args;
 
 kda_status glu_fwd(const glu_fwd_args *args, kda_stream_t stream);
@@ -476,6 +484,7 @@ typedef struct {
     long long ld_dw_up;
     void *workspace;       /* glu_bwd_workspace bytes */
     size_t workspace_bytes;
+    void *status;          /* as the forward's */
 } glu_bwd_args;
 
 /* Bytes of workspace (0 on bad args): the gradients of the two products. */
