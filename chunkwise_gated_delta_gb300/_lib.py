@@ -154,7 +154,7 @@ class SsmScanStepArgs(ctypes.Structure):
                 ("y", _P), ("ld_y", _L)]
 
 
-GATED_SCAN_STATE_ROWS = 32
+GATED_SCAN_STATE_ROWS = 64
 GROUP_NORM_FLAG_CENTER = 1
 GROUP_NORM_FLAG_SHARED = 2
 GLU_FLAG_GELU = 1

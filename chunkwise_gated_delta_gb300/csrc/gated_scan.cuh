@@ -15,25 +15,47 @@
 namespace mixer {
 namespace gs {
 
-constexpr int WARPS = 8, THREADS = 32 * WARPS;
-constexpr int COLS = 64;            // channels of a block, two per lane
-constexpr int SAVE = GATED_SCAN_STATE_ROWS;  // rows from one saved state to the next (a tile of the backward)
+constexpr int WARPS = 8, LANES = 32 * WARPS;     // warps that walk rows, their threads
+constexpr int ROWS = 8, TILE = ROWS * WARPS;      // rows of a warp and of a block's tile
+constexpr int COLS = 64;                          // channels of a block, two per lane
+constexpr int SAVE = GATED_SCAN_STATE_ROWS;       // rows from one saved state to the next
+static_assert(SAVE == TILE, "a saved state enters every tile of the backward");
 
-// Two neighbouring channels of a row as they lie in memory: one access, or two with the channel past an odd
-// end replaced by the last.
-template <class T, bool VEC> struct Raw {
-    Lanes<T, 2> v;
-    __device__ __forceinline__ void load(const T *row, int c, int) { v.load(row + c); }
-    __device__ __forceinline__ f2 pair() const { return v.pair(0); }
-};
-template <class T> struct Raw<T, false> {
-    uint32_t w[2];
-    __device__ __forceinline__ void load(const T *row, int c, int D) {
-        w[0] = load_bits(row + c);
-        w[1] = load_bits(row + min(c + 1, D - 1));
+// A tile's rows of one tensor in shared memory, and how they get there: accesses of CP bytes, asynchronous ones of 16 or
+// 4 bytes, or single bfloat16 elements (CP = 2).  Rows past the chain are its first or last, channels past D are
+// left out (their lanes write nothing).
+template <class T, int CP> struct Stage {
+    static constexpr int ROW = COLS * (int)sizeof(T), BYTES = TILE * ROW;
+    static constexpr int PER = ROW / CP, STEP = LANES / PER < 1 ? 1 : LANES / PER;    // accesses of a row, rows at a time
+    static constexpr int E = CP / (int)sizeof(T) < 1 ? 1 : CP / (int)sizeof(T);       // elements of an access
+    static __device__ __forceinline__ void bring(char *to, const T *from, long long ld, int c0, int D, long long r0, int lo, int hi) {
+        const int t = threadIdx.x, at = t % PER * E, row = t / PER;
+        if (c0 + at >= D) return;
+        const T *p = from + c0 + at;
+        char *q = to + row * ROW + at * (int)sizeof(T);
+        if (r0 >= lo && r0 + TILE <= hi) {               // a tile inside: one stride
+            const T *s = p + (r0 + row) * ld;
+#pragma unroll
+            for (int k = 0; k < TILE / STEP; ++k, s += STEP * ld) one(q + k * STEP * ROW, s);
+        } else {
+#pragma unroll
+            for (int k = 0; k < TILE / STEP; ++k) {
+                const long long r = r0 + row + k * STEP;
+                one(q + k * STEP * ROW, p + (r < lo ? lo : r >= hi ? hi - 1 : r) * ld);
+            }
+        }
     }
-    __device__ __forceinline__ f2 pair() const { return pack2(bits_f<T>(w[0]), bits_f<T>(w[1])); }
+    static __device__ __forceinline__ void one(char *to, const T *from) {
+        if constexpr (CP == 2) *reinterpret_cast<unsigned short *>(to) = __ldg(reinterpret_cast<const unsigned short *>(from));
+        else copy_async<CP>(to, from);
+    }
+    static __device__ __forceinline__ f2 pair(const char *tile, int row, int lane) {
+        Lanes<T, 2> v;
+        v.load_shared(tile + row * ROW + lane * 2 * (int)sizeof(T));
+        return v.pair(0);
+    }
 };
+// Two neighbouring channels: one access, or two with the channel past an odd end left out.
 template <class T, bool VEC> __device__ __forceinline__ void store_pair(T *row, int c, int D, f2 v) {
     float lo, hi;
     unpack2(v, lo, hi);
@@ -43,6 +65,9 @@ template <class T, bool VEC> __device__ __forceinline__ void store_pair(T *row, 
         row[c] = from_f<T>(lo);
         if (c + 1 < D) row[c + 1] = from_f<T>(hi);
     }
+}
+template <class T> __device__ __forceinline__ f2 load_pair(const T *row, int c, int D) {
+    return pack2(bits_f<T>(load_bits(row + c)), bits_f<T>(load_bits(row + min(c + 1, D - 1))));
 }
 // The float32 vectors of D channels (states) have no row stride: pairs are aligned where D is even.
 __device__ __forceinline__ f2 load_state(const float *row, int c, int D) { return pack2(row[c], row[min(c + 1, D - 1)]); }
@@ -59,19 +84,39 @@ __device__ __forceinline__ f2 coefficients(const GatedScanParams &p, int c) {
     return pack2(p.scale * softplus_of(p.rate[c]), p.scale * softplus_of(p.rate[min(c + 1, p.D - 1)]));
 }
 
-// p = 1 - exp(-q), q >= 0.  Below 1/4 six terms of the series: the seventh is below 5e-8 of the first.
-__device__ __forceinline__ f2 one_less_exp(f2 q) {
+// p = 1 - exp(-q) for 0 <= q < 1/4: six terms of the series, the seventh is below 5e-8 of the first; and for any q >= 0.
+constexpr float SMALL = 0.25f;
+__device__ __forceinline__ f2 one_less_exp_small(f2 q) {
     f2 s = fma2(q, both(-1.f / 720.f), both(1.f / 120.f));
     s = fma2(s, q, both(-1.f / 24.f));
     s = fma2(s, q, both(1.f / 6.f));
     s = fma2(s, q, both(-0.5f));
     s = fma2(s, q, both(1.f));
-    s = mul2(s, q);
+    return mul2(s, q);
+}
+__device__ __forceinline__ f2 one_less_exp(f2 q) {
     float s0, s1, q0, q1, e0, e1;
-    unpack2(s, s0, s1);
+    unpack2(one_less_exp_small(q), s0, s1);
     unpack2(q, q0, q1);
     unpack2(mul2(q, both(-kLog2e)), e0, e1);
-    return pack2(q0 < 0.25f ? s0 : 1.f - ex2(e0), q1 < 0.25f ? s1 : 1.f - ex2(e1));
+    return pack2(q0 < SMALL ? s0 : 1.f - ex2(e0), q1 < SMALL ? s1 : 1.f - ex2(e1));
+}
+// Of several at once: a warp whose exponents are all small leaves the exponential out (the same values).
+template <int N> __device__ __forceinline__ void one_less_exps(f2 (&q)[N]) {
+    bool large = false;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        float lo, hi;
+        unpack2(q[j], lo, hi);
+        large |= !(lo < SMALL && hi < SMALL);
+    }
+    if (__any_sync(~0u, large)) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) q[j] = one_less_exp(q[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) q[j] = one_less_exp_small(q[j]);
+    }
 }
 __device__ __forceinline__ float sqrt_fast(float v) {
     float r;
@@ -83,12 +128,9 @@ __device__ __forceinline__ float rsqrt_fast(float v) {
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
-// The decay and the input's weight without its gate: a and 1 - a^2.
-__device__ __forceinline__ void decay_of(f2 q, f2 &a, f2 &w) {
-    const f2 p = one_less_exp(q);
-    a = fma2(p, both(-1.f), both(1.f));
-    w = fma2(p, a, p);
-}
+// From p: the decay a = 1 - p, and 1 - a^2 = p (1 + a).
+__device__ __forceinline__ f2 decay_of(f2 p) { return fma2(p, both(-1.f), both(1.f)); }
+__device__ __forceinline__ f2 rest_of(f2 p, f2 a) { return fma2(p, a, p); }
 __device__ __forceinline__ f2 sqrt2(f2 v) {
     float lo, hi;
     unpack2(v, lo, hi);
@@ -127,9 +169,10 @@ __device__ __forceinline__ Chain chain_of(const int32_t *cu, int B, int T, int P
     return k;
 }
 
-// Where sequences begin and end among the N rows from r0 that a warp holds (bit j: row r0 + j), and the
+// Where sequences begin and end among the rows from r0 that a warp holds (bit j: row r0 + j), and the
 // sequence of row r0 + lane.  The warp keeps the sequence of its last row: rows inside it take no search.
-template <int N> struct Marks {
+struct Marks {
+    static constexpr int N = ROWS;
     int lo = 1, hi = 0;                  // the kept sequence's rows
     unsigned starts, ends;
     int seq;

@@ -44,7 +44,7 @@ kda_status gated_bwd(const gated_scan_bwd_args *a, mixer::GatedScanParams &p, si
     p.dx = a->dx; p.ddecay = a->ddecay; p.dgate = a->dgate; p.drate = a->drate; p.dh0 = a->dh0;
     p.ld_dy = stride_or(a->ld_dy, a->D); p.ld_dx = stride_or(a->ld_dx, a->D);
     p.ld_ddecay = stride_or(a->ld_ddecay, a->D); p.ld_dgate = stride_or(a->ld_dgate, a->D);
-    const size_t part = mixer::gated_scan_part_floats(p), saved = mixer::gated_scan_saved_rows(p);
+    const size_t part = mixer::gated_scan_part_floats(p, a->dtype == KDA_BF16), saved = mixer::gated_scan_saved_rows(p);
     states = a->states ? 0 : (saved * a->D + 3) / 4 * 16;
     need = states + part * 4;
     const long long rows = (long long)(a->cu_seqlens ? 1 : a->B) * a->T;

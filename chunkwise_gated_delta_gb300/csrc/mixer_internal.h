@@ -67,7 +67,7 @@ struct GatedScanParams {
     long long ld_x, ld_decay, ld_gate, ld_y, ld_dy, ld_dx, ld_ddecay, ld_dgate;
     const float *rate, *h0, *dht;
     void *y, *dx, *ddecay, *dgate;
-    float *ht, *states;               // states: [ceil(rows / 32)][D], the state that enters each 32nd row
+    float *ht, *states;               // states: [ceil(rows / 64)][D], the state that enters each 64th row
     float *drate, *dh0, *part;        // part: [chains cluster][D]
     const int32_t *cu_seqlens;
     // single tokens
@@ -125,7 +125,7 @@ cudaError_t launch_gated_scan_fwd(const GatedScanParams &p, bool bf16, cudaStrea
 cudaError_t launch_gated_scan_bwd(const GatedScanParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_gated_scan_step(const GatedScanParams &p, bool bf16, cudaStream_t s);
 size_t gated_scan_saved_rows(const GatedScanParams &p);
-size_t gated_scan_part_floats(const GatedScanParams &p);
+size_t gated_scan_part_floats(const GatedScanParams &p, bool bf16);
 
 cudaError_t launch_group_norm_fwd(const GroupNormParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_group_norm_bwd(const GroupNormParams &p, bool bf16, cudaStream_t s);

@@ -41,7 +41,7 @@ def gated_scan_fwd(x, decay, gate, rate, h0=None, *, scale=8.0, output_final_sta
 
     x, decay, gate: [B, T, D] (one dtype, bf16 or fp32); rate: [D] fp32; h0: [B, D] fp32 or None (zeros).
     y has x's dtype, ht is fp32 [B, D] (None when ``output_final_state`` is false).  states: what
-    :func:`gated_scan_bwd` would otherwise compute again, fp32 [ceil(B T / 32), D].
+    :func:`gated_scan_bwd` would otherwise compute again, fp32 [ceil(B T / 64), D].
     """
     dev, code, ptrs = _gated_inputs(x, decay, gate, rate, scale, 3)
     B, T, D = x.shape

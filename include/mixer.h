@@ -286,7 +286,7 @@ kda_status ssm_scan_step(const ssm_scan_step_args *args, kda_stream_t stream);
 
 /* ------------------------------------------------------------ gated recurrence */
 
-#define GATED_SCAN_STATE_ROWS 32
+#define GATED_SCAN_STATE_ROWS 64
 
 typedef struct {
     int B, T, D;           /* sequences, tokens, channels */
@@ -304,7 +304,7 @@ typedef struct {
     long long ld_y;
     float *ht;             /* [B, D] out, or NULL */
     float *states;         /* [ceil(rows / GATED_SCAN_STATE_ROWS), D] out, rows as they lie (B T, packed: T): the state that
-                              enters every 32nd row, for gated_scan_bwd; or NULL (not kept) */
+                              enters every 64th row, for gated_scan_bwd; or NULL (not kept) */
     const int32_t *cu_seqlens;
 } gated_scan_fwd_args;
 
