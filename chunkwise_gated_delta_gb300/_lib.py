@@ -154,7 +154,7 @@ class SsmScanStepArgs(ctypes.Structure):
                 ("y", _P), ("ld_y", _L)]
 
 
-GATED_SCAN_STATE_ROWS = 64
+GATED_SCAN_STATE_ROWS = 8
 GROUP_NORM_FLAG_CENTER = 1
 GROUP_NORM_FLAG_SHARED = 2
 GLU_FLAG_GELU = 1
@@ -163,7 +163,7 @@ GLU_FLAG_GELU = 1
 class GatedScanFwdArgs(ctypes.Structure):
     _fields_ = [("B", _I), ("T", _I), ("D", _I), ("dtype", _I), ("scale", _F), ("x", _P), ("ld_x", _L), ("decay", _P),
                 ("ld_decay", _L), ("gate", _P), ("ld_gate", _L), ("rate", _P), ("h0", _P), ("y", _P), ("ld_y", _L),
-                ("ht", _P), ("states", _P), ("cu_seqlens", _P)]
+                ("ht", _P), ("states", _P), ("workspace", _P), ("workspace_bytes", _Z), ("cu_seqlens", _P)]
 
 
 class GatedScanBwdArgs(ctypes.Structure):
@@ -221,6 +221,7 @@ MIXER_EXPORTS = {
     "ssm_scan_bwd_workspace": (SsmScanBwdArgs, False),
     "ssm_scan_bwd": (SsmScanBwdArgs, True),
     "ssm_scan_step": (SsmScanStepArgs, True),
+    "gated_scan_fwd_workspace": (GatedScanFwdArgs, False),
     "gated_scan_fwd": (GatedScanFwdArgs, True),
     "gated_scan_bwd_workspace": (GatedScanBwdArgs, False),
     "gated_scan_bwd": (GatedScanBwdArgs, True),

@@ -1,15 +1,21 @@
 // Gated recurrence (one state per channel), forward, backward and single tokens.
 //
-// All rows of a chain of sequences form one axis.  Tiles of it, 64 rows by 64 channels, go to the blocks of a cluster in
-// turn; the next tile is on its way to shared memory while one is worked on.  Of a tile every warp has 8 neighbouring
-// rows and a lane two channels.  A warp reduces its rows to h_out = h + A h_in, the block's warps and then the cluster's
-// blocks exchange these pairs through shared memory, and each warp walks its rows again from the state that enters them.
-// So every tensor is read once and written once, whatever the sequences' lengths, and the order of the sums is
-// fixed.  Where a sequence begins inside a tile the link is cut by selection (never by a product with 0: a state
-// of an earlier sequence may be an infinity).
+// All rows of a call form one axis, cut where a sequence begins, in segments of 16 to 64 rows whatever the sequences' lengths.
+// A warp has a segment's rows and 64 channels, a lane two of them, eight rows in registers and the next eight on their way:
 //
-// The backward runs the same walk from the end, with G_t = dy_t + a_{t+1} G_{t+1}; the states that enter its
-// tiles are the forward's, saved every 64 rows in float32 (3 % of one bfloat16 tensor), so that it too reads each tensor once.
+//   local pass      what a segment does to a state: h_out = h + A h_in (A, h), or h alone where a sequence begins in it
+//   boundary pass   the states that enter the segments, in order
+//   walk            the segment again from the state that enters it; y, final states, the states before every 8th row
+//
+// Warps wait for no other, and every pass is as parallel as the call has rows and channels.  The walk goes through the segments
+// from the last, whose inputs the local pass has left in L2 (its 126 MB hold all inputs of 10 million bfloat16 row-channels).
+// Gates are computed twice; carrying the states in one pass through clusters of blocks that exchange them took 109 us for a
+// prompt of 16384 x 1024 and 104 us for 4 of 4096 x 2048, bound by the exchange: WALK_TIMES.
+// Where a sequence begins the link is cut by selection (never by a product with 0: a state of an earlier sequence
+// may be an infinity).
+//
+// The backward does the same from the end, with G_t = dy_t + a_{t+1} G_{t+1}: its local pass takes decay and dy alone, and its walk
+// has the state before every eighth row from the forward.
 #include "gated_scan.cuh"
 #include "tc_common.cuh"
 
@@ -18,420 +24,406 @@ namespace {
 
 using namespace gs;
 
-constexpr int MAX_CLUSTER = 8;
+__host__ __device__ __forceinline__ long long rows_of(const GatedScanParams &p) { return (long long)(p.cu_seqlens ? 1 : p.B) * p.T; }
 
-// ------------------------------------------------------------------------------------------ exchange
-// 16 bytes, and a word, into the same place of another block's shared memory.
-__device__ __forceinline__ void store_remote(const float4 *at, unsigned rank, float4 v) {
-    const uint32_t a = kda::tc::map_to_rank((uint32_t)__cvta_generic_to_shared(at), rank);
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
-}
-__device__ __forceinline__ void store_remote(const int *at, unsigned rank, int v) {
-    const uint32_t a = kda::tc::map_to_rank((uint32_t)__cvta_generic_to_shared(at), rank);
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
-__device__ __forceinline__ void cluster_arrive_release() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void sync_rows() { asm volatile("bar.sync 1, %0;" ::"n"(LANES) : "memory"); }
-// All N threads of the block; whether the predicate holds in any of them.
-template <int N> __device__ __forceinline__ bool sync_any(bool v) {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 2, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(r) : "r"((uint32_t)v), "n"(N) : "memory");
-    return r != 0;
-}
-__device__ __forceinline__ float4 quad(f2 a, f2 b) {
-    float4 r;
-    unpack2(a, r.x, r.y);
-    unpack2(b, r.z, r.w);
-    return r;
-}
-
-// What the warps of a block and the blocks of a cluster tell each other of a tile, in two sets that take turns:
-// h_out = h + A h_in of their rows (A, h), or h_out = h alone where the link is cut (a sequence begins; ends, in the backward).
-struct Exchange {
-    float4 warp[2][WARPS][32];
-    float4 block[2][MAX_CLUSTER][32];
-    int warp_cut[2][WARPS], block_cut[2][MAX_CLUSTER];
-};
-// h_out of the rows that (A, h) stand for.
-__device__ __forceinline__ f2 through(float4 g, f2 h) { return fma2(pack2(g.x, g.y), h, pack2(g.z, g.w)); }
-__device__ __forceinline__ f2 through(float4 g, bool cut, f2 h) { return cut ? pack2(g.z, g.w) : through(g, h); }
-
-// The state (or its gradient) that enters this warp's rows, and the one that leaves the cluster's tiles (carry).
-// REV: warps and blocks count from the last row.  prod, out: this warp's pair.
-template <bool REV, bool CLUSTER>
-__device__ __forceinline__ f2 enter(Exchange &ex, int buf, int warp, int lane, unsigned rank, int blocks, f2 prod, f2 out, bool cut,
-                                    f2 &carry) {
-    ex.warp[buf][warp][lane] = quad(prod, out);
-    if (lane == 0) ex.warp_cut[buf][warp] = cut;
-    const bool any = sync_any<LANES + (CLUSTER ? 32 : 0)>(cut);
-    if constexpr (!CLUSTER) {
-        f2 mine = carry;
-        if (!any) {
-#pragma unroll
-            for (int i = 0; i < WARPS; ++i) {
-                const int k = REV ? WARPS - 1 - i : i;
-                if (k == warp) mine = carry;
-                carry = through(ex.warp[buf][k][lane], carry);
-            }
-        } else {
-            for (int i = 0; i < WARPS; ++i) {
-                const int k = REV ? WARPS - 1 - i : i;
-                if (k == warp) mine = carry;
-                carry = through(ex.warp[buf][k][lane], ex.warp_cut[buf][k], carry);
-            }
-        }
-        return mine;
-    }
-    cluster_arrive_relaxed();            // (the warp that writes to other blocks releases)
-    // the pair of the warps before this one
-    f2 ma = both(1.f), mh = both(0.f);
-    bool mc = false;
-    const int before = REV ? WARPS - 1 - warp : warp;
-    for (int i = 0; i < before; ++i) {
-        const int k = REV ? WARPS - 1 - i : i;
-        const float4 g = ex.warp[buf][k][lane];
-        const bool c = any && ex.warp_cut[buf][k];
-        mh = i == 0 ? pack2(g.z, g.w) : through(g, c, mh);
-        ma = mul2(ma, pack2(g.x, g.y));
-        mc |= c;
-    }
-    cluster_wait();
-    f2 into = carry;
-    for (int i = 0; i < blocks; ++i) {
-        const int k = REV ? blocks - 1 - i : i;
-        if (k == (int)rank) into = carry;
-        carry = through(ex.block[buf][k][lane], ex.block_cut[buf][k], carry);
-    }
-    return before == 0 ? into : mc ? mh : fma2(ma, into, mh);
-}
-
-// The warp that tells the other blocks of a cluster what a tile of this one does to a state.  A warp of its own, for its release
-// must not wait for rows that the others are still storing.
-template <bool REV> __device__ __forceinline__ void exchange_warp(Exchange &ex, int turns, int lane, unsigned rank, int blocks) {
-    for (int i = 0; i < turns; ++i) {
-        const int buf = i & 1;
-        const bool any = sync_any<LANES + 32>(false);
-        f2 pa = both(1.f), ph = both(0.f);
-        bool pc = false;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-            const int k = REV ? WARPS - 1 - w : w;
-            const float4 g = ex.warp[buf][k][lane];
-            const bool c = any && ex.warp_cut[buf][k];
-            ph = w == 0 ? pack2(g.z, g.w) : through(g, c, ph);
-            pa = mul2(pa, pack2(g.x, g.y));
-            pc |= c;
-        }
-        for (int b = 0; b < blocks; ++b) store_remote(&ex.block[buf][rank][lane], b, quad(pa, ph));
-        if (lane < blocks) store_remote(&ex.block_cut[buf][rank], lane, (int)pc);
-        cluster_arrive_release();
-        cluster_wait();
-    }
-}
-
-// Where a block works.
+// Where a warp works: segment, channels.
 struct Where {
-    int warp, lane, blocks, c0, c, cl;   // c: this lane's first channel, cl: the same or, of idle lanes, one inside
-    unsigned rank;
-    bool on;
-    Chain k;
-    long long tile0;
-    int turns;
+    int lane, c, cl;             // c: this lane's first channel; cl: the same or, of idle lanes, one inside
+    long long seg, segs, r0;     // the segment, their number, the segment's first row
+    bool any, on;
+    Extent k;
 };
-__device__ __forceinline__ Where where(const GatedScanParams &p) {
+template <bool BACK> __device__ __forceinline__ Where where(const GatedScanParams &p) {
     Where w;
-    w.warp = threadIdx.x >> 5;
     w.lane = threadIdx.x & 31;
-    w.blocks = p.cluster;
-    w.rank = blockIdx.x % (unsigned)p.cluster;
-    w.c0 = (int)(blockIdx.x / (unsigned)p.cluster) * COLS;
-    w.c = w.c0 + w.lane * 2;
+    const long long cols = (p.D - 1) / COLS + 1;
+    w.segs = (rows_of(p) + p.seg - 1) / p.seg;
+    long long unit = (long long)blockIdx.x * WARPS + (threadIdx.x >> 5);
+    w.any = unit < cols * w.segs;
+    if (BACK) unit = cols * w.segs - 1 - unit;
+    w.seg = unit / cols;
+    w.r0 = w.seg * p.seg;
+    const int c0 = (int)(unit - w.seg * cols) * COLS;
+    w.c = c0 + w.lane * 2;
     w.on = w.c < p.D;
-    w.cl = w.on ? w.c : w.c0;
-    w.k = chain_of(p.cu_seqlens, p.B, p.T, p.chains, blockIdx.y);
-    w.tile0 = w.k.c0 / TILE;
-    const long long tiles = ((long long)w.k.c1 + TILE - 1) / TILE - w.tile0;
-    w.turns = (int)((tiles + w.blocks - 1) / w.blocks);
+    w.cl = w.on ? w.c : c0;
+    w.k = extent_of(p);
     return w;
 }
 
-// ------------------------------------------------------------------------------------------ forward
-template <class T, int CP, bool CLUSTER>
-__global__ void __launch_bounds__(LANES + (CLUSTER ? 32 : 0), sizeof(T) == 2 ? 3 : 2) gated_scan_fwd_kernel(GatedScanParams p) {
+// The gates of a row: p = 1 - a, and m u x.
+template <bool SMALL_Q> __device__ __forceinline__ f2 decay_p(f2 coef, f2 d) { return one_less_exp_if<SMALL_Q>(mul2(coef, sigmoid2(d))); }
+__device__ __forceinline__ f2 input_v(f2 q, f2 a, f2 g, f2 x) { return mul2(mul2(sqrt2(rest_of(q, a)), sigmoid2(g)), x); }
+
+// Rows on their way: a ring of this warp's in shared memory, eight rows of N tensors per stage, STAGES - 1 of them in flight.
+// BACK: from the last rows to the first.
+constexpr int STAGES = 3;
+template <class T, int CP, int N, bool BACK> struct Ring {
     using S = Stage<T, CP>;
-    constexpr bool VEC = CP > (int)sizeof(T);
-    extern __shared__ __align__(16) char stages[];   // [2][3][S::BYTES]
-    __shared__ Exchange ex;
-    const Where w = where(p);
-    const Chain &k = w.k;
-    const int warp = w.warp, lane = w.lane, c = w.c, D = p.D;
-    if (p.cu_seqlens && p.ht && w.rank == 0 && w.on && warp < WARPS)   // empty sequences: the state passes through
-        for (int s = k.s0 + warp; s < k.s1; s += WARPS) {
-            const int lo = clamped(p.cu_seqlens[s], 0, p.T), hi = clamped(p.cu_seqlens[s + 1], lo, p.T);
-            if (lo == hi) store_state(p.ht + (long long)s * D, c, D, p.h0 ? load_state(p.h0 + (long long)s * D, c, D) : both(0.f));
+    static constexpr int SIZE = N * S::BYTES, BYTES = STAGES * SIZE;
+    char *base;
+    int to, read;                        // byte offsets of the stage that is filled next, and of the one that is read
+    const T *at[N];                      // this lane's access of the rows that come next
+    long long ld[N];
+    long long next, last;                // those rows' first, and the first of the last ones
+    int left;
+    Extent k;
+
+    __device__ __forceinline__ void begin(char *all, const GatedScanParams &p, const Where &w, const void *const (&from)[N],
+                                          const long long (&stride)[N]) {
+        base = all + (threadIdx.x >> 5) * BYTES;
+        to = 0;
+        read = -SIZE;
+        k = w.k;
+        const long long end = min((long long)k.hi, w.r0 + p.seg), behind = w.r0 + (end - 1 - w.r0) / ROWS * ROWS;
+        next = BACK ? behind : w.r0;
+        last = BACK ? w.r0 : behind;
+        const int c = w.c - w.lane * 2 + S::col();
+        left = p.D - c;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            ld[n] = stride[n];
+            at[n] = static_cast<const T *>(from[n]) + (next + S::row()) * ld[n] + c;
         }
-    if (k.c0 >= k.c1) return;                        // (the whole cluster)
-    if constexpr (CLUSTER) {
-        kda::tc::cluster_sync_all();                 // every block has begun: its shared memory may be written
-        if (warp == WARPS) {
-            exchange_warp<false>(ex, w.turns, lane, w.rank, w.blocks);
-            return;
-        }
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; ++i) bring();
     }
-    const f2 coef = coefficients(p, w.cl);
-    auto bring = [&](int buf, long long r0) {
-        char *to = stages + buf * 3 * S::BYTES;
-        S::bring(to, static_cast<const T *>(p.x), p.ld_x, w.c0, D, r0, k.c0, k.c1);
-        S::bring(to + S::BYTES, static_cast<const T *>(p.decay), p.ld_decay, w.c0, D, r0, k.c0, k.c1);
-        S::bring(to + 2 * S::BYTES, static_cast<const T *>(p.gate), p.ld_gate, w.c0, D, r0, k.c0, k.c1);
+    __device__ __forceinline__ void bring() {
+        if (BACK ? next >= last : next <= last) {
+            if (next >= k.lo && next + ROWS <= k.hi) {
+#pragma unroll
+                for (int n = 0; n < N; ++n) S::bring(base + to + n * S::BYTES, at[n], ld[n], left);
+            } else {
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+                    S::bring_clamped(base + to + n * S::BYTES, at[n] - (next + S::row()) * ld[n], ld[n], left, next, k.lo, k.hi);
+            }
+#pragma unroll
+            for (int n = 0; n < N; ++n) at[n] += (BACK ? -ROWS : ROWS) * ld[n];
+            next += BACK ? -ROWS : ROWS;
+            to = to == (STAGES - 1) * SIZE ? 0 : to + SIZE;
+        }
         copies_end();
-    };
-    long long t0 = (w.tile0 + w.rank) * TILE;        // the tile's first row
-    bring(0, t0);
+    }
+    // The next stage is there, and the one before it has been read by all lanes and is filled again.
+    __device__ __forceinline__ const char *step() {
+        copies_wait<STAGES - 2>();
+        __syncwarp();
+        bring();
+        read = read == (STAGES - 1) * SIZE ? 0 : read + SIZE;
+        return base + read;
+    }
+    static __device__ __forceinline__ f2 pair(const char *st, int n, int row, int lane) { return S::pair(st + n * S::BYTES, row, lane); }
+};
+
+// ------------------------------------------------------------------------------------------ forward
+// A segment's effect is kept as A >= 0 and h; A = -1 says that the link is cut and h alone counts.  (A, h) of a pair of channels
+// lie together, rows of pairs are as wide as D rounded up to even.
+__device__ __forceinline__ void store_segment(const GatedScanParams &p, const Where &w, f2 a, f2 h) {
+    float4 q;
+    unpack2(a, q.x, q.z);
+    unpack2(h, q.y, q.w);
+    reinterpret_cast<float4 *>(p.seg_pair)[(w.seg * ((p.D + 1) & ~1) + w.c) / 2] = q;
+}
+template <class T, int CP, bool WALK, bool SMALL_Q>
+__device__ __forceinline__ void forward_rows(const GatedScanParams &p, const Where &w, f2 coef, Ring<T, CP, 3, false> &ring) {
+    constexpr bool VEC = CP > (int)sizeof(T);
+    const int D = p.D, lane = w.lane;
+    const long long end = min((long long)w.k.hi, w.r0 + p.seg);
+    f2 h = both(0.f), prod = both(1.f);
+    bool cut = false;
+    if (WALK && p.seg_in) h = load_state(p.seg_in + w.seg * D, w.cl, D);      // (the boundary pass leaves there what enters)
     Marks marks;
-    f2 carry = both(0.f);
-    for (int i = 0; i < w.turns; ++i, t0 += (long long)w.blocks * TILE) {
-        copies_wait<0>();
-        sync_rows();                                 // the tile is there, the one before has been read
-        if (i + 1 < w.turns) bring(i + 1 & 1, t0 + (long long)w.blocks * TILE);
-        const char *sx = stages + (i & 1) * 3 * S::BYTES + warp * ROWS * S::ROW, *sd = sx + S::BYTES, *sg = sd + S::BYTES;
-        const long long r0 = t0 + warp * ROWS;
+    for (long long r0 = w.r0; r0 < end; r0 += ROWS) {
+        const char *st = ring.step();
         f2 a[ROWS], v[ROWS];
 #pragma unroll
-        for (int j = 0; j < ROWS; ++j) a[j] = mul2(coef, sigmoid2(S::pair(sd, j, lane)));
-        one_less_exps(a);
-#pragma unroll
         for (int j = 0; j < ROWS; ++j) {
-            const f2 q = a[j];
+            const f2 q = decay_p<SMALL_Q>(coef, ring.pair(st, 1, j, lane));
             a[j] = decay_of(q);
-            v[j] = mul2(mul2(sqrt2(rest_of(q, a[j])), sigmoid2(S::pair(sg, j, lane))), S::pair(sx, j, lane));
+            v[j] = input_v(q, a[j], ring.pair(st, 2, j, lane), ring.pair(st, 0, j, lane));
         }
-        marks.find(p, k, r0);
+        marks.find(p, w.k, r0);
         const unsigned starts = marks.starts, ends = marks.ends;
-        f2 h = v[0], prod = a[0];
-        if (starts == 0) {
+        if (WALK && p.states && r0 >= w.k.lo && w.on) store_state(p.states + r0 / ROWS * D, w.c, D, h);
+        if ((starts | ends) == 0 && r0 >= w.k.lo && r0 + ROWS <= w.k.hi) {
+            T *y = static_cast<T *>(p.y) + r0 * p.ld_y + w.c;
 #pragma unroll
-            for (int j = 1; j < ROWS; ++j) {
+            for (int j = 0; j < ROWS; ++j) {
                 h = fma2(a[j], h, v[j]);
-                prod = mul2(prod, a[j]);
+                if (WALK) v[j] = h;
+                else prod = mul2(prod, a[j]);
             }
+            if (WALK && p.y && w.on)
+#pragma unroll
+                for (int j = 0; j < ROWS; ++j, y += p.ld_y) store_pair<T, VEC>(y, 0, D - w.c, v[j]);
         } else {
 #pragma unroll
             for (int j = 0; j < ROWS; ++j) {
+                const long long r = r0 + j;
+                if (r < w.k.lo || r >= w.k.hi) continue;         // (the same for all lanes)
                 if (starts >> j & 1) {
                     h = p.h0 ? fma2(a[j], load_state(p.h0 + (long long)marks.sequence(j) * D, w.cl, D), v[j]) : v[j];
-                    v[j] = h;                        // the walk below begins here anew
-                } else if (j) {
+                    cut = true;
+                } else {
                     h = fma2(a[j], h, v[j]);
                 }
-                if (j) prod = mul2(prod, a[j]);
-            }
-        }
-        h = enter<false, CLUSTER>(ex, i & 1, warp, lane, w.rank, w.blocks, prod, h, starts != 0, carry);
-        if (p.states && warp == 0 && r0 >= k.c0 && r0 < k.c1 && w.on) store_state(p.states + r0 / SAVE * D, c, D, h);
-        if ((starts | ends) == 0 && r0 >= k.c0 && r0 + ROWS <= k.c1) {
-            if (p.y == nullptr) continue;            // (the states alone)
-            T *y = static_cast<T *>(p.y) + r0 * p.ld_y;
-#pragma unroll
-            for (int j = 0; j < ROWS; ++j, y += p.ld_y) {
-                h = fma2(a[j], h, v[j]);
-                if (w.on) store_pair<T, VEC>(y, c, D, h);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < ROWS; ++j) {
-                h = starts >> j & 1 ? v[j] : fma2(a[j], h, v[j]);
-                const long long r = r0 + j;
-                if (w.on && r >= k.c0 && r < k.c1 && p.y) store_pair<T, VEC>(static_cast<T *>(p.y) + r * p.ld_y, c, D, h);
+                if (!WALK) {
+                    prod = mul2(prod, a[j]);
+                    continue;
+                }
+                if (w.on && p.y) store_pair<T, VEC>(static_cast<T *>(p.y) + r * p.ld_y, w.c, D, h);
                 if (ends >> j & 1) {
                     const int s = marks.sequence(j);
-                    if (p.ht && w.on) store_state(p.ht + (long long)s * D, c, D, h);
+                    if (p.ht && w.on) store_state(p.ht + (long long)s * D, w.c, D, h);
                 }
             }
+        }
+    }
+    if (!WALK && w.on) {
+        store_segment(p, w, cut ? both(-1.f) : prod, h);
+    }
+}
+
+template <class T, int CP, bool WALK> __global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 6 : 3) gated_scan_fwd_kernel(GatedScanParams p) {
+    extern __shared__ __align__(16) char rings[];        // [WARPS][Ring::BYTES]
+    const Where w = where<WALK>(p);
+    kda::tc::grid_dep_launch();
+    if (!w.any) return;
+    const bool some = w.r0 < w.k.hi && w.r0 + p.seg > w.k.lo;
+    Ring<T, CP, 3, false> ring;
+    if (some) ring.begin(rings, p, w, {p.x, p.decay, p.gate}, {p.ld_x, p.ld_decay, p.ld_gate});      // (the inputs wait for no pass)
+    const f2 coef = coefficients(p, w.cl);
+    float lo, hi;
+    unpack2(coef, lo, hi);
+    const bool small = __all_sync(~0u, lo < SMALL && hi < SMALL);        // exponents are at most their coefficients
+    if (WALK) kda::tc::grid_dep_wait();
+    if (WALK && p.cu_seqlens && p.ht && w.on)        // empty sequences: the state passes through
+        for (long long s = w.seg; s < p.B; s += w.segs) {
+            const int a = clamped(p.cu_seqlens[s], 0, p.T), b = clamped(p.cu_seqlens[s + 1], a, p.T);
+            if (a == b) store_state(p.ht + s * p.D, w.c, p.D, p.h0 ? load_state(p.h0 + s * p.D, w.c, p.D) : both(0.f));
+        }
+    if (!some) return;
+    if (small) forward_rows<T, CP, WALK, true>(p, w, coef, ring);
+    else forward_rows<T, CP, WALK, false>(p, w, coef, ring);
+}
+
+// What enters each segment.  32 channels to a block, its warps 8 segments each at a time; BACK: from the last segment to the first.
+constexpr int BWARPS = 16, BEACH = 8;
+template <bool BACK> __global__ void __launch_bounds__(32 * BWARPS) gated_scan_boundary_kernel(GatedScanParams p) {
+    __shared__ float2 sm[BWARPS][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, D = p.D, pitch = (D + 1) & ~1;
+    const int c = min((int)blockIdx.x * 32 + lane, D - 1);               // (lanes past the end repeat the last channel)
+    const int segs = (int)((rows_of(p) + p.seg - 1) / p.seg);
+    const Extent k = extent_of(p);
+    const int s0 = k.lo / p.seg, s1 = min(segs, (int)(((long long)k.hi + p.seg - 1) / p.seg)), n = s1 - s0;
+    kda::tc::grid_dep_launch();
+    kda::tc::grid_dep_wait();
+    float carry = 0.f;
+    for (int base = 0; base < n; base += BWARPS * BEACH) {
+        const int i0 = base + warp * BEACH, at = BACK ? s1 - 1 - i0 : s0 + i0;
+        const float2 *from = reinterpret_cast<const float2 *>(p.seg_pair) + (long long)at * pitch + c;
+        float2 g[BEACH];
+#pragma unroll
+        for (int j = 0; j < BEACH; ++j) g[j] = i0 + j < n ? from[(BACK ? -j : j) * (long long)pitch] : make_float2(1.f, 0.f);
+        float pa = 1.f, ph = 0.f;
+        bool cut = false;
+#pragma unroll
+        for (int j = 0; j < BEACH; ++j) {
+            const bool here = g[j].x == -1.f;
+            ph = here || j == 0 ? g[j].y : fmaf(g[j].x, ph, g[j].y);
+            cut |= here;
+            pa *= g[j].x;
+        }
+        __syncthreads();                             // the last round's pairs have been read
+        sm[warp][lane] = make_float2(cut ? -1.f : pa, ph);
+        __syncthreads();
+        float in = carry;
+#pragma unroll
+        for (int q = 0; q < BWARPS; ++q) {
+            if (q == warp) in = carry;
+            const float2 t = sm[q][lane];
+            carry = t.x == -1.f ? t.y : fmaf(t.x, carry, t.y);
+        }
+        float *to = p.seg_in + (long long)at * D + c;
+#pragma unroll
+        for (int j = 0; j < BEACH; ++j) {
+            if (i0 + j < n) to[(BACK ? -j : j) * (long long)D] = in;
+            in = g[j].x == -1.f ? g[j].y : fmaf(g[j].x, in, g[j].y);
         }
     }
 }
 
 // ------------------------------------------------------------------------------------------ backward
-// With q the exponent, s and u the two sigmoids, v = u x and G_t the gradient of h_t:
-//     dq = G (v a^2 / m - a h_{t-1}),  ddecay = dq q (1 - s),  drate = scale sigmoid(rate) sum dq s,
-//     dx = G m u,  dgate = G m x u (1 - u),  dh0 = a G of the first token.
-// The first walk keeps 1 - a, m v and dy in registers; the second takes the inputs from shared memory once more.
-template <class T, int CP, bool CLUSTER>
-__global__ void __launch_bounds__(LANES + (CLUSTER ? 32 : 0), sizeof(T) == 2 ? 2 : 1) gated_scan_bwd_kernel(GatedScanParams p) {
-    using S = Stage<T, CP>;
-    constexpr bool VEC = CP > (int)sizeof(T);
-    extern __shared__ __align__(16) char stages[];   // [2][4][S::BYTES]
-    __shared__ Exchange ex;
-    __shared__ float4 fwd[2][WARPS][32];             // (A, h) of the warps' rows, first to last
-    __shared__ int fwd_cut[2][WARPS];
-    const Where w = where(p);
-    const Chain &k = w.k;
-    const int warp = w.warp, lane = w.lane, c = w.c, D = p.D;
-    float *part = p.part + ((long long)blockIdx.y * w.blocks + w.rank) * D;
-    if (p.cu_seqlens && p.dh0 && w.rank == 0 && w.on && warp < WARPS)  // empty sequences hand the gradient through
-        for (int s = k.s0 + warp; s < k.s1; s += WARPS) {
-            const int lo = clamped(p.cu_seqlens[s], 0, p.T), hi = clamped(p.cu_seqlens[s + 1], lo, p.T);
-            if (lo == hi) store_state(p.dh0 + (long long)s * D, c, D, p.dht ? load_state(p.dht + (long long)s * D, c, D) : both(0.f));
-        }
-    if (k.c0 >= k.c1) {                              // (the whole cluster)
-        if (warp == 0 && w.on) store_state(part, c, D, both(0.f));
-        return;
-    }
-    if constexpr (CLUSTER) {
-        kda::tc::cluster_sync_all();                 // every block has begun: its shared memory may be written
-        if (warp == WARPS) {
-            exchange_warp<true>(ex, w.turns, lane, w.rank, w.blocks);
-            return;
-        }
-    }
-    const f2 coef = coefficients(p, w.cl), minus = both(-1.f), one = both(1.f);
-    auto bring = [&](int buf, long long r0) {
-        char *to = stages + buf * 4 * S::BYTES;
-        S::bring(to, static_cast<const T *>(p.x), p.ld_x, w.c0, D, r0, k.c0, k.c1);
-        S::bring(to + S::BYTES, static_cast<const T *>(p.decay), p.ld_decay, w.c0, D, r0, k.c0, k.c1);
-        S::bring(to + 2 * S::BYTES, static_cast<const T *>(p.gate), p.ld_gate, w.c0, D, r0, k.c0, k.c1);
-        S::bring(to + 3 * S::BYTES, static_cast<const T *>(p.dy), p.ld_dy, w.c0, D, r0, k.c0, k.c1);
-        copies_end();
-    };
-    // The state that enters a tile (one that begins outside the chain has none and needs none).
-    auto saved_at = [&](long long top) {
-        return top >= k.c0 && top < k.c1 ? load_state(p.states + top / SAVE * D, w.cl, D) : both(0.f);
-    };
-    // The cluster's tiles of a turn are neighbours, the last block's the last; turns go from the end.
-    const long long step = (long long)w.blocks * TILE;
-    long long t0 = (w.tile0 + (long long)(w.turns - 1) * w.blocks + w.rank) * TILE;
-    bring(0, t0);
-    f2 saved = saved_at(t0);
+// The first row of a segment's last eight.
+__device__ __forceinline__ long long last_rows(const GatedScanParams &p, const Where &w) {
+    const long long end = min((long long)w.k.hi, w.r0 + p.seg);
+    return w.r0 + (end - 1 - w.r0) / ROWS * ROWS;
+}
+// The local pass: what a segment does to the gradient that comes from behind it, a_t G_t of its first token.
+template <class T, int CP, bool SMALL_Q>
+__device__ __forceinline__ void backward_local(const GatedScanParams &p, const Where &w, f2 coef, Ring<T, CP, 2, true> &ring) {
+    const int D = p.D, lane = w.lane;
+    f2 g = both(0.f), prod = both(1.f);
+    bool cut = false;
     Marks marks;
-    f2 carry = both(0.f), sum = both(0.f);
-    for (int i = 0; i < w.turns; ++i, t0 -= step) {
-        copies_wait<0>();
-        sync_rows();                                 // the tile is there, the one before has been read
-        f2 h = saved;
-        if (i + 1 < w.turns) {
-            bring(i + 1 & 1, t0 - step);
-            saved = saved_at(t0 - step);
-        }
-        const char *sx = stages + (i & 1) * 4 * S::BYTES + warp * ROWS * S::ROW, *sd = sx + S::BYTES, *sg = sd + S::BYTES, *sy = sg + S::BYTES;
-        const long long r0 = t0 + warp * ROWS;
-        f2 q[ROWS], v[ROWS], gy[ROWS];               // 1 - a; m u x, then the state before each row; dy
-#pragma unroll
-        for (int j = 0; j < ROWS; ++j) q[j] = mul2(coef, sigmoid2(S::pair(sd, j, lane)));
-        one_less_exps(q);
+    for (long long r0 = last_rows(p, w); r0 >= w.r0; r0 -= ROWS) {
+        const char *st = ring.step();
+        f2 a[ROWS], gy[ROWS];
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
-            v[j] = mul2(mul2(sqrt2(rest_of(q[j], decay_of(q[j]))), sigmoid2(S::pair(sg, j, lane))), S::pair(sx, j, lane));
-            gy[j] = S::pair(sy, j, lane);
+            a[j] = decay_of(decay_p<SMALL_Q>(coef, ring.pair(st, 0, j, lane)));
+            gy[j] = ring.pair(st, 1, j, lane);
         }
-        marks.find(p, k, r0);
-        const unsigned starts = marks.starts, ends = marks.ends;
-        // both walks over this warp's rows alone: the states from 0, the gradients from 0
-        f2 hw = v[0], prod = decay_of(q[0]), gw = mul2(decay_of(q[ROWS - 1]), gy[ROWS - 1]);
-        if ((starts | ends) == 0) {
-#pragma unroll
-            for (int j = 1; j < ROWS; ++j) {
-                const f2 a = decay_of(q[j]);
-                hw = fma2(a, hw, v[j]);
-                prod = mul2(prod, a);
-            }
-#pragma unroll
-            for (int j = ROWS - 2; j >= 0; --j) gw = mul2(decay_of(q[j]), add2(gy[j], gw));
-        } else {
-#pragma unroll
-            for (int j = 0; j < ROWS; ++j) {
-                const f2 a = decay_of(q[j]);
-                if (starts >> j & 1) hw = p.h0 ? fma2(a, load_state(p.h0 + (long long)marks.sequence(j) * D, w.cl, D), v[j]) : v[j];
-                else if (j) hw = fma2(a, hw, v[j]);
-                if (j) prod = mul2(prod, a);
-            }
+        marks.find(p, w.k, r0);
+        const unsigned ends = marks.ends;
+        if (ends == 0 && r0 >= w.k.lo && r0 + ROWS <= w.k.hi) {
 #pragma unroll
             for (int j = ROWS - 1; j >= 0; --j) {
-                const f2 a = decay_of(q[j]);
-                if (ends >> j & 1) {
-                    const f2 g = p.dht ? load_state(p.dht + (long long)marks.sequence(j) * D, w.cl, D) : both(0.f);
-                    gy[j] = add2(gy[j], g);          // the walk below begins here anew
-                    gw = mul2(a, gy[j]);
-                } else if (j < ROWS - 1) {
-                    gw = mul2(a, add2(gy[j], gw));
-                }
-            }
-        }
-        fwd[i & 1][warp][lane] = quad(prod, hw);
-        if (lane == 0) fwd_cut[i & 1][warp] = starts != 0;
-        f2 grad = enter<true, CLUSTER>(ex, i & 1, warp, lane, w.rank, w.blocks, prod, gw, ends != 0, carry);
-        for (int b = 0; b < warp; ++b) h = through(fwd[i & 1][b][lane], fwd_cut[i & 1][b], h);
-        // the state before each row takes the place of its input
-        if (starts == 0) {
-#pragma unroll
-            for (int j = 0; j < ROWS; ++j) {
-                const f2 t = v[j];
-                v[j] = h;
-                h = fma2(decay_of(q[j]), h, t);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < ROWS; ++j) {
-                if (starts >> j & 1) h = p.h0 ? load_state(p.h0 + (long long)marks.sequence(j) * D, w.cl, D) : both(0.f);
-                const f2 t = v[j];
-                v[j] = h;
-                h = fma2(decay_of(q[j]), h, t);
-            }
-        }
-        auto row = [&](int j, f2 G, f2 aG, T *pd, T *px, T *pg) {
-            const f2 s = sigmoid2(S::pair(sd, j, lane)), u = sigmoid2(S::pair(sg, j, lane)), a = decay_of(q[j]), r = rest_of(q[j], a);
-            float w0, w1;
-            unpack2(r, w0, w1);      // 1 - a^2 of 0 (no decay at all): its root's reciprocal stays finite, so that times q = 0 it is 0
-            const f2 rm = pack2(rsqrt_fast(fmaxf(w0, 1e-36f)), rsqrt_fast(fmaxf(w1, 1e-36f)));
-            const f2 vx = mul2(u, S::pair(sx, j, lane)), gm = mul2(G, mul2(r, rm));
-            const f2 ds = mul2(mul2(aG, fma2(mul2(vx, a), rm, mul2(v[j], minus))), s);      // a G (v a / m - h) s
-            sum = add2(sum, ds);
-            if (!w.on) return;
-            store_pair<T, VEC>(pd, c, D, mul2(mul2(ds, coef), fma2(s, minus, one)));
-            store_pair<T, VEC>(px, c, D, mul2(gm, u));
-            store_pair<T, VEC>(pg, c, D, mul2(mul2(gm, vx), fma2(u, minus, one)));
-        };
-        T *od = static_cast<T *>(p.ddecay) + (r0 + ROWS - 1) * p.ld_ddecay, *ox = static_cast<T *>(p.dx) + (r0 + ROWS - 1) * p.ld_dx,
-          *og = static_cast<T *>(p.dgate) + (r0 + ROWS - 1) * p.ld_dgate;
-        if ((starts | ends) == 0 && r0 >= k.c0 && r0 + ROWS <= k.c1) {
-#pragma unroll
-            for (int j = ROWS - 1; j >= 0; --j) {
-                const f2 G = add2(gy[j], grad);
-                grad = mul2(decay_of(q[j]), G);
-                row(j, G, grad, od, ox, og);
-                od -= p.ld_ddecay;
-                ox -= p.ld_dx;
-                og -= p.ld_dgate;
+                g = mul2(a[j], add2(gy[j], g));
+                prod = mul2(prod, a[j]);
             }
         } else {
 #pragma unroll
             for (int j = ROWS - 1; j >= 0; --j) {
                 const long long r = r0 + j;
-                const f2 G = ends >> j & 1 ? gy[j] : add2(gy[j], grad);
-                grad = mul2(decay_of(q[j]), G);
-                if (starts >> j & 1) {
-                    const int b = marks.sequence(j);
-                    if (p.dh0 && w.on) store_state(p.dh0 + (long long)b * D, c, D, grad);
+                if (r < w.k.lo || r >= w.k.hi) continue;
+                if (ends >> j & 1) {
+                    g = p.dht ? load_state(p.dht + (long long)marks.sequence(j) * D, w.cl, D) : both(0.f);
+                    cut = true;
                 }
-                if (r >= k.c0 && r < k.c1) row(j, G, grad, od, ox, og);      // (the same for all lanes of a warp)
-                od -= p.ld_ddecay;
-                ox -= p.ld_dx;
-                og -= p.ld_dgate;
+                g = mul2(a[j], add2(gy[j], g));
+                prod = mul2(prod, a[j]);
             }
         }
     }
-    sync_rows();                                     // the exchange's last set has been read
-    ex.warp[0][warp][lane] = quad(sum, sum);
-    sync_rows();
-    if (warp == 0 && w.on) {
-        f2 t = both(0.f);
+    if (w.on) {
+        store_segment(p, w, cut ? both(-1.f) : prod, g);
+    }
+}
+template <class T, int CP> __global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 6 : 4) gated_scan_bwd_local_kernel(GatedScanParams p) {
+    extern __shared__ __align__(16) char rings[];        // [WARPS][Ring::BYTES]
+    const Where w = where<false>(p);
+    kda::tc::grid_dep_launch();
+    if (!w.any || w.r0 >= w.k.hi || w.r0 + p.seg <= w.k.lo) return;
+    Ring<T, CP, 2, true> ring;
+    ring.begin(rings, p, w, {p.decay, p.dy}, {p.ld_decay, p.ld_dy});
+    const f2 coef = coefficients(p, w.cl);
+    float lo, hi;
+    unpack2(coef, lo, hi);
+    if (__all_sync(~0u, lo < SMALL && hi < SMALL)) backward_local<T, CP, true>(p, w, coef, ring);
+    else backward_local<T, CP, false>(p, w, coef, ring);
+}
+
+// With q the exponent, s and u the two sigmoids, v = u x and G_t the gradient of h_t:
+//     dq = G (v a^2 / m - a h_{t-1}),  ddecay = dq q (1 - s),  drate = scale sigmoid(rate) sum dq s,
+//     dx = G m u,  dgate = G m x u (1 - u),  dh0 = a G of the first token.
+// Eight rows at a time from the last: forward through them from the saved state, then back.  Their inputs wait in a ring
+// of this warp's in shared memory, for both ways take them.
+template <class T, int CP, bool SMALL_Q>
+__device__ __forceinline__ f2 backward_rows(const GatedScanParams &p, const Where &w, f2 coef, Ring<T, CP, 4, true> &ring) {
+    using S = Stage<T, CP>;
+    constexpr bool VEC = CP > (int)sizeof(T);
+    const int D = p.D, lane = w.lane;
+    const f2 minus = both(-1.f), one = both(1.f);
+    // (eight rows of which the first lie outside have no saved state and need none)
+    auto saved_at = [&](long long r0) { return r0 >= w.k.lo ? load_state(p.states + r0 / ROWS * D, w.cl, D) : both(0.f); };
+    f2 sum = both(0.f);
+    Marks marks;
+    long long r0 = last_rows(p, w);
+    f2 saved = saved_at(r0);
+    f2 grad = p.seg_in ? load_state(p.seg_in + w.seg * D, w.cl, D) : both(0.f);
+    for (; r0 >= w.r0; r0 -= ROWS) {
+        const char *sx = ring.step();
+        f2 h = saved;
+        if (r0 > w.r0) saved = saved_at(r0 - ROWS);
+        const char *sd = sx + S::BYTES, *sg = sd + S::BYTES, *sy = sg + S::BYTES;
+        marks.find(p, w.k, r0);
+        const unsigned starts = marks.starts, ends = marks.ends;
+        f2 q[ROWS], before[ROWS];        // 1 - a; the state before each row
+        if (starts == 0) {
 #pragma unroll
-        for (int b = 0; b < WARPS; ++b) t = add2(t, pack2(ex.warp[0][b][lane].x, ex.warp[0][b][lane].y));
-        const float e0 = p.rate[c], e1 = p.rate[min(c + 1, D - 1)];
-        store_state(part, c, D, mul2(t, pack2(p.scale * sigmoid(e0), p.scale * sigmoid(e1))));
+            for (int j = 0; j < ROWS; ++j) {
+                q[j] = decay_p<SMALL_Q>(coef, S::pair(sd, j, lane));
+                before[j] = h;
+                if (j + 1 < ROWS) {
+                    const f2 a = decay_of(q[j]);
+                    h = fma2(a, h, input_v(q[j], a, S::pair(sg, j, lane), S::pair(sx, j, lane)));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j) {
+                q[j] = decay_p<SMALL_Q>(coef, S::pair(sd, j, lane));
+                if (starts >> j & 1) h = p.h0 ? load_state(p.h0 + (long long)marks.sequence(j) * D, w.cl, D) : both(0.f);
+                before[j] = h;
+                const f2 a = decay_of(q[j]);
+                h = fma2(a, h, input_v(q[j], a, S::pair(sg, j, lane), S::pair(sx, j, lane)));
+            }
+        }
+        // a row's outputs from G; leaves a G in grad
+        auto row = [&](int j, f2 G, T *pd, T *px, T *pg) {
+            const f2 s = sigmoid2(S::pair(sd, j, lane)), u = sigmoid2(S::pair(sg, j, lane)), a = decay_of(q[j]), r = rest_of(q[j], a);
+            float w0, w1;
+            unpack2(r, w0, w1);          // 1 - a^2 of 0 (no decay at all): its root's reciprocal stays finite, so that times q = 0 it is 0
+            const f2 rm = pack2(rsqrt_fast(fmaxf(w0, 1e-36f)), rsqrt_fast(fmaxf(w1, 1e-36f)));
+            const f2 v = mul2(u, S::pair(sx, j, lane)), gm = mul2(G, mul2(r, rm));
+            grad = mul2(a, G);
+            const f2 ds = mul2(mul2(grad, fma2(mul2(v, a), rm, mul2(before[j], minus))), s);     // a G (v a / m - h) s
+            sum = add2(sum, ds);
+            if (!w.on) return;
+            store_pair<T, VEC>(pd, w.c, D, mul2(mul2(ds, coef), fma2(s, minus, one)));
+            store_pair<T, VEC>(px, w.c, D, mul2(gm, u));
+            store_pair<T, VEC>(pg, w.c, D, mul2(mul2(gm, v), fma2(u, minus, one)));
+        };
+        T *od = static_cast<T *>(p.ddecay) + (r0 + ROWS - 1) * p.ld_ddecay, *ox = static_cast<T *>(p.dx) + (r0 + ROWS - 1) * p.ld_dx,
+          *og = static_cast<T *>(p.dgate) + (r0 + ROWS - 1) * p.ld_dgate;
+        if ((starts | ends) == 0 && r0 >= w.k.lo && r0 + ROWS <= w.k.hi) {
+#pragma unroll
+            for (int j = ROWS - 1; j >= 0; --j, od -= p.ld_ddecay, ox -= p.ld_dx, og -= p.ld_dgate)
+                row(j, add2(S::pair(sy, j, lane), grad), od, ox, og);
+        } else {
+#pragma unroll
+            for (int j = ROWS - 1; j >= 0; --j, od -= p.ld_ddecay, ox -= p.ld_dx, og -= p.ld_dgate) {
+                const long long r = r0 + j;
+                if (r < w.k.lo || r >= w.k.hi) continue;         // (the same for all lanes)
+                if (ends >> j & 1) grad = p.dht ? load_state(p.dht + (long long)marks.sequence(j) * D, w.cl, D) : both(0.f);
+                row(j, add2(S::pair(sy, j, lane), grad), od, ox, og);
+                if (starts >> j & 1) {
+                    const int b = marks.sequence(j);
+                    if (p.dh0 && w.on) store_state(p.dh0 + (long long)b * D, w.c, D, grad);
+                }
+            }
+        }
+    }
+    return sum;
+}
+template <class T, int CP> __global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 4 : 2) gated_scan_bwd_kernel(GatedScanParams p) {
+    extern __shared__ __align__(16) char rings[];        // [WARPS][Ring::BYTES]
+    const Where w = where<false>(p);
+    kda::tc::grid_dep_launch();
+    if (!w.any) return;
+    const bool some = w.r0 < w.k.hi && w.r0 + p.seg > w.k.lo;
+    Ring<T, CP, 4, true> ring;
+    if (some) ring.begin(rings, p, w, {p.x, p.decay, p.gate, p.dy}, {p.ld_x, p.ld_decay, p.ld_gate, p.ld_dy});   // (the inputs wait for no pass)
+    kda::tc::grid_dep_wait();
+    const int D = p.D;
+    if (p.cu_seqlens && p.dh0 && w.on)                   // empty sequences hand the gradient through
+        for (long long s = w.seg; s < p.B; s += w.segs) {
+            const int a = clamped(p.cu_seqlens[s], 0, p.T), b = clamped(p.cu_seqlens[s + 1], a, p.T);
+            if (a == b) store_state(p.dh0 + s * D, w.c, D, p.dht ? load_state(p.dht + s * D, w.c, D) : both(0.f));
+        }
+    f2 sum = both(0.f);
+    if (some) {
+        const f2 coef = coefficients(p, w.cl);
+        float lo, hi;
+        unpack2(coef, lo, hi);
+        if (__all_sync(~0u, lo < SMALL && hi < SMALL)) sum = backward_rows<T, CP, true>(p, w, coef, ring);
+        else sum = backward_rows<T, CP, false>(p, w, coef, ring);
+    }
+    if (w.on) {
+        const float e0 = p.rate[w.c], e1 = p.rate[min(w.c + 1, D - 1)];
+        store_state(p.part + w.seg * D, w.c, D, mul2(sum, pack2(p.scale * sigmoid(e0), p.scale * sigmoid(e1))));
     }
 }
 
@@ -453,7 +445,7 @@ template <class T, bool VEC> __global__ void __launch_bounds__(128) gated_scan_s
     float *state = p.state + (long long)slot * D;
     const f2 old = load_state(state, c, D);
     const f2 q = one_less_exp(mul2(coefficients(p, c), sigmoid2(d))), a = decay_of(q);
-    const f2 h = fma2(a, old, mul2(mul2(sqrt2(rest_of(q, a)), sigmoid2(g)), x));
+    const f2 h = fma2(a, old, input_v(q, a, g, x));
     store_state(state, c, D, h);
     store_pair<T, VEC>(y, c, D, h);
 }
@@ -461,7 +453,7 @@ template <class T, bool VEC> __global__ void __launch_bounds__(128) gated_scan_s
 // The largest access (16, 4 bytes, or an element) that the bases, the rows and D of a call's tensors allow.
 int access_of(const GatedScanParams &p, bool bf16) {
     const size_t es = bf16 ? 2 : 4;
-    for (int n = 16; n > (int)es; n = n == 16 ? 4 : 0)
+    for (int n = 16; n > (int)es; n = n == 16 ? (bf16 ? 4 : 8) : 0)
         if (p.D * es % n == 0 && rows_aligned(p.x, p.ld_x, es, n) && rows_aligned(p.decay, p.ld_decay, es, n) &&
             rows_aligned(p.gate, p.ld_gate, es, n) && rows_aligned(p.y, p.ld_y, es, n) && rows_aligned(p.dy, p.ld_dy, es, n) &&
             rows_aligned(p.dx, p.ld_dx, es, n) && rows_aligned(p.ddecay, p.ld_ddecay, es, n) && rows_aligned(p.dgate, p.ld_dgate, es, n))
@@ -469,72 +461,103 @@ int access_of(const GatedScanParams &p, bool bf16) {
     return (int)es;
 }
 
-template <class T, int CP, bool CLUSTER, bool BWD> cudaError_t launch(const GatedScanParams &p, cudaStream_t s) {
-    const auto kernel = BWD ? gated_scan_bwd_kernel<T, CP, CLUSTER> : gated_scan_fwd_kernel<T, CP, CLUSTER>;
+// Rows of a segment: 64, or as few as 16 where that leaves less than eight warps to an SM.
+int segment_of(const GatedScanParams &p) {
+    const long long cols = (p.D - 1) / COLS + 1, rows = rows_of(p);
+    int seg = 64;
+    while (seg > 16 && cols * ((rows + seg - 1) / seg) < 8LL * sm_count()) seg /= 2;
+    return seg;
+}
+long long segments_of(const GatedScanParams &p) {
+    const int seg = segment_of(p);
+    return (rows_of(p) + seg - 1) / seg;
+}
+unsigned blocks_of(const GatedScanParams &p) {
+    const long long cols = (p.D - 1) / COLS + 1;
+    return (unsigned)((cols * segments_of(p) + WARPS - 1) / WARPS);
+}
+
+// A kernel whose blocks may set up while the one before it ends; they wait for it themselves.
+cudaError_t launch(void (*kernel)(GatedScanParams), unsigned grid, int threads, size_t smem, bool after, const GatedScanParams &p, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.D - 1) / COLS + 1) * p.cluster, p.chains);
-    cfg.blockDim = dim3(LANES + (CLUSTER ? 32 : 0));
-    cfg.dynamicSmemBytes = 2 * (BWD ? 4 : 3) * Stage<T, CP>::BYTES;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
-    if (e != cudaSuccess) return e;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = p.cluster;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = CLUSTER ? 1 : 0;
+    cfg.numAttrs = after ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
-template <class T, int CP, bool BWD> cudaError_t launch(const GatedScanParams &p, cudaStream_t s) {
-    return p.cluster > 1 ? launch<T, CP, true, BWD>(p, s) : launch<T, CP, false, BWD>(p, s);
+
+template <class T, int CP> cudaError_t forward(GatedScanParams &p, cudaStream_t s) {
+    constexpr size_t smem = WARPS * Ring<T, CP, 3, false>::BYTES;
+    const unsigned n = blocks_of(p);
+    if (segments_of(p) == 1) {
+        p.seg_in = nullptr;            // nothing enters the only segment
+        return launch(gated_scan_fwd_kernel<T, CP, true>, n, THREADS, smem, false, p, s);
+    }
+    cudaError_t e = launch(gated_scan_fwd_kernel<T, CP, false>, n, THREADS, smem, false, p, s);
+    if (e == cudaSuccess) e = launch(gated_scan_boundary_kernel<false>, (unsigned)((p.D - 1) / 32 + 1), 32 * BWARPS, 0, true, p, s);
+    if (e == cudaSuccess) e = launch(gated_scan_fwd_kernel<T, CP, true>, n, THREADS, smem, true, p, s);
+    return e;
 }
-template <bool BWD> cudaError_t launch(const GatedScanParams &p, bool bf16_, cudaStream_t s) {
+template <class T, int CP> cudaError_t backward(GatedScanParams &p, cudaStream_t s) {
+    const unsigned n = blocks_of(p);
+    const bool one = segments_of(p) == 1;
+    cudaError_t e = cudaSuccess;
+    if (one) p.seg_in = nullptr;
+    else {
+        e = launch(gated_scan_bwd_local_kernel<T, CP>, n, THREADS, WARPS * Ring<T, CP, 2, true>::BYTES, false, p, s);
+        if (e == cudaSuccess) e = launch(gated_scan_boundary_kernel<true>, (unsigned)((p.D - 1) / 32 + 1), 32 * BWARPS, 0, true, p, s);
+    }
+    if (e == cudaSuccess) e = launch(gated_scan_bwd_kernel<T, CP>, n, THREADS, WARPS * Ring<T, CP, 4, true>::BYTES, !one, p, s);
+    return e;
+}
+template <bool BWD, class T, int CP> cudaError_t run(GatedScanParams &p, cudaStream_t s) {
+    if constexpr (BWD) return backward<T, CP>(p, s);
+    else return forward<T, CP>(p, s);
+}
+template <bool BWD> cudaError_t run(GatedScanParams &p, bool bf16_, cudaStream_t s) {
+    p.seg = segment_of(p);
     const int n = access_of(p, bf16_);
-    if (bf16_) return n == 16 ? launch<bf16, 16, BWD>(p, s) : n == 4 ? launch<bf16, 4, BWD>(p, s) : launch<bf16, 2, BWD>(p, s);
-    return n == 16 ? launch<float, 16, BWD>(p, s) : launch<float, 4, BWD>(p, s);
+    if (bf16_) return n == 16 ? run<BWD, bf16, 16>(p, s) : n == 4 ? run<BWD, bf16, 4>(p, s) : run<BWD, bf16, 2>(p, s);
+    return n == 16 ? run<BWD, float, 16>(p, s) : n == 8 ? run<BWD, float, 8>(p, s) : run<BWD, float, 4>(p, s);
 }
-
-long long rows_of(const GatedScanParams &p) { return (long long)(p.cu_seqlens ? 1 : p.B) * p.T; }
-
-// Chains side by side cost nothing, so there are as many as fill the GPU, up to one per sequence; what they leave idle,
-// clusters of up to eight blocks fill by sharing a chain's tiles.  All blocks run at once: a few more than fit would run alone
-// after the others.
-void split(GatedScanParams &p, int per_sm) {
-    const long long cols = (p.D - 1) / COLS + 1, room = (long long)per_sm * sm_count(), rows = rows_of(p);
-    long long each = (cols * p.B + room - 1) / room;             // sequences of a chain
-    if (each < 1) each = 1;
-    p.chains = (int)((p.B + each - 1) / each);
-    p.cluster = 1;
-    // (a cluster's blocks need a place in one group of SMs: of these up to a seventh stays empty)
-    while (p.cluster < MAX_CLUSTER && cols * p.chains * p.cluster * 2 <= room * 6 / 7 && rows > (long long)TILE * p.chains * p.cluster)
-        p.cluster *= 2;
-}
-void split_fwd(GatedScanParams &p, bool bf16_) { split(p, bf16_ ? 3 : 2); }
-void split_bwd(GatedScanParams &p, bool bf16_) { split(p, bf16_ ? 2 : 1); }
 
 }  // namespace
 
-size_t gated_scan_saved_rows(const GatedScanParams &p) { return (size_t)((rows_of(p) + SAVE - 1) / SAVE); }
+size_t gated_scan_saved_rows(const GatedScanParams &p) { return (size_t)((rows_of(p) + ROWS - 1) / ROWS); }
 
-size_t gated_scan_part_floats(const GatedScanParams &p, bool bf16_) {
-    GatedScanParams q = p;
-    split_bwd(q, bf16_);
-    return (size_t)q.chains * q.cluster * p.D;
+static size_t pair_floats(const GatedScanParams &p) { return 2 * (size_t)segments_of(p) * ((p.D + 1) & ~1); }
+size_t gated_scan_fwd_floats(const GatedScanParams &p) {
+    const size_t n = (size_t)segments_of(p);
+    return n > 1 ? pair_floats(p) + n * p.D : 0;
+}
+size_t gated_scan_bwd_floats(const GatedScanParams &p) { return pair_floats(p) + 2 * (size_t)segments_of(p) * p.D; }
+void gated_scan_carve(GatedScanParams &p, float *ws) {
+    const size_t n = (size_t)segments_of(p) * p.D;
+    p.seg_pair = ws;                     // (16-byte aligned)
+    p.seg_in = ws + pair_floats(p);
+    p.part = p.seg_in + n;               // (the forward has no such part)
 }
 
 cudaError_t launch_gated_scan_fwd(const GatedScanParams &q, bool bf16_, cudaStream_t s) {
     GatedScanParams p = q;
-    split_fwd(p, bf16_);
-    return launch<false>(p, bf16_, s);
+    return run<false>(p, bf16_, s);
 }
 
 cudaError_t launch_gated_scan_bwd(const GatedScanParams &q, bool bf16_, cudaStream_t s) {
     GatedScanParams p = q;
-    split_bwd(p, bf16_);
-    const cudaError_t e = launch<true>(p, bf16_, s);
+    const cudaError_t e = run<true>(p, bf16_, s);
     if (e != cudaSuccess) return e;
-    return launch_sum_rows(p.part, p.chains * p.cluster, SumOut{p.drate, p.D, false}, SumOut{nullptr, 0, false}, s);
+    return launch_sum_rows(p.part, (int)segments_of(p), SumOut{p.drate, p.D, false}, SumOut{nullptr, 0, false}, s);
 }
 
 cudaError_t launch_gated_scan_step(const GatedScanParams &p, bool bf16_, cudaStream_t s) {

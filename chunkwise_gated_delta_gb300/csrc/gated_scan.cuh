@@ -15,43 +15,62 @@
 namespace mixer {
 namespace gs {
 
-constexpr int WARPS = 8, LANES = 32 * WARPS;     // warps that walk rows, their threads
-constexpr int ROWS = 8, TILE = ROWS * WARPS;      // rows of a warp and of a block's tile
-constexpr int COLS = 64;                          // channels of a block, two per lane
-constexpr int SAVE = GATED_SCAN_STATE_ROWS;       // rows from one saved state to the next
-static_assert(SAVE == TILE, "a saved state enters every tile of the backward");
+constexpr int WARPS = 4, THREADS = 32 * WARPS;
+constexpr int COLS = 64;                          // channels of a warp, two per lane
+constexpr int ROWS = GATED_SCAN_STATE_ROWS;       // rows that a warp has in hand at a time
 
-// A tile's rows of one tensor in shared memory, and how they get there: accesses of CP bytes, asynchronous ones of 16 or
-// 4 bytes, or single bfloat16 elements (CP = 2).  Rows past the chain are its first or last, channels past D are
+// Two neighbouring channels of a row as they lie in memory: one access, or two with the channel past an odd end
+// replaced by the last.
+template <class T, bool VEC> struct Raw {
+    Lanes<T, 2> v;
+    __device__ __forceinline__ void load(const T *row, int c, int) { v.load(row + c); }
+    __device__ __forceinline__ f2 pair() const { return v.pair(0); }
+};
+template <class T> struct Raw<T, false> {
+    uint32_t w[2];
+    __device__ __forceinline__ void load(const T *row, int c, int D) {
+        w[0] = load_bits(row + c);
+        w[1] = load_bits(row + min(c + 1, D - 1));
+    }
+    __device__ __forceinline__ f2 pair() const { return pack2(bits_f<T>(w[0]), bits_f<T>(w[1])); }
+};
+// ROWS rows of a warp's channels in shared memory, and how they get there: accesses of CP bytes, asynchronous ones of 16
+// or 4 bytes, or single bfloat16 elements (CP = 2).  Rows past the call's are its first or last, channels past D are
 // left out (their lanes write nothing).
 template <class T, int CP> struct Stage {
-    static constexpr int ROW = COLS * (int)sizeof(T), BYTES = TILE * ROW;
-    static constexpr int PER = ROW / CP, STEP = LANES / PER < 1 ? 1 : LANES / PER;    // accesses of a row, rows at a time
-    static constexpr int E = CP / (int)sizeof(T) < 1 ? 1 : CP / (int)sizeof(T);       // elements of an access
-    static __device__ __forceinline__ void bring(char *to, const T *from, long long ld, int c0, int D, long long r0, int lo, int hi) {
-        const int t = threadIdx.x, at = t % PER * E, row = t / PER;
-        if (c0 + at >= D) return;
-        const T *p = from + c0 + at;
-        char *q = to + row * ROW + at * (int)sizeof(T);
-        if (r0 >= lo && r0 + TILE <= hi) {               // a tile inside: one stride
-            const T *s = p + (r0 + row) * ld;
+    static constexpr int ROW = COLS * (int)sizeof(T), BYTES = ROWS * ROW;
+    static constexpr int PER = ROW / CP, STEP = PER < 32 ? 32 / PER : 1, PARTS = PER > 32 ? PER / 32 : 1;
+    static constexpr int E = CP / (int)sizeof(T);        // elements of an access
+    // This lane's first access of a row: its row of the first STEP, its channel of COLS.
+    static __device__ __forceinline__ int row() { return (int)(threadIdx.x & 31) / PER; }
+    static __device__ __forceinline__ int col() { return (int)(threadIdx.x & 31) % PER * E; }
+    // Rows that lie inside; at: this lane's access of the first ones.  left: channels from this lane's to D.
+    static __device__ __forceinline__ void bring(char *to, const T *at, long long ld, int left) {
+        to += row() * ROW + col() * (int)sizeof(T);
 #pragma unroll
-            for (int k = 0; k < TILE / STEP; ++k, s += STEP * ld) one(q + k * STEP * ROW, s);
-        } else {
+        for (int k = 0; k < ROWS / STEP; ++k, at += STEP * ld)
 #pragma unroll
-            for (int k = 0; k < TILE / STEP; ++k) {
-                const long long r = r0 + row + k * STEP;
-                one(q + k * STEP * ROW, p + (r < lo ? lo : r >= hi ? hi - 1 : r) * ld);
-            }
+            for (int part = 0; part < PARTS; ++part)
+                if (part * 32 * E < left) one(to + k * STEP * ROW + part * 32 * CP, at + part * 32 * E);
+    }
+    static __device__ __forceinline__ void bring_clamped(char *to, const T *from, long long ld, int left, long long r0, int lo, int hi) {
+        to += row() * ROW + col() * (int)sizeof(T);
+#pragma unroll 1
+        for (int k = 0; k < ROWS / STEP; ++k) {
+            const long long r = r0 + row() + k * STEP;
+            const T *at = from + (r < lo ? lo : r >= hi ? hi - 1 : r) * ld;
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part)
+                if (part * 32 * E < left) one(to + k * STEP * ROW + part * 32 * CP, at + part * 32 * E);
         }
     }
     static __device__ __forceinline__ void one(char *to, const T *from) {
         if constexpr (CP == 2) *reinterpret_cast<unsigned short *>(to) = __ldg(reinterpret_cast<const unsigned short *>(from));
         else copy_async<CP>(to, from);
     }
-    static __device__ __forceinline__ f2 pair(const char *tile, int row, int lane) {
+    static __device__ __forceinline__ f2 pair(const char *rows, int row, int lane) {
         Lanes<T, 2> v;
-        v.load_shared(tile + row * ROW + lane * 2 * (int)sizeof(T));
+        v.load_shared(rows + row * ROW + lane * 2 * (int)sizeof(T));
         return v.pair(0);
     }
 };
@@ -101,23 +120,7 @@ __device__ __forceinline__ f2 one_less_exp(f2 q) {
     unpack2(mul2(q, both(-kLog2e)), e0, e1);
     return pack2(q0 < SMALL ? s0 : 1.f - ex2(e0), q1 < SMALL ? s1 : 1.f - ex2(e1));
 }
-// Of several at once: a warp whose exponents are all small leaves the exponential out (the same values).
-template <int N> __device__ __forceinline__ void one_less_exps(f2 (&q)[N]) {
-    bool large = false;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-        float lo, hi;
-        unpack2(q[j], lo, hi);
-        large |= !(lo < SMALL && hi < SMALL);
-    }
-    if (__any_sync(~0u, large)) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) q[j] = one_less_exp(q[j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j) q[j] = one_less_exp_small(q[j]);
-    }
-}
+template <bool ALL_SMALL> __device__ __forceinline__ f2 one_less_exp_if(f2 q) { return ALL_SMALL ? one_less_exp_small(q) : one_less_exp(q); }
 __device__ __forceinline__ float sqrt_fast(float v) {
     float r;
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -137,36 +140,14 @@ __device__ __forceinline__ f2 sqrt2(f2 v) {
     return pack2(sqrt_fast(lo), sqrt_fast(hi));
 }
 
-// The rows and sequences of one chain: neighbouring sequences that blocks walk one after the other, as one
-// axis that is cut at every sequence's first row.  Dense batches: B / P sequences each.  Packed ones: the
-// sequences that begin in the p-th of P equal parts of the T rows.
-struct Chain {
-    int s0, s1;         // sequences
-    int c0, c1;         // rows
+// The rows that the sequences of a call cover: one axis, which is cut where a sequence begins.
+struct Extent {
+    int lo, hi;
 };
-__device__ __forceinline__ int first_at(const int32_t *cu, int B, long long row) {
-    int lo = 0, hi = B;                  // the first sequence that begins at or behind the row
-    while (lo < hi) {
-        const int mid = (int)(((long long)lo + hi) >> 1);
-        if (cu[mid] >= row) hi = mid;
-        else lo = mid + 1;
-    }
-    return lo;
-}
-__device__ __forceinline__ Chain chain_of(const int32_t *cu, int B, int T, int P, int p) {
-    Chain k;
-    if (!cu) {
-        k.s0 = (int)((long long)p * B / P);
-        k.s1 = (int)((long long)(p + 1) * B / P);
-        k.c0 = k.s0 * T;
-        k.c1 = k.s1 * T;
-    } else {
-        k.s0 = p ? first_at(cu, B, (long long)p * T / P) : 0;
-        k.s1 = p + 1 < P ? first_at(cu, B, (long long)(p + 1) * T / P) : B;
-        k.c0 = clamped(cu[k.s0], 0, T);
-        k.c1 = k.s1 > k.s0 ? clamped(cu[k.s1], k.c0, T) : k.c0;
-    }
-    return k;
+__device__ __forceinline__ Extent extent_of(const GatedScanParams &p) {
+    if (!p.cu_seqlens) return {0, (int)((long long)p.B * p.T)};
+    const int lo = clamped(p.cu_seqlens[0], 0, p.T);
+    return {lo, clamped(p.cu_seqlens[p.B], lo, p.T)};
 }
 
 // Where sequences begin and end among the rows from r0 that a warp holds (bit j: row r0 + j), and the
@@ -176,20 +157,20 @@ struct Marks {
     int lo = 1, hi = 0;                  // the kept sequence's rows
     unsigned starts, ends;
     int seq;
-    __device__ __forceinline__ void find(const GatedScanParams &p, const Chain &k, long long r0) {
+    __device__ __forceinline__ void find(const GatedScanParams &p, const Extent &k, long long r0) {
         starts = ends = 0;
         if (r0 > lo && r0 + N < hi) return;
         const int lane = threadIdx.x & 31;
         const long long row = r0 + lane;
         bool first = false, last = false;
         int a = 1, b = 0;
-        if (lane < N && row >= k.c0 && row < k.c1) {
+        if (lane < N && row >= k.lo && row < k.hi) {
             if (!p.cu_seqlens) {
                 seq = (int)((unsigned)row / (unsigned)p.T);
                 a = seq * p.T;
                 b = a + p.T;
             } else {
-                int x = k.s0, y = k.s1 - 1;          // the last sequence that begins at or before the row
+                int x = 0, y = p.B - 1;          // the last sequence that begins at or before the row
                 while (x < y) {
                     const int mid = (int)(((long long)x + y + 1) >> 1);
                     if (p.cu_seqlens[mid] <= row) x = mid;

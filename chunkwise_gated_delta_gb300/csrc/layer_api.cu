@@ -16,19 +16,21 @@ template <class A> void gated_fill(const A *a, mixer::GatedScanParams &p) {
     p.ld_x = stride_or(a->ld_x, a->D); p.ld_decay = stride_or(a->ld_decay, a->D); p.ld_gate = stride_or(a->ld_gate, a->D);
 }
 
-kda_status gated_fwd(const gated_scan_fwd_args *a, mixer::GatedScanParams &p) {
+kda_status gated_fwd(const gated_scan_fwd_args *a, mixer::GatedScanParams &p, size_t &need) {
     if (!a || !sizes_ok(a->B, a->T, a->D, a->cu_seqlens) || !a->y) return KDA_ERR_INVALID_ARG;
     const kda_status st = gated_common(a);
     if (st != KDA_OK) return st;
     gated_fill(a, p);
     p.T = a->T; p.h0 = a->h0; p.y = a->y; p.ht = a->ht; p.states = a->states; p.cu_seqlens = a->cu_seqlens;
     p.ld_y = stride_or(a->ld_y, a->D);
+    need = mixer::gated_scan_fwd_floats(p) * 4;
     const long long rows = (long long)(a->cu_seqlens ? 1 : a->B) * a->T;
     const size_t es = es_of(a->dtype);
     const Block in[] = {{a->x, rows, a->D, p.ld_x, es}, {a->decay, rows, a->D, p.ld_decay, es}, {a->gate, rows, a->D, p.ld_gate, es},
                         dense(a->rate, 1, a->D, 4), dense(a->h0, a->B, a->D, 4), dense(a->cu_seqlens, 1, (long long)a->B + 1, 4)};
     const Block out[] = {{a->y, rows, a->D, p.ld_y, es}, dense(a->ht, a->B, a->D, 4),
-                         dense(a->states, (long long)mixer::gated_scan_saved_rows(p), a->D, 4)};
+                         dense(a->states, (long long)mixer::gated_scan_saved_rows(p), a->D, 4),
+                         dense(need ? a->workspace : nullptr, 1, (long long)a->workspace_bytes, 1)};
     return blocks_ok(in, out) ? KDA_OK : KDA_ERR_INVALID_ARG;
 }
 
@@ -44,7 +46,7 @@ kda_status gated_bwd(const gated_scan_bwd_args *a, mixer::GatedScanParams &p, si
     p.dx = a->dx; p.ddecay = a->ddecay; p.dgate = a->dgate; p.drate = a->drate; p.dh0 = a->dh0;
     p.ld_dy = stride_or(a->ld_dy, a->D); p.ld_dx = stride_or(a->ld_dx, a->D);
     p.ld_ddecay = stride_or(a->ld_ddecay, a->D); p.ld_dgate = stride_or(a->ld_dgate, a->D);
-    const size_t part = mixer::gated_scan_part_floats(p, a->dtype == KDA_BF16), saved = mixer::gated_scan_saved_rows(p);
+    const size_t part = mixer::gated_scan_bwd_floats(p), saved = mixer::gated_scan_saved_rows(p);
     states = a->states ? 0 : (saved * a->D + 3) / 4 * 16;
     need = states + part * 4;
     const long long rows = (long long)(a->cu_seqlens ? 1 : a->B) * a->T;
@@ -161,10 +163,22 @@ kda_status glu_bwd_params(const glu_bwd_args *a, mixer::GluParams &p, size_t &ne
 
 extern "C" {
 
+size_t gated_scan_fwd_workspace(const gated_scan_fwd_args *a) {
+    mixer::GatedScanParams p{};
+    size_t need = 0;
+    return gated_fwd(a, p, need) == KDA_OK ? need : 0;
+}
+
 kda_status gated_scan_fwd(const gated_scan_fwd_args *a, kda_stream_t stream) {
     mixer::GatedScanParams p{};
-    const kda_status st = gated_fwd(a, p);
-    return st != KDA_OK ? st : from(mixer::launch_gated_scan_fwd(p, a->dtype == KDA_BF16, stream_of(stream)));
+    size_t need = 0;
+    kda_status st = gated_fwd(a, p, need);
+    if (st != KDA_OK) return st;
+    if (need) {
+        if ((st = check_space(a->workspace, a->workspace_bytes, need)) != KDA_OK) return st;
+        mixer::gated_scan_carve(p, static_cast<float *>(a->workspace));
+    }
+    return from(mixer::launch_gated_scan_fwd(p, a->dtype == KDA_BF16, stream_of(stream)));
 }
 
 size_t gated_scan_bwd_workspace(const gated_scan_bwd_args *a) {
@@ -183,10 +197,11 @@ kda_status gated_scan_bwd(const gated_scan_bwd_args *a, kda_stream_t stream) {
     const bool bf16 = a->dtype == KDA_BF16;
     if (states) {                        // the forward's walk again, for the states alone
         p.states = reinterpret_cast<float *>(ws);
+        mixer::gated_scan_carve(p, reinterpret_cast<float *>(ws + states));
         const cudaError_t e = mixer::launch_gated_scan_fwd(p, bf16, stream_of(stream));
         if (e != cudaSuccess) return from(e);
     }
-    p.part = reinterpret_cast<float *>(ws + states);
+    mixer::gated_scan_carve(p, reinterpret_cast<float *>(ws + states));
     return from(mixer::launch_gated_scan_bwd(p, bf16, stream_of(stream)));
 }
 

@@ -61,14 +61,16 @@ struct ScanParams {
 
 struct GatedScanParams {
     int B, T, D;
-    int chains, cluster;              // grid: chains of sequences side by side, blocks that share a chain
+    int seg;                          // rows of a segment
     float scale;
     const void *x, *decay, *gate, *dy;
     long long ld_x, ld_decay, ld_gate, ld_y, ld_dy, ld_dx, ld_ddecay, ld_dgate;
     const float *rate, *h0, *dht;
     void *y, *dx, *ddecay, *dgate;
-    float *ht, *states;               // states: [ceil(rows / 64)][D], the state that enters each 64th row
-    float *drate, *dh0, *part;        // part: [chains cluster][D]
+    float *ht, *states;               // states: [ceil(rows / 8)][D], the state that enters each 8th row
+    float *drate, *dh0;
+    // workspace: what each segment does to a state (pairs of floats), what enters it; sums of drate
+    float *seg_pair, *seg_in, *part;
     const int32_t *cu_seqlens;
     // single tokens
     int slots;
@@ -125,7 +127,10 @@ cudaError_t launch_gated_scan_fwd(const GatedScanParams &p, bool bf16, cudaStrea
 cudaError_t launch_gated_scan_bwd(const GatedScanParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_gated_scan_step(const GatedScanParams &p, bool bf16, cudaStream_t s);
 size_t gated_scan_saved_rows(const GatedScanParams &p);
-size_t gated_scan_part_floats(const GatedScanParams &p, bool bf16);
+// Workspace floats; carve() points the parameter block into a workspace of that size.
+size_t gated_scan_fwd_floats(const GatedScanParams &p);
+size_t gated_scan_bwd_floats(const GatedScanParams &p);     // (the forward's states aside)
+void gated_scan_carve(GatedScanParams &p, float *ws);
 
 cudaError_t launch_group_norm_fwd(const GroupNormParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_group_norm_bwd(const GroupNormParams &p, bool bf16, cudaStream_t s);

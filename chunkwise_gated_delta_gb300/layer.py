@@ -41,7 +41,7 @@ def gated_scan_fwd(x, decay, gate, rate, h0=None, *, scale=8.0, output_final_sta
 
     x, decay, gate: [B, T, D] (one dtype, bf16 or fp32); rate: [D] fp32; h0: [B, D] fp32 or None (zeros).
     y has x's dtype, ht is fp32 [B, D] (None when ``output_final_state`` is false).  states: what
-    :func:`gated_scan_bwd` would otherwise compute again, fp32 [ceil(B T / 64), D].
+    :func:`gated_scan_bwd` would otherwise compute again, fp32 [ceil(B T / 8), D].
     """
     dev, code, ptrs = _gated_inputs(x, decay, gate, rate, scale, 3)
     B, T, D = x.shape
@@ -54,7 +54,10 @@ def gated_scan_fwd(x, decay, gate, rate, h0=None, *, scale=8.0, output_final_sta
             ht, htp = _dense_out(on, ht, "ht", (n, D), _F32)
         if save_states:
             states, sp = _dense_out(on, None, "states", _state_shape(B * T, D), _F32)
-        on.launch("gated_scan_fwd", _lib.GatedScanFwdArgs(n, T, D, code, scale, *ptrs, hp, yp, ldy, htp, sp, cu))
+        args = _lib.GatedScanFwdArgs(n, T, D, code, scale, *ptrs, hp, yp, ldy, htp, sp, None, 0, cu)
+        ws = on.workspace("gated_scan_fwd_workspace", args)
+        on.launch("gated_scan_fwd", args)
+        del ws
     return (y, ht, states) if save_states else (y, ht)
 
 

@@ -286,7 +286,7 @@ kda_status ssm_scan_step(const ssm_scan_step_args *args, kda_stream_t stream);
 
 /* ------------------------------------------------------------ gated recurrence */
 
-#define GATED_SCAN_STATE_ROWS 64
+#define GATED_SCAN_STATE_ROWS 8
 
 typedef struct {
     int B, T, D;           /* sequences, tokens, channels */
@@ -304,9 +304,14 @@ typedef struct {
     long long ld_y;
     float *ht;             /* [B, D] out, or NULL */
     float *states;         /* [ceil(rows / GATED_SCAN_STATE_ROWS), D] out, rows as they lie (B T, packed: T): the state that
-                              enters every 64th row, for gated_scan_bwd; or NULL (not kept) */
+                              enters every 8th row, for gated_scan_bwd; or NULL (not kept) */
+    void *workspace;       /* gated_scan_fwd_workspace bytes */
+    size_t workspace_bytes;
     const int32_t *cu_seqlens;
 } gated_scan_fwd_args;
+
+/* Bytes of workspace (0 on bad args and where a call takes none): what segments of the rows do to a state. */
+size_t gated_scan_fwd_workspace(const gated_scan_fwd_args *args);
 
 kda_status gated_scan_fwd(const gated_scan_fwd_args *args, kda_stream_t stream);
 
@@ -338,7 +343,8 @@ typedef struct {
     const int32_t *cu_seqlens;
 } gated_scan_bwd_args;
 
-/* Bytes of workspace (0 on bad args): partial sums of drate, and the states where the caller has none. */
+/* Bytes of workspace (0 on bad args): what segments of the rows do to a gradient, partial sums of drate, and the
+   states where the caller has none. */
 size_t gated_scan_bwd_workspace(const gated_scan_bwd_args *args);
 
 /*
