@@ -461,20 +461,21 @@ int access_of(const GatedScanParams &p, bool bf16) {
     return (int)es;
 }
 
-// Rows of a segment: 64, or as few as 16 where that leaves less than eight warps to an SM.
-int segment_of(const GatedScanParams &p) {
-    const long long cols = (p.D - 1) / COLS + 1, rows = rows_of(p);
-    int seg = 64;
-    while (seg > 16 && cols * ((rows + seg - 1) / seg) < 8LL * sm_count()) seg /= 2;
-    return seg;
+// Rows of a segment, such that the warps of a pass (`warps` to an SM) all run at once, or in as few rounds as make segments of at most
+// MOST rows: a last round that is not full costs as much as a full one.
+constexpr int MOST = 96;
+int segment_of(const GatedScanParams &p, int warps) {
+    const long long cols = (p.D - 1) / COLS + 1, rows = rows_of(p), places = (long long)warps * sm_count();
+    const long long rounds = (cols * rows + places * MOST - 1) / (places * MOST), segs = max(1LL, places * rounds / cols);
+    const long long seg = ((rows + segs - 1) / segs + ROWS - 1) / ROWS * ROWS;
+    return (int)max(seg, 16LL);
 }
-long long segments_of(const GatedScanParams &p) {
-    const int seg = segment_of(p);
-    return (rows_of(p) + seg - 1) / seg;
-}
+int fwd_segment(const GatedScanParams &p) { return segment_of(p, 24); }
+int bwd_segment(const GatedScanParams &p) { return segment_of(p, 16); }
+long long segments_of(const GatedScanParams &p, int seg) { return (rows_of(p) + seg - 1) / seg; }
 unsigned blocks_of(const GatedScanParams &p) {
     const long long cols = (p.D - 1) / COLS + 1;
-    return (unsigned)((cols * segments_of(p) + WARPS - 1) / WARPS);
+    return (unsigned)((cols * segments_of(p, p.seg) + WARPS - 1) / WARPS);
 }
 
 // A kernel whose blocks may set up while the one before it ends; they wait for it themselves.
@@ -499,7 +500,7 @@ cudaError_t launch(void (*kernel)(GatedScanParams), unsigned grid, int threads, 
 template <class T, int CP> cudaError_t forward(GatedScanParams &p, cudaStream_t s) {
     constexpr size_t smem = WARPS * Ring<T, CP, 3, false>::BYTES;
     const unsigned n = blocks_of(p);
-    if (segments_of(p) == 1) {
+    if (segments_of(p, p.seg) == 1) {
         p.seg_in = nullptr;            // nothing enters the only segment
         return launch(gated_scan_fwd_kernel<T, CP, true>, n, THREADS, smem, false, p, s);
     }
@@ -510,7 +511,7 @@ template <class T, int CP> cudaError_t forward(GatedScanParams &p, cudaStream_t 
 }
 template <class T, int CP> cudaError_t backward(GatedScanParams &p, cudaStream_t s) {
     const unsigned n = blocks_of(p);
-    const bool one = segments_of(p) == 1;
+    const bool one = segments_of(p, p.seg) == 1;
     cudaError_t e = cudaSuccess;
     if (one) p.seg_in = nullptr;
     else {
@@ -524,8 +525,18 @@ template <bool BWD, class T, int CP> cudaError_t run(GatedScanParams &p, cudaStr
     if constexpr (BWD) return backward<T, CP>(p, s);
     else return forward<T, CP>(p, s);
 }
+size_t pair_floats(const GatedScanParams &p, size_t segs) { return 2 * segs * ((p.D + 1) & ~1); }
+// Points the parameter block into its workspace (the forward has no `part`).
+void carve(GatedScanParams &p) {
+    const size_t n = (size_t)segments_of(p, p.seg);
+    p.seg_pair = p.ws;                   // (16-byte aligned)
+    p.seg_in = p.ws + pair_floats(p, n);
+    p.part = p.seg_in + n * p.D;
+}
+
 template <bool BWD> cudaError_t run(GatedScanParams &p, bool bf16_, cudaStream_t s) {
-    p.seg = segment_of(p);
+    p.seg = BWD ? bwd_segment(p) : fwd_segment(p);
+    carve(p);
     const int n = access_of(p, bf16_);
     if (bf16_) return n == 16 ? run<BWD, bf16, 16>(p, s) : n == 4 ? run<BWD, bf16, 4>(p, s) : run<BWD, bf16, 2>(p, s);
     return n == 16 ? run<BWD, float, 16>(p, s) : n == 8 ? run<BWD, float, 8>(p, s) : run<BWD, float, 4>(p, s);
@@ -535,19 +546,14 @@ template <bool BWD> cudaError_t run(GatedScanParams &p, bool bf16_, cudaStream_t
 
 size_t gated_scan_saved_rows(const GatedScanParams &p) { return (size_t)((rows_of(p) + ROWS - 1) / ROWS); }
 
-static size_t pair_floats(const GatedScanParams &p) { return 2 * (size_t)segments_of(p) * ((p.D + 1) & ~1); }
 size_t gated_scan_fwd_floats(const GatedScanParams &p) {
-    const size_t n = (size_t)segments_of(p);
-    return n > 1 ? pair_floats(p) + n * p.D : 0;
+    const size_t n = (size_t)segments_of(p, fwd_segment(p));
+    return n > 1 ? pair_floats(p, n) + n * p.D : 0;
 }
-size_t gated_scan_bwd_floats(const GatedScanParams &p) { return pair_floats(p) + 2 * (size_t)segments_of(p) * p.D; }
-void gated_scan_carve(GatedScanParams &p, float *ws) {
-    const size_t n = (size_t)segments_of(p) * p.D;
-    p.seg_pair = ws;                     // (16-byte aligned)
-    p.seg_in = ws + pair_floats(p);
-    p.part = p.seg_in + n;               // (the forward has no such part)
+size_t gated_scan_bwd_floats(const GatedScanParams &p) {
+    const size_t n = (size_t)segments_of(p, bwd_segment(p));
+    return max(pair_floats(p, n) + 2 * n * p.D, gated_scan_fwd_floats(p));
 }
-
 cudaError_t launch_gated_scan_fwd(const GatedScanParams &q, bool bf16_, cudaStream_t s) {
     GatedScanParams p = q;
     return run<false>(p, bf16_, s);
@@ -557,7 +563,7 @@ cudaError_t launch_gated_scan_bwd(const GatedScanParams &q, bool bf16_, cudaStre
     GatedScanParams p = q;
     const cudaError_t e = run<true>(p, bf16_, s);
     if (e != cudaSuccess) return e;
-    return launch_sum_rows(p.part, (int)segments_of(p), SumOut{p.drate, p.D, false}, SumOut{nullptr, 0, false}, s);
+    return launch_sum_rows(p.part, (int)segments_of(p, p.seg), SumOut{p.drate, p.D, false}, SumOut{nullptr, 0, false}, s);
 }
 
 cudaError_t launch_gated_scan_step(const GatedScanParams &p, bool bf16_, cudaStream_t s) {

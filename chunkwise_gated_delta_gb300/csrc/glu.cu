@@ -183,7 +183,7 @@ template <class T> cudaError_t bwd(const GluParams &p, cudaStream_t s) {
 }  // namespace
 
 long long glu_grad_stride(const GluParams &p, bool bf16_) {
-    const long long n = bf16_ ? 8 : 4;                       // rows of 16-byte accesses
+    const long long n = bf16_ ? 16 : 4;                      // rows of 32-byte sectors, of 16-byte accesses
     return (p.F + n - 1) / n * n;
 }
 

@@ -153,17 +153,21 @@ __device__ __forceinline__ Tile tile_of(const TcArgs &t, int i) {
     return q;
 }
 
-// A value of the epilogue's row and 32 columns from c; `inside` of them belong to the output.
+// 32 bytes in one access: a whole sector of a row per lane.
+__device__ __forceinline__ void store_sector(void *to, const uint32_t (&q)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(q[0]), "r"(q[1]), "r"(q[2]), "r"(q[3]), "r"(q[4]),
+                 "r"(q[5]), "r"(q[6]), "r"(q[7])
+                 : "memory");
+}
+// The epilogue's row and 32 columns; `inside` of them belong to the output.  wide: rows of whole sectors.
 __device__ __forceinline__ void store_row(bf16 *out, const float (&v)[32], int inside, bool wide) {
     if (wide && inside >= 32) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            uint4 q;
-            q.x = pack_bf16(v[8 * k], v[8 * k + 1]);
-            q.y = pack_bf16(v[8 * k + 2], v[8 * k + 3]);
-            q.z = pack_bf16(v[8 * k + 4], v[8 * k + 5]);
-            q.w = pack_bf16(v[8 * k + 6], v[8 * k + 7]);
-            reinterpret_cast<uint4 *>(out)[k] = q;
+        for (int k = 0; k < 2; ++k) {
+            uint32_t q[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q[e] = pack_bf16(v[16 * k + 2 * e], v[16 * k + 2 * e + 1]);
+            store_sector(out + 16 * k, q);
         }
     } else {
 #pragma unroll
@@ -174,7 +178,12 @@ __device__ __forceinline__ void store_row(bf16 *out, const float (&v)[32], int i
 __device__ __forceinline__ void store_row(float *out, const float (&v)[32], int inside, bool wide) {
     if (wide && inside >= 32) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) reinterpret_cast<float4 *>(out)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        for (int k = 0; k < 4; ++k) {
+            uint32_t q[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q[e] = __float_as_uint(v[8 * k + e]);
+            store_sector(out + 8 * k, q);
+        }
     } else {
 #pragma unroll
         for (int k = 0; k < 32; ++k)
@@ -182,7 +191,7 @@ __device__ __forceinline__ void store_row(float *out, const float (&v)[32], int 
     }
 }
 __device__ __forceinline__ bool wide_rows(const void *p, long long ld, int es) {
-    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * es % 16 == 0;
+    return (reinterpret_cast<uintptr_t>(p) & 31) == 0 && ld * es % 32 == 0;
 }
 
 // The outputs of one row (of the call) and a tile's columns.  get(c, v): 32 accumulator columns from c.
@@ -190,7 +199,7 @@ template <Mode MODE, class Get> __device__ __forceinline__ void finish(const Glu
     if constexpr (MODE == FWD || MODE == RECOMPUTE) {
         const int n0 = q.n * HALF;
         bf16 *h = static_cast<bf16 *>(p.h), *dg = static_cast<bf16 *>(p.dg), *du = static_cast<bf16 *>(p.du);
-        const bool wide = MODE == FWD ? wide_rows(p.h, p.ld_h, 2) : true, keep = wide_rows(p.g, p.F, 4) && wide_rows(p.u, p.F, 4);
+        const bool wide = MODE == FWD ? wide_rows(p.h, p.ld_h, 2) : wide_rows(p.dg, p.ld_d, 2) && wide_rows(p.du, p.ld_d, 2), keep = wide_rows(p.g, p.F, 4) && wide_rows(p.u, p.F, 4);
 #pragma unroll 1
         for (int c = 0; c < HALF; c += 32) {
             float g[32], u[32];

@@ -176,7 +176,7 @@ kda_status gated_scan_fwd(const gated_scan_fwd_args *a, kda_stream_t stream) {
     if (st != KDA_OK) return st;
     if (need) {
         if ((st = check_space(a->workspace, a->workspace_bytes, need)) != KDA_OK) return st;
-        mixer::gated_scan_carve(p, static_cast<float *>(a->workspace));
+        p.ws = static_cast<float *>(a->workspace);
     }
     return from(mixer::launch_gated_scan_fwd(p, a->dtype == KDA_BF16, stream_of(stream)));
 }
@@ -195,13 +195,12 @@ kda_status gated_scan_bwd(const gated_scan_bwd_args *a, kda_stream_t stream) {
     if ((st = check_space(a->workspace, a->workspace_bytes, need)) != KDA_OK) return st;
     char *ws = static_cast<char *>(a->workspace);
     const bool bf16 = a->dtype == KDA_BF16;
+    p.ws = reinterpret_cast<float *>(ws + states);
     if (states) {                        // the forward's walk again, for the states alone
         p.states = reinterpret_cast<float *>(ws);
-        mixer::gated_scan_carve(p, reinterpret_cast<float *>(ws + states));
         const cudaError_t e = mixer::launch_gated_scan_fwd(p, bf16, stream_of(stream));
         if (e != cudaSuccess) return from(e);
     }
-    mixer::gated_scan_carve(p, reinterpret_cast<float *>(ws + states));
     return from(mixer::launch_gated_scan_bwd(p, bf16, stream_of(stream)));
 }
 

@@ -69,7 +69,7 @@ struct GatedScanParams {
     void *y, *dx, *ddecay, *dgate;
     float *ht, *states;               // states: [ceil(rows / 8)][D], the state that enters each 8th row
     float *drate, *dh0;
-    // workspace: what each segment does to a state (pairs of floats), what enters it; sums of drate
+    float *ws;                        // workspace: what each segment does to a state (pairs of floats), what enters it, sums of drate
     float *seg_pair, *seg_in, *part;
     const int32_t *cu_seqlens;
     // single tokens
@@ -127,10 +127,9 @@ cudaError_t launch_gated_scan_fwd(const GatedScanParams &p, bool bf16, cudaStrea
 cudaError_t launch_gated_scan_bwd(const GatedScanParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_gated_scan_step(const GatedScanParams &p, bool bf16, cudaStream_t s);
 size_t gated_scan_saved_rows(const GatedScanParams &p);
-// Workspace floats; carve() points the parameter block into a workspace of that size.
+// Workspace floats (the backward's: the states aside, but also enough for the forward).
 size_t gated_scan_fwd_floats(const GatedScanParams &p);
-size_t gated_scan_bwd_floats(const GatedScanParams &p);     // (the forward's states aside)
-void gated_scan_carve(GatedScanParams &p, float *ws);
+size_t gated_scan_bwd_floats(const GatedScanParams &p);
 
 cudaError_t launch_group_norm_fwd(const GroupNormParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_group_norm_bwd(const GroupNormParams &p, bool bf16, cudaStream_t s);
