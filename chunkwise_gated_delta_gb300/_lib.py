@@ -196,7 +196,7 @@ class GroupNormBwdArgs(ctypes.Structure):
 class GluFwdArgs(ctypes.Structure):
     _fields_ = [("rows", _L), ("D", _I), ("F", _I), ("dtype", _I), ("flags", _U), ("x", _P), ("ld_x", _L),
                 ("w_gate", _P), ("ld_w_gate", _L), ("w_up", _P), ("ld_w_up", _L), ("h", _P), ("ld_h", _L), ("g", _P),
-                ("u", _P), ("status", _P)]
+                ("u", _P), ("workspace", _P), ("workspace_bytes", _Z), ("status", _P)]
 
 
 class GluBwdArgs(ctypes.Structure):
@@ -229,6 +229,7 @@ MIXER_EXPORTS = {
     "group_norm_fwd": (GroupNormFwdArgs, True),
     "group_norm_bwd_workspace": (GroupNormBwdArgs, False),
     "group_norm_bwd": (GroupNormBwdArgs, True),
+    "glu_fwd_workspace": (GluFwdArgs, False),
     "glu_fwd": (GluFwdArgs, True),
     "glu_bwd_workspace": (GluBwdArgs, False),
     "glu_bwd": (GluBwdArgs, True),

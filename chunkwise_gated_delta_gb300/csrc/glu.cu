@@ -1,134 +1,178 @@
-// Gated feed-forward product on the CUDA cores, in float32: the form of float32 calls (whose products the tensor
-// cores would round).
+// Gated feed-forward product: choice of form, float32 calls, and what surrounds the tensor cores' products.
 //
 //   forward   h = act(x Wg^T) (x Wu^T), both products in one tile
 //   backward  dg = dh u act'(g), du = dh act(g); dx = dg Wg + du Wu; dWg = dg^T x, dWu = du^T x
 //
-// A block of 256 threads has a tile of 128 x 128 products, a thread 8 x 8 of them in two quads per axis; in the
-// forward the left half of the columns is Wg's and the right half Wu's, so a thread has both of its outputs' products.
+// float32 products run on the CUDA cores, which do not round their operands.  A block of 256 threads has a tile of SIDE x
+// SIDE products, a thread two quads (SIDE = 64: one) per axis; in the forward the left half of the columns is Wg's and the right
+// half Wu's.  Where tiles of 128 leave the GPU idle, tiles of 64 are used and a cluster of up to eight blocks shares the sum
+// of a tile, joined in the blocks' order through shared memory.
 #include "glu.cuh"
+#include "tc_common.cuh"
 
 namespace mixer {
 namespace {
 
 using namespace glu;
 
-constexpr int TILE = 128, KT = 16, PITCH = TILE + 4;
+enum Mode { FWD, RECOMPUTE, DX, DW };
 
-// 8 elements of an operand's tile [KT][TILE] per thread: along k, or along the rows, whichever lies contiguous.
-template <class T, bool KMAJOR> struct Stage {
-    float v[8];
-    // row0, k0: the tile's corner; rows, ks: the operand's extent; ld: stride between the non-contiguous axis' elements.
-    __device__ __forceinline__ void load(const T *p, long long ld, long long row0, long long rows, long long k0, long long ks) {
-        const int t = threadIdx.x;
+template <int SIDE> struct Tiles {
+    static constexpr int KT = SIDE == 128 ? 16 : 32, PITCH = SIDE + 4, E = SIDE * KT / 256, Q = SIDE / 64;
+    static constexpr int STAGE = KT * PITCH;                 // floats of an operand's tile
+    static constexpr int FLOATS = 4 * STAGE > SIDE * (SIDE + 1) ? 4 * STAGE : SIDE * (SIDE + 1);
+};
+
+// E elements of an operand's tile [KT][SIDE] per thread: along k, or along the rows, whichever lies contiguous.
+template <int SIDE, bool KMAJOR> struct Operand {
+    using S = Tiles<SIDE>;
+    static constexpr int PER = (KMAJOR ? S::KT : SIDE) / S::E;      // threads of a contiguous stretch
+    float v[S::E];
+    // row0, k0: the tile's corner; rows, ks: the operand's extent; ld: stride of the axis that is not contiguous.
+    __device__ __forceinline__ void load(const float *p, long long ld, long long row0, long long rows, long long k0, long long ks) {
+        const int t = threadIdx.x, in = t % PER * S::E, out = t / PER;
+        const long long r0 = row0 + (KMAJOR ? out : in), c0 = k0 + (KMAJOR ? in : out);
+        const float *q = p + (KMAJOR ? r0 * ld + c0 : c0 * ld + r0);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const long long r = row0 + (KMAJOR ? t / 2 : t % 16 * 8 + e), k = k0 + (KMAJOR ? t % 2 * 8 + e : t / 16);
-            v[e] = r < rows && k < ks ? to_f(p[KMAJOR ? r * ld + k : k * ld + r]) : 0.f;
-        }
+        for (int e = 0; e < S::E; ++e)
+            v[e] = (KMAJOR ? r0 < rows && c0 + e < ks : r0 + e < rows && c0 < ks) ? __ldg(q + e) : 0.f;
     }
-    __device__ __forceinline__ void store(float (*sm)[PITCH], int at) const {
-        const int t = threadIdx.x;
+    __device__ __forceinline__ void store(float *sm) const {
+        const int t = threadIdx.x, in = t % PER * S::E, out = t / PER;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (KMAJOR) sm[t % 2 * 8 + e][at + t / 2] = v[e];
-            else sm[t / 16][at + t % 16 * 8 + e] = v[e];
+        for (int e = 0; e < S::E; ++e) {
+            if (KMAJOR) sm[(in + e) * S::PITCH + out] = v[e];
+            else sm[out * S::PITCH + in + e] = v[e];
         }
     }
 };
 
-enum Mode { FWD, RECOMPUTE, DX, DW };
+// One element's outputs from its sums (second: u, in the forward's modes).
+template <Mode MODE> __device__ __forceinline__ void finish(const GluParams &p, bool up, long long m, long long n, float first, float second) {
+    if constexpr (MODE == FWD) {
+        static_cast<float *>(p.h)[m * p.ld_h + n] = act(first, p.gelu) * second;
+        if (p.g) {
+            p.g[m * p.F + n] = first;
+            p.u[m * p.F + n] = second;
+        }
+    } else if constexpr (MODE == RECOMPUTE) {
+        const Act f = act_and_slope(first, p.gelu);
+        const float d = static_cast<const float *>(p.dh)[m * p.ld_dh + n];
+        static_cast<float *>(p.dg)[m * p.ld_d + n] = d * second * f.d;
+        static_cast<float *>(p.du)[m * p.ld_d + n] = d * f.v;
+    } else if constexpr (MODE == DX) {
+        static_cast<float *>(p.dx)[m * p.ld_dx + n] = first;
+    } else {
+        if (up) static_cast<float *>(p.dwu)[m * p.ld_dwu + n] = first;
+        else static_cast<float *>(p.dwg)[m * p.ld_dwg + n] = first;
+    }
+}
 
-template <class T, Mode MODE> __global__ void __launch_bounds__(256, 2) glu_simt_kernel(GluParams p) {
-    __shared__ __align__(16) float sa[2][KT][PITCH], sb[2][KT][PITCH];
+template <int SIDE, Mode MODE> __global__ void __launch_bounds__(256, 2) glu_f32_kernel(GluParams p, int blocks) {
+    using S = Tiles<SIDE>;
+    extern __shared__ __align__(16) float sm[];              // operands' tiles [2][2][STAGE], then the block's sums [SIDE][SIDE + 1]
     constexpr bool DUAL = MODE == FWD || MODE == RECOMPUTE, AK = MODE != DW, BK = DUAL;
+    constexpr int TN = DUAL ? SIDE / 2 : SIDE, N = 4 * S::Q;
     const int t = threadIdx.x, tx = t % 16, ty = t / 16;
-    constexpr int TN = DUAL ? TILE / 2 : TILE;
     const bool up = MODE == DW && blockIdx.y;
     const long long ms = MODE == DW ? p.F : p.M, ns = DUAL ? p.F : p.D, ks = MODE == DW ? p.M : MODE == DX ? p.F : p.D;
-    const unsigned cols = (unsigned)((ns + TN - 1) / TN);    // tiles of a row of tiles
-    const long long m0 = (long long)(blockIdx.x / cols) * TILE, n0 = (long long)(blockIdx.x % cols) * TN;
-    float acc[8][8];
+    const unsigned cols = (unsigned)((ns + TN - 1) / TN), tile = blockIdx.x / blocks;
+    const int rank = (int)(blockIdx.x % blocks);
+    const long long m0 = (long long)(tile / cols) * SIDE, n0 = (long long)(tile % cols) * TN;
+    float acc[N][N];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
-    Stage<T, AK> a;
-    Stage<T, BK> b;
-    const long long per = (ks + KT - 1) / KT, steps = MODE == DX ? 2 * per : per;
+        for (int j = 0; j < N; ++j) acc[i][j] = 0.f;
+    Operand<SIDE, AK> a;
+    Operand<SIDE, BK> b;
+    const long long per = (ks + S::KT - 1) / S::KT, steps = MODE == DX ? 2 * per : per;
+    const long long first = steps * rank / blocks, end = steps * (rank + 1) / blocks;
     auto fetch = [&](long long i) {
         if constexpr (DUAL) {
-            a.load(static_cast<const T *>(p.x), p.ld_x, m0, ms, i * KT, ks);
-            // rows 0 .. 63 of the tile from Wg, 64 .. 127 from Wu (threads 0 .. 127 and 128 .. 255)
+            a.load(static_cast<const float *>(p.x), p.ld_x, m0, ms, i * S::KT, ks);
+            // the tile's first half of rows from Wg, the second from Wu (threads 0 .. 127 and 128 .. 255)
             const bool right = t >= 128;
-            const T *w = static_cast<const T *>(right ? p.wu : p.wg);
-            b.load(w, right ? p.ld_wu : p.ld_wg, right ? n0 - TILE / 2 : n0, ns, i * KT, ks);
+            b.load(static_cast<const float *>(right ? p.wu : p.wg), right ? p.ld_wu : p.ld_wg, right ? n0 - TN : n0, ns, i * S::KT, ks);
         } else if constexpr (MODE == DX) {
             const bool second = i >= per;
-            const long long k0 = (second ? i - per : i) * KT;
-            a.load(static_cast<const T *>(second ? p.du : p.dg), p.ld_d, m0, ms, k0, ks);
-            b.load(static_cast<const T *>(second ? p.wu : p.wg), second ? p.ld_wu : p.ld_wg, n0, ns, k0, ks);
+            const long long k0 = (second ? i - per : i) * S::KT;
+            a.load(static_cast<const float *>(second ? p.du : p.dg), p.ld_d, m0, ms, k0, ks);
+            b.load(static_cast<const float *>(second ? p.wu : p.wg), second ? p.ld_wu : p.ld_wg, n0, ns, k0, ks);
         } else {
-            a.load(static_cast<const T *>(up ? p.du : p.dg), p.ld_d, m0, ms, i * KT, ks);
-            b.load(static_cast<const T *>(p.x), p.ld_x, n0, ns, i * KT, ks);
+            a.load(static_cast<const float *>(up ? p.du : p.dg), p.ld_d, m0, ms, i * S::KT, ks);
+            b.load(static_cast<const float *>(p.x), p.ld_x, n0, ns, i * S::KT, ks);
         }
     };
-    fetch(0);
-    a.store(sa[0], 0);
-    b.store(sb[0], 0);
+    float *sa = sm, *sb = sm + 2 * S::STAGE;
+    if (first < end) {
+        fetch(first);
+        a.store(sa);
+        b.store(sb);
+    }
     __syncthreads();
-    for (long long i = 0; i < steps; ++i) {
-        const int cur = i & 1;
-        if (i + 1 < steps) fetch(i + 1);
+    for (long long i = first; i < end; ++i) {
+        const int cur = (int)(i - first) & 1;
+        if (i + 1 < end) fetch(i + 1);
+        const float *pa = sa + cur * S::STAGE + ty * 4, *pb = sb + cur * S::STAGE + tx * 4;
 #pragma unroll
-        for (int k = 0; k < KT; ++k) {
-            float av[8], bv[8];
-            *reinterpret_cast<float4 *>(av) = *reinterpret_cast<const float4 *>(&sa[cur][k][ty * 4]);
-            *reinterpret_cast<float4 *>(av + 4) = *reinterpret_cast<const float4 *>(&sa[cur][k][64 + ty * 4]);
-            *reinterpret_cast<float4 *>(bv) = *reinterpret_cast<const float4 *>(&sb[cur][k][tx * 4]);
-            *reinterpret_cast<float4 *>(bv + 4) = *reinterpret_cast<const float4 *>(&sb[cur][k][64 + tx * 4]);
+        for (int k = 0; k < S::KT; ++k) {
+            float av[N], bv[N];
 #pragma unroll
-            for (int y = 0; y < 8; ++y)
+            for (int q = 0; q < S::Q; ++q) {
+                *reinterpret_cast<float4 *>(av + 4 * q) = *reinterpret_cast<const float4 *>(pa + k * S::PITCH + 64 * q);
+                *reinterpret_cast<float4 *>(bv + 4 * q) = *reinterpret_cast<const float4 *>(pb + k * S::PITCH + 64 * q);
+            }
 #pragma unroll
-                for (int x = 0; x < 8; ++x) acc[y][x] = fmaf(av[y], bv[x], acc[y][x]);
+            for (int y = 0; y < N; ++y)
+#pragma unroll
+                for (int x = 0; x < N; ++x) acc[y][x] = fmaf(av[y], bv[x], acc[y][x]);
         }
-        if (i + 1 < steps) {
-            a.store(sa[cur ^ 1], 0);
-            b.store(sb[cur ^ 1], 0);
+        if (i + 1 < end) {
+            a.store(sa + (cur ^ 1) * S::STAGE);
+            b.store(sb + (cur ^ 1) * S::STAGE);
         }
         __syncthreads();
     }
+    if constexpr (SIDE == 128) {
 #pragma unroll
-    for (int y = 0; y < 8; ++y) {
-        const long long m = m0 + (y < 4 ? ty * 4 + y : 60 + ty * 4 + y);
-        if (m >= ms) continue;
-        if constexpr (DUAL) {
+        for (int y = 0; y < 8; ++y) {
+            const long long m = m0 + (y < 4 ? ty * 4 + y : 60 + ty * 4 + y);
+            if (m >= ms) continue;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const long long n = n0 + tx * 4 + x;
-                if (n >= ns) continue;
-                const float g = acc[y][x], u = acc[y][x + 4];
-                if constexpr (MODE == FWD) {
-                    static_cast<T *>(p.h)[m * p.ld_h + n] = from_f<T>(act(g, p.gelu) * u);
-                    if (p.g) {
-                        p.g[m * p.F + n] = g;
-                        p.u[m * p.F + n] = u;
-                    }
-                } else {
-                    const Act f = act_and_slope(g, p.gelu);
-                    const float d = to_f(static_cast<const T *>(p.dh)[m * p.ld_dh + n]);
-                    static_cast<T *>(p.dg)[m * p.ld_d + n] = from_f<T>(d * u * f.d);
-                    static_cast<T *>(p.du)[m * p.ld_d + n] = from_f<T>(d * f.v);
-                }
-            }
-        } else {
-            T *out = static_cast<T *>(MODE == DX ? p.dx : up ? p.dwu : p.dwg) + m * (MODE == DX ? p.ld_dx : up ? p.ld_dwu : p.ld_dwg);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
+            for (int x = 0; x < (DUAL ? 4 : 8); ++x) {
                 const long long n = n0 + (x < 4 ? tx * 4 + x : 60 + tx * 4 + x);
-                if (n < ns) out[n] = from_f<T>(acc[y][x]);
+                if (n < ns) finish<MODE>(p, up, m, n, acc[y][x], DUAL ? acc[y][x + 4] : 0.f);
             }
         }
+    } else {
+        // the block's sums where the others of its cluster can read them; each finishes a part of the tile's rows
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) sm[(ty * 4 + y) * (SIDE + 1) + tx * 4 + x] = acc[y][x];
+        if (blocks > 1) kda::tc::cluster_sync_all();
+        else __syncthreads();
+        const uint32_t local = kda::tc::smem_u32(sm);
+        const int rows = SIDE / blocks;
+        for (int i = t; i < rows * TN; i += 256) {
+            const int y = rank * rows + i / TN, x = i % TN;
+            const long long m = m0 + y, n = n0 + x;
+            if (m >= ms || n >= ns) continue;
+            float v = 0.f, u = 0.f;
+            for (int r = 0; r < blocks; ++r) {
+                const uint32_t at = kda::tc::map_to_rank(local + (y * (SIDE + 1) + x) * 4, r);
+                float g;
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(g) : "r"(at) : "memory");
+                v += g;
+                if (DUAL) {
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(g) : "r"(at + TN * 4) : "memory");
+                    u += g;
+                }
+            }
+            finish<MODE>(p, up, m, n, v, u);
+        }
+        if (blocks > 1) kda::tc::cluster_sync_all();         // nobody leaves while others read its sums
     }
 }
 
@@ -152,13 +196,43 @@ template <class T, int V> __global__ void __launch_bounds__(256) glu_slope_kerne
     store_vec<T, V>(static_cast<T *>(p.du) + m * p.ld_d + n, du);
 }
 
-template <class T, Mode MODE> cudaError_t run_simt(const GluParams &p, cudaStream_t s) {
+// A matrix's rows to where they are 16-byte aligned.
+__global__ void __launch_bounds__(256) glu_align_kernel(const bf16 *from, long long ld, bf16 *to, long long pitch, long long rows, int cols) {
+    for (long long r = blockIdx.y; r < rows; r += gridDim.y) {
+        const int c = (int)blockIdx.x * 1024 + (int)threadIdx.x;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (c + k * 256 < cols) to[r * pitch + c + k * 256] = from[r * ld + c + k * 256];
+    }
+}
+
+template <int SIDE, Mode MODE> cudaError_t run_side(const GluParams &p, long long tiles, int blocks, cudaStream_t s) {
+    const auto kernel = glu_f32_kernel<SIDE, MODE>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * blocks), MODE == DW ? 2 : 1);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = Tiles<SIDE>::FLOATS * 4;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = blocks;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = blocks > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p, blocks);
+}
+template <Mode MODE> cudaError_t run_f32(const GluParams &p, cudaStream_t s) {
     constexpr bool DUAL = MODE == FWD || MODE == RECOMPUTE;
-    const long long ms = MODE == DW ? p.F : p.M, ns = DUAL ? p.F : p.D, tn = DUAL ? TILE / 2 : TILE;
-    const long long gy = (ms + TILE - 1) / TILE;
-    const long long tiles = gy * ((ns + tn - 1) / tn);
-    glu_simt_kernel<T, MODE><<<dim3((unsigned)tiles, MODE == DW ? 2 : 1), 256, 0, s>>>(p);
-    return cudaGetLastError();
+    const long long ms = MODE == DW ? p.F : p.M, ns = DUAL ? p.F : p.D, ks = MODE == DW ? p.M : MODE == DX ? 2LL * p.F : p.D;
+    auto tiles = [&](int side) {
+        const int tn = DUAL ? side / 2 : side;
+        return ((ms + side - 1) / side) * ((ns + tn - 1) / tn);
+    };
+    const long long z = MODE == DW ? 2 : 1, room = 2LL * sm_count();
+    if (tiles(128) * z > room / 2) return tiles(128) > 0x7fffffffLL ? cudaErrorNotSupported : run_side<128, MODE>(p, tiles(128), 1, s);
+    int blocks = 1;                      // (a block of the cluster has four steps of 32 at least)
+    while (blocks < 8 && tiles(64) * z * blocks * 2 <= room && ks >= 256LL * blocks) blocks *= 2;
+    return run_side<64, MODE>(p, tiles(64), blocks, s);
 }
 
 template <class T> cudaError_t slopes(const GluParams &p, cudaStream_t s) {
@@ -166,35 +240,76 @@ template <class T> cudaError_t slopes(const GluParams &p, cudaStream_t s) {
     const bool wide = p.F % W == 0 && rows_aligned(p.dh, p.ld_dh, sizeof(T), 16) && rows_aligned(p.dg, p.ld_d, sizeof(T), 16) &&
                       aligned_to(p.du, 16) && aligned_to(p.g, 16) && aligned_to(p.u, 16);
     const int v = wide ? W : 1;
-    const long long n = (p.F + v - 1) / v * p.M;
-    const unsigned grid = (unsigned)((n + 255) / 256);
+    const unsigned grid = (unsigned)(((p.F + v - 1) / v * p.M + 255) / 256);
     if (wide) glu_slope_kernel<T, W><<<grid, 256, 0, s>>>(p);
     else glu_slope_kernel<T, 1><<<grid, 256, 0, s>>>(p);
     return cudaGetLastError();
 }
 
-template <class T> cudaError_t bwd(const GluParams &p, cudaStream_t s) {
-    cudaError_t e = p.g ? slopes<T>(p, s) : run_simt<T, RECOMPUTE>(p, s);
-    if (e == cudaSuccess) e = run_simt<T, DX>(p, s);
-    if (e == cudaSuccess) e = run_simt<T, DW>(p, s);
-    return e;
+// Operands of bfloat16 products that TMA could not read where they are (bases or rows off 16 bytes) move into the workspace.
+struct Moved {
+    const void **p;
+    long long *ld, rows;
+};
+size_t moved_bytes(const Moved &m, int D) { return ((size_t)m.rows * ((D + 7) / 8 * 8) * 2 + 255) / 256 * 256; }
+template <class F> cudaError_t each_moved(GluParams &p, F f) {
+    const Moved all[] = {{&p.x, &p.ld_x, p.M}, {&p.wg, &p.ld_wg, p.F}, {&p.wu, &p.ld_wu, p.F}};
+    for (const Moved &m : all)
+        if (!rows_aligned(*m.p, *m.ld, 2, 16)) {
+            const cudaError_t e = f(m);
+            if (e != cudaSuccess) return e;
+        }
+    return cudaSuccess;
+}
+cudaError_t align(GluParams &p, char *ws, cudaStream_t s) {
+    return each_moved(p, [&](const Moved &m) {
+        const long long pitch = (p.D + 7) / 8 * 8;
+        const unsigned gx = (unsigned)((p.D + 1023) / 1024), gy = (unsigned)(m.rows < 32768 ? m.rows : 32768);
+        glu_align_kernel<<<dim3(gx, gy), 256, 0, s>>>(static_cast<const bf16 *>(*m.p), *m.ld, reinterpret_cast<bf16 *>(ws), pitch, m.rows, p.D);
+        *m.p = ws;
+        *m.ld = pitch;
+        ws += moved_bytes(m, p.D);
+        return cudaGetLastError();
+    });
 }
 
 }  // namespace
+
+size_t glu_moved_bytes(const GluParams &q, bool bf16_) {
+    GluParams p = q;
+    size_t n = 0;
+    if (bf16_)
+        each_moved(p, [&](const Moved &m) {
+            n += moved_bytes(m, p.D);
+            return cudaSuccess;
+        });
+    return n;
+}
 
 long long glu_grad_stride(const GluParams &p, bool bf16_) {
     const long long n = bf16_ ? 16 : 4;                      // rows of 32-byte sectors, of 16-byte accesses
     return (p.F + n - 1) / n * n;
 }
 
-cudaError_t launch_glu_fwd(const GluParams &p, bool bf16_, cudaStream_t s) {
-    if (!bf16_) return run_simt<float, FWD>(p, s);
-    if (glu_rows_takes(p)) return launch_glu_rows(p, s);
-    return glu_tc_takes(p) ? launch_glu_tc_fwd(p, s) : run_simt<bf16, FWD>(p, s);
+cudaError_t launch_glu_fwd(const GluParams &q, bool bf16_, char *ws, cudaStream_t s) {
+    if (!bf16_) return run_f32<FWD>(q, s);
+    if (glu_rows_takes(q)) return launch_glu_rows(q, s);
+    GluParams p = q;
+    const cudaError_t e = align(p, ws, s);
+    return e == cudaSuccess ? launch_glu_tc_fwd(p, s) : e;
 }
-cudaError_t launch_glu_bwd(const GluParams &p, bool bf16_, cudaStream_t s) {
-    if (!bf16_ || !glu_tc_takes(p)) return bf16_ ? bwd<bf16>(p, s) : bwd<float>(p, s);
-    cudaError_t e = p.g ? slopes<bf16>(p, s) : launch_glu_tc_grads(p, s);
+
+cudaError_t launch_glu_bwd(const GluParams &q, bool bf16_, char *ws, cudaStream_t s) {
+    cudaError_t e;
+    if (!bf16_) {
+        e = q.g ? slopes<float>(q, s) : run_f32<RECOMPUTE>(q, s);
+        if (e == cudaSuccess) e = run_f32<DX>(q, s);
+        if (e == cudaSuccess) e = run_f32<DW>(q, s);
+        return e;
+    }
+    GluParams p = q;
+    e = align(p, ws, s);
+    if (e == cudaSuccess) e = p.g ? slopes<bf16>(p, s) : launch_glu_tc_grads(p, s);
     if (e == cudaSuccess) e = launch_glu_tc_dx(p, s);
     if (e == cudaSuccess) e = launch_glu_tc_dw(p, s);
     return e;

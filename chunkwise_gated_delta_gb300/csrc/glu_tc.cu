@@ -59,6 +59,7 @@ struct Shared {
     uint32_t tmem;
     int abort;
     unsigned issued[2];                     // stages that each CTA of the pair began to load
+    float turn[EPI_WARPS][32][33];
 };
 
 // ------------------------------------------------------------------------------------- pair forms
@@ -159,47 +160,54 @@ __device__ __forceinline__ void store_sector(void *to, const uint32_t (&q)[8]) {
                  "r"(q[5]), "r"(q[6]), "r"(q[7])
                  : "memory");
 }
-// The epilogue's row and 32 columns; `inside` of them belong to the output.  wide: rows of whole sectors.
-__device__ __forceinline__ void store_row(bf16 *out, const float (&v)[32], int inside, bool wide) {
-    if (wide && inside >= 32) {
+__device__ __forceinline__ void put(bf16 *to, float v) { *to = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put(float *to, float v) { *to = v; }
+__device__ __forceinline__ void store_whole(bf16 *out, const float (&v)[32]) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            uint32_t q[8];
+    for (int k = 0; k < 2; ++k) {
+        uint32_t q[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) q[e] = pack_bf16(v[16 * k + 2 * e], v[16 * k + 2 * e + 1]);
-            store_sector(out + 16 * k, q);
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < 32; ++k)
-            if (k < inside) out[k] = __float2bfloat16_rn(v[k]);
+        for (int e = 0; e < 8; ++e) q[e] = pack_bf16(v[16 * k + 2 * e], v[16 * k + 2 * e + 1]);
+        store_sector(out + 16 * k, q);
     }
 }
-__device__ __forceinline__ void store_row(float *out, const float (&v)[32], int inside, bool wide) {
-    if (wide && inside >= 32) {
+__device__ __forceinline__ void store_whole(float *out, const float (&v)[32]) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            uint32_t q[8];
+    for (int k = 0; k < 4; ++k) {
+        uint32_t q[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) q[e] = __float_as_uint(v[8 * k + e]);
-            store_sector(out + 8 * k, q);
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < 32; ++k)
-            if (k < inside) out[k] = v[k];
+        for (int e = 0; e < 8; ++e) q[e] = __float_as_uint(v[8 * k + e]);
+        store_sector(out + 8 * k, q);
     }
+}
+// 32 rows of a warp, 32 columns: v is this lane's row, `first` the warp's first row, of which `rows` belong to the output, as
+// `inside` of the columns.  Rows of whole sectors go out by lanes; others turn in shared memory, so that a row's neighbours leave
+// together.
+template <class T> __device__ __forceinline__ void store_rows(T *first, long long ld, const float (&v)[32], int rows, int inside, bool wide, float (*turn)[33]) {
+    const int lane = threadIdx.x & 31;
+    if (wide && inside >= 32) {
+        if (lane < rows) store_whole(first + lane * ld, v);
+        return;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 32; ++k) turn[lane][k] = v[k];
+    __syncwarp();
+    for (int r = 0; r < rows; ++r, first += ld)
+        if (lane < inside) put(first + lane, turn[r][lane]);
 }
 __device__ __forceinline__ bool wide_rows(const void *p, long long ld, int es) {
     return (reinterpret_cast<uintptr_t>(p) & 31) == 0 && ld * es % 32 == 0;
 }
 
-// The outputs of one row (of the call) and a tile's columns.  get(c, v): 32 accumulator columns from c.
-template <Mode MODE, class Get> __device__ __forceinline__ void finish(const GluParams &p, const Tile &q, long long row, bool on, Get get) {
+// The outputs of a warp's 32 rows from row0 (of the call), `rows` of which belong to it, and a tile's columns.  get(c, v): this
+// lane's row of 32 accumulator columns from c.
+template <Mode MODE, class Get>
+__device__ __forceinline__ void finish(const GluParams &p, const Tile &q, long long row0, int rows, float (*turn)[33], Get get) {
     if constexpr (MODE == FWD || MODE == RECOMPUTE) {
         const int n0 = q.n * HALF;
-        bf16 *h = static_cast<bf16 *>(p.h), *dg = static_cast<bf16 *>(p.dg), *du = static_cast<bf16 *>(p.du);
-        const bool wide = MODE == FWD ? wide_rows(p.h, p.ld_h, 2) : wide_rows(p.dg, p.ld_d, 2) && wide_rows(p.du, p.ld_d, 2), keep = wide_rows(p.g, p.F, 4) && wide_rows(p.u, p.F, 4);
+        const bool wide = MODE == FWD ? wide_rows(p.h, p.ld_h, 2) : wide_rows(p.dg, p.ld_d, 2) && wide_rows(p.du, p.ld_d, 2);
+        const bool keep = wide_rows(p.g, p.F, 4) && wide_rows(p.u, p.F, 4);
 #pragma unroll 1
         for (int c = 0; c < HALF; c += 32) {
             float g[32], u[32];
@@ -207,17 +215,18 @@ template <Mode MODE, class Get> __device__ __forceinline__ void finish(const Glu
             get(c, g);
             get(HALF + c, u);
             const int n = n0 + c, inside = p.F - n;
-            if (!on || inside <= 0) continue;
+            if (inside <= 0 || rows <= 0) continue;
             if constexpr (MODE == FWD) {
                 if (p.g) {
-                    store_row(p.g + row * p.F + n, g, inside, keep);
-                    store_row(p.u + row * p.F + n, u, inside, keep);
+                    store_rows(p.g + row0 * p.F + n, p.F, g, rows, inside, keep, turn);
+                    store_rows(p.u + row0 * p.F + n, p.F, u, rows, inside, keep, turn);
                 }
 #pragma unroll
                 for (int k = 0; k < 32; ++k) u[k] *= act(g[k], p.gelu);
-                store_row(h + row * p.ld_h + n, u, inside, wide);
+                store_rows(static_cast<bf16 *>(p.h) + row0 * p.ld_h + n, p.ld_h, u, rows, inside, wide, turn);
             } else {
-                const bf16 *dh = static_cast<const bf16 *>(p.dh) + row * p.ld_dh + n;
+                const int lane = threadIdx.x & 31;
+                const bf16 *dh = static_cast<const bf16 *>(p.dh) + (row0 + min(lane, rows - 1)) * p.ld_dh + n;
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {
                     const Act f = act_and_slope(g[k], p.gelu);
@@ -225,8 +234,8 @@ template <Mode MODE, class Get> __device__ __forceinline__ void finish(const Glu
                     g[k] = d * u[k] * f.d;
                     u[k] = d * f.v;
                 }
-                store_row(dg + row * p.ld_d + n, g, inside, wide);
-                store_row(du + row * p.ld_d + n, u, inside, wide);
+                store_rows(static_cast<bf16 *>(p.dg) + row0 * p.ld_d + n, p.ld_d, g, rows, inside, wide, turn);
+                store_rows(static_cast<bf16 *>(p.du) + row0 * p.ld_d + n, p.ld_d, u, rows, inside, wide, turn);
             }
         }
     } else {
@@ -241,7 +250,7 @@ template <Mode MODE, class Get> __device__ __forceinline__ void finish(const Glu
             __syncwarp();
             get(c, v);
             const int inside = p.D - n0 - c;
-            if (on && inside > 0) store_row(out + row * ld + n0 + c, v, inside, wide);
+            if (inside > 0 && rows > 0) store_rows(out + row0 * ld + n0 + c, ld, v, rows, inside, wide, turn);
         }
     }
 }
@@ -360,17 +369,17 @@ template <bool PAIR, Mode MODE> __global__ void __launch_bounds__(THREADS, 1) gl
             if (lane == 0) ok = wait(&sh.acc_full[buf], n / 2 & 1);
             ok = __shfl_sync(~0u, ok, 0);
             tc_fence_after();
-            const long long row = (long long)q.m * C::ROWS + rank * HALF + quarter * 32 + lane;
-            const bool on = row < (MODE == DW ? (long long)t.p.F : t.p.M);
+            const long long row0 = (long long)q.m * C::ROWS + rank * HALF + quarter * 32;
+            const int rows = (int)max(0LL, min(32LL, (MODE == DW ? (long long)t.p.F : t.p.M) - row0));
             const uint32_t at = tmem + ((uint32_t)quarter << 21) + buf * COLS;
             if (ok) {
-                finish<MODE>(t.p, q, row, on, [&](int c, float (&v)[32]) { tmem_ld32(at + c, v); });
+                finish<MODE>(t.p, q, row0, rows, sh.turn[quarter], [&](int c, float (&v)[32]) { tmem_ld32(at + c, v); });
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive_cluster(leader_bar(&sh.acc_empty[buf]));
             } else {                                     // broken off: the tile's outputs say so
                 const float bad = __int_as_float(0x7fc00000);
-                finish<MODE>(t.p, q, row, on, [&](int, float (&v)[32]) {
+                finish<MODE>(t.p, q, row0, rows, sh.turn[quarter], [&](int, float (&v)[32]) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) v[k] = bad;
                 });
@@ -493,10 +502,6 @@ template <Mode MODE> cudaError_t run(const GluParams &p, int *status, cudaStream
 
 }  // namespace
 
-// What TMA asks of the operands: 16-byte aligned bases and rows.
-bool glu_tc_takes(const GluParams &p) {
-    return rows_aligned(p.x, p.ld_x, 2, 16) && rows_aligned(p.wg, p.ld_wg, 2, 16) && rows_aligned(p.wu, p.ld_wu, 2, 16);
-}
 cudaError_t launch_glu_tc_fwd(const GluParams &p, cudaStream_t s) { return run<FWD>(p, p.status, s); }
 cudaError_t launch_glu_tc_grads(const GluParams &p, cudaStream_t s) { return run<RECOMPUTE>(p, p.status, s); }
 cudaError_t launch_glu_tc_dx(const GluParams &p, cudaStream_t s) { return run<DX>(p, p.status, s); }

@@ -128,19 +128,20 @@ template <class A> kda_status glu_common(const A *a, mixer::GluParams &p) {
     return KDA_OK;
 }
 
-kda_status glu_fwd_params(const glu_fwd_args *a, mixer::GluParams &p) {
+kda_status glu_fwd_params(const glu_fwd_args *a, mixer::GluParams &p, size_t &need) {
     if (!a || !a->h) return KDA_ERR_INVALID_ARG;
     const kda_status st = glu_common(a, p);
     if (st != KDA_OK) return st;
     p.h = a->h; p.ld_h = stride_or(a->ld_h, a->F); p.g = a->g; p.u = a->u;
+    need = mixer::glu_moved_bytes(p, a->dtype == KDA_BF16);
     const size_t es = es_of(a->dtype);
     const Block in[] = {{a->x, a->rows, a->D, p.ld_x, es}, {a->w_gate, a->F, a->D, p.ld_wg, es}, {a->w_up, a->F, a->D, p.ld_wu, es}};
     const Block out[] = {{a->h, a->rows, a->F, p.ld_h, es}, dense(a->g, a->rows, a->F, 4), dense(a->u, a->rows, a->F, 4),
-                         dense(a->status, 1, 256, 1)};
+                         dense(a->status, 1, 256, 1), dense(need ? a->workspace : nullptr, 1, (long long)a->workspace_bytes, 1)};
     return blocks_ok(in, out) ? KDA_OK : KDA_ERR_INVALID_ARG;
 }
 
-kda_status glu_bwd_params(const glu_bwd_args *a, mixer::GluParams &p, size_t &need) {
+kda_status glu_bwd_params(const glu_bwd_args *a, mixer::GluParams &p, size_t &need, size_t &grads) {
     if (!a || !a->dh || !a->dx || !a->dw_gate || !a->dw_up) return KDA_ERR_INVALID_ARG;
     const kda_status st = glu_common(a, p);
     if (st != KDA_OK) return st;
@@ -150,7 +151,8 @@ kda_status glu_bwd_params(const glu_bwd_args *a, mixer::GluParams &p, size_t &ne
     p.ld_dwg = stride_or(a->ld_dw_gate, a->D); p.ld_dwu = stride_or(a->ld_dw_up, a->D);
     const size_t es = es_of(a->dtype);
     p.ld_d = mixer::glu_grad_stride(p, a->dtype == KDA_BF16);
-    need = 2 * (size_t)a->rows * p.ld_d * es;
+    grads = (2 * (size_t)a->rows * p.ld_d * es + 255) / 256 * 256;
+    need = grads + mixer::glu_moved_bytes(p, a->dtype == KDA_BF16);
     const Block in[] = {{a->x, a->rows, a->D, p.ld_x, es}, {a->w_gate, a->F, a->D, p.ld_wg, es}, {a->w_up, a->F, a->D, p.ld_wu, es},
                         {a->dh, a->rows, a->F, p.ld_dh, es}, dense(a->g, a->rows, a->F, 4), dense(a->u, a->rows, a->F, 4)};
     const Block out[] = {{a->dx, a->rows, a->D, p.ld_dx, es}, {a->dw_gate, a->F, a->D, p.ld_dwg, es},
@@ -245,28 +247,37 @@ kda_status group_norm_bwd(const group_norm_bwd_args *a, kda_stream_t stream) {
     return from(mixer::launch_group_norm_bwd(p, a->dtype == KDA_BF16, stream_of(stream)));
 }
 
+size_t glu_fwd_workspace(const glu_fwd_args *a) {
+    mixer::GluParams p{};
+    size_t need = 0;
+    return glu_fwd_params(a, p, need) == KDA_OK ? need : 0;
+}
+
 kda_status glu_fwd(const glu_fwd_args *a, kda_stream_t stream) {
     mixer::GluParams p{};
-    const kda_status st = glu_fwd_params(a, p);
-    return st != KDA_OK ? st : from(mixer::launch_glu_fwd(p, a->dtype == KDA_BF16, stream_of(stream)));
+    size_t need = 0;
+    kda_status st = glu_fwd_params(a, p, need);
+    if (st != KDA_OK) return st;
+    if (need && (st = check_space(a->workspace, a->workspace_bytes, need)) != KDA_OK) return st;
+    return from(mixer::launch_glu_fwd(p, a->dtype == KDA_BF16, static_cast<char *>(a->workspace), stream_of(stream)));
 }
 
 size_t glu_bwd_workspace(const glu_bwd_args *a) {
     mixer::GluParams p{};
-    size_t need = 0;
-    return glu_bwd_params(a, p, need) == KDA_OK ? need : 0;
+    size_t need = 0, grads = 0;
+    return glu_bwd_params(a, p, need, grads) == KDA_OK ? need : 0;
 }
 
 kda_status glu_bwd(const glu_bwd_args *a, kda_stream_t stream) {
     mixer::GluParams p{};
-    size_t need = 0;
-    kda_status st = glu_bwd_params(a, p, need);
+    size_t need = 0, grads = 0;
+    kda_status st = glu_bwd_params(a, p, need, grads);
     if (st != KDA_OK) return st;
     if ((st = check_space(a->workspace, a->workspace_bytes, need)) != KDA_OK) return st;
     char *ws = static_cast<char *>(a->workspace);
     p.dg = ws;
-    p.du = ws + need / 2;
-    return from(mixer::launch_glu_bwd(p, a->dtype == KDA_BF16, stream_of(stream)));
+    p.du = ws + (size_t)a->rows * p.ld_d * es_of(a->dtype);
+    return from(mixer::launch_glu_bwd(p, a->dtype == KDA_BF16, ws + grads, stream_of(stream)));
 }
 
 }  // extern "C"

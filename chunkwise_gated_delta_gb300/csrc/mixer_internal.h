@@ -135,11 +135,11 @@ cudaError_t launch_group_norm_fwd(const GroupNormParams &p, bool bf16, cudaStrea
 cudaError_t launch_group_norm_bwd(const GroupNormParams &p, bool bf16, cudaStream_t s);
 size_t group_norm_part_floats(const GroupNormParams &p, bool bf16);
 
-cudaError_t launch_glu_fwd(const GluParams &p, bool bf16, cudaStream_t s);
-cudaError_t launch_glu_bwd(const GluParams &p, bool bf16, cudaStream_t s);
+cudaError_t launch_glu_fwd(const GluParams &p, bool bf16, char *ws, cudaStream_t s);
+cudaError_t launch_glu_bwd(const GluParams &p, bool bf16, char *ws, cudaStream_t s);
 long long glu_grad_stride(const GluParams &p, bool bf16);
+size_t glu_moved_bytes(const GluParams &p, bool bf16);       // of ws
 // Forms of bfloat16 calls: the tensor cores' products, and a few rows past the weights.
-bool glu_tc_takes(const GluParams &p);
 cudaError_t launch_glu_tc_fwd(const GluParams &p, cudaStream_t s);
 cudaError_t launch_glu_tc_grads(const GluParams &p, cudaStream_t s);
 cudaError_t launch_glu_tc_dx(const GluParams &p, cudaStream_t s);

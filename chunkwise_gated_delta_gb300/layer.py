@@ -243,7 +243,10 @@ def glu_fwd(x, w_gate, w_up, *, activation="silu", save=False, y=None, status=No
         if save:
             g, gp = _dense_out(on, None, "g", shape, _F32)
             u, up = _dense_out(on, None, "u", shape, _F32)
-        on.launch("glu_fwd", _lib.GluFwdArgs(rows, D, F, code, flags, *ptrs, yp, ldy, gp, up, stp))
+        args = _lib.GluFwdArgs(rows, D, F, code, flags, *ptrs, yp, ldy, gp, up, None, 0, stp)
+        ws = on.workspace("glu_fwd_workspace", args)
+        on.launch("glu_fwd", args)
+        del ws
     return (y, g, u) if save else y
 
 

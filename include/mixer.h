@@ -443,10 +443,11 @@ kda_status group_norm_bwd(const group_norm_bwd_args *args, kda_stream_t stream);
 #define GLU_FLAG_GELU 1u    /* act(g) = g Phi(g); cleared: g sigmoid(g) */
 
 /*
- * bfloat16 products run on the tensor cores where bases and rows of x and of the weights are 16-byte aligned (a
- * few rows aside); everything else runs on the CUDA cores.  The former's waits are bounded: where one
- * runs out, the call leaves NaN in what it did not finish.  With a status block (the head of kda.h's workspaces:
- * 256 bytes, 16-byte aligned, zero at first, word 7 the wait budget) kda_status_read then answers KDA_ERR_TIMEOUT.
+ * bfloat16 products run on the tensor cores (x and weights whose base or rows are off 16 bytes move into the workspace
+ * first), those of a few rows in one pass over the weights, float32 products on the CUDA cores.  The
+ * first one's waits are bounded: where one runs out, the call leaves NaN in what it did not finish.  With a status block (the head
+ * of kda.h's workspaces: 256 bytes, 16-byte aligned, zero at first, word 7 the wait budget) kda_status_read then
+ * answers KDA_ERR_TIMEOUT.
  */
 
 typedef struct {
@@ -463,8 +464,13 @@ typedef struct {
     void *h;               /* [rows, F] out */
     long long ld_h;
     float *g, *u;          /* [rows, F] out, the two products for glu_bwd; or both NULL (not kept) */
-    void *status;          /* 256-byte status block (below), or NULL */
+    void *workspace;       /* glu_fwd_workspace bytes, or NULL when that is 0 */
+    size_t workspace_bytes;
+    void *status;          /* 256-byte status block (above), or NULL */
 } glu_fwd_args;
+
+/* Bytes of workspace (0 on bad args): operands of bfloat16 products that lie off 16 bytes. */
+size_t glu_fwd_workspace(const glu_fwd_args *args);
 
 kda_status glu_fwd(const glu_fwd_args *args, kda_stream_t stream);
 
@@ -493,7 +499,7 @@ typedef struct {
     void *status;          /* as the forward's */
 } glu_bwd_args;
 
-/* Bytes of workspace (0 on bad args): the gradients of the two products. */
+/* Bytes of workspace (0 on bad args): the gradients of the two products, and operands that lie off 16 bytes. */
 size_t glu_bwd_workspace(const glu_bwd_args *args);
 
 /*
