@@ -7,6 +7,8 @@
 // SIDE products, a thread two quads (SIDE = 64: one) per axis; in the forward the left half of the columns is Wg's and the right
 // half Wu's.  Where tiles of 128 leave the GPU idle, tiles of 64 are used and a cluster of up to eight blocks shares the sum
 // of a tile, joined in the blocks' order through shared memory.
+#include <type_traits>
+
 #include "glu.cuh"
 #include "tc_common.cuh"
 
@@ -23,27 +25,43 @@ template <int SIDE> struct Tiles {
     static constexpr int FLOATS = 4 * STAGE > SIDE * (SIDE + 1) ? 4 * STAGE : SIDE * (SIDE + 1);
 };
 
-// E elements of an operand's tile [KT][SIDE] per thread: along k, or along the rows, whichever lies contiguous.
+// E elements of an operand's tile [KT][SIDE] per thread, neighbouring threads along the axis that lies contiguous (k, or the rows).
 template <int SIDE, bool KMAJOR> struct Operand {
     using S = Tiles<SIDE>;
-    static constexpr int PER = (KMAJOR ? S::KT : SIDE) / S::E;      // threads of a contiguous stretch
+    static constexpr int LEN = KMAJOR ? S::KT : SIDE, STEP = 256 / LEN;      // of a stretch; stretches at a time
     float v[S::E];
-    // row0, k0: the tile's corner; rows, ks: the operand's extent; ld: stride of the axis that is not contiguous.
-    __device__ __forceinline__ void load(const float *p, long long ld, long long row0, long long rows, long long k0, long long ks) {
-        const int t = threadIdx.x, in = t % PER * S::E, out = t / PER;
-        const long long r0 = row0 + (KMAJOR ? out : in), c0 = k0 + (KMAJOR ? in : out);
-        const float *q = p + (KMAJOR ? r0 * ld + c0 : c0 * ld + r0);
+    // p: the tile's first element; left_r, left_k: the operand's extent from there; ld: stride of the axis that is not contiguous.
+    __device__ __forceinline__ void load(const float *p, long long ld, long long left_r, long long left_k) {
+        const int in = threadIdx.x % LEN, out = threadIdx.x / LEN;
+        p += out * ld + in;
+        const bool inside = in < (KMAJOR ? left_k : left_r);
 #pragma unroll
-        for (int e = 0; e < S::E; ++e)
-            v[e] = (KMAJOR ? r0 < rows && c0 + e < ks : r0 + e < rows && c0 < ks) ? __ldg(q + e) : 0.f;
+        for (int e = 0; e < S::E; ++e, p += STEP * ld) v[e] = inside && out + e * STEP < (KMAJOR ? left_r : left_k) ? __ldg(p) : 0.f;
     }
     __device__ __forceinline__ void store(float *sm) const {
-        const int t = threadIdx.x, in = t % PER * S::E, out = t / PER;
+        const int in = threadIdx.x % LEN, out = threadIdx.x / LEN;
+#pragma unroll
+        for (int e = 0; e < S::E; ++e) sm[KMAJOR ? in * S::PITCH + out + e * STEP : (out + e * STEP) * S::PITCH + in] = v[e];
+    }
+};
+// The forward's tile of weights: its first half of rows from Wg, its second from Wu, k contiguous.
+template <int SIDE> struct Weights {
+    using S = Tiles<SIDE>;
+    static constexpr int STEP = 256 / S::KT, TN = SIDE / 2;
+    float v[S::E];
+    __device__ __forceinline__ void load(const float *g, long long ldg, const float *u, long long ldu, long long left_r, long long left_k) {
+        const int in = threadIdx.x % S::KT, out = threadIdx.x / S::KT;
 #pragma unroll
         for (int e = 0; e < S::E; ++e) {
-            if (KMAJOR) sm[(in + e) * S::PITCH + out] = v[e];
-            else sm[out * S::PITCH + in + e] = v[e];
+            const int r = (out + e * STEP) % TN;
+            const float *p = e * STEP < TN ? g + r * ldg : u + r * ldu;
+            v[e] = in < left_k && r < left_r ? __ldg(p + in) : 0.f;
         }
+    }
+    __device__ __forceinline__ void store(float *sm) const {
+        const int in = threadIdx.x % S::KT, out = threadIdx.x / S::KT;
+#pragma unroll
+        for (int e = 0; e < S::E; ++e) sm[in * S::PITCH + out + e * STEP] = v[e];
     }
 };
 
@@ -85,23 +103,23 @@ template <int SIDE, Mode MODE> __global__ void __launch_bounds__(256, 2) glu_f32
 #pragma unroll
         for (int j = 0; j < N; ++j) acc[i][j] = 0.f;
     Operand<SIDE, AK> a;
-    Operand<SIDE, BK> b;
+    std::conditional_t<DUAL, Weights<SIDE>, Operand<SIDE, BK>> b;
     const long long per = (ks + S::KT - 1) / S::KT, steps = MODE == DX ? 2 * per : per;
     const long long first = steps * rank / blocks, end = steps * (rank + 1) / blocks;
     auto fetch = [&](long long i) {
+        const long long k0 = (MODE == DX && i >= per ? i - per : i) * S::KT;
         if constexpr (DUAL) {
-            a.load(static_cast<const float *>(p.x), p.ld_x, m0, ms, i * S::KT, ks);
-            // the tile's first half of rows from Wg, the second from Wu (threads 0 .. 127 and 128 .. 255)
-            const bool right = t >= 128;
-            b.load(static_cast<const float *>(right ? p.wu : p.wg), right ? p.ld_wu : p.ld_wg, right ? n0 - TN : n0, ns, i * S::KT, ks);
+            a.load(static_cast<const float *>(p.x) + m0 * p.ld_x + k0, p.ld_x, ms - m0, ks - k0);
+            b.load(static_cast<const float *>(p.wg) + n0 * p.ld_wg + k0, p.ld_wg, static_cast<const float *>(p.wu) + n0 * p.ld_wu + k0, p.ld_wu,
+                   ns - n0, ks - k0);
         } else if constexpr (MODE == DX) {
             const bool second = i >= per;
-            const long long k0 = (second ? i - per : i) * S::KT;
-            a.load(static_cast<const float *>(second ? p.du : p.dg), p.ld_d, m0, ms, k0, ks);
-            b.load(static_cast<const float *>(second ? p.wu : p.wg), second ? p.ld_wu : p.ld_wg, n0, ns, k0, ks);
+            a.load(static_cast<const float *>(second ? p.du : p.dg) + m0 * p.ld_d + k0, p.ld_d, ms - m0, ks - k0);
+            const long long ld = second ? p.ld_wu : p.ld_wg;
+            b.load(static_cast<const float *>(second ? p.wu : p.wg) + k0 * ld + n0, ld, ns - n0, ks - k0);
         } else {
-            a.load(static_cast<const float *>(up ? p.du : p.dg), p.ld_d, m0, ms, i * S::KT, ks);
-            b.load(static_cast<const float *>(p.x), p.ld_x, n0, ns, i * S::KT, ks);
+            a.load(static_cast<const float *>(up ? p.du : p.dg) + k0 * p.ld_d + m0, p.ld_d, ms - m0, ks - k0);
+            b.load(static_cast<const float *>(p.x) + k0 * p.ld_x + n0, p.ld_x, ns - n0, ks - k0);
         }
     };
     float *sa = sm, *sb = sm + 2 * S::STAGE;
