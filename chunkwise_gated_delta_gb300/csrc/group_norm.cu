@@ -44,6 +44,26 @@ int slots_per_row(int G, int slots) {
     return n;
 }
 
+// Rows on their way: every thread copies its own vectors of N tensors into its own places of shared memory, DEPTH rows ahead,
+// and reads them back, so nobody waits for anybody.  (Single bfloat16 elements are too short for asynchronous copies.)
+template <class T, int V, int ITEMS, int N> struct Ahead {
+    static constexpr int DEPTH = ITEMS == 1 ? 4 : 2, BYTES = V * (int)sizeof(T) < 4 ? 4 : V * (int)sizeof(T);
+    static constexpr int STAGE = N * ITEMS * TPB * BYTES, SMEM = DEPTH * STAGE;
+    static __device__ __forceinline__ char *place(char *sm, int stage, int n, int k) {
+        return sm + stage * STAGE + ((n * ITEMS + k) * TPB + threadIdx.x) * BYTES;
+    }
+    static __device__ __forceinline__ void bring(char *sm, int stage, int n, int k, const T *from) {
+        char *to = place(sm, stage, n, k);
+        if constexpr (V * sizeof(T) < 4) *reinterpret_cast<uint32_t *>(to) = load_bits(from);
+        else copy_async<BYTES>(to, from);
+    }
+    static __device__ __forceinline__ Lanes<T, V> take(char *sm, int stage, int n, int k) {
+        Lanes<T, V> v;
+        v.load_shared(place(sm, stage, n, k));
+        return v;
+    }
+};
+
 template <class T, int V, int ITEMS, int L, bool GATE>
 __global__ void __launch_bounds__(TPB) group_norm_fwd_kernel(GroupNormParams p, int per) {
     constexpr int P = (V + 1) / 2;
@@ -65,31 +85,42 @@ __global__ void __launch_bounds__(TPB) group_norm_fwd_kernel(GroupNormParams p, 
         if (p.weight) load_param_pairs<V>(w[k], p.weight, c, p.w_bf16);
         if (p.bias) load_param_pairs<V>(b[k], p.bias, c, p.w_bf16);
     }
-    Lanes<T, V> nx[ITEMS], ng[ITEMS];
-    auto fetch = [&](long long row) {
-        if (row >= p.rows) row = p.rows - 1;
-        const T *x = static_cast<const T *>(p.x) + row * p.ld_x + col;
-        const T *g = static_cast<const T *>(p.gate) + row * p.ld_gate + col;
+    using A = Ahead<T, V, ITEMS, GATE ? 2 : 1>;
+    extern __shared__ __align__(16) char sm[];
+    const long long step = (long long)gridDim.x * q.rows;
+    long long row = (long long)blockIdx.x * q.rows + q.row, next = row;
+    auto bring = [&](int stage) {                    // rows past the end: the last
+        const long long r = next < p.rows ? next : p.rows - 1;
+        const T *x = static_cast<const T *>(p.x) + r * p.ld_x + col;
+        const T *g = static_cast<const T *>(p.gate) + r * p.ld_gate + col;
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
-            nx[k].load(x + at[k]);
-            if (GATE) ng[k].load(g + at[k]);
+            A::bring(sm, stage, 0, k, x + at[k]);
+            if (GATE) A::bring(sm, stage, 1, k, g + at[k]);
         }
+        copies_end();
+        next += step;
     };
-    const long long step = (long long)gridDim.x * q.rows;
-    long long row = (long long)blockIdx.x * q.rows + q.row;
-    fetch(row);
+#pragma unroll
+    for (int d = 0; d < A::DEPTH; ++d) bring(d);
     // every lane goes through as many visits as the block's first row takes: their sums are taken together
+    int stage = 0;
     for (long long base = (long long)blockIdx.x * q.rows; base < p.rows; base += step, row += step) {
+        copies_wait<A::DEPTH - 1>();
         f2 v[ITEMS][P], z[ITEMS][P];
 #pragma unroll
-        for (int k = 0; k < ITEMS; ++k)
+        for (int k = 0; k < ITEMS; ++k) {
+            const Lanes<T, V> x = A::take(sm, stage, 0, k);
 #pragma unroll
-            for (int e = 0; e < P; ++e) {
-                v[k][e] = nx[k].pair(e);
-                if (GATE) z[k][e] = ng[k].pair(e);
+            for (int e = 0; e < P; ++e) v[k][e] = x.pair(e);
+            if (GATE) {
+                const Lanes<T, V> g = A::take(sm, stage, 1, k);
+#pragma unroll
+                for (int e = 0; e < P; ++e) z[k][e] = g.pair(e);
             }
-        if (base + step < p.rows) fetch(row + step);
+        }
+        bring(stage);
+        stage = stage + 1 == A::DEPTH ? 0 : stage + 1;
         float mean = 0.f;
         if (p.center) {
             f2 acc = both(0.f);
@@ -131,8 +162,9 @@ __global__ void __launch_bounds__(TPB) group_norm_fwd_kernel(GroupNormParams p, 
     }
 }
 
-template <class T, int V, int ITEMS, int L, bool GATE>
-__global__ void __launch_bounds__(TPB) group_norm_bwd_kernel(GroupNormParams p, int per) {
+// BIAS: the call has a bias or wants its gradient.
+template <class T, int V, int ITEMS, int L, bool GATE, bool BIAS>
+__global__ void __launch_bounds__(TPB, ITEMS == 1 ? 3 : 1) group_norm_bwd_kernel(GroupNormParams p, int per) {
     constexpr int P = (V + 1) / 2, SLOTS = TPB / L;
     const Place q = place_of<L>(p, per);
     const int lane = threadIdx.x % L, nv = p.C / V;
@@ -150,57 +182,69 @@ __global__ void __launch_bounds__(TPB) group_norm_bwd_kernel(GroupNormParams p, 
         }
         const long long c = p.shared ? at[k] : col + at[k];
         if (p.weight) load_param_pairs<V>(w[k], p.weight, c, p.w_bf16);
-        if (GATE && p.bias) load_param_pairs<V>(b[k], p.bias, c, p.w_bf16);
+        if (GATE && BIAS && p.bias) load_param_pairs<V>(b[k], p.bias, c, p.w_bf16);
     }
-    Lanes<T, V> nx[ITEMS], ng[ITEMS], nd[ITEMS];
-    float nm, nr;
-    auto fetch = [&](long long row) {
-        if (row >= p.rows) row = p.rows - 1;
-        const T *x = static_cast<const T *>(p.x) + row * p.ld_x + col;
-        const T *g = static_cast<const T *>(p.gate) + row * p.ld_gate + col;
-        const T *d = static_cast<const T *>(p.dy) + row * p.ld_dy + col;
-        nm = p.mean ? __ldg(p.mean + row * p.G + q.group) : 0.f;
-        nr = __ldg(p.rstd + row * p.G + q.group);
+    using A = Ahead<T, V, ITEMS, GATE ? 3 : 2>;
+    extern __shared__ __align__(16) char sm[];
+    float2 *stats = reinterpret_cast<float2 *>(sm + A::SMEM);        // [DEPTH][TPB] mean and rstd
+    const long long step = (long long)gridDim.x * q.rows;
+    long long row = (long long)blockIdx.x * q.rows + q.row, next = row;
+    auto bring = [&](int stage) {
+        const long long r = next < p.rows ? next : p.rows - 1;
+        const T *x = static_cast<const T *>(p.x) + r * p.ld_x + col;
+        const T *d = static_cast<const T *>(p.dy) + r * p.ld_dy + col;
+        const T *g = static_cast<const T *>(p.gate) + r * p.ld_gate + col;
+        float2 *to = stats + stage * TPB + threadIdx.x;
+        if (p.center) copy_async<4>(&to->x, p.mean + r * p.G + q.group);
+        copy_async<4>(&to->y, p.rstd + r * p.G + q.group);
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
-            nx[k].load(x + at[k]);
-            nd[k].load(d + at[k]);
-            if (GATE) ng[k].load(g + at[k]);
+            A::bring(sm, stage, 0, k, x + at[k]);
+            A::bring(sm, stage, 1, k, d + at[k]);
+            if (GATE) A::bring(sm, stage, 2, k, g + at[k]);
         }
+        copies_end();
+        next += step;
     };
-    const long long step = (long long)gridDim.x * q.rows;
-    long long row = (long long)blockIdx.x * q.rows + q.row;
-    fetch(row);
+#pragma unroll
+    for (int d = 0; d < A::DEPTH; ++d) bring(d);
+    int stage = 0;
     for (long long base = (long long)blockIdx.x * q.rows; base < p.rows; base += step, row += step) {
+        copies_wait<A::DEPTH - 1>();
         const bool live = q.on && row < p.rows;
         f2 xh[ITEMS][P], g[ITEMS][P], s0 = both(0.f), s1 = both(0.f);
-        const float rstd = nr;
+        const float2 stat = stats[stage * TPB + threadIdx.x];
+        const float nm = p.center ? stat.x : 0.f, rstd = stat.y;
         T *dgate = static_cast<T *>(p.dgate) + row * p.ld_dgate + col;
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
             const bool in = live && lane + k * L < nv;
             f2 dz[P];
+            const Lanes<T, V> vx = A::take(sm, stage, 0, k), vd = A::take(sm, stage, 1, k);
+            Lanes<T, V> vg;
+            if (GATE) vg = A::take(sm, stage, 2, k);
 #pragma unroll
             for (int e = 0; e < P; ++e) {
-                f2 d = nd[k].pair(e);
-                xh[k][e] = mul2(add2(nx[k].pair(e), both(-nm)), both(rstd));
+                f2 d = vd.pair(e);
+                xh[k][e] = mul2(add2(vx.pair(e), both(-nm)), both(rstd));
                 if (GATE) {
-                    const f2 z = ng[k].pair(e), sg = sigmoid2(z), sz = mul2(sg, z);
+                    const f2 z = vg.pair(e), sg = sigmoid2(z), sz = mul2(sg, z);
                     // d silu / dz = sg + sz - sz sg
-                    dz[e] = mul2(mul2(d, fma2(xh[k][e], w[k][e], b[k][e])), fma2(sz, mul2(sg, both(-1.f)), add2(sg, sz)));
+                    dz[e] = mul2(mul2(d, BIAS ? fma2(xh[k][e], w[k][e], b[k][e]) : mul2(xh[k][e], w[k][e])), fma2(sz, mul2(sg, both(-1.f)), add2(sg, sz)));
                     d = mul2(d, sz);
                 }
                 g[k][e] = mul2(d, w[k][e]);
                 if (in) {                        // (what stands in for a row past the end is not counted: by selection)
                     aw[k][e] = fma2(d, xh[k][e], aw[k][e]);
-                    ab[k][e] = add2(ab[k][e], d);
+                    if (BIAS) ab[k][e] = add2(ab[k][e], d);
                     s0 = add2(s0, g[k][e]);
                     s1 = fma2(g[k][e], xh[k][e], s1);
                 }
             }
             if (GATE && in) store_lanes<T, V>(dgate + at[k], dz);
         }
-        if (base + step < p.rows) fetch(row + step);
+        bring(stage);
+        stage = stage + 1 == A::DEPTH ? 0 : stage + 1;
         const float mg = p.center ? lanes_sum<L>(pair_sum<V>(s0)) * -inv : 0.f;
         const float mgx = lanes_sum<L>(pair_sum<V>(s1)) * -inv;
         if (!live) continue;
@@ -216,7 +260,8 @@ __global__ void __launch_bounds__(TPB) group_norm_bwd_kernel(GroupNormParams p, 
     }
     if (!p.part) return;
     // the block's sums, over the slots that have the same weight, in their order
-    __shared__ float sm[SLOTS][L][2 * V];
+    auto sums = reinterpret_cast<float (*)[L][2 * V]>(sm);     // [SLOTS]; every copy into this memory has been waited for below
+    copies_wait<0>();
     const int keys = p.shared ? 1 : per, key = threadIdx.x / L, cols = p.shared ? p.C : p.G * p.C;
     const long long rowp = p.shared ? (long long)blockIdx.y * gridDim.x + blockIdx.x : blockIdx.x;
     const int kg = (int)blockIdx.y * per + key;              // (unshared: the key's group)
@@ -227,9 +272,9 @@ __global__ void __launch_bounds__(TPB) group_norm_bwd_kernel(GroupNormParams p, 
         for (int e = 0; e < V; ++e) {
             float lo, hi;
             unpack2(aw[k][e / 2], lo, hi);
-            sm[threadIdx.x / L][lane][e] = e & 1 ? hi : lo;
+            sums[threadIdx.x / L][lane][e] = e & 1 ? hi : lo;
             unpack2(ab[k][e / 2], lo, hi);
-            sm[threadIdx.x / L][lane][V + e] = e & 1 ? hi : lo;
+            sums[threadIdx.x / L][lane][V + e] = e & 1 ? hi : lo;
         }
         __syncthreads();
         if (key < keys && (p.shared || kg < p.G) && lane + k * L < nv) {
@@ -238,7 +283,7 @@ __global__ void __launch_bounds__(TPB) group_norm_bwd_kernel(GroupNormParams p, 
             for (int e = 0; e < 2 * V; ++e) t[e] = 0.f;
             for (int s = key; s < SLOTS; s += keys)
 #pragma unroll
-                for (int e = 0; e < 2 * V; ++e) t[e] += sm[s][lane][e];
+                for (int e = 0; e < 2 * V; ++e) t[e] += sums[s][lane][e];
             float *out = p.part + rowp * 2 * cols + (p.shared ? 0 : (long long)kg * p.C) + at[k];
 #pragma unroll
             for (int e = 0; e < V; ++e) {
@@ -373,7 +418,7 @@ Plan plan_of(const GroupNormParams &p, bool bf16_, bool bwd) {
                       rows_aligned(p.dgate, p.ld_dgate, es, 16) && aligned_to(p.weight, 16) && aligned_to(p.bias, 16);
     if (!wide) q.V = 1;
     const int nv = p.C / q.V;
-    q.L = 1;
+    q.L = 4;
     while (q.L < nv && q.L < 32) q.L *= 2;
     q.items = 1;
     while (q.L * q.items < nv) q.items *= 2;
@@ -387,29 +432,38 @@ Plan plan_of(const GroupNormParams &p, bool bf16_, bool bwd) {
     q.gy = (unsigned)((p.G - 1) / q.per + 1);
     const int rows = TPB / q.L / q.per;                      // rows of a block's visit
     const long long visits = (p.rows + rows - 1) / rows;
-    long long gx = (long long)sms * (bwd ? 3 : 6) / q.gy;
+    long long gx = (long long)sms * (bwd ? 3 : 4) / q.gy;            // (as many blocks as an SM holds)
     if (gx < 1) gx = 1;
     q.gx = (unsigned)(visits < gx ? visits : gx);
     q.parts = (int)(p.shared ? q.gx * q.gy : q.gx);
     return q;
 }
 
+cudaError_t launch(void (*kernel)(GroupNormParams, int), const GroupNormParams &p, const Plan &q, size_t smem, cudaStream_t s) {
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    kernel<<<dim3(q.gx, q.gy), TPB, smem, s>>>(p, q.per);
+    return cudaGetLastError();
+}
+template <class T, int V, int ITEMS, int L, bool GATE, bool BIAS> cudaError_t run_bwd(const GroupNormParams &p, const Plan &q, cudaStream_t s) {
+    using A = Ahead<T, V, ITEMS, GATE ? 3 : 2>;
+    const size_t smem = A::SMEM + A::DEPTH * TPB * sizeof(float2), sums = TPB * 2 * V * sizeof(float);
+    return launch(group_norm_bwd_kernel<T, V, ITEMS, L, GATE, BIAS>, p, q, smem > sums ? smem : sums, s);
+}
 template <class T, int V, int ITEMS, int L>
 cudaError_t run_one(const GroupNormParams &p, const Plan &q, bool bwd, cudaStream_t s) {
-    const dim3 grid(q.gx, q.gy);
     if (bwd) {
-        if (p.gate) group_norm_bwd_kernel<T, V, ITEMS, L, true><<<grid, TPB, 0, s>>>(p, q.per);
-        else group_norm_bwd_kernel<T, V, ITEMS, L, false><<<grid, TPB, 0, s>>>(p, q.per);
-    } else {
-        if (p.gate) group_norm_fwd_kernel<T, V, ITEMS, L, true><<<grid, TPB, 0, s>>>(p, q.per);
-        else group_norm_fwd_kernel<T, V, ITEMS, L, false><<<grid, TPB, 0, s>>>(p, q.per);
+        const bool bias = p.bias || p.dbias;
+        if (p.gate) return bias ? run_bwd<T, V, ITEMS, L, true, true>(p, q, s) : run_bwd<T, V, ITEMS, L, true, false>(p, q, s);
+        return bias ? run_bwd<T, V, ITEMS, L, false, true>(p, q, s) : run_bwd<T, V, ITEMS, L, false, false>(p, q, s);
     }
-    return cudaGetLastError();
+    if (p.gate) return launch(group_norm_fwd_kernel<T, V, ITEMS, L, true>, p, q, Ahead<T, V, ITEMS, 2>::SMEM, s);
+    return launch(group_norm_fwd_kernel<T, V, ITEMS, L, false>, p, q, Ahead<T, V, ITEMS, 1>::SMEM, s);
 }
 template <class T, int V> cudaError_t run_v(const GroupNormParams &p, const Plan &q, bool bwd, cudaStream_t s) {
     switch (q.L * q.items) {
-        case 1: return run_one<T, V, 1, 1>(p, q, bwd, s);
-        case 2: return run_one<T, V, 1, 2>(p, q, bwd, s);
         case 4: return run_one<T, V, 1, 4>(p, q, bwd, s);
         case 8: return run_one<T, V, 1, 8>(p, q, bwd, s);
         case 16: return run_one<T, V, 1, 16>(p, q, bwd, s);
