@@ -1,4 +1,4 @@
-"""Two token-mixer blocks on the library's operators: train a step, read a prompt, then decode.
+"""Token-mixer blocks and a whole layer on the library's operators: train a step, read a prompt, then decode.
 
     python examples/mixer_block.py            # needs the GPU and the built library
 
@@ -10,6 +10,11 @@ SsmBlock   norm -> projection to x and a gate z -> short causal convolution -> p
 KdaBlock   norm -> one projection to q, k and v -> short causal convolution over all of their
            channels -> the gated delta rule (kda_chunk_fwd): the same first operators in front of
            the other mixer.
+
+RecurrentLayer   norm -> one projection to x, the two gates of the recurrence and an output gate -> short causal
+           convolution -> gated recurrence -> norm over heads with the output gate -> projection back, added to the
+           input; then norm -> gated feed-forward product -> projection back, added again.  ``train``, ``prompt``
+           and ``step`` as above.
 
 The gradient buffers of x and z are halves of one tensor, those of the step, B and C parts of another,
 so the projections' gradients are one matrix product each and nothing is copied together.
@@ -103,6 +108,73 @@ class SsmBlock:
         return out, g
 
 
+class RecurrentLayer:
+    def __init__(self, model: int, heads: int, width: int = 128, inner: int | None = None, dtype=torch.bfloat16, device="cuda", seed: int = 0):
+        g = torch.Generator(device=device).manual_seed(seed)
+        rn = lambda *s: torch.randn(*s, generator=g, device=device)  # noqa: E731
+        self.heads, self.d, inner = heads, heads * width, inner or 4 * model
+        lin = lambda out, cols: (rn(out, cols) / math.sqrt(cols)).to(dtype)  # noqa: E731
+        one = lambda n: torch.ones(n, dtype=dtype, device=device)  # noqa: E731
+        keep = 0.9 + 0.099 * torch.rand(self.d, generator=g, device=device)      # of the state, where its gate is wide open
+        self.p = dict(norm1=one(model), w_in=lin(4 * self.d, model), conv_w=((2 * torch.rand(self.d, 4, generator=g, device=device) - 1) / 2).to(dtype),
+                      rate=torch.log(torch.expm1(-torch.log(keep) / 8.0)), head_norm=one(width), w_out=lin(model, self.d), norm2=one(model),
+                      w_gate=lin(inner, model), w_up=lin(inner, model), w_down=lin(model, inner))
+
+    def _mixer(self, u, conv_state, state, save):
+        p, d = self.p, self.d
+        n, mean, rstd = lib.layer_norm_fwd(u, p["norm1"])
+        proj = n @ p["w_in"].t()
+        x, conv_state = lib.short_conv_fwd(proj[..., :d], p["conv_w"], None, conv_state)
+        y, state, *states = lib.gated_scan_fwd(x, proj[..., d:2 * d], proj[..., 2 * d:3 * d], p["rate"], state, save_states=save)
+        o, _, orstd = lib.group_norm_fwd(y, self.heads, p["head_norm"], None, proj[..., 3 * d:], center=False)
+        return u + o @ p["w_out"].t(), (conv_state, state), dict(n=n, mean=mean, rstd=rstd, proj=proj, x=x, y=y, states=states, o=o, orstd=orstd)
+
+    def _feed_forward(self, v, save):
+        p = self.p
+        n, mean, rstd = lib.layer_norm_fwd(v, p["norm2"])
+        h = lib.glu_fwd(n, p["w_gate"], p["w_up"], save=save)
+        h, *pre = h if save else (h,)
+        return v + h @ p["w_down"].t(), dict(n=n, mean=mean, rstd=rstd, h=h, pre=pre)
+
+    def prompt(self, u, state=(None, None)):
+        v, state, _ = self._mixer(u, *state, False)
+        return self._feed_forward(v, False)[0], state
+
+    def step(self, u, state, slots=None):
+        p, d = self.p, self.d
+        n, _, _ = lib.layer_norm_fwd(u, p["norm1"])
+        proj = n @ p["w_in"].t()
+        x = lib.short_conv_step(proj[..., :d], p["conv_w"], None, state[0], slots=slots)
+        y = lib.gated_scan_step(x, proj[..., d:2 * d], proj[..., 2 * d:3 * d], p["rate"], state[1], slots=slots)
+        o, _, _ = lib.group_norm_fwd(y, self.heads, p["head_norm"], None, proj[..., 3 * d:], center=False)
+        return self._feed_forward(u + o @ p["w_out"].t(), False)[0]
+
+    def train(self, u, dout):
+        """Forward and backward: (outputs, gradients of u and of every parameter by its name)."""
+        p, d, flat, g = self.p, self.d, lambda t: t.reshape(-1, t.shape[-1]), {}
+        v, _, a = self._mixer(u, None, None, True)
+        out, b = self._feed_forward(v, True)
+        g["w_down"] = flat(dout).t() @ flat(b["h"])
+        e = lib.glu_bwd(b["n"], p["w_gate"], p["w_up"], dout @ p["w_down"], *b["pre"])
+        g["w_gate"], g["w_up"] = e["dw_gate"], e["dw_up"]
+        e = lib.layer_norm_bwd(e["dx"], v, p["norm2"], b["mean"], b["rstd"], bias=False)
+        g["norm2"], dv = e["dweight"], dout + e["dx"]
+        g["w_out"] = flat(dv).t() @ flat(a["o"])
+        dproj = torch.empty_like(a["proj"])
+        part = lambda k: dproj[..., k * d:(k + 1) * d]  # noqa: E731
+        e = lib.group_norm_bwd(dv @ p["w_out"], a["y"], self.heads, p["head_norm"], None, a["proj"][..., 3 * d:], None, a["orstd"],
+                               grads=dict(dgate=part(3)))
+        g["head_norm"] = e["dweight"]
+        e = lib.gated_scan_bwd(a["x"], a["proj"][..., d:2 * d], a["proj"][..., 2 * d:3 * d], p["rate"], None, e["dx"], states=a["states"][0],
+                               grads=dict(ddecay=part(1), dgate=part(2)))
+        g["rate"] = e["drate"]
+        g["conv_w"] = lib.short_conv_bwd(a["proj"][..., :d], p["conv_w"], None, None, e["dx"], grads=dict(dx=part(0)))["dweight"]
+        g["w_in"] = flat(dproj).t() @ flat(a["n"])
+        e = lib.layer_norm_bwd(dproj @ p["w_in"], u, p["norm1"], a["mean"], a["rstd"], bias=False)
+        g["norm1"], g["u"] = e["dweight"], dv + e["dx"]
+        return out, g
+
+
 class KdaBlock:
     def __init__(self, model: int, heads: int, dtype=torch.bfloat16, device="cuda", seed: int = 0):
         g = torch.Generator(device=device).manual_seed(seed)
@@ -138,10 +210,16 @@ def main():
     tail = torch.stack([block.step(u[:, t], state) for t in range(192, 200)], 1)
     diff = float((torch.cat([a, b, tail], 1).float() - out.float()).norm() / out.float().norm())
     print(f"prompt in parts, then single tokens, against one pass: relative difference {diff:.2e}")
+    layer = RecurrentLayer(model=512, heads=4)
+    out, grads = layer.train(u, torch.randn_like(u))
+    a, state = layer.prompt(u[:, :192].contiguous())
+    tail = torch.stack([layer.step(u[:, t], state) for t in range(192, 200)], 1)
+    rest = float((torch.cat([a, tail], 1).float() - out.float()).norm() / out.float().norm())
+    print(f"recurrent layer: gradients of {len(grads)}, prompt and single tokens against one pass: {rest:.2e}")
     kda = KdaBlock(model=512, heads=4)
     whole, _ = kda.prompt(u)
     print("gated delta-rule block:", tuple(whole.shape))
-    return diff
+    return max(diff, rest)
 
 
 if __name__ == "__main__":

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import chunkwise_gated_delta_gb300 as lib
+from chunkwise_gated_delta_gb300 import _lib
 import layer_ref as ref
 from mixer_ref import half_step, rel
 
@@ -137,3 +138,24 @@ def test_equal_calls_streams_and_graphs(M):
     torch.cuda.synchronize()
     fresh = call(s)
     assert all(torch.equal(got[k], fresh[k]) for k in got) and not torch.equal(got["h"], want["h"])
+
+
+@pytest.mark.parametrize("M", [100, 700])
+def test_a_wait_that_runs_out(M):
+    """A budget of one poll is too small for the waits of a real launch: the call ends, says so, and leaves NaN in what it did not
+    finish; the next one is unharmed.  One CTA alone, and pairs."""
+    s = make(M, 512, 640, torch.bfloat16)
+    want = call(s)
+    status = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    status.view(torch.int32)[7] = 1
+    h, g, u = lib.glu_fwd(s["x"], s["wg"], s["wu"], save=True, status=status)
+    assert lib.status_read(status) == _lib.KDA_ERR_TIMEOUT
+    assert bool(torch.isnan(h).any()) and bool(torch.isnan(g).any()) and lib.status_read(status) == 0
+    for kept in ((want["g"], want["u"]), (None, None)):
+        out = lib.glu_bwd(s["x"], s["wg"], s["wu"], s["dh"], *kept, status=status)
+        assert lib.status_read(status) == _lib.KDA_ERR_TIMEOUT
+        assert all(bool(torch.isnan(v).any()) for v in out.values())
+    status.zero_()
+    h, g, u = lib.glu_fwd(s["x"], s["wg"], s["wu"], save=True, status=status)
+    got = dict(h=h, g=g, u=u, **lib.glu_bwd(s["x"], s["wg"], s["wu"], s["dh"], g, u, status=status))
+    assert lib.status_read(status) == 0 and all(torch.equal(got[k], want[k]) for k in want)

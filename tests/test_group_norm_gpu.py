@@ -1,9 +1,12 @@
 """Gated norm over groups on the GPU against its definition in float64: every form (lanes per group, vectors per lane, groups
 longer than a warp's registers), weights of each kind, odd widths, strides, infinities."""
+import ctypes
+
 import pytest
 import torch
 
 import chunkwise_gated_delta_gb300 as lib
+from chunkwise_gated_delta_gb300 import _lib
 import layer_ref as ref
 from mixer_ref import half_step, rel
 
@@ -129,3 +132,22 @@ def test_equal_calls_streams_and_graphs():
     torch.cuda.synchronize()
     fresh = call(s, 16, False)
     assert all(torch.equal(got[k], fresh[k]) for k in got) and not torch.equal(got["y"], want["y"])
+
+
+@pytest.mark.parametrize("gate", [False, True])
+def test_gradient_of_an_absent_bias(gate):
+    """The C call may ask for dbias of a norm without one: the sum of what reaches it."""
+    s = make(37, 3, 64, torch.float32, gate=gate, bias=False)
+    want = definition({**s, "bias": torch.zeros(192, device=DEV)}, 3, True)
+    y, mean, rstd = lib.group_norm_fwd(s["x"], 3, s["weight"], None, s["gate"], eps=EPS)
+    out = {k: torch.full_like(s["x"], 7.0) for k in ("dx", "dgate")}
+    dw, db = torch.zeros(192, device=DEV), torch.zeros(192, device=DEV)
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    a = _lib.GroupNormBwdArgs(37, 3, 64, _lib.KDA_F32, _lib.KDA_F32, _lib.GROUP_NORM_FLAG_CENTER, ptr(s["dy"]), 0, ptr(s["x"]), 0, ptr(s["gate"]), 0,
+                              ptr(s["weight"]), None, ptr(mean), ptr(rstd), ptr(out["dx"]), 0, ptr(out["dgate"]) if gate else None, 0,
+                              ptr(dw), ptr(db), None, 0)
+    n = _lib.load().group_norm_bwd_workspace(ctypes.byref(a))
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    a.workspace, a.workspace_bytes = ws.data_ptr(), n
+    assert _lib.load().group_norm_bwd(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == 0
+    check(dict(dx=out["dx"], dweight=dw, dbias=db), want, 37, 64)
