@@ -479,22 +479,20 @@ unsigned blocks_of(const GatedScanParams &p) {
 }
 
 // A kernel whose blocks may set up while the one before it ends; they wait for it themselves.
-cudaError_t launch(void (*kernel)(GatedScanParams), unsigned grid, int threads, size_t smem, bool after, const GatedScanParams &p, cudaStream_t s) {
+template <auto KERNEL> cudaError_t launch(unsigned grid, int threads, size_t smem, bool after, const GatedScanParams &p, cudaStream_t s) {
+    const cudaError_t e = allow_shared<KERNEL>(smem);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = after ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    return cudaLaunchKernelEx(&cfg, KERNEL, p);
 }
 
 template <class T, int CP> cudaError_t forward(GatedScanParams &p, cudaStream_t s) {
@@ -502,11 +500,11 @@ template <class T, int CP> cudaError_t forward(GatedScanParams &p, cudaStream_t 
     const unsigned n = blocks_of(p);
     if (segments_of(p, p.seg) == 1) {
         p.seg_in = nullptr;            // nothing enters the only segment
-        return launch(gated_scan_fwd_kernel<T, CP, true>, n, THREADS, smem, false, p, s);
+        return launch<gated_scan_fwd_kernel<T, CP, true>>(n, THREADS, smem, false, p, s);
     }
-    cudaError_t e = launch(gated_scan_fwd_kernel<T, CP, false>, n, THREADS, smem, false, p, s);
-    if (e == cudaSuccess) e = launch(gated_scan_boundary_kernel<false>, (unsigned)((p.D - 1) / 32 + 1), 32 * BWARPS, 0, true, p, s);
-    if (e == cudaSuccess) e = launch(gated_scan_fwd_kernel<T, CP, true>, n, THREADS, smem, true, p, s);
+    cudaError_t e = launch<gated_scan_fwd_kernel<T, CP, false>>(n, THREADS, smem, false, p, s);
+    if (e == cudaSuccess) e = launch<gated_scan_boundary_kernel<false>>((unsigned)((p.D - 1) / 32 + 1), 32 * BWARPS, 0, true, p, s);
+    if (e == cudaSuccess) e = launch<gated_scan_fwd_kernel<T, CP, true>>(n, THREADS, smem, true, p, s);
     return e;
 }
 template <class T, int CP> cudaError_t backward(GatedScanParams &p, cudaStream_t s) {
@@ -515,10 +513,10 @@ template <class T, int CP> cudaError_t backward(GatedScanParams &p, cudaStream_t
     cudaError_t e = cudaSuccess;
     if (one) p.seg_in = nullptr;
     else {
-        e = launch(gated_scan_bwd_local_kernel<T, CP>, n, THREADS, WARPS * Ring<T, CP, 2, true>::BYTES, false, p, s);
-        if (e == cudaSuccess) e = launch(gated_scan_boundary_kernel<true>, (unsigned)((p.D - 1) / 32 + 1), 32 * BWARPS, 0, true, p, s);
+        e = launch<gated_scan_bwd_local_kernel<T, CP>>(n, THREADS, WARPS * Ring<T, CP, 2, true>::BYTES, false, p, s);
+        if (e == cudaSuccess) e = launch<gated_scan_boundary_kernel<true>>((unsigned)((p.D - 1) / 32 + 1), 32 * BWARPS, 0, true, p, s);
     }
-    if (e == cudaSuccess) e = launch(gated_scan_bwd_kernel<T, CP>, n, THREADS, WARPS * Ring<T, CP, 4, true>::BYTES, !one, p, s);
+    if (e == cudaSuccess) e = launch<gated_scan_bwd_kernel<T, CP>>(n, THREADS, WARPS * Ring<T, CP, 4, true>::BYTES, !one, p, s);
     return e;
 }
 template <bool BWD, class T, int CP> cudaError_t run(GatedScanParams &p, cudaStream_t s) {

@@ -436,8 +436,8 @@ bool make_map(CUtensorMap *m, const void *p, long long rows, long long cols, lon
 
 template <bool PAIR, Mode MODE> cudaError_t launch(TcArgs &t, cudaStream_t s) {
     using C = Cfg<PAIR>;
-    const auto kernel = glu_tc_kernel<PAIR, MODE>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    constexpr auto kernel = glu_tc_kernel<PAIR, MODE>;
+    const cudaError_t e = allow_shared<glu_tc_kernel<PAIR, MODE>>(C::SMEM);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(THREADS);
@@ -451,14 +451,13 @@ template <bool PAIR, Mode MODE> cudaError_t launch(TcArgs &t, cudaStream_t s) {
     cfg.numAttrs = 1;
     int workers = sm_count();
     if (PAIR) {                             // pairs of SMs that can run at once: a pair past them would run alone, after the others
-        static std::atomic<int> pairs[64];  // by device
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
-        int n = dev < 64 ? pairs[dev].load(std::memory_order_relaxed) : 0;
+        static std::atomic<int> pairs[DEVICES];
+        const int dev = current_device();
+        int n = dev < DEVICES ? pairs[dev].load(std::memory_order_relaxed) : 0;
         if (n < 1) {
             cfg.gridDim = dim3(2 * (workers / 2));
             if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) n = workers / 2;
-            if (dev < 64) pairs[dev].store(n, std::memory_order_relaxed);
+            if (dev < DEVICES) pairs[dev].store(n, std::memory_order_relaxed);
         }
         workers = n;
     }

@@ -439,18 +439,16 @@ Plan plan_of(const GroupNormParams &p, bool bf16_, bool bwd) {
     return q;
 }
 
-cudaError_t launch(void (*kernel)(GroupNormParams, int), const GroupNormParams &p, const Plan &q, size_t smem, cudaStream_t s) {
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
-    kernel<<<dim3(q.gx, q.gy), TPB, smem, s>>>(p, q.per);
+template <auto KERNEL> cudaError_t launch(const GroupNormParams &p, const Plan &q, size_t smem, cudaStream_t s) {
+    const cudaError_t e = allow_shared<KERNEL>(smem);
+    if (e != cudaSuccess) return e;
+    KERNEL<<<dim3(q.gx, q.gy), TPB, smem, s>>>(p, q.per);
     return cudaGetLastError();
 }
 template <class T, int V, int ITEMS, int L, bool GATE, bool BIAS> cudaError_t run_bwd(const GroupNormParams &p, const Plan &q, cudaStream_t s) {
     using A = Ahead<T, V, ITEMS, GATE ? 3 : 2>;
     const size_t smem = A::SMEM + A::DEPTH * TPB * sizeof(float2), sums = TPB * 2 * V * sizeof(float);
-    return launch(group_norm_bwd_kernel<T, V, ITEMS, L, GATE, BIAS>, p, q, smem > sums ? smem : sums, s);
+    return launch<group_norm_bwd_kernel<T, V, ITEMS, L, GATE, BIAS>>(p, q, smem > sums ? smem : sums, s);
 }
 template <class T, int V, int ITEMS, int L>
 cudaError_t run_one(const GroupNormParams &p, const Plan &q, bool bwd, cudaStream_t s) {
@@ -459,8 +457,8 @@ cudaError_t run_one(const GroupNormParams &p, const Plan &q, bool bwd, cudaStrea
         if (p.gate) return bias ? run_bwd<T, V, ITEMS, L, true, true>(p, q, s) : run_bwd<T, V, ITEMS, L, true, false>(p, q, s);
         return bias ? run_bwd<T, V, ITEMS, L, false, true>(p, q, s) : run_bwd<T, V, ITEMS, L, false, false>(p, q, s);
     }
-    if (p.gate) return launch(group_norm_fwd_kernel<T, V, ITEMS, L, true>, p, q, Ahead<T, V, ITEMS, 2>::SMEM, s);
-    return launch(group_norm_fwd_kernel<T, V, ITEMS, L, false>, p, q, Ahead<T, V, ITEMS, 1>::SMEM, s);
+    if (p.gate) return launch<group_norm_fwd_kernel<T, V, ITEMS, L, true>>(p, q, Ahead<T, V, ITEMS, 2>::SMEM, s);
+    return launch<group_norm_fwd_kernel<T, V, ITEMS, L, false>>(p, q, Ahead<T, V, ITEMS, 1>::SMEM, s);
 }
 template <class T, int V> cudaError_t run_v(const GroupNormParams &p, const Plan &q, bool bwd, cudaStream_t s) {
     switch (q.L * q.items) {

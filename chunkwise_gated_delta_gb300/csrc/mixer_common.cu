@@ -1,4 +1,6 @@
 // Second step of the sums over tokens: partial sums of blocks, in a fixed order.
+#include <atomic>
+
 #include "mixer_common.cuh"
 
 namespace mixer {
@@ -42,11 +44,18 @@ cudaError_t launch_sum_rows(const float *part, int rows, SumOut o0, SumOut o1, c
     return cudaGetLastError();
 }
 
+int current_device() {
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 ? dev : 0;
+}
+
 int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        n < 1)
-        return 152;
+    static std::atomic<int> known[DEVICES];          // queries of a device's attributes cost a call as much as a check of all its arguments
+    const int dev = current_device();
+    int n = dev < DEVICES ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (n > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 152;
+    if (dev < DEVICES) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 

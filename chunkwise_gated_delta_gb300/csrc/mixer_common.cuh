@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "mixer_seq.cuh"
 
 namespace mixer {
@@ -268,6 +270,21 @@ cudaError_t launch_sum_rows(const float *part, int rows, SumOut o0, SumOut o1, c
 
 // Streaming multiprocessors of the current device (152 if the query fails: sizes only).
 int sm_count();
+int current_device();
+constexpr int DEVICES = 64;              // for which answers are kept
+
+// Lets KERNEL have `bytes` of dynamic shared memory (one size per kernel), asking the driver once per device.
+template <auto KERNEL> cudaError_t allow_shared(size_t bytes) {
+    static std::atomic<unsigned long long> done;
+    static_assert(DEVICES == 64, "a bit each");
+    if (bytes <= 48 * 1024) return cudaSuccess;
+    const int dev = current_device();
+    const unsigned long long bit = dev < DEVICES ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 inline bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 // Rows of `es`-byte elements that may be read n bytes at a time (a NULL pointer may).

@@ -186,6 +186,8 @@ def _dense_out(on, given, name, shape, dtype):
 def _known(grads, names, **inputs):
     """The caller's gradient tensors by name.  ``inputs``: for names that depend on it, whether the call has the
     input (or asks for the gradient): a tensor for another would come back unwritten."""
+    if not grads:
+        return {}
     grads = {k: v for k, v in (grads or {}).items() if v is not None or k not in names}
     extra = set(grads) - set(names)
     if extra:
