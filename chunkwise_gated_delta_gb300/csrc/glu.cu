@@ -22,7 +22,8 @@ enum Mode { FWD, RECOMPUTE, DX, DW };
 template <int SIDE> struct Tiles {
     static constexpr int KT = SIDE == 128 ? 16 : 32, PITCH = SIDE + 4, E = SIDE * KT / 256, Q = SIDE / 64;
     static constexpr int STAGE = KT * PITCH;                 // floats of an operand's tile
-    static constexpr int FLOATS = 4 * STAGE > SIDE * (SIDE + 1) ? 4 * STAGE : SIDE * (SIDE + 1);
+    static constexpr int SUMS = SIDE == 64 ? SIDE * (SIDE + 1) : 0, FLOATS = 4 * STAGE > SUMS ? 4 * STAGE : SUMS;
+    static_assert(FLOATS * 4 <= 48 * 1024, "no more than every kernel may have");
 };
 
 // E elements of an operand's tile [KT][SIDE] per thread, neighbouring threads along the axis that lies contiguous (k, or the rows).
@@ -88,7 +89,7 @@ template <Mode MODE> __device__ __forceinline__ void finish(const GluParams &p, 
 
 template <int SIDE, Mode MODE> __global__ void __launch_bounds__(256, 2) glu_f32_kernel(GluParams p, int blocks) {
     using S = Tiles<SIDE>;
-    extern __shared__ __align__(16) float sm[];              // operands' tiles [2][2][STAGE], then the block's sums [SIDE][SIDE + 1]
+    extern __shared__ __align__(16) float sm[];              // operands' tiles [2][2][STAGE], then (tiles of 64) the block's sums [SIDE][SIDE + 1]
     constexpr bool DUAL = MODE == FWD || MODE == RECOMPUTE, AK = MODE != DW, BK = DUAL;
     constexpr int TN = DUAL ? SIDE / 2 : SIDE, N = 4 * S::Q;
     const int t = threadIdx.x, tx = t % 16, ty = t / 16;

@@ -59,8 +59,9 @@ bool sizes_ok(int B, int T, int D, bool packed = false) {
 Block dense(const void *p, long long rows, long long cols, size_t es) { return {p, rows, cols, cols, es}; }
 
 kda_status from(cudaError_t e) {
-    if (e == cudaErrorNotSupported) return KDA_ERR_UNSUPPORTED;
-    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    if (e == cudaSuccess) return KDA_OK;
+    cudaGetLastError();                  // a launch that was refused is this call's answer, not the next one's too
+    return e == cudaErrorNotSupported ? KDA_ERR_UNSUPPORTED : KDA_ERR_CUDA;
 }
 
 kda_status check_space(const void *ws, size_t have, size_t need) {

@@ -64,6 +64,14 @@ def test_sizes(M, D, F, dtype):
     check(call(s, save=False), want, dtype, M, D, F)
 
 
+@pytest.mark.parametrize("M,D,F", [(2142, 16, 8320), (1500, 1411, 130), (700, 3000, 2051)])
+def test_many_tiles_in_float32(M, D, F):
+    s = make(M, D, F, torch.float32)
+    want = definition(s, "silu")
+    check(call(s), want, torch.float32, M, D, F)
+    check(call(s, save=False), want, torch.float32, M, D, F)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("M", [1, 40, 200])
 def test_gelu(M, dtype):
