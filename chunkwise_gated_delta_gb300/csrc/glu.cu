@@ -3,10 +3,10 @@
 //   forward   h = act(x Wg^T) (x Wu^T), both products in one tile
 //   backward  dg = dh u act'(g), du = dh act(g); dx = dg Wg + du Wu; dWg = dg^T x, dWu = du^T x
 //
-// float32 products run on the CUDA cores, which do not round their operands.  A block of 256 threads has a tile of SIDE x
-// SIDE products, a thread two quads (SIDE = 64: one) per axis; in the forward the left half of the columns is Wg's and the right
-// half Wu's.  Where tiles of 128 leave the GPU idle, tiles of 64 are used and a cluster of up to eight blocks shares the sum
-// of a tile, joined in the blocks' order through shared memory.
+// float32 products run on the CUDA cores, which do not round their operands.  A block has a tile of SIDE x SIDE products, a thread
+// two quads of them per axis, two columns to a packed multiplication; in the forward the left half of the columns is Wg's and the
+// right half Wu's.  Where tiles of 128 leave the GPU idle, tiles of 64 are used, and a cluster of up to eight blocks shares the
+// sum of a tile, joined in the blocks' order through shared memory.
 #include <type_traits>
 
 #include "glu.cuh"
@@ -20,49 +20,54 @@ using namespace glu;
 enum Mode { FWD, RECOMPUTE, DX, DW };
 
 template <int SIDE> struct Tiles {
-    static constexpr int KT = SIDE == 128 ? 16 : 32, PITCH = SIDE + 4, E = SIDE * KT / 256, Q = SIDE / 64;
+    static constexpr int THREADS = SIDE * SIDE / 64, KT = 16, PITCH = SIDE + 4, E = SIDE * KT / THREADS;
     static constexpr int STAGE = KT * PITCH;                 // floats of an operand's tile
     static constexpr int SUMS = SIDE == 64 ? SIDE * (SIDE + 1) : 0, FLOATS = 4 * STAGE > SUMS ? 4 * STAGE : SUMS;
     static_assert(FLOATS * 4 <= 48 * 1024, "no more than every kernel may have");
 };
 
-// E elements of an operand's tile [KT][SIDE] per thread, neighbouring threads along the axis that lies contiguous (k, or the rows).
-template <int SIDE, bool KMAJOR> struct Operand {
+// E elements of an operand's tile [KT][SIDE] per thread, V (1 or 4) per access, neighbouring threads along the axis that lies
+// contiguous (k, or the rows).  With V = 4 that axis' extent is a multiple of 4.
+template <int SIDE, bool KMAJOR, int V> struct Operand {
     using S = Tiles<SIDE>;
-    static constexpr int LEN = KMAJOR ? S::KT : SIDE, STEP = 256 / LEN;      // of a stretch; stretches at a time
-    float v[S::E];
+    static constexpr int LEN = (KMAJOR ? S::KT : SIDE) / V, STEP = S::THREADS / LEN, N = S::E / V;   // accesses of a stretch; stretches at a time
+    Vec<float, V> v[N];
     // p: the tile's first element; left_r, left_k: the operand's extent from there; ld: stride of the axis that is not contiguous.
     __device__ __forceinline__ void load(const float *p, long long ld, long long left_r, long long left_k) {
-        const int in = threadIdx.x % LEN, out = threadIdx.x / LEN;
+        const int in = threadIdx.x % LEN * V, out = threadIdx.x / LEN;
         p += out * ld + in;
         const bool inside = in < (KMAJOR ? left_k : left_r);
 #pragma unroll
-        for (int e = 0; e < S::E; ++e, p += STEP * ld) v[e] = inside && out + e * STEP < (KMAJOR ? left_r : left_k) ? __ldg(p) : 0.f;
+        for (int e = 0; e < N; ++e, p += STEP * ld) one(e, p, inside && out + e * STEP < (KMAJOR ? left_r : left_k));
+    }
+    __device__ __forceinline__ void one(int e, const float *p, bool on) {
+        if (on) v[e] = load_const<float, V>(p);
+        else
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[e].e[i] = 0.f;
     }
     __device__ __forceinline__ void store(float *sm) const {
-        const int in = threadIdx.x % LEN, out = threadIdx.x / LEN;
+        const int in = threadIdx.x % LEN * V, out = threadIdx.x / LEN;
 #pragma unroll
-        for (int e = 0; e < S::E; ++e) sm[KMAJOR ? in * S::PITCH + out + e * STEP : (out + e * STEP) * S::PITCH + in] = v[e];
+        for (int e = 0; e < N; ++e) {
+            if (KMAJOR)
+#pragma unroll
+                for (int i = 0; i < V; ++i) sm[(in + i) * S::PITCH + out + e * STEP] = v[e].e[i];
+            else store_vec<float, V>(sm + (out + e * STEP) * S::PITCH + in, v[e]);
+        }
     }
 };
 // The forward's tile of weights: its first half of rows from Wg, its second from Wu, k contiguous.
-template <int SIDE> struct Weights {
-    using S = Tiles<SIDE>;
-    static constexpr int STEP = 256 / S::KT, TN = SIDE / 2;
-    float v[S::E];
+template <int SIDE, int V> struct Weights : Operand<SIDE, true, V> {
+    using O = Operand<SIDE, true, V>;
+    static constexpr int TN = SIDE / 2;
     __device__ __forceinline__ void load(const float *g, long long ldg, const float *u, long long ldu, long long left_r, long long left_k) {
-        const int in = threadIdx.x % S::KT, out = threadIdx.x / S::KT;
+        const int in = threadIdx.x % O::LEN * V, out = threadIdx.x / O::LEN;
 #pragma unroll
-        for (int e = 0; e < S::E; ++e) {
-            const int r = (out + e * STEP) % TN;
-            const float *p = e * STEP < TN ? g + r * ldg : u + r * ldu;
-            v[e] = in < left_k && r < left_r ? __ldg(p + in) : 0.f;
+        for (int e = 0; e < O::N; ++e) {
+            const int row = out + e * O::STEP, r = row % TN;
+            this->one(e, (row < TN ? g + r * ldg : u + r * ldu) + in, in < left_k && r < left_r);
         }
-    }
-    __device__ __forceinline__ void store(float *sm) const {
-        const int in = threadIdx.x % S::KT, out = threadIdx.x / S::KT;
-#pragma unroll
-        for (int e = 0; e < S::E; ++e) sm[in * S::PITCH + out + e * STEP] = v[e];
     }
 };
 
@@ -87,24 +92,24 @@ template <Mode MODE> __device__ __forceinline__ void finish(const GluParams &p, 
     }
 }
 
-template <int SIDE, Mode MODE> __global__ void __launch_bounds__(256, 2) glu_f32_kernel(GluParams p, int blocks) {
+template <int SIDE, Mode MODE, int V> __global__ void __launch_bounds__(Tiles<SIDE>::THREADS, SIDE == 128 ? 2 : 8) glu_f32_kernel(GluParams p, int blocks) {
     using S = Tiles<SIDE>;
     extern __shared__ __align__(16) float sm[];              // operands' tiles [2][2][STAGE], then (tiles of 64) the block's sums [SIDE][SIDE + 1]
     constexpr bool DUAL = MODE == FWD || MODE == RECOMPUTE, AK = MODE != DW, BK = DUAL;
-    constexpr int TN = DUAL ? SIDE / 2 : SIDE, N = 4 * S::Q;
-    const int t = threadIdx.x, tx = t % 16, ty = t / 16;
+    constexpr int TN = DUAL ? SIDE / 2 : SIDE, HALF = SIDE / 2, SPAN = SIDE / 8;     // a thread's quads: columns tx 4 and HALF + tx 4
+    const int t = threadIdx.x, tx = t % SPAN, ty = t / SPAN;
     const bool up = MODE == DW && blockIdx.y;
     const long long ms = MODE == DW ? p.F : p.M, ns = DUAL ? p.F : p.D, ks = MODE == DW ? p.M : MODE == DX ? p.F : p.D;
     const unsigned cols = (unsigned)((ns + TN - 1) / TN), tile = blockIdx.x / blocks;
     const int rank = (int)(blockIdx.x % blocks);
     const long long m0 = (long long)(tile / cols) * SIDE, n0 = (long long)(tile % cols) * TN;
-    float acc[N][N];
+    f2 acc[8][4];
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int j = 0; j < N; ++j) acc[i][j] = 0.f;
-    Operand<SIDE, AK> a;
-    std::conditional_t<DUAL, Weights<SIDE>, Operand<SIDE, BK>> b;
+        for (int j = 0; j < 4; ++j) acc[i][j] = both(0.f);
+    Operand<SIDE, AK, V> a;
+    std::conditional_t<DUAL, Weights<SIDE, V>, Operand<SIDE, BK, V>> b;
     const long long per = (ks + S::KT - 1) / S::KT, steps = MODE == DX ? 2 * per : per;
     const long long first = steps * rank / blocks, end = steps * (rank + 1) / blocks;
     auto fetch = [&](long long i) {
@@ -136,16 +141,19 @@ template <int SIDE, Mode MODE> __global__ void __launch_bounds__(256, 2) glu_f32
         const float *pa = sa + cur * S::STAGE + ty * 4, *pb = sb + cur * S::STAGE + tx * 4;
 #pragma unroll
         for (int k = 0; k < S::KT; ++k) {
-            float av[N], bv[N];
+            float av[8];
+            f2 bv[4];
 #pragma unroll
-            for (int q = 0; q < S::Q; ++q) {
-                *reinterpret_cast<float4 *>(av + 4 * q) = *reinterpret_cast<const float4 *>(pa + k * S::PITCH + 64 * q);
-                *reinterpret_cast<float4 *>(bv + 4 * q) = *reinterpret_cast<const float4 *>(pb + k * S::PITCH + 64 * q);
+            for (int q = 0; q < 2; ++q) {
+                *reinterpret_cast<float4 *>(av + 4 * q) = *reinterpret_cast<const float4 *>(pa + k * S::PITCH + HALF * q);
+                const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(pb + k * S::PITCH + HALF * q);
+                bv[2 * q] = w.x;
+                bv[2 * q + 1] = w.y;
             }
 #pragma unroll
-            for (int y = 0; y < N; ++y)
+            for (int y = 0; y < 8; ++y)
 #pragma unroll
-                for (int x = 0; x < N; ++x) acc[y][x] = fmaf(av[y], bv[x], acc[y][x]);
+                for (int x = 0; x < 4; ++x) acc[y][x] = fma2(both(av[y]), bv[x], acc[y][x]);
         }
         if (i + 1 < end) {
             a.store(sa + (cur ^ 1) * S::STAGE);
@@ -153,28 +161,35 @@ template <int SIDE, Mode MODE> __global__ void __launch_bounds__(256, 2) glu_f32
         }
         __syncthreads();
     }
+    auto row_of = [&](int y) { return (y < 4 ? 0 : HALF - 4) + ty * 4 + y; };
+    auto col_of = [&](int x) { return (x < 4 ? 0 : HALF - 4) + tx * 4 + x; };
+    auto value = [&](int y, int x) {
+        float lo, hi;
+        unpack2(acc[y][x / 2], lo, hi);
+        return x & 1 ? hi : lo;
+    };
     if constexpr (SIDE == 128) {
 #pragma unroll
         for (int y = 0; y < 8; ++y) {
-            const long long m = m0 + (y < 4 ? ty * 4 + y : 60 + ty * 4 + y);
+            const long long m = m0 + row_of(y);
             if (m >= ms) continue;
 #pragma unroll
             for (int x = 0; x < (DUAL ? 4 : 8); ++x) {
-                const long long n = n0 + (x < 4 ? tx * 4 + x : 60 + tx * 4 + x);
-                if (n < ns) finish<MODE>(p, up, m, n, acc[y][x], DUAL ? acc[y][x + 4] : 0.f);
+                const long long n = n0 + col_of(x);
+                if (n < ns) finish<MODE>(p, up, m, n, value(y, x), DUAL ? value(y, x + 4) : 0.f);
             }
         }
     } else {
         // the block's sums where the others of its cluster can read them; each finishes a part of the tile's rows
 #pragma unroll
-        for (int y = 0; y < 4; ++y)
+        for (int y = 0; y < 8; ++y)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) sm[(ty * 4 + y) * (SIDE + 1) + tx * 4 + x] = acc[y][x];
+            for (int x = 0; x < 8; ++x) sm[row_of(y) * (SIDE + 1) + col_of(x)] = value(y, x);
         if (blocks > 1) kda::tc::cluster_sync_all();
         else __syncthreads();
         const uint32_t local = kda::tc::smem_u32(sm);
         const int rows = SIDE / blocks;
-        for (int i = t; i < rows * TN; i += 256) {
+        for (int i = t; i < rows * TN; i += S::THREADS) {
             const int y = rank * rows + i / TN, x = i % TN;
             const long long m = m0 + y, n = n0 + x;
             if (m >= ms || n >= ns) continue;
@@ -225,11 +240,10 @@ __global__ void __launch_bounds__(256) glu_align_kernel(const bf16 *from, long l
     }
 }
 
-template <int SIDE, Mode MODE> cudaError_t run_side(const GluParams &p, long long tiles, int blocks, cudaStream_t s) {
-    const auto kernel = glu_f32_kernel<SIDE, MODE>;
+template <int SIDE, Mode MODE, int V> cudaError_t run_side(const GluParams &p, long long tiles, int blocks, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * blocks), MODE == DW ? 2 : 1);
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(Tiles<SIDE>::THREADS);
     cfg.dynamicSmemBytes = Tiles<SIDE>::FLOATS * 4;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -238,8 +252,10 @@ template <int SIDE, Mode MODE> cudaError_t run_side(const GluParams &p, long lon
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = blocks > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, p, blocks);
+    return cudaLaunchKernelEx(&cfg, glu_f32_kernel<SIDE, MODE, V>, p, blocks);
 }
+// Tiles of 128 where they fill the SMs' places (two to an SM) twice over, else tiles of 64 (eight), a cluster of blocks to each
+// where those leave half of the places empty and every block has eight steps.
 template <Mode MODE> cudaError_t run_f32(const GluParams &p, cudaStream_t s) {
     constexpr bool DUAL = MODE == FWD || MODE == RECOMPUTE;
     const long long ms = MODE == DW ? p.F : p.M, ns = DUAL ? p.F : p.D, ks = MODE == DW ? p.M : MODE == DX ? 2LL * p.F : p.D;
@@ -247,11 +263,14 @@ template <Mode MODE> cudaError_t run_f32(const GluParams &p, cudaStream_t s) {
         const int tn = DUAL ? side / 2 : side;
         return ((ms + side - 1) / side) * ((ns + tn - 1) / tn);
     };
-    const long long z = MODE == DW ? 2 : 1, room = 2LL * sm_count();
-    if (tiles(128) * z > room / 2) return tiles(128) > 0x7fffffffLL ? cudaErrorNotSupported : run_side<128, MODE>(p, tiles(128), 1, s);
-    int blocks = 1;                      // (a block of the cluster has four steps of 32 at least)
-    while (blocks < 8 && tiles(64) * z * blocks * 2 <= room && ks >= 256LL * blocks) blocks *= 2;
-    return run_side<64, MODE>(p, tiles(64), blocks, s);
+    bool wide = p.D % 4 == 0 && rows_aligned(p.x, p.ld_x, 4, 16) && rows_aligned(p.wg, p.ld_wg, 4, 16) && rows_aligned(p.wu, p.ld_wu, 4, 16);
+    if (!DUAL) wide = wide && p.F % 4 == 0 && rows_aligned(p.dg, p.ld_d, 4, 16) && aligned_to(p.du, 16);
+    const long long z = MODE == DW ? 2 : 1, sms = sm_count();
+    if (tiles(64) * z * 8 > 0x7fffffffLL) return cudaErrorNotSupported;
+    if (tiles(128) * z >= 4 * sms) return wide ? run_side<128, MODE, 4>(p, tiles(128), 1, s) : run_side<128, MODE, 1>(p, tiles(128), 1, s);
+    int blocks = 1;
+    while (blocks < 8 && tiles(64) * z * blocks * 2 <= 8 * sms && ks >= 256LL * blocks) blocks *= 2;
+    return wide ? run_side<64, MODE, 4>(p, tiles(64), blocks, s) : run_side<64, MODE, 1>(p, tiles(64), blocks, s);
 }
 
 template <class T> cudaError_t slopes(const GluParams &p, cudaStream_t s) {

@@ -95,16 +95,16 @@ template <int NT, int U> __global__ void __launch_bounds__(THREADS) glu_rows_ker
 
 }  // namespace
 
-// Up to 32 rows, and reads of 16 bytes.
+// Up to 16 rows (of 4096 x 11008: 31 us up to 8, 38 up to 16, as the tensor cores' form takes from 1 to 128; 24 rows here 57), and
+// reads of 16 bytes.
 bool glu_rows_takes(const GluParams &p) {
-    return p.M <= 32 && p.D % 8 == 0 && rows_aligned(p.x, p.ld_x, 2, 16) && rows_aligned(p.wg, p.ld_wg, 2, 16) &&
+    return p.M <= 16 && p.D % 8 == 0 && rows_aligned(p.x, p.ld_x, 2, 16) && rows_aligned(p.wg, p.ld_wg, 2, 16) &&
            rows_aligned(p.wu, p.ld_wu, 2, 16);
 }
 cudaError_t launch_glu_rows(const GluParams &p, cudaStream_t s) {
     const unsigned grid = (unsigned)((p.F - 1) / ROWS + 1);
     if (p.M <= 8) glu_rows_kernel<1, 4><<<grid, THREADS, 0, s>>>(p);
-    else if (p.M <= 16) glu_rows_kernel<2, 2><<<grid, THREADS, 0, s>>>(p);
-    else glu_rows_kernel<4, 2><<<grid, THREADS, 0, s>>>(p);
+    else glu_rows_kernel<2, 2><<<grid, THREADS, 0, s>>>(p);
     return cudaGetLastError();
 }
 

@@ -51,6 +51,9 @@ struct TcArgs {
     GluParams p;
     int tiles_m, tiles_n, tiles;            // tiles: over both outputs in DW
     int kb, segments;                       // K blocks of a segment, and segments (DX: dg Wg, then du Wu)
+    int splits;                             // parts of K, each a unit of work with its own sums (DX, DW)
+    float *part;                            // [splits][outputs][rows][pitch] those sums, where there are several parts
+    long long pitch;
     int *status;
 };
 
@@ -140,10 +143,16 @@ __device__ __noinline__ void drain(uint64_t *bar, uint32_t parity) {
 // ------------------------------------------------------------------------------------- tiles
 struct Tile {
     int z, m, n;            // output (DW), row and column of tiles
+    int split, k0, k1;      // part of K, its blocks
 };
 // Bands of 8 rows of tiles, column by column: the blocks that run together share rows of A and columns of B.
 __device__ __forceinline__ Tile tile_of(const TcArgs &t, int i) {
     Tile q;
+    q.split = i % t.splits;
+    i /= t.splits;
+    const int kbs = t.kb * t.segments;
+    q.k0 = (int)((long long)kbs * q.split / t.splits);
+    q.k1 = (int)((long long)kbs * (q.split + 1) / t.splits);
     const int per = t.tiles_m * t.tiles_n;
     q.z = i / per;
     i -= q.z * per;
@@ -203,7 +212,8 @@ __device__ __forceinline__ bool wide_rows(const void *p, long long ld, int es) {
 // The outputs of a warp's 32 rows from row0 (of the call), `rows` of which belong to it, and a tile's columns.  get(c, v): this
 // lane's row of 32 accumulator columns from c.
 template <Mode MODE, class Get>
-__device__ __forceinline__ void finish(const GluParams &p, const Tile &q, long long row0, int rows, float (*turn)[33], Get get) {
+__device__ __forceinline__ void finish(const TcArgs &t, const Tile &q, long long row0, int rows, float (*turn)[33], Get get) {
+    const GluParams &p = t.p;
     if constexpr (MODE == FWD || MODE == RECOMPUTE) {
         const int n0 = q.n * HALF;
         const bool wide = MODE == FWD ? wide_rows(p.h, p.ld_h, 2) : wide_rows(p.dg, p.ld_d, 2) && wide_rows(p.du, p.ld_d, 2);
@@ -243,14 +253,18 @@ __device__ __forceinline__ void finish(const GluParams &p, const Tile &q, long l
         const bool second = MODE == DW && q.z;
         bf16 *out = static_cast<bf16 *>(MODE == DX ? p.dx : second ? p.dwu : p.dwg);
         const long long ld = MODE == DX ? p.ld_dx : second ? p.ld_dwu : p.ld_dwg;
-        const bool wide = wide_rows(out, ld, 2);
+        const bool wide = wide_rows(out, ld, 2), whole = wide_rows(t.part, t.pitch, 4);
 #pragma unroll 1
         for (int c = 0; c < COLS; c += 32) {
             float v[32];
             __syncwarp();
             get(c, v);
             const int inside = p.D - n0 - c;
-            if (inside > 0 && rows > 0) store_rows(out + row0 * ld + n0 + c, ld, v, rows, inside, wide, turn);
+            if (inside <= 0 || rows <= 0) continue;
+            if (t.splits > 1) {
+                const long long all = MODE == DW ? p.F : p.M, z = (long long)q.split * (MODE == DW ? 2 : 1) + q.z;
+                store_rows(t.part + (z * all + row0) * t.pitch + n0 + c, t.pitch, v, rows, inside, whole, turn);
+            } else store_rows(out + row0 * ld + n0 + c, ld, v, rows, inside, wide, turn);
         }
     }
 }
@@ -287,7 +301,6 @@ template <bool PAIR, Mode MODE> __global__ void __launch_bounds__(THREADS, 1) gl
     const uint32_t tmem = sh.tmem;
     const int budget = t.status ? t.status[kda::kStatusBoundWord] : 0;
     const Waits wait{&sh.abort, t.status, budget > 0 ? (uint32_t)budget : kWaitBound};
-    const int kbs = t.kb * t.segments;
     unsigned used = 0;                                   // stages that the products have waited for
 
     if (warp == 0) {
@@ -297,7 +310,7 @@ template <bool PAIR, Mode MODE> __global__ void __launch_bounds__(THREADS, 1) gl
             for (int i = worker; ok && i < t.tiles; i += workers) {
                 const Tile q = tile_of(t, i);
                 const int m0 = q.m * C::ROWS + (int)rank * HALF, n0 = q.n * (B_MN ? COLS : HALF);
-                for (int k = 0; k < kbs; ++k, ++it) {
+                for (int k = q.k0; k < q.k1; ++k, ++it) {
                     const int s = it % C::STAGES;
                     if (it >= C::STAGES && !(ok = wait(&sh.empty[s], it / C::STAGES - 1 & 1))) break;
                     const uint32_t bar = leader_bar(&sh.full[s]);
@@ -344,7 +357,8 @@ template <bool PAIR, Mode MODE> __global__ void __launch_bounds__(THREADS, 1) gl
                 const int buf = n & 1;
                 if (n >= 2 && !(ok = wait(&sh.acc_empty[buf], (n / 2 - 1) & 1))) break;
                 tc_fence_after();
-                for (int k = 0; k < kbs; ++k, ++it) {
+                const Tile q = tile_of(t, i);
+                for (int k = q.k0; k < q.k1; ++k, ++it) {
                     const int s = it % C::STAGES;
                     if (!(ok = wait(&sh.full[s], it / C::STAGES & 1))) break;
                     tc_fence_after();
@@ -352,7 +366,7 @@ template <bool PAIR, Mode MODE> __global__ void __launch_bounds__(THREADS, 1) gl
 #pragma unroll
                     for (int ks = 0; ks < BK / 16; ++ks)
                         mma<PAIR>(tmem + buf * COLS, A_MN ? desc_mnmajor(a, BK, ks) : desc_kmajor(a, HALF, ks),
-                                  B_MN ? desc_mnmajor(b, BK, ks) : desc_kmajor(b, HALF, ks), idesc, k > 0 || ks > 0);
+                                  B_MN ? desc_mnmajor(b, BK, ks) : desc_kmajor(b, HALF, ks), idesc, k > q.k0 || ks > 0);
                     commit<PAIR>(&sh.empty[s]);
                 }
                 if (ok) commit<PAIR>(&sh.acc_full[buf]);
@@ -373,13 +387,13 @@ template <bool PAIR, Mode MODE> __global__ void __launch_bounds__(THREADS, 1) gl
             const int rows = (int)max(0LL, min(32LL, (MODE == DW ? (long long)t.p.F : t.p.M) - row0));
             const uint32_t at = tmem + ((uint32_t)quarter << 21) + buf * COLS;
             if (ok) {
-                finish<MODE>(t.p, q, row0, rows, sh.turn[quarter], [&](int c, float (&v)[32]) { tmem_ld32(at + c, v); });
+                finish<MODE>(t, q, row0, rows, sh.turn[quarter], [&](int c, float (&v)[32]) { tmem_ld32(at + c, v); });
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive_cluster(leader_bar(&sh.acc_empty[buf]));
             } else {                                     // broken off: the tile's outputs say so
                 const float bad = __int_as_float(0x7fc00000);
-                finish<MODE>(t.p, q, row0, rows, sh.turn[quarter], [&](int, float (&v)[32]) {
+                finish<MODE>(t, q, row0, rows, sh.turn[quarter], [&](int, float (&v)[32]) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) v[k] = bad;
                 });
@@ -466,22 +480,75 @@ template <bool PAIR, Mode MODE> cudaError_t launch(TcArgs &t, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, kernel, t);
 }
 
+// The joined sums of the parts of K, in their order: four columns per thread.
+__global__ void __launch_bounds__(256) glu_join_kernel(const float *part, int splits, long long rows, int cols, long long pitch, long long apart, bf16 *out,
+                                                        long long ld) {
+    const long long per = pitch / 4, i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= rows * per) return;
+    const long long r = i / per;
+    const int c = (int)(i - r * per) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < splits; ++k) {
+        const float4 g = *reinterpret_cast<const float4 *>(part + k * apart + r * pitch + c);
+        v.x += g.x;
+        v.y += g.y;
+        v.z += g.z;
+        v.w += g.w;
+    }
+    bf16 *to = out + r * ld + c;
+    const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (c + k < cols) to[k] = __float2bfloat16_rn(f[k]);
+}
+
+// Where the tiles of a product (or pairs of CTAs for them) leave half of the SMs idle, K is cut into parts that fill them, each of four
+// blocks of 64 at least.
+struct Shape {
+    bool pair;
+    long long tm, tn, kbs;
+    int splits;
+    long long pitch;
+};
+template <Mode MODE> Shape shape_of(const GluParams &p) {
+    constexpr bool DUAL = MODE == FWD || MODE == RECOMPUTE;
+    Shape q;
+    const long long ms = MODE == DW ? p.F : p.M, ks = DUAL ? p.D : MODE == DX ? p.F : p.M;
+    q.pair = ms > HALF;
+    const int rows = q.pair ? 2 * HALF : HALF, cols = DUAL ? HALF : COLS;
+    q.tm = (ms + rows - 1) / rows;
+    q.tn = ((DUAL ? p.F : p.D) + (long long)cols - 1) / cols;
+    q.kbs = (ks + BK - 1) / BK * (MODE == DX ? 2 : 1);
+    q.splits = 1;
+    q.pitch = (p.D + 7) / 8 * 8;
+    if (!DUAL) {
+        const long long places = sm_count() / (q.pair ? 2 : 1), tiles = q.tm * q.tn * (MODE == DW ? 2 : 1);
+        const long long n = places / tiles, most = q.kbs / 4;
+        if (n > 1 && most > 1) q.splits = (int)(n < most ? n : most);
+    }
+    return q;
+}
+template <Mode MODE> size_t part_bytes(const GluParams &p) {
+    const Shape q = shape_of<MODE>(p);
+    return q.splits > 1 ? (size_t)q.splits * (MODE == DW ? 2 * (size_t)p.F : (size_t)p.M) * q.pitch * 4 : 0;
+}
+
 template <Mode MODE> cudaError_t run(const GluParams &p, int *status, cudaStream_t s) {
     TcArgs t;
     t.p = p;
     t.status = status;
     constexpr bool DUAL = MODE == FWD || MODE == RECOMPUTE;
-    const long long ms = MODE == DW ? p.F : p.M;
-    const bool pair = ms > HALF;
-    const int rows = pair ? 2 * HALF : HALF, cols = DUAL ? HALF : COLS;
-    const long long tm = (ms + rows - 1) / rows, tn = ((DUAL ? p.F : p.D) + (long long)cols - 1) / cols;
-    if (tm * tn * 2 > 0x7fffffffLL) return cudaErrorNotSupported;
-    t.tiles_m = (int)tm;
-    t.tiles_n = (int)tn;
-    t.tiles = (int)(tm * tn * (MODE == DW ? 2 : 1));
-    const long long ks = DUAL ? p.D : MODE == DX ? p.F : p.M;
-    t.kb = (int)((ks + BK - 1) / BK);
+    const Shape q = shape_of<MODE>(p);
+    const bool pair = q.pair;
+    if (q.tm * q.tn * 2 * q.splits > 0x7fffffffLL) return cudaErrorNotSupported;
+    t.tiles_m = (int)q.tm;
+    t.tiles_n = (int)q.tn;
+    t.splits = q.splits;
+    t.part = static_cast<float *>(p.part);
+    t.pitch = q.pitch;
+    t.tiles = (int)(q.tm * q.tn * (MODE == DW ? 2 : 1) * q.splits);
     t.segments = MODE == DX ? 2 : 1;
+    t.kb = (int)(q.kbs / t.segments);
     bool ok;
     if constexpr (DUAL) {
         ok = make_map(&t.a0, p.x, p.M, p.D, p.ld_x, HALF) && make_map(&t.b0, p.wg, p.F, p.D, p.ld_wg, HALF) &&
@@ -496,11 +563,25 @@ template <Mode MODE> cudaError_t run(const GluParams &p, int *status, cudaStream
         t.b1 = t.b0;
     }
     if (!ok) return cudaErrorInvalidValue;
-    return pair ? launch<true, MODE>(t, s) : launch<false, MODE>(t, s);
+    cudaError_t e = pair ? launch<true, MODE>(t, s) : launch<false, MODE>(t, s);
+    if (e != cudaSuccess || q.splits == 1) return e;
+    const long long rows = MODE == DW ? p.F : p.M, apart = rows * q.pitch * (MODE == DW ? 2 : 1);
+    const unsigned grid = (unsigned)((rows * (q.pitch / 4) + 255) / 256);
+    for (int z = 0; z < (MODE == DW ? 2 : 1); ++z) {
+        bf16 *out = static_cast<bf16 *>(MODE == DX ? p.dx : z ? p.dwu : p.dwg);
+        glu_join_kernel<<<grid, 256, 0, s>>>(t.part + z * rows * q.pitch, q.splits, rows, p.D, q.pitch, apart, out,
+                                             MODE == DX ? p.ld_dx : z ? p.ld_dwu : p.ld_dwg);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace
 
+size_t glu_tc_part_bytes(const GluParams &p) {
+    const size_t x = part_bytes<DX>(p), w = part_bytes<DW>(p);
+    return x > w ? x : w;
+}
 cudaError_t launch_glu_tc_fwd(const GluParams &p, cudaStream_t s) { return run<FWD>(p, p.status, s); }
 cudaError_t launch_glu_tc_grads(const GluParams &p, cudaStream_t s) { return run<RECOMPUTE>(p, p.status, s); }
 cudaError_t launch_glu_tc_dx(const GluParams &p, cudaStream_t s) { return run<DX>(p, p.status, s); }

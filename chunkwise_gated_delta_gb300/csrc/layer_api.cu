@@ -141,7 +141,8 @@ kda_status glu_fwd_params(const glu_fwd_args *a, mixer::GluParams &p, size_t &ne
     return blocks_ok(in, out) ? KDA_OK : KDA_ERR_INVALID_ARG;
 }
 
-kda_status glu_bwd_params(const glu_bwd_args *a, mixer::GluParams &p, size_t &need, size_t &grads) {
+// need: the two products' gradients, then operands that move, then sums of parts of a product.
+kda_status glu_bwd_params(const glu_bwd_args *a, mixer::GluParams &p, size_t &need, size_t &grads, size_t &moved) {
     if (!a || !a->dh || !a->dx || !a->dw_gate || !a->dw_up) return KDA_ERR_INVALID_ARG;
     const kda_status st = glu_common(a, p);
     if (st != KDA_OK) return st;
@@ -152,7 +153,8 @@ kda_status glu_bwd_params(const glu_bwd_args *a, mixer::GluParams &p, size_t &ne
     const size_t es = es_of(a->dtype);
     p.ld_d = mixer::glu_grad_stride(p, a->dtype == KDA_BF16);
     grads = (2 * (size_t)a->rows * p.ld_d * es + 255) / 256 * 256;
-    need = grads + mixer::glu_moved_bytes(p, a->dtype == KDA_BF16);
+    moved = mixer::glu_moved_bytes(p, a->dtype == KDA_BF16);
+    need = grads + moved + (a->dtype == KDA_BF16 ? mixer::glu_tc_part_bytes(p) : 0);
     const Block in[] = {{a->x, a->rows, a->D, p.ld_x, es}, {a->w_gate, a->F, a->D, p.ld_wg, es}, {a->w_up, a->F, a->D, p.ld_wu, es},
                         {a->dh, a->rows, a->F, p.ld_dh, es}, dense(a->g, a->rows, a->F, 4), dense(a->u, a->rows, a->F, 4)};
     const Block out[] = {{a->dx, a->rows, a->D, p.ld_dx, es}, {a->dw_gate, a->F, a->D, p.ld_dwg, es},
@@ -264,19 +266,20 @@ kda_status glu_fwd(const glu_fwd_args *a, kda_stream_t stream) {
 
 size_t glu_bwd_workspace(const glu_bwd_args *a) {
     mixer::GluParams p{};
-    size_t need = 0, grads = 0;
-    return glu_bwd_params(a, p, need, grads) == KDA_OK ? need : 0;
+    size_t need = 0, grads = 0, moved = 0;
+    return glu_bwd_params(a, p, need, grads, moved) == KDA_OK ? need : 0;
 }
 
 kda_status glu_bwd(const glu_bwd_args *a, kda_stream_t stream) {
     mixer::GluParams p{};
-    size_t need = 0, grads = 0;
-    kda_status st = glu_bwd_params(a, p, need, grads);
+    size_t need = 0, grads = 0, moved = 0;
+    kda_status st = glu_bwd_params(a, p, need, grads, moved);
     if (st != KDA_OK) return st;
     if ((st = check_space(a->workspace, a->workspace_bytes, need)) != KDA_OK) return st;
     char *ws = static_cast<char *>(a->workspace);
     p.dg = ws;
     p.du = ws + (size_t)a->rows * p.ld_d * es_of(a->dtype);
+    p.part = ws + grads + moved;
     return from(mixer::launch_glu_bwd(p, a->dtype == KDA_BF16, ws + grads, stream_of(stream)));
 }
 

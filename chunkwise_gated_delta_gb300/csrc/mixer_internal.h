@@ -101,6 +101,7 @@ struct GluParams {
     float *g, *u;                     // [M][F] the two products, or NULL
     void *dg, *du;                    // workspace [M][ld_d]: their gradients
     long long ld_d;
+    void *part;                       // workspace: sums of parts of K (glu_tc_part_bytes)
     int *status;                      // status block, or NULL
 };
 
@@ -140,6 +141,7 @@ cudaError_t launch_glu_bwd(const GluParams &p, bool bf16, char *ws, cudaStream_t
 long long glu_grad_stride(const GluParams &p, bool bf16);
 size_t glu_moved_bytes(const GluParams &p, bool bf16);       // of ws
 // Forms of bfloat16 calls: the tensor cores' products, and a few rows past the weights.
+size_t glu_tc_part_bytes(const GluParams &p);
 cudaError_t launch_glu_tc_fwd(const GluParams &p, cudaStream_t s);
 cudaError_t launch_glu_tc_grads(const GluParams &p, cudaStream_t s);
 cudaError_t launch_glu_tc_dx(const GluParams &p, cudaStream_t s);

@@ -499,7 +499,8 @@ typedef struct {
     void *status;          /* as the forward's */
 } glu_bwd_args;
 
-/* Bytes of workspace (0 on bad args): the gradients of the two products, and operands that lie off 16 bytes. */
+/* Bytes of workspace (0 on bad args): the gradients of the two products, operands that lie off 16 bytes, and sums of parts
+   of a product that has few tiles. */
 size_t glu_bwd_workspace(const glu_bwd_args *args);
 
 /*

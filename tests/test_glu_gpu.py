@@ -1,5 +1,6 @@
 """Gated feed-forward product on the GPU against its definition in float64: sizes that end inside every tile, one row to many,
 strides, both activations, saved and recomputed products."""
+import ctypes
 import math
 
 import pytest
@@ -50,7 +51,7 @@ def call(s, activation="silu", save=True):
 
 SIZES = [(1, 1, 1), (1, 64, 128), (2, 8, 8), (3, 40, 72), (8, 128, 64), (9, 256, 136), (16, 512, 264), (17, 72, 520), (33, 136, 128),
          (64, 256, 256), (65, 200, 136), (127, 64, 264), (128, 128, 128), (129, 264, 520), (300, 72, 1000), (257, 513, 129), (70, 517, 1031),
-         (1, 517, 1031), (5, 9, 1000), (512, 512, 512), (1000, 24, 40)]
+         (1, 517, 1031), (5, 9, 1000), (512, 512, 512), (1000, 24, 40), (20, 264, 2051), (3000, 72, 40)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
@@ -167,3 +168,20 @@ def test_a_wait_that_runs_out(M):
     h, g, u = lib.glu_fwd(s["x"], s["wg"], s["wu"], save=True, status=status)
     got = dict(h=h, g=g, u=u, **lib.glu_bwd(s["x"], s["wg"], s["wu"], s["dh"], g, u, status=status))
     assert lib.status_read(status) == 0 and all(torch.equal(got[k], want[k]) for k in want)
+
+
+def test_workspaces_need_no_more_than_16_bytes():
+    """Sums of parts of a product (few tiles, a long K) and the products' gradients in a workspace that begins off 32 bytes."""
+    M, D, F = 40, 264, 4104
+    s = make(M, D, F, torch.bfloat16)
+    want = definition(s, "silu")
+    out = dict(dx=torch.empty(M, D, device=DEV, dtype=torch.bfloat16), dw_gate=torch.empty(F, D, device=DEV, dtype=torch.bfloat16),
+               dw_up=torch.empty(F, D, device=DEV, dtype=torch.bfloat16))
+    a = _lib.GluBwdArgs(M, D, F, _lib.KDA_BF16, 0, s["x"].data_ptr(), 0, s["wg"].data_ptr(), 0, s["wu"].data_ptr(), 0, s["dh"].data_ptr(), 0, None, None,
+                        out["dx"].data_ptr(), 0, out["dw_gate"].data_ptr(), 0, out["dw_up"].data_ptr(), 0, None, 0, None)
+    n = _lib.load().glu_bwd_workspace(ctypes.byref(a))
+    assert n > 2 * M * F * 2
+    ws = torch.empty(n + 64, dtype=torch.uint8, device=DEV)
+    a.workspace, a.workspace_bytes = ws.data_ptr() + 16, n
+    assert _lib.load().glu_bwd(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == 0
+    check(out, want, torch.bfloat16, M, D, F)
