@@ -5,7 +5,7 @@
 //
 // float32 products run on the CUDA cores, which do not round their operands.  A block has a tile of SIDE x SIDE products, a thread
 // two quads of them per axis, two columns to a packed multiplication; in the forward the left half of the columns is Wg's and the
-// right half Wu's.  Where tiles of 128 leave the GPU idle, tiles of 64 are used, and a cluster of up to eight blocks shares the
+// right half Wu's.  Where tiles of 128 leave the GPU idle, tiles of 64 are used, and a cluster of up to sixteen blocks shares the
 // sum of a tile, joined in the blocks' order through shared memory.
 #include <type_traits>
 
@@ -252,10 +252,14 @@ template <int SIDE, Mode MODE, int V> cudaError_t run_side(const GluParams &p, l
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = blocks > 1 ? 1 : 0;
+    if (blocks > 8) {
+        const cudaError_t e = allow_large_clusters<glu_f32_kernel<SIDE, MODE, V>>();
+        if (e != cudaSuccess) return e;
+    }
     return cudaLaunchKernelEx(&cfg, glu_f32_kernel<SIDE, MODE, V>, p, blocks);
 }
 // Tiles of 128 where they fill the SMs' places (two to an SM) twice over, else tiles of 64 (eight), a cluster of blocks to each
-// where those leave half of the places empty and every block has eight steps.
+// of up to sixteen blocks to each where those leave half of the places empty and every block has eight steps.
 template <Mode MODE> cudaError_t run_f32(const GluParams &p, cudaStream_t s) {
     constexpr bool DUAL = MODE == FWD || MODE == RECOMPUTE;
     const long long ms = MODE == DW ? p.F : p.M, ns = DUAL ? p.F : p.D, ks = MODE == DW ? p.M : MODE == DX ? 2LL * p.F : p.D;
@@ -269,7 +273,7 @@ template <Mode MODE> cudaError_t run_f32(const GluParams &p, cudaStream_t s) {
     if (tiles(64) * z * 8 > 0x7fffffffLL) return cudaErrorNotSupported;
     if (tiles(128) * z >= 4 * sms) return wide ? run_side<128, MODE, 4>(p, tiles(128), 1, s) : run_side<128, MODE, 1>(p, tiles(128), 1, s);
     int blocks = 1;
-    while (blocks < 8 && tiles(64) * z * blocks * 2 <= 8 * sms && ks >= 256LL * blocks) blocks *= 2;
+    while (blocks < 16 && tiles(64) * z * blocks * 2 <= 8 * sms && ks >= 256LL * blocks) blocks *= 2;
     return wide ? run_side<64, MODE, 4>(p, tiles(64), blocks, s) : run_side<64, MODE, 1>(p, tiles(64), blocks, s);
 }
 

@@ -273,18 +273,21 @@ int sm_count();
 int current_device();
 constexpr int DEVICES = 64;              // for which answers are kept
 
-// Lets KERNEL have `bytes` of dynamic shared memory (one size per kernel), asking the driver once per device.
-template <auto KERNEL> cudaError_t allow_shared(size_t bytes) {
+// Sets an attribute of KERNEL (to one value for each), asking the driver once per device.
+template <auto KERNEL, cudaFuncAttribute WHAT> cudaError_t set_once(int value) {
     static std::atomic<unsigned long long> done;
     static_assert(DEVICES == 64, "a bit each");
-    if (bytes <= 48 * 1024) return cudaSuccess;
     const int dev = current_device();
     const unsigned long long bit = dev < DEVICES ? 1ull << dev : 0;
     if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    const cudaError_t e = cudaFuncSetAttribute(KERNEL, WHAT, value);
     if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
     return e;
 }
+template <auto KERNEL> cudaError_t allow_shared(size_t bytes) {
+    return bytes <= 48 * 1024 ? cudaSuccess : set_once<KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize>((int)bytes);
+}
+template <auto KERNEL> cudaError_t allow_large_clusters() { return set_once<KERNEL, cudaFuncAttributeNonPortableClusterSizeAllowed>(1); }
 
 inline bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 // Rows of `es`-byte elements that may be read n bytes at a time (a NULL pointer may).
