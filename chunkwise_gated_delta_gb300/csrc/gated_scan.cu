@@ -1,6 +1,6 @@
 // Gated recurrence (one state per channel), forward, backward and single tokens.
 //
-// All rows of a call form one axis, cut where a sequence begins, in segments of 16 to 64 rows whatever the sequences' lengths.
+// All rows of a call form one axis, cut where a sequence begins, in segments of 16 to 128 rows whatever the sequences' lengths.
 // A warp has a segment's rows and 64 channels, a lane two of them, eight rows in registers and the next eight on their way:
 //
 //   local pass      what a segment does to a state: h_out = h + A h_in (A, h), or h alone where a sequence begins in it
@@ -8,9 +8,11 @@
 //   walk            the segment again from the state that enters it; y, final states, the states before every 8th row
 //
 // Warps wait for no other, and every pass is as parallel as the call has rows and channels.  The walk goes through the segments
-// from the last, whose inputs the local pass has left in L2 (its 126 MB hold all inputs of 10 million bfloat16 row-channels).
-// Gates are computed twice; carrying the states in one pass through clusters of blocks that exchange them took 109 us for a
-// prompt of 16384 x 1024 and 104 us for 4 of 4096 x 2048, bound by the exchange: WALK_TIMES.
+// from the last, whose inputs the local pass has left in L2.
+// Gates are computed twice, and instructions are what bounds it (57 and 64 per row and pair of channels, 66 % of the issue slots):
+// 4 sequences of 4096 x 2048 bfloat16 take 87 us, of which local pass 41, boundary 5, walk 43 (traffic of one pass: 39); one of
+// 16384 x 1024 takes 53.  One pass was slower: clusters of blocks that carry the state through shared memory took 104 and 109 us,
+// tiles that take what enters from the tiles before by flags in memory 154 and 93, both waiting for each other most of the time.
 // Where a sequence begins the link is cut by selection (never by a product with 0: a state of an earlier sequence
 // may be an infinity).
 //
@@ -462,10 +464,13 @@ int access_of(const GatedScanParams &p, bool bf16) {
 }
 
 // Rows of a segment, such that the warps of a pass (`warps` to an SM) all run at once, or in as few rounds as make segments of at most
-// MOST rows: a last round that is not full costs as much as a full one.
-constexpr int MOST = 96;
+// MOST rows: a last round that is not full costs as much as a full one (B4 T4096 D2048: 90 us in segments of 64, 88 so).  Up to FEW
+// rows are one segment, a launch instead of three: calls of 128 x 512 back to back take 22 us for 30 (with gradients 62 for 77),
+// waited for one by one 43 for 40.
+constexpr int MOST = 96, FEW = 128;
 int segment_of(const GatedScanParams &p, int warps) {
     const long long cols = (p.D - 1) / COLS + 1, rows = rows_of(p), places = (long long)warps * sm_count();
+    if (rows <= FEW) return (int)((rows + ROWS - 1) / ROWS * ROWS);
     const long long rounds = (cols * rows + places * MOST - 1) / (places * MOST), segs = max(1LL, places * rounds / cols);
     const long long seg = ((rows + segs - 1) / segs + ROWS - 1) / ROWS * ROWS;
     return (int)max(seg, 16LL);

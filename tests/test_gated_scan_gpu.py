@@ -60,7 +60,8 @@ def compare(got, want, dtype, rows=None):
         assert rel(v, w) <= tol(v.dtype if k in ("ht", "drate", "dh0") else dtype), k
 
 
-DENSE = [(1, 1, 1), (1, 1, 64), (3, 1, 130), (2, 2, 2), (1, 31, 63), (2, 32, 64), (1, 33, 65), (2, 63, 66), (1, 64, 128), (3, 65, 8),
+# (up to 128 rows are one segment)
+DENSE = [(1, 1, 1), (2, 64, 70), (1, 128, 34), (1, 129, 34), (4, 100, 20), (1, 1, 64), (3, 1, 130), (2, 2, 2), (1, 31, 63), (2, 32, 64), (1, 33, 65), (2, 63, 66), (1, 64, 128), (3, 65, 8),
          (2, 200, 514), (9, 17, 37)]
 
 
@@ -74,7 +75,7 @@ def test_dense(B, T, D, dtype):
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("lens,D,h0", [([5, 1, 0, 64, 3, 31, 1, 1, 40], 70, True), ([0, 0, 7], 64, True), ([129, 1, 300, 0, 62], 33, True),
-                                       ([1] * 77, 12, True), ([64, 64, 32, 32], 128, False), ([333], 2, False), ([0], 3, True)])
+                                       ([1] * 77, 12, True), ([1] * 200, 12, True), ([100, 0, 28], 34, True), ([64, 64, 32, 32], 128, False), ([333], 2, False), ([0], 3, True)])
 def test_packed(lens, D, h0, dtype):
     n, rows = len(lens), max(1, sum(lens))
     s = make(rows, n, D, dtype, seed=D, h0=h0)
