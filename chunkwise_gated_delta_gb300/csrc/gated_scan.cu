@@ -9,7 +9,8 @@
 //
 // Warps wait for no other, and every pass is as parallel as the call has rows and channels.  The walk goes through the segments
 // from the last, whose inputs the local pass has left in L2.
-// Gates are computed twice, and instructions are what bounds it (57 and 64 per row and pair of channels, 66 % of the issue slots):
+// Gates are computed twice, and the passes are bound by instructions and their latency (57 and 64 per row and pair of channels, 66 %
+// of the issue slots at 20 warps to an SM; four channels to a lane, a seventh fewer instructions at 12 or 16 warps, takes as long):
 // 4 sequences of 4096 x 2048 bfloat16 take 87 us, of which local pass 41, boundary 5, walk 43 (traffic of one pass: 39); one of
 // 16384 x 1024 takes 53.  One pass was slower: clusters of blocks that carry the state through shared memory took 104 and 109 us,
 // tiles that take what enters from the tiles before by flags in memory 154 and 93, both waiting for each other most of the time.

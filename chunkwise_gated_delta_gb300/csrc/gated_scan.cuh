@@ -19,21 +19,6 @@ constexpr int WARPS = 4, THREADS = 32 * WARPS;
 constexpr int COLS = 64;                          // channels of a warp, two per lane
 constexpr int ROWS = GATED_SCAN_STATE_ROWS;       // rows that a warp has in hand at a time
 
-// Two neighbouring channels of a row as they lie in memory: one access, or two with the channel past an odd end
-// replaced by the last.
-template <class T, bool VEC> struct Raw {
-    Lanes<T, 2> v;
-    __device__ __forceinline__ void load(const T *row, int c, int) { v.load(row + c); }
-    __device__ __forceinline__ f2 pair() const { return v.pair(0); }
-};
-template <class T> struct Raw<T, false> {
-    uint32_t w[2];
-    __device__ __forceinline__ void load(const T *row, int c, int D) {
-        w[0] = load_bits(row + c);
-        w[1] = load_bits(row + min(c + 1, D - 1));
-    }
-    __device__ __forceinline__ f2 pair() const { return pack2(bits_f<T>(w[0]), bits_f<T>(w[1])); }
-};
 // ROWS rows of a warp's channels in shared memory, and how they get there: accesses of CP bytes, asynchronous ones of 16
 // or 4 bytes, or single bfloat16 elements (CP = 2).  Rows past the call's are its first or last, channels past D are
 // left out (their lanes write nothing).
