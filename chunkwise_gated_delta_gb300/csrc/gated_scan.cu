@@ -466,7 +466,7 @@ int access_of(const GatedScanParams &p, bool bf16) {
 
 // Rows of a segment, such that the warps of a pass (`warps` to an SM) all run at once, or in as few rounds as make segments of at most
 // MOST rows: a last round that is not full costs as much as a full one (B4 T4096 D2048: 90 us in segments of 64, 88 so).  Up to FEW
-// rows are one segment, a launch instead of three: calls of 128 x 512 back to back take 22 us for 30 (with gradients 62 for 77),
+// rows are one segment, a launch instead of three: calls of 128 x 512 back to back take 22 us for 30 (with gradients 58 for 77),
 // waited for one by one 43 for 40.
 constexpr int MOST = 96, FEW = 128;
 int segment_of(const GatedScanParams &p, int warps) {
@@ -504,10 +504,7 @@ template <auto KERNEL> cudaError_t launch(unsigned grid, int threads, size_t sme
 template <class T, int CP> cudaError_t forward(GatedScanParams &p, cudaStream_t s) {
     constexpr size_t smem = WARPS * Ring<T, CP, 3, false>::BYTES;
     const unsigned n = blocks_of(p);
-    if (segments_of(p, p.seg) == 1) {
-        p.seg_in = nullptr;            // nothing enters the only segment
-        return launch<gated_scan_fwd_kernel<T, CP, true>>(n, THREADS, smem, false, p, s);
-    }
+    if (segments_of(p, p.seg) == 1) return launch<gated_scan_fwd_kernel<T, CP, true>>(n, THREADS, smem, false, p, s);
     cudaError_t e = launch<gated_scan_fwd_kernel<T, CP, false>>(n, THREADS, smem, false, p, s);
     if (e == cudaSuccess) e = launch<gated_scan_boundary_kernel<false>>((unsigned)((p.D - 1) / 32 + 1), 32 * BWARPS, 0, true, p, s);
     if (e == cudaSuccess) e = launch<gated_scan_fwd_kernel<T, CP, true>>(n, THREADS, smem, true, p, s);
@@ -517,8 +514,7 @@ template <class T, int CP> cudaError_t backward(GatedScanParams &p, cudaStream_t
     const unsigned n = blocks_of(p);
     const bool one = segments_of(p, p.seg) == 1;
     cudaError_t e = cudaSuccess;
-    if (one) p.seg_in = nullptr;
-    else {
+    if (!one) {
         e = launch<gated_scan_bwd_local_kernel<T, CP>>(n, THREADS, WARPS * Ring<T, CP, 2, true>::BYTES, false, p, s);
         if (e == cudaSuccess) e = launch<gated_scan_boundary_kernel<true>>((unsigned)((p.D - 1) / 32 + 1), 32 * BWARPS, 0, true, p, s);
     }
@@ -530,9 +526,14 @@ template <bool BWD, class T, int CP> cudaError_t run(GatedScanParams &p, cudaStr
     else return forward<T, CP>(p, s);
 }
 size_t pair_floats(const GatedScanParams &p, size_t segs) { return 2 * segs * ((p.D + 1) & ~1); }
-// Points the parameter block into its workspace (the forward has no `part`).
+// Points the parameter block into its workspace (the forward has no `part`).  One segment takes none: nothing enters it.
 void carve(GatedScanParams &p) {
     const size_t n = (size_t)segments_of(p, p.seg);
+    if (n == 1) {
+        p.seg_pair = p.seg_in = nullptr;
+        p.part = p.drate;
+        return;
+    }
     p.seg_pair = p.ws;                   // (16-byte aligned)
     p.seg_in = p.ws + pair_floats(p, n);
     p.part = p.seg_in + n * p.D;
@@ -556,7 +557,7 @@ size_t gated_scan_fwd_floats(const GatedScanParams &p) {
 }
 size_t gated_scan_bwd_floats(const GatedScanParams &p) {
     const size_t n = (size_t)segments_of(p, bwd_segment(p));
-    return max(pair_floats(p, n) + 2 * n * p.D, gated_scan_fwd_floats(p));
+    return n > 1 ? max(pair_floats(p, n) + 2 * n * p.D, gated_scan_fwd_floats(p)) : 0;
 }
 cudaError_t launch_gated_scan_fwd(const GatedScanParams &q, bool bf16_, cudaStream_t s) {
     GatedScanParams p = q;
@@ -566,8 +567,9 @@ cudaError_t launch_gated_scan_fwd(const GatedScanParams &q, bool bf16_, cudaStre
 cudaError_t launch_gated_scan_bwd(const GatedScanParams &q, bool bf16_, cudaStream_t s) {
     GatedScanParams p = q;
     const cudaError_t e = run<true>(p, bf16_, s);
-    if (e != cudaSuccess) return e;
-    return launch_sum_rows(p.part, (int)segments_of(p, p.seg), SumOut{p.drate, p.D, false}, SumOut{nullptr, 0, false}, s);
+    const int segs = (int)segments_of(p, p.seg);
+    if (e != cudaSuccess || segs == 1) return e;             // (one segment's sums are drate)
+    return launch_sum_rows(p.part, segs, SumOut{p.drate, p.D, false}, SumOut{nullptr, 0, false}, s);
 }
 
 cudaError_t launch_gated_scan_step(const GatedScanParams &p, bool bf16_, cudaStream_t s) {

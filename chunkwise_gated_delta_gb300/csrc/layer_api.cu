@@ -57,7 +57,7 @@ kda_status gated_bwd(const gated_scan_bwd_args *a, mixer::GatedScanParams &p, si
                         dense(a->cu_seqlens, 1, (long long)a->B + 1, 4)};
     const Block out[] = {{a->dx, rows, a->D, p.ld_dx, es}, {a->ddecay, rows, a->D, p.ld_ddecay, es},
                          {a->dgate, rows, a->D, p.ld_dgate, es}, dense(a->drate, 1, a->D, 4), dense(a->dh0, a->B, a->D, 4),
-                         dense(a->workspace, 1, (long long)a->workspace_bytes, 1)};
+                         dense(need ? a->workspace : nullptr, 1, (long long)a->workspace_bytes, 1)};
     return blocks_ok(in, out) ? KDA_OK : KDA_ERR_INVALID_ARG;
 }
 
@@ -196,7 +196,7 @@ kda_status gated_scan_bwd(const gated_scan_bwd_args *a, kda_stream_t stream) {
     size_t need = 0, states = 0;
     kda_status st = gated_bwd(a, p, need, states);
     if (st != KDA_OK) return st;
-    if ((st = check_space(a->workspace, a->workspace_bytes, need)) != KDA_OK) return st;
+    if (need && (st = check_space(a->workspace, a->workspace_bytes, need)) != KDA_OK) return st;
     char *ws = static_cast<char *>(a->workspace);
     const bool bf16 = a->dtype == KDA_BF16;
     p.ws = reinterpret_cast<float *>(ws + states);

@@ -89,6 +89,7 @@ def test_refusals_before_any_launch(lib, name, over, code):
 def test_workspace_sizes(lib):
     size = lambda n, **o: getattr(lib, n + "_workspace")(ctypes.byref(_args(n, **o)))  # noqa: E731
     assert size("gated_scan_fwd", B=1, T=128) == 0 and size("gated_scan_fwd") > 0           # one segment takes none
+    assert size("gated_scan_bwd", B=1, T=128) == 0 and size("gated_scan_bwd", B=1, T=128, states=None) >= 16 * 64 * 4
     kept, again = size("gated_scan_bwd"), size("gated_scan_bwd", states=None)
     assert again >= kept + 125 * 64 * 4                                                     # a state before every eighth of 1000 rows
     # a packed batch has as many rows as tokens
