@@ -6,7 +6,8 @@
 // float32 products run on the CUDA cores, which do not round their operands.  A block has a tile of SIDE x SIDE products, a thread
 // two quads of them per axis, two columns to a packed multiplication; in the forward the left half of the columns is Wg's and the
 // right half Wu's.  Where tiles of 128 leave the GPU idle, tiles of 64 are used, and a cluster of up to sixteen blocks shares the
-// sum of a tile, joined in the blocks' order through shared memory.
+// sum of a tile, joined in the blocks' order through shared memory.  Bound by the multiplications: 2048 x 1024 x 2048 takes 359 us,
+// 48 TFLOP/s (with one multiplication per instruction and 4-byte loads 431).
 #include <type_traits>
 
 #include "glu.cuh"

@@ -13,6 +13,11 @@
 // or with K outermost (weights in DX, dg, du and x in DW), which the matrix descriptors express; TMA fills what lies past an
 // extent with zeros.
 //
+// Bound by the tensor cores and, in a run of such products, by the power limit: 8192 x 2048 x 8192 takes 305 us (1.80 PFLOP/s) after a
+// pause and 350 (1.57) back to back, where 8192^3 of cuBLAS reach 1.90 and 1.71.  Six stages of 32 KB are what shared memory
+// holds; a pair needs half of a lone CTA's reads of B.  4096 x 2048 x 5632 with its saved products (230 MB out) takes 128 us: stores of whole
+// 32-byte sectors, of 16 bytes 153.  DX and DW of that size take 119 and 112, in one launch with a balanced schedule as long.
+//
 // Waits are bounded.  Where one runs out the kernel stops its work, lets what is in flight arrive, frees TMEM, leaves NaN in
 // the outputs of tiles that it did not finish, and records the timeout in the caller's status block if there is one.
 #include <cuda.h>

@@ -8,6 +8,10 @@
 // A group of up to 32 vectors of 16 bytes takes a part of a warp (a power of two of lanes), a longer one a whole
 // warp with several vectors per lane, so sums cross lanes only.  A thread keeps its group, and with it the
 // weights and their sums, and goes down the rows.
+//
+// Bound by HBM and, not far behind, by instructions (66 to 73 % of the issue slots): 16384 rows of 16 groups of 128 bfloat16 with a
+// gate take 34 us forward (5.9 TB/s), 8192 rows of 32 groups 35 forward and 56 backward (6.0 TB/s), the sums over blocks 4 more.  With the
+// next row in registers, and the bias' sums always kept, they took 39 and 86: too few bytes on their way.
 #include "mixer_common.cuh"
 #include "mixer_internal.h"
 
