@@ -213,7 +213,7 @@ template <int SIDE, Mode MODE, int V> __global__ void __launch_bounds__(Tiles<SI
 
 // dg and du of saved products: V columns per thread.
 template <class T, int V> __global__ void __launch_bounds__(256) glu_slope_kernel(GluParams p) {
-    const long long per = (p.F + V - 1) / V, i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const long long per = (p.F - 1) / V + 1, i = (long long)blockIdx.x * 256 + threadIdx.x;
     if (i >= per * p.M) return;
     const long long m = i / per, n = (i - m * per) * V;
     float g[V], u[V];
@@ -234,10 +234,10 @@ template <class T, int V> __global__ void __launch_bounds__(256) glu_slope_kerne
 // A matrix's rows to where they are 16-byte aligned.
 __global__ void __launch_bounds__(256) glu_align_kernel(const bf16 *from, long long ld, bf16 *to, long long pitch, long long rows, int cols) {
     for (long long r = blockIdx.y; r < rows; r += gridDim.y) {
-        const int c = (int)blockIdx.x * 1024 + (int)threadIdx.x;
+        const unsigned c = blockIdx.x * 1024 + threadIdx.x;      // (without a sign: a step past a width near 2^31 does not wrap)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (c + k * 256 < cols) to[r * pitch + c + k * 256] = from[r * ld + c + k * 256];
+            if (c + k * 256 < (unsigned)cols) to[r * pitch + c + k * 256] = from[r * ld + c + k * 256];
     }
 }
 
@@ -283,7 +283,7 @@ template <class T> cudaError_t slopes(const GluParams &p, cudaStream_t s) {
     const bool wide = p.F % W == 0 && rows_aligned(p.dh, p.ld_dh, sizeof(T), 16) && rows_aligned(p.dg, p.ld_d, sizeof(T), 16) &&
                       aligned_to(p.du, 16) && aligned_to(p.g, 16) && aligned_to(p.u, 16);
     const int v = wide ? W : 1;
-    const unsigned grid = (unsigned)(((p.F + v - 1) / v * p.M + 255) / 256);
+    const unsigned grid = (unsigned)((((p.F - 1) / v + 1) * p.M + 255) / 256);
     if (wide) glu_slope_kernel<T, W><<<grid, 256, 0, s>>>(p);
     else glu_slope_kernel<T, 1><<<grid, 256, 0, s>>>(p);
     return cudaGetLastError();
@@ -294,7 +294,8 @@ struct Moved {
     const void **p;
     long long *ld, rows;
 };
-size_t moved_bytes(const Moved &m, int D) { return ((size_t)m.rows * ((D + 7) / 8 * 8) * 2 + 255) / 256 * 256; }
+long long moved_pitch(int D) { return (D + 7LL) / 8 * 8; }
+size_t moved_bytes(const Moved &m, int D) { return ((size_t)m.rows * moved_pitch(D) * 2 + 255) / 256 * 256; }
 template <class F> cudaError_t each_moved(GluParams &p, F f) {
     const Moved all[] = {{&p.x, &p.ld_x, p.M}, {&p.wg, &p.ld_wg, p.F}, {&p.wu, &p.ld_wu, p.F}};
     for (const Moved &m : all)
@@ -306,8 +307,8 @@ template <class F> cudaError_t each_moved(GluParams &p, F f) {
 }
 cudaError_t align(GluParams &p, char *ws, cudaStream_t s) {
     return each_moved(p, [&](const Moved &m) {
-        const long long pitch = (p.D + 7) / 8 * 8;
-        const unsigned gx = (unsigned)((p.D + 1023) / 1024), gy = (unsigned)(m.rows < 32768 ? m.rows : 32768);
+        const long long pitch = moved_pitch(p.D);
+        const unsigned gx = (unsigned)((p.D - 1) / 1024 + 1), gy = (unsigned)(m.rows < 32768 ? m.rows : 32768);
         glu_align_kernel<<<dim3(gx, gy), 256, 0, s>>>(static_cast<const bf16 *>(*m.p), *m.ld, reinterpret_cast<bf16 *>(ws), pitch, m.rows, p.D);
         *m.p = ws;
         *m.ld = pitch;

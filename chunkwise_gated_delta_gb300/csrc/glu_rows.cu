@@ -45,12 +45,13 @@ template <int NT, int U> __global__ void __launch_bounds__(THREADS) glu_rows_ker
             for (int e = 0; e < 4; ++e) acc[i][n][e] = 0.f;
     // the warps' steps take turns, so that together they read whole stretches of a row
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    for (int k0 = warp * 32 * U; k0 < p.D; k0 += WARPS * 32 * U) {
+    const unsigned D = (unsigned)p.D;                        // (columns without a sign: a step past a width near 2^31 does not wrap)
+    for (unsigned k0 = warp * 32 * U; k0 < D; k0 += WARPS * 32 * U) {
         uint4 a[U][4], b[U][NT];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int k = k0 + u * 32;
-            const bool in = k + q * 8 < p.D;                 // (D is a multiple of 8: all of a lane's elements or none)
+            const unsigned k = k0 + u * 32;
+            const bool in = k + q * 8 < D;                 // (D is a multiple of 8: all of a lane's elements or none)
 #pragma unroll
             for (int i = 0; i < 4; ++i) a[u][i] = in ? load_stream(w[i] + k) : zero;
 #pragma unroll

@@ -525,7 +525,7 @@ template <Mode MODE> Shape shape_of(const GluParams &p) {
     q.tn = ((DUAL ? p.F : p.D) + (long long)cols - 1) / cols;
     q.kbs = (ks + BK - 1) / BK * (MODE == DX ? 2 : 1);
     q.splits = 1;
-    q.pitch = (p.D + 7) / 8 * 8;
+    q.pitch = (p.D + 7LL) / 8 * 8;
     if (!DUAL) {
         const long long places = sm_count() / (q.pair ? 2 : 1), tiles = q.tm * q.tn * (MODE == DW ? 2 : 1);
         const long long n = places / tiles, most = q.kbs / 4;

@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(TPB) group_norm_fwd_kernel(GroupNormParams p, 
                 store_lanes<T, V>(y + at[k], o);
             }
     }
+    copies_wait<0>();                                        // (rows past the end were on their way too)
 }
 
 // BIAS: the call has a bias or wants its gradient.
@@ -262,10 +263,10 @@ __global__ void __launch_bounds__(TPB, ITEMS == 1 ? 3 : 1) group_norm_bwd_kernel
                 store_lanes<T, V>(dx + at[k], o);
             }
     }
+    copies_wait<0>();                                        // (rows past the end were on their way too)
     if (!p.part) return;
     // the block's sums, over the slots that have the same weight, in their order
-    auto sums = reinterpret_cast<float (*)[L][2 * V]>(sm);     // [SLOTS]; every copy into this memory has been waited for below
-    copies_wait<0>();
+    auto sums = reinterpret_cast<float (*)[L][2 * V]>(sm);     // [SLOTS]
     const int keys = p.shared ? 1 : per, key = threadIdx.x / L, cols = p.shared ? p.C : p.G * p.C;
     const long long rowp = p.shared ? (long long)blockIdx.y * gridDim.x + blockIdx.x : blockIdx.x;
     const int kg = (int)blockIdx.y * per + key;              // (unshared: the key's group)
@@ -434,6 +435,11 @@ Plan plan_of(const GroupNormParams &p, bool bf16_, bool bwd) {
     }
     q.per = slots_per_row(p.G, TPB / q.L);
     q.gy = (unsigned)((p.G - 1) / q.per + 1);
+    if (q.gy > 65535) {                       // (a grid's second axis: more than four million groups go one by one)
+        q.items = 0;
+        q.parts = (int)(p.rows < 64 ? p.rows : 64);
+        return q;
+    }
     const int rows = TPB / q.L / q.per;                      // rows of a block's visit
     const long long visits = (p.rows + rows - 1) / rows;
     long long gx = (long long)sms * (bwd ? 3 : 4) / q.gy;            // (as many blocks as an SM holds)

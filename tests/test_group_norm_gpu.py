@@ -151,3 +151,10 @@ def test_gradient_of_an_absent_bias(gate):
     a.workspace, a.workspace_bytes = ws.data_ptr(), n
     assert _lib.load().group_norm_bwd(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == 0
     check(dict(dx=out["dx"], dweight=dw, dbias=db), want, 37, 64)
+
+
+def test_more_groups_than_a_grid_has_rows():
+    """Four million groups and more go one by one."""
+    groups, C = 4_200_000, 3
+    s = make(1, groups, C, torch.float32, shared=True)
+    check(call(s, groups, True), definition(s, groups, True), groups, C)
