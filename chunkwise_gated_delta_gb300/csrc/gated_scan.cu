@@ -555,9 +555,10 @@ size_t gated_scan_fwd_floats(const GatedScanParams &p) {
     const size_t n = (size_t)segments_of(p, fwd_segment(p));
     return n > 1 ? pair_floats(p, n) + n * p.D : 0;
 }
+// Without the forward's states its walk runs here first, in segments of its own: it may take space where the backward takes none.
 size_t gated_scan_bwd_floats(const GatedScanParams &p) {
-    const size_t n = (size_t)segments_of(p, bwd_segment(p));
-    return n > 1 ? max(pair_floats(p, n) + 2 * n * p.D, gated_scan_fwd_floats(p)) : 0;
+    const size_t n = (size_t)segments_of(p, bwd_segment(p)), own = n > 1 ? pair_floats(p, n) + 2 * n * p.D : 0;
+    return p.states ? own : max(own, gated_scan_fwd_floats(p));
 }
 cudaError_t launch_gated_scan_fwd(const GatedScanParams &q, bool bf16_, cudaStream_t s) {
     GatedScanParams p = q;

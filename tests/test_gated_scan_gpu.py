@@ -105,6 +105,16 @@ def test_without_saved_states_the_same_bits():
         assert torch.equal(a[k], b[k]), k
 
 
+@pytest.mark.parametrize("T", [129, 160])
+def test_states_again_where_only_the_forward_has_segments(T):
+    """So many channels that the backward's rows are one segment and the forward's, which it runs for the states, several."""
+    s = make(T, 1, 77890, torch.bfloat16)
+    a, b = call(s, (1, T, 77890)), call(s, (1, T, 77890), states=False)
+    for k in a:
+        assert torch.equal(a[k], b[k]), k
+    compare(b, definition(s, spans_of([T]), True), torch.bfloat16)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
 def test_strided_rows_and_supplied_outputs(dtype):
     B, T, D = 2, 70, 64

@@ -101,6 +101,15 @@ def test_workspace_sizes(lib):
     assert size("glu_bwd") >= 2 * 8 * 128 * 2
 
 
+@pytest.mark.parametrize("T", [129, 144, 160, 192])
+def test_a_backward_without_states_has_the_forwards_space(lib, T):
+    """Its rows may be one segment where the forward's, which it runs for the states, are several."""
+    size = lambda n, **o: getattr(lib, n + "_workspace")(ctypes.byref(_args(n, B=1, T=T, **o)))  # noqa: E731
+    for D in (64, 77888, 77890, 104000, 166400, 230016):
+        states = (-(-T // 8) * D * 4 + 15) // 16 * 16
+        assert size("gated_scan_bwd", D=D, ld_x=D, states=None) >= states + size("gated_scan_fwd", D=D, ld_x=D), D
+
+
 def test_state_rows_are_the_headers():
     src = open(kbuild.INCLUDE + "/mixer.h").read()
     for name in ("GATED_SCAN_STATE_ROWS", "GROUP_NORM_FLAG_CENTER", "GROUP_NORM_FLAG_SHARED", "GLU_FLAG_GELU"):
