@@ -443,11 +443,12 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     return fn;
 }
 
-// A matrix [rows][cols] with row stride ld; boxes of 64 columns by `box` rows, 128-byte swizzle.
+// A matrix [rows][cols] with row stride ld (of a single row, which has no next one, any); boxes of 64 columns by `box` rows, 128-byte
+// swizzle.
 bool make_map(CUtensorMap *m, const void *p, long long rows, long long cols, long long ld, int box) {
     const auto enc = encoder();
     if (!enc) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)(rows > 1 ? ld : (cols + 7) / 8 * 8) * 2};
     const cuuint32_t boxes[2] = {64, (cuuint32_t)box}, one[2] = {1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), dims, strides, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
