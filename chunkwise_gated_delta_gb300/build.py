@@ -19,7 +19,7 @@ LIB = os.path.join(BUILD, "libkda.so")
 
 SOURCES = ["kda_api.cu", "kda_fwd_simt.cu", "kda_fwd_tc.cu", "kda_noalloc.cu", "dplr_fwd_simt.cu", "kda_bwd_simt.cu", "dplr_bwd_simt.cu",
            "mixer_api.cu", "mixer_common.cu", "layer_norm.cu", "short_conv.cu", "ssm_scan_fwd.cu", "ssm_scan_bwd.cu",
-           "layer_api.cu", "gated_scan.cu", "group_norm.cu", "glu.cu", "glu_tc.cu", "glu_rows.cu"]
+           "layer_api.cu", "gated_scan.cu", "group_norm.cu", "group_norm_bf16.cu", "glu.cu", "glu_tc.cu", "glu_rows.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

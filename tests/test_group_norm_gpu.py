@@ -61,6 +61,19 @@ def test_forms(rows, groups, C, dtype):
         check(call(s, groups, center), definition(s, groups, center), rows * (groups if shared else 1), C)
 
 
+# groups of several warps: their lanes' sums cross them; rows enough for several visits of a block
+WIDE = [(700, 1, 512), (3, 5, 520), (9, 3, 1024), (500, 1, 1031), (40, 1, 2048), (500, 2, 1028), (1, 3, 2049), (200, 1, 4096), (7, 2, 4104), (310, 1, 8192),
+        (2, 2, 8200), (33, 9, 260)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("rows,groups,C", WIDE)
+def test_groups_of_several_warps(rows, groups, C, dtype):
+    for k, (center, shared, gate, bias) in enumerate([(True, True, True, True), (False, False, True, False), (True, False, False, False)]):
+        s = make(rows, groups, C, dtype, shared=shared, gate=gate, bias=bias, seed=k)
+        check(call(s, groups, center), definition(s, groups, center), rows * (groups if shared else 1), C)
+
+
 @pytest.mark.parametrize("weight,bias", [(False, False), (True, False), (False, True)])
 def test_absent_parameters_and_mixed_types(weight, bias):
     for dtype, wdt in ((torch.bfloat16, torch.float32), (torch.float32, torch.bfloat16)):
