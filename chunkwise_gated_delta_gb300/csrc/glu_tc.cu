@@ -207,8 +207,34 @@ template <class T> __device__ __forceinline__ void store_rows(T *first, long lon
 #pragma unroll
     for (int k = 0; k < 32; ++k) turn[lane][k] = v[k];
     __syncwarp();
-    for (int r = 0; r < rows; ++r, first += ld)
-        if (lane < inside) put(first + lane, turn[r][lane]);
+    if constexpr (sizeof(T) == 2)
+        if ((inside >= 32 || inside % 2 == 0) && ((reinterpret_cast<uintptr_t>(first) | (uintptr_t)ld * 2) & 3) == 0) {   // pairs, two rows at a time
+            const int c = lane % 16 * 2;
+            first += lane / 16 * ld + c;
+#pragma unroll 1
+            for (int r0 = 0; r0 < 32; r0 += 8) {
+                uint32_t q[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float *from = turn[r0 + 2 * k + lane / 16] + c;
+                    q[k] = pack_bf16(from[0], from[1]);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k, first += 2 * ld)
+                    if (r0 + 2 * k + lane / 16 < rows && c < inside) *reinterpret_cast<uint32_t *>(first) = q[k];
+            }
+            return;
+        }
+    first += lane;
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += 8) {
+        float q[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) q[k] = turn[r0 + k][lane];
+#pragma unroll
+        for (int k = 0; k < 8; ++k, first += ld)
+            if (r0 + k < rows && lane < inside) put(first, q[k]);
+    }
 }
 __device__ __forceinline__ bool wide_rows(const void *p, long long ld, int es) {
     return (reinterpret_cast<uintptr_t>(p) & 31) == 0 && ld * es % 32 == 0;

@@ -65,6 +65,15 @@ def test_sizes(M, D, F, dtype):
     check(call(s, save=False), want, dtype, M, D, F)
 
 
+@pytest.mark.parametrize("M,D,F", [(130, 70, 518), (20, 266, 1030), (301, 1182, 98), (3, 34, 2), (1027, 130, 66)])
+def test_even_widths_in_bfloat16(M, D, F):
+    """Rows of whole pairs, but not of 16 bytes: operands that move and outputs that leave by pairs."""
+    s = make(M, D, F, torch.bfloat16)
+    want = definition(s, "silu")
+    check(call(s), want, torch.bfloat16, M, D, F)
+    check(call(s, save=False), want, torch.bfloat16, M, D, F)
+
+
 @pytest.mark.parametrize("M,D,F", [(2142, 16, 8320), (1500, 1411, 130), (700, 3000, 2051)])
 def test_many_tiles_in_float32(M, D, F):
     s = make(M, D, F, torch.float32)
@@ -83,7 +92,7 @@ def test_gelu(M, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
-@pytest.mark.parametrize("M,shift,pad", [(6, 0, 8), (6, 1, 9), (150, 0, 8), (150, 1, 9), (150, 0, 1)])
+@pytest.mark.parametrize("M,shift,pad", [(6, 0, 8), (6, 1, 9), (150, 0, 8), (150, 1, 9), (150, 0, 1), (6, 2, 10), (150, 2, 10), (50, 4, 14)])
 def test_strides(M, shift, pad, dtype):
     """Inputs and outputs inside wider buffers, from aligned columns and from odd ones; three axes."""
     D, F = 136, 264
