@@ -50,7 +50,7 @@ template <bool BACK> __device__ __forceinline__ Where where(const GatedScanParam
     w.c = c0 + w.lane * 2;
     w.on = w.c < p.D;
     w.cl = w.on ? w.c : c0;
-    w.k = extent_of(p);
+    w.k = extent_of(p.cu_seqlens, p.B, p.T);
     return w;
 }
 
@@ -99,7 +99,7 @@ template <class T, int CP, int N, bool BACK> struct Ring {
             } else {
 #pragma unroll
                 for (int n = 0; n < N; ++n)
-                    S::bring_clamped(base + to + n * S::BYTES, at[n] - (next + S::row()) * ld[n], ld[n], left, next, k.lo, k.hi);
+                    S::bring_clamped(base + to + n * S::BYTES, at[n] - (next + S::row()) * ld[n], ld[n], left, next, k);
             }
 #pragma unroll
             for (int n = 0; n < N; ++n) at[n] += (BACK ? -ROWS : ROWS) * ld[n];
@@ -193,7 +193,7 @@ template <class T, int CP, bool WALK> __global__ void __launch_bounds__(THREADS,
     const Where w = where<WALK>(p);
     kda::tc::grid_dep_launch();
     if (!w.any) return;
-    const bool some = w.r0 < w.k.hi && w.r0 + p.seg > w.k.lo;
+    const bool some = covers(w.k, w.r0, p.seg);
     Ring<T, CP, 3, false> ring;
     if (some) ring.begin(rings, p, w, {p.x, p.decay, p.gate}, {p.ld_x, p.ld_decay, p.ld_gate});      // (the inputs wait for no pass)
     const f2 coef = coefficients(p, w.cl);
@@ -218,8 +218,8 @@ template <bool BACK> __global__ void __launch_bounds__(32 * BWARPS) gated_scan_b
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, D = p.D, pitch = (D + 1) & ~1;
     const int c = min((int)blockIdx.x * 32 + lane, D - 1);               // (lanes past the end repeat the last channel)
     const int segs = (int)((rows_of(p) + p.seg - 1) / p.seg);
-    const Extent k = extent_of(p);
-    const int s0 = k.lo / p.seg, s1 = min(segs, (int)(((long long)k.hi + p.seg - 1) / p.seg)), n = s1 - s0;
+    const Extent k = extent_of(p.cu_seqlens, p.B, p.T);
+    const int s0 = k.lo / p.seg, s1 = min(segs, (int)(((long long)k.hi + p.seg - 1) / p.seg)), n = k.lo < k.hi ? s1 - s0 : 0;
     kda::tc::grid_dep_launch();
     kda::tc::grid_dep_wait();
     float carry = 0.f;
@@ -308,7 +308,7 @@ template <class T, int CP> __global__ void __launch_bounds__(THREADS, sizeof(T) 
     extern __shared__ __align__(16) char rings[];        // [WARPS][Ring::BYTES]
     const Where w = where<false>(p);
     kda::tc::grid_dep_launch();
-    if (!w.any || w.r0 >= w.k.hi || w.r0 + p.seg <= w.k.lo) return;
+    if (!w.any || !covers(w.k, w.r0, p.seg)) return;
     Ring<T, CP, 2, true> ring;
     ring.begin(rings, p, w, {p.decay, p.dy}, {p.ld_decay, p.ld_dy});
     const f2 coef = coefficients(p, w.cl);
@@ -406,7 +406,7 @@ template <class T, int CP> __global__ void __launch_bounds__(THREADS, sizeof(T) 
     const Where w = where<false>(p);
     kda::tc::grid_dep_launch();
     if (!w.any) return;
-    const bool some = w.r0 < w.k.hi && w.r0 + p.seg > w.k.lo;
+    const bool some = covers(w.k, w.r0, p.seg);
     Ring<T, CP, 4, true> ring;
     if (some) ring.begin(rings, p, w, {p.x, p.decay, p.gate, p.dy}, {p.ld_x, p.ld_decay, p.ld_gate, p.ld_dy});   // (the inputs wait for no pass)
     kda::tc::grid_dep_wait();

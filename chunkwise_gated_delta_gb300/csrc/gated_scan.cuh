@@ -38,15 +38,14 @@ template <class T, int CP> struct Stage {
             for (int part = 0; part < PARTS; ++part)
                 if (part * 32 * E < left) one(to + k * STEP * ROW + part * 32 * CP, at + part * 32 * E);
     }
-    static __device__ __forceinline__ void bring_clamped(char *to, const T *from, long long ld, int left, long long r0, int lo, int hi) {
+    static __device__ __forceinline__ void bring_clamped(char *to, const T *from, long long ld, int left, long long r0, const Extent &k) {
         to += row() * ROW + col() * (int)sizeof(T);
 #pragma unroll 1
-        for (int k = 0; k < ROWS / STEP; ++k) {
-            const long long r = r0 + row() + k * STEP;
-            const T *at = from + (r < lo ? lo : r >= hi ? hi - 1 : r) * ld;
+        for (int i = 0; i < ROWS / STEP; ++i) {
+            const T *at = from + nearest_row(k, r0 + row() + i * STEP) * ld;
 #pragma unroll
             for (int part = 0; part < PARTS; ++part)
-                if (part * 32 * E < left) one(to + k * STEP * ROW + part * 32 * CP, at + part * 32 * E);
+                if (part * 32 * E < left) one(to + i * STEP * ROW + part * 32 * CP, at + part * 32 * E);
         }
     }
     static __device__ __forceinline__ void one(char *to, const T *from) {
@@ -123,16 +122,6 @@ __device__ __forceinline__ f2 sqrt2(f2 v) {
     float lo, hi;
     unpack2(v, lo, hi);
     return pack2(sqrt_fast(lo), sqrt_fast(hi));
-}
-
-// The rows that the sequences of a call cover: one axis, which is cut where a sequence begins.
-struct Extent {
-    int lo, hi;
-};
-__device__ __forceinline__ Extent extent_of(const GatedScanParams &p) {
-    if (!p.cu_seqlens) return {0, (int)((long long)p.B * p.T)};
-    const int lo = clamped(p.cu_seqlens[0], 0, p.T);
-    return {lo, clamped(p.cu_seqlens[p.B], lo, p.T)};
 }
 
 // Where sequences begin and end among the rows from r0 that a warp holds (bit j: row r0 + j), and the

@@ -67,6 +67,20 @@ __host__ __device__ inline long long slot_at(const int32_t *cu, int T, int seg, 
     return (cu ? first_slot(cu, T, seg, b) : b * ((T + (long long)seg - 1) / seg)) + t0 / seg;
 }
 
+// The rows that the sequences of a call cover, for kernels that cut them in segments whatever the sequences' lengths.
+struct Extent {
+    int lo, hi;
+};
+__host__ __device__ inline Extent extent_of(const int32_t *cu, int B, int T) {
+    if (!cu) return {0, (int)((long long)B * T)};
+    const int lo = clamped(cu[0], 0, T);
+    return {lo, clamped(cu[B], lo, T)};
+}
+// Whether any of the rows r0 .. r0 + n - 1 is covered.  (No row is where all sequences are empty, wherever they lie.)
+__host__ __device__ inline bool covers(const Extent &k, long long r0, int n) { return k.lo < k.hi && r0 < k.hi && r0 + n > k.lo; }
+// The covered row nearest to r, of an extent that covers some.
+__host__ __device__ inline long long nearest_row(const Extent &k, long long r) { return r < k.lo ? k.lo : r >= k.hi ? k.hi - 1 : r; }
+
 // A kernel that walks `len` tokens in tiles counts tokens past the end too: the last tile's, and those of the
 // tiles that it looks ahead.  Lengths reach 2^31 - 1, so these positions have no sign.
 __host__ __device__ inline int tiles_of(int len, int tile) { return (int)(((unsigned)len + tile - 1) / tile); }

@@ -261,3 +261,22 @@ def test_equal_calls_other_streams_and_graphs():
     torch.cuda.synchronize()
     fresh = call(s, (2, 300, 192))
     assert all(torch.equal(got[k], fresh[k]) for k in got) and not torch.equal(got["y"], want["y"])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("T,D,cu", [(5, 40, [5, 5]), (150, 33, [150, 150, 150]), (150, 64, [151, 400]), (300, 70, [300, 300]), (300, 70, [77, 77, 77])])
+def test_none_but_empty_sequences_anywhere(T, D, cu, dtype):
+    """States and their gradients pass through, no row is written, the sum of drate is 0; what the uncovered rows hold does not matter."""
+    n = len(cu) - 1
+    s = make(T, n, D, dtype)
+    for k in ("x", "decay", "gate", "dy"):
+        s[k][:] = float("nan")
+    off = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    v = {k: t.view(1, T, D) if k in ("x", "decay", "gate", "dy") else t for k, t in s.items()}
+    args = (v["x"], v["decay"], v["gate"], v["rate"], v["h0"])
+    buf = {k: torch.full((1, T, D), 7.0, device=DEV, dtype=dtype) for k in ("y", "dx", "ddecay", "dgate")}
+    _, ht, states = lib.gated_scan_fwd(*args, scale=SCALE, y=buf["y"], save_states=True, cu_seqlens=off)
+    for kept in (states, None):
+        g = lib.gated_scan_bwd(*args, v["dy"], v["dht"], states=kept, scale=SCALE, cu_seqlens=off, grads={k: buf[k] for k in ("dx", "ddecay", "dgate")})
+        assert torch.equal(ht, s["h0"]) and torch.equal(g["dh0"], s["dht"]) and not bool(g["drate"].any())
+        assert all(bool((t == 7).all()) for t in buf.values())

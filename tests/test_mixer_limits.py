@@ -44,6 +44,16 @@ def test_positions_past_the_longest_length(tmp_path):
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
 
 
+def test_rows_that_the_gated_recurrence_reads(tmp_path):
+    """None but covered rows, also where all packed sequences are empty and lie at the end."""
+    exe = tmp_path / "extent_check"
+    r = subprocess.run([_nvcc(), "-O1", "-std=c++17", "-I", kbuild.CSRC, os.path.join(kbuild.ROOT, "tests", "host", "extent_check.cu"),
+                        "-o", str(exe)], capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stderr[-2000:]
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
 # ------------------------------------------------------------------------------------ Python binding
 class _Stream:
     """Stands in for a CUDA stream."""
