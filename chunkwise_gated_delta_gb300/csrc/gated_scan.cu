@@ -54,9 +54,9 @@ template <bool BACK> __device__ __forceinline__ Where where(const GatedScanParam
     return w;
 }
 
-// The gates of a row: p = 1 - a, and m u x.
-template <bool SMALL_Q> __device__ __forceinline__ f2 decay_p(f2 coef, f2 d) { return one_less_exp_if<SMALL_Q>(mul2(coef, sigmoid2(d))); }
-__device__ __forceinline__ f2 input_v(f2 q, f2 a, f2 g, f2 x) { return mul2(mul2(sqrt2(rest_of(q, a)), sigmoid2(g)), x); }
+// The gates of a row: the decay's exponent, and m u x.
+__device__ __forceinline__ f2 exponent(f2 coef, f2 d) { return mul2(coef, sigmoid2(d)); }
+__device__ __forceinline__ f2 input_v(const Decay &d, f2 g, f2 x) { return mul2(mul2(sqrt2(rest_of(d)), sigmoid2(g)), x); }
 
 // Rows on their way: a ring of this warp's in shared memory, eight rows of N tensors per stage, STAGES - 1 of them in flight.
 // BACK: from the last rows to the first.
@@ -142,9 +142,9 @@ __device__ __forceinline__ void forward_rows(const GatedScanParams &p, const Whe
         f2 a[ROWS], v[ROWS];
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
-            const f2 q = decay_p<SMALL_Q>(coef, ring.pair(st, 1, j, lane));
-            a[j] = decay_of(q);
-            v[j] = input_v(q, a[j], ring.pair(st, 2, j, lane), ring.pair(st, 0, j, lane));
+            const Decay d = decay_at<SMALL_Q>(exponent(coef, ring.pair(st, 1, j, lane)));
+            a[j] = d.a;
+            v[j] = input_v(d, ring.pair(st, 2, j, lane), ring.pair(st, 0, j, lane));
         }
         marks.find(p, w.k, r0);
         const unsigned starts = marks.starts, ends = marks.ends;
@@ -275,7 +275,7 @@ __device__ __forceinline__ void backward_local(const GatedScanParams &p, const W
         f2 a[ROWS], gy[ROWS];
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
-            a[j] = decay_of(decay_p<SMALL_Q>(coef, ring.pair(st, 0, j, lane)));
+            a[j] = decay_at<SMALL_Q>(exponent(coef, ring.pair(st, 0, j, lane))).a;
             gy[j] = ring.pair(st, 1, j, lane);
         }
         marks.find(p, w.k, r0);
@@ -343,30 +343,32 @@ __device__ __forceinline__ f2 backward_rows(const GatedScanParams &p, const Wher
         const char *sd = sx + S::BYTES, *sg = sd + S::BYTES, *sy = sg + S::BYTES;
         marks.find(p, w.k, r0);
         const unsigned starts = marks.starts, ends = marks.ends;
-        f2 q[ROWS], before[ROWS];        // 1 - a; the state before each row
+        f2 q[ROWS], before[ROWS];        // the decay, kept in one number; the state before each row
         if (starts == 0) {
 #pragma unroll
             for (int j = 0; j < ROWS; ++j) {
-                q[j] = decay_p<SMALL_Q>(coef, S::pair(sd, j, lane));
+                q[j] = kept_decay<SMALL_Q>(exponent(coef, S::pair(sd, j, lane)));
                 before[j] = h;
                 if (j + 1 < ROWS) {
-                    const f2 a = decay_of(q[j]);
-                    h = fma2(a, h, input_v(q[j], a, S::pair(sg, j, lane), S::pair(sx, j, lane)));
+                    const Decay d = decay_of<SMALL_Q>(q[j]);
+                    h = fma2(d.a, h, input_v(d, S::pair(sg, j, lane), S::pair(sx, j, lane)));
                 }
             }
         } else {
 #pragma unroll
             for (int j = 0; j < ROWS; ++j) {
-                q[j] = decay_p<SMALL_Q>(coef, S::pair(sd, j, lane));
+                q[j] = kept_decay<SMALL_Q>(exponent(coef, S::pair(sd, j, lane)));
                 if (starts >> j & 1) h = p.h0 ? load_state(p.h0 + (long long)marks.sequence(j) * D, w.cl, D) : both(0.f);
                 before[j] = h;
-                const f2 a = decay_of(q[j]);
-                h = fma2(a, h, input_v(q[j], a, S::pair(sg, j, lane), S::pair(sx, j, lane)));
+                const Decay d = decay_of<SMALL_Q>(q[j]);
+                h = fma2(d.a, h, input_v(d, S::pair(sg, j, lane), S::pair(sx, j, lane)));
             }
         }
         // a row's outputs from G; leaves a G in grad
         auto row = [&](int j, f2 G, T *pd, T *px, T *pg) {
-            const f2 s = sigmoid2(S::pair(sd, j, lane)), u = sigmoid2(S::pair(sg, j, lane)), a = decay_of(q[j]), r = rest_of(q[j], a);
+            const f2 s = sigmoid2(S::pair(sd, j, lane)), u = sigmoid2(S::pair(sg, j, lane));
+            const Decay d = decay_of<SMALL_Q>(q[j]);
+            const f2 a = d.a, r = rest_of(d);
             float w0, w1;
             unpack2(r, w0, w1);          // 1 - a^2 of 0 (no decay at all): its root's reciprocal stays finite, so that times q = 0 it is 0
             const f2 rm = pack2(rsqrt_fast(fmaxf(w0, 1e-36f)), rsqrt_fast(fmaxf(w1, 1e-36f)));
@@ -447,8 +449,8 @@ template <class T, bool VEC> __global__ void __launch_bounds__(128) gated_scan_s
              g = load_pair(static_cast<const T *>(p.gate) + b * p.ld_gate, c, D);
     float *state = p.state + (long long)slot * D;
     const f2 old = load_state(state, c, D);
-    const f2 q = one_less_exp(mul2(coefficients(p, c), sigmoid2(d))), a = decay_of(q);
-    const f2 h = fma2(a, old, input_v(q, a, g, x));
+    const Decay q = decay_at<false>(exponent(coefficients(p, c), d));
+    const f2 h = fma2(q.a, old, input_v(q, g, x));
     store_state(state, c, D, h);
     store_pair<T, VEC>(y, c, D, h);
 }

@@ -3,9 +3,10 @@
 //   q = scale softplus(rate) sigmoid(decay),  a = exp(-q),  m = sqrt(1 - a^2),
 //   h_t = a_t h_{t-1} + m_t sigmoid(gate_t) x_t
 //
-// a is close to 1 for channels that remember long, and 1 - a^2 then loses its digits.  Both come from
-// p = 1 - exp(-q), a series where q < 1/4: a = 1 - p and 1 - a^2 = p (1 + a).  The difference 1 - p is
-// rounded without a bias, which a long product of decays would multiply.
+// a is close to 1 for channels that remember long, and 1 - a^2 then loses its digits.  Where q < 1/4 both come from
+// p = 1 - exp(-q), a series: a = 1 - p and 1 - a^2 = p (1 + a).  The difference 1 - p is rounded without a bias, which a
+// long product of decays would multiply.  From 1/4 on a = exp(-q) is what has the digits, and p = 1 - a: gradients are products with
+// a, and 1 - p would leave an error of 2^-25 where a may be 2^-25 itself (q = 17).
 #pragma once
 
 #include "mixer.h"
@@ -87,7 +88,11 @@ __device__ __forceinline__ f2 coefficients(const GatedScanParams &p, int c) {
     return pack2(p.scale * softplus_of(p.rate[c]), p.scale * softplus_of(p.rate[min(c + 1, p.D - 1)]));
 }
 
-// p = 1 - exp(-q) for 0 <= q < 1/4: six terms of the series, the seventh is below 5e-8 of the first; and for any q >= 0.
+// A row's decay a, and p = 1 - a.
+struct Decay {
+    f2 p, a;
+};
+// p for 0 <= q < 1/4: six terms of the series, the seventh is below 5e-8 of the first.
 constexpr float SMALL = 0.25f;
 __device__ __forceinline__ f2 one_less_exp_small(f2 q) {
     f2 s = fma2(q, both(-1.f / 720.f), both(1.f / 120.f));
@@ -97,14 +102,42 @@ __device__ __forceinline__ f2 one_less_exp_small(f2 q) {
     s = fma2(s, q, both(1.f));
     return mul2(s, q);
 }
-__device__ __forceinline__ f2 one_less_exp(f2 q) {
+__device__ __forceinline__ f2 one_less(f2 v) { return fma2(v, both(-1.f), both(1.f)); }
+// From one number per channel, which is what a pass keeps that takes a row's decay twice: p, or -a (a sign bit, also of 0) from 1/4 on.
+// ALL_SMALL: no channel's exponent reaches 1/4.
+template <bool ALL_SMALL> __device__ __forceinline__ f2 kept_decay(f2 q) {
+    const f2 s = one_less_exp_small(q);
+    if constexpr (ALL_SMALL) return s;
     float s0, s1, q0, q1, e0, e1;
-    unpack2(one_less_exp_small(q), s0, s1);
+    unpack2(s, s0, s1);
     unpack2(q, q0, q1);
     unpack2(mul2(q, both(-kLog2e)), e0, e1);
-    return pack2(q0 < SMALL ? s0 : 1.f - ex2(e0), q1 < SMALL ? s1 : 1.f - ex2(e1));
+    return pack2(q0 < SMALL ? s0 : -ex2(e0), q1 < SMALL ? s1 : -ex2(e1));
 }
-template <bool ALL_SMALL> __device__ __forceinline__ f2 one_less_exp_if(f2 q) { return ALL_SMALL ? one_less_exp_small(q) : one_less_exp(q); }
+template <bool ALL_SMALL> __device__ __forceinline__ Decay decay_of(f2 kept) {
+    if constexpr (ALL_SMALL) return {kept, one_less(kept)};
+    float k0, k1;
+    unpack2(kept, k0, k1);
+    const float t0 = fabsf(k0), t1 = fabsf(k1), o0 = 1.f - t0, o1 = 1.f - t1;
+    const bool n0 = __float_as_int(k0) < 0, n1 = __float_as_int(k1) < 0;
+    return {pack2(n0 ? o0 : t0, n1 ? o1 : t1), pack2(n0 ? t0 : o0, n1 ? t1 : o1)};
+}
+// Both at once, of exponents q >= 0.
+template <bool ALL_SMALL> __device__ __forceinline__ Decay decay_at(f2 q) {
+    const f2 s = one_less_exp_small(q);
+    if constexpr (ALL_SMALL) return {s, one_less(s)};
+    float s0, s1, o0, o1, q0, q1, e0, e1;
+    unpack2(s, s0, s1);
+    unpack2(one_less(s), o0, o1);
+    unpack2(q, q0, q1);
+    unpack2(mul2(q, both(-kLog2e)), e0, e1);
+    e0 = ex2(e0);
+    e1 = ex2(e1);
+    float c0, c1;
+    unpack2(one_less(pack2(e0, e1)), c0, c1);
+    const bool b0 = q0 < SMALL, b1 = q1 < SMALL;
+    return {pack2(b0 ? s0 : c0, b1 ? s1 : c1), pack2(b0 ? o0 : e0, b1 ? o1 : e1)};
+}
 __device__ __forceinline__ float sqrt_fast(float v) {
     float r;
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -115,9 +148,8 @@ __device__ __forceinline__ float rsqrt_fast(float v) {
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
-// From p: the decay a = 1 - p, and 1 - a^2 = p (1 + a).
-__device__ __forceinline__ f2 decay_of(f2 p) { return fma2(p, both(-1.f), both(1.f)); }
-__device__ __forceinline__ f2 rest_of(f2 p, f2 a) { return fma2(p, a, p); }
+// 1 - a^2 = p (1 + a).
+__device__ __forceinline__ f2 rest_of(const Decay &d) { return fma2(d.p, d.a, d.p); }
 __device__ __forceinline__ f2 sqrt2(f2 v) {
     float lo, hi;
     unpack2(v, lo, hi);

@@ -280,3 +280,66 @@ def test_none_but_empty_sequences_anywhere(T, D, cu, dtype):
         g = lib.gated_scan_bwd(*args, v["dy"], v["dht"], states=kept, scale=SCALE, cu_seqlens=off, grads={k: buf[k] for k in ("dx", "ddecay", "dgate")})
         assert torch.equal(ht, s["h0"]) and torch.equal(g["dh0"], s["dht"]) and not bool(g["drate"].any())
         assert all(bool((t == 7).all()) for t in buf.values())
+
+
+# Fast decays.  The exponent q = coefficient times sigmoid is off by at most 10 roundings of its size (sigmoid's exponential, sum and
+# reciprocal, softplus' two functions, the products with scale, coefficient and log2 e), so a = exp(-q) by 10 q roundings of its own
+# size and 4 of the exponential.  Rates reach 3 here: q <= 8 softplus(3) = 24.4.  The factor 1 - sigmoid(decay) of ddecay is
+# at least 1 - sigmoid(3) = 0.047, from a sigmoid off by 3 roundings: 64 more.  The rest of a gradient's factors: 12.
+FAST = (10 * 24.4 + 4 + 64 + 12) * 2.0 ** -24
+
+
+def make_fast(rows, n, D, dtype, seed=0):
+    """Rates from a memory of hundreds of tokens to one of less than a token, decays' gates open."""
+    s = make(rows, n, D, dtype, seed)
+    g = torch.Generator(device=DEV).manual_seed(seed + 1)
+    s["rate"] = torch.linspace(-5, 3, D, device=DEV)[torch.randperm(D, generator=g, device=DEV)]
+    s["decay"] = (2 + 0.5 * torch.randn(rows, D, generator=g, device=DEV)).clamp(max=3).to(dtype)
+    return s
+
+
+def by_channel(got, want):
+    """The largest relative error of a channel."""
+    d = (got.double().reshape(want.shape) - want).flatten(0, -2).norm(dim=0)
+    return float((d / want.flatten(0, -2).norm(dim=0)).max())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("lens,D,packed", [([256], 64, False), ([150, 150], 130, False), ([70, 0, 1, 200, 33], 67, True), ([40], 128, False)])
+def test_gradients_of_fast_decays_by_channel(lens, D, packed, dtype):
+    rows, n = sum(lens), len(lens)
+    s = make_fast(rows, n, D, dtype, seed=D)
+    cu = torch.tensor([0] + list(torch.tensor(lens).cumsum(0)), dtype=torch.int32, device=DEV) if packed else None
+    got = call(s, (1, rows, D) if packed else (n, rows // n, D), cu)
+    want = definition(s, spans_of(lens), True)
+    bound = FAST + STATE
+    for k in ("y", "dx", "ddecay", "dgate"):
+        assert by_channel(got[k], want[k]) <= bound + (half_step(dtype) if dtype != torch.float32 else 0), k
+    # ht = sum of v_t a_{t+1} .. a_T (and of h0 a_1 .. a_T), dh0 = sum of a_1 .. a_t dy_t (and dht): terms of both signs, where a channel may
+    # have one such sum that cancels, so each is relative to the sum of its terms' sizes, which the same recurrence gives for the
+    # sizes of x, h0, dy and dht (no decay or gate is negative).  A term of k decays is off by k (10 q + 4) roundings and e^(-q k) of the
+    # whole, at most 10 q + 4 for fast decays; STATE has the slow ones.
+    size = definition({**s, **{k: s[k].abs() for k in ("x", "h0", "dy", "dht")}}, spans_of(lens), True)
+    for k in ("ht", "dh0"):
+        assert float(((got[k].double() - want[k]).abs() / size[k]).max()) <= bound, k
+    # drate sums terms of both signs: relative to their sizes, scale sigmoid(rate) |ddecay| s / (q (1 - s))
+    sg, rate = torch.sigmoid(s["decay"].double()), s["rate"].double()
+    size = (want["ddecay"].abs() / (torch.nn.functional.softplus(rate) * (1 - sg)) * torch.sigmoid(rate)).sum(0)
+    assert float(((got["drate"].double() - want["drate"]).abs() / size).max()) <= bound
+
+
+def test_states_of_fast_decays_by_element():
+    """With nothing let in, a state is the product of its decays: each as exact as its exponent."""
+    T, D = 5, 66
+    s = make_fast(T, 1, D, torch.float32)
+    s["gate"][:] = -float("inf")
+    s["h0"] = torch.full((1, D), 1e7, device=DEV)
+    y, ht = lib.gated_scan_fwd(*(s[k].view(1, T, D) for k in ("x", "decay", "gate")), s["rate"], s["h0"], scale=SCALE)
+    want = definition(s, [(0, T)])["y"]
+    some = want > 1e-30                      # (below, float32 has no digits to lose)
+    t = torch.arange(1, T + 1, device=DEV, dtype=torch.float64)[:, None].expand(T, D)
+    off = ((y[0].double() - want).abs() / want)[some]
+    assert bool((off <= t[some] * (10 * 24.4 + 5) * 2.0 ** -24).all()) and torch.equal(ht[0], y[0, -1])
+    state = s["h0"].clone()
+    y1 = lib.gated_scan_step(s["x"][:1], s["decay"][:1], s["gate"][:1], s["rate"], state, scale=SCALE)
+    assert float(((y1.double() - want[:1]).abs() / want[:1]).max()) <= (10 * 24.4 + 5) * 2.0 ** -24 and torch.equal(state, y1)
