@@ -121,10 +121,15 @@ template <class T, int CP, int N, bool BACK> struct Ring {
 
 // ------------------------------------------------------------------------------------------ forward
 // A segment's effect is kept as A >= 0 and h; A = -1 says that the link is cut and h alone counts.  (A, h) of a pair of channels
-// lie together, rows of pairs are as wide as D rounded up to even.
-__device__ __forceinline__ void store_segment(const GatedScanParams &p, const Where &w, f2 a, f2 h) {
+// lie together, rows of pairs are as wide as D rounded up to even.  A product of positive decays that underflows is kept at the smallest
+// normal number: an infinity that enters then leaves as one, not as 0 times infinity.  (Of a finite state that is 2^-126 of itself, where
+// a test for infinities in the chain of segments would take 2 us of the 51 of the long prompt.)
+constexpr float LEAST = 1.17549435e-38f;
+__device__ __forceinline__ void store_segment(const GatedScanParams &p, const Where &w, f2 a, f2 h, bool cut) {
     float4 q;
     unpack2(a, q.x, q.z);
+    q.x = cut ? -1.f : fmaxf(q.x, LEAST);
+    q.z = cut ? -1.f : fmaxf(q.z, LEAST);
     unpack2(h, q.y, q.w);
     reinterpret_cast<float4 *>(p.seg_pair)[(w.seg * ((p.D + 1) & ~1) + w.c) / 2] = q;
 }
@@ -184,7 +189,7 @@ __device__ __forceinline__ void forward_rows(const GatedScanParams &p, const Whe
         }
     }
     if (!WALK && w.on) {
-        store_segment(p, w, cut ? both(-1.f) : prod, h);
+        store_segment(p, w, prod, h, cut);
     }
 }
 
@@ -239,7 +244,7 @@ template <bool BACK> __global__ void __launch_bounds__(32 * BWARPS) gated_scan_b
             pa *= g[j].x;
         }
         __syncthreads();                             // the last round's pairs have been read
-        sm[warp][lane] = make_float2(cut ? -1.f : pa, ph);
+        sm[warp][lane] = make_float2(cut ? -1.f : fmaxf(pa, LEAST), ph);
         __syncthreads();
         float in = carry;
 #pragma unroll
@@ -301,7 +306,7 @@ __device__ __forceinline__ void backward_local(const GatedScanParams &p, const W
         }
     }
     if (w.on) {
-        store_segment(p, w, cut ? both(-1.f) : prod, g);
+        store_segment(p, w, prod, g, cut);
     }
 }
 template <class T, int CP> __global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 6 : 4) gated_scan_bwd_local_kernel(GatedScanParams p) {

@@ -343,3 +343,26 @@ def test_states_of_fast_decays_by_element():
     state = s["h0"].clone()
     y1 = lib.gated_scan_step(s["x"][:1], s["decay"][:1], s["gate"][:1], s["rate"], state, scale=SCALE)
     assert float(((y1.double() - want[:1]).abs() / want[:1]).max()) <= (10 * 24.4 + 5) * 2.0 ** -24 and torch.equal(state, y1)
+
+
+@pytest.mark.parametrize("lens", [[300], [200, 0, 250]])
+def test_an_infinite_state_stays_infinite(lens):
+    """Products of a segment's decays underflow where each of them is positive: an infinity that enters is one that leaves, with its sign,
+    and so are the gradients that an infinite one of the final state has."""
+    D, n, rows = 40, len(lens), sum(lens)
+    s = make(rows, n, D, torch.float32, seed=4)
+    s["rate"][:] = 0.0
+    cu = torch.tensor([0] + list(torch.tensor(lens).cumsum(0)), dtype=torch.int32, device=DEV)
+    clean = call(s, (1, rows, D), cu)
+    inf = float("inf")
+    s["h0"][0, 5], s["h0"][0, 9], s["dht"][0, 7], s["dht"][0, 11] = inf, -inf, inf, -inf
+    got = call(s, (1, rows, D), cu)
+    first = lens[0]
+    for c, sign in ((5, 1), (9, -1)):
+        assert bool((got["y"][0, :first, c] == sign * inf).all()) and float(got["ht"][0, c]) == sign * inf
+    for c, sign in ((7, 1), (11, -1)):
+        assert bool((got["dx"][0, :first, c] == sign * inf).all()) and float(got["dh0"][0, c]) == sign * inf
+    keep = torch.ones(rows, D, dtype=torch.bool, device=DEV)
+    keep[:first, [5, 7, 9, 11]] = False
+    for k in ("y", "dx", "ddecay", "dgate"):
+        assert torch.equal(got[k][0][keep], clean[k][0][keep]), k
