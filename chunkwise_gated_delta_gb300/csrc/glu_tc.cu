@@ -407,11 +407,11 @@ template <bool PAIR, Mode MODE> __global__ void __launch_bounds__(THREADS, 1) gl
     } else {
         const int quarter = warp & 3;                    // the lanes of TMEM that this warp may read
         unsigned n = 0;
+        int ok = 1;                                      // until a tile was not finished: none after it is, and its buffer's phase stands still
         for (int i = worker; i < t.tiles; i += workers, ++n) {
             const Tile q = tile_of(t, i);
             const int buf = n & 1;
-            int ok = 1;
-            if (lane == 0) ok = wait(&sh.acc_full[buf], n / 2 & 1);
+            if (ok && lane == 0) ok = wait(&sh.acc_full[buf], n / 2 & 1);
             ok = __shfl_sync(~0u, ok, 0);
             tc_fence_after();
             const long long row0 = (long long)q.m * C::ROWS + rank * HALF + quarter * 32;

@@ -194,3 +194,23 @@ def test_workspaces_need_no_more_than_16_bytes():
     a.workspace, a.workspace_bytes = ws.data_ptr() + 16, n
     assert _lib.load().glu_bwd(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == 0
     check(out, want, torch.bfloat16, M, D, F)
+
+
+@pytest.mark.parametrize("M,D,F", [(4096, 64, 8192), (4096, 4096, 2048), (100, 64, 70000)])
+def test_a_wait_that_runs_out_with_many_tiles_to_a_worker(M, D, F):
+    """Whatever was not finished is NaN: every element of every output is, or it is what an undisturbed call gives."""
+    s = make(M, D, F, torch.bfloat16)
+    want = call(s)
+    status = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    status.view(torch.int32)[7] = 1
+    same = lambda a, b: bool((torch.isnan(a) | (a == b)).all())  # noqa: E731
+    for _ in range(3):
+        h, g, u = lib.glu_fwd(s["x"], s["wg"], s["wu"], save=True, status=status)
+        assert lib.status_read(status) == _lib.KDA_ERR_TIMEOUT
+        for k, v in dict(h=h, g=g, u=u).items():
+            assert same(v, want[k]) and bool(torch.isnan(v).any()), k
+        for kept in ((want["g"], want["u"]), (None, None)):
+            out = lib.glu_bwd(s["x"], s["wg"], s["wu"], s["dh"], *kept, status=status)
+            assert lib.status_read(status) == _lib.KDA_ERR_TIMEOUT
+            for k, v in out.items():
+                assert same(v, want[k]), k
