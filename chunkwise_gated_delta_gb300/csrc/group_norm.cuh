@@ -52,20 +52,20 @@ template <int L> struct Sums {
     }
 };
 
-// Where a thread works: groups count in slots of L lanes, `per` (a power of two) of them to a row.
+// Where a thread works: groups count in slots of L lanes, `per` (a power of two) of them to a row.  `part`: which `per` groups.
 struct Place {
     int group, row, rows;       // group, first row and rows of a block's visit
     bool on;
 };
-template <int L> __device__ __forceinline__ Place place_of(const GroupNormParams &p, int per) {
+template <int L> __device__ __forceinline__ Place place_of(const GroupNormParams &p, int per, unsigned part) {
     constexpr int SLOTS = TPB / L;
     const int slot = threadIdx.x / L;
     Place q;
-    q.group = (int)blockIdx.y * per + slot % per;
+    const unsigned group = part * per + slot % per;          // (without a sign: slots past 2^31 - 1 groups do not wrap)
     q.row = slot / per;
     q.rows = SLOTS / per;
-    q.on = q.group < p.G;
-    if (!q.on) q.group = p.G - 1;
+    q.on = group < (unsigned)p.G;
+    q.group = q.on ? (int)group : p.G - 1;
     return q;
 }
 int slots_per_row(int G, int slots) {
@@ -95,9 +95,9 @@ template <class T, int V, int ITEMS, int N> struct Ahead {
 };
 
 template <class T, int V, int ITEMS, int L, bool GATE>
-__global__ void __launch_bounds__(TPB) group_norm_fwd_kernel(GroupNormParams p, int per) {
+__global__ void __launch_bounds__(TPB) group_norm_fwd_kernel(GroupNormParams p, int per, unsigned first) {
     constexpr int P = (V + 1) / 2;
-    const Place q = place_of<L>(p, per);
+    const Place q = place_of<L>(p, per, first + blockIdx.y);
     const int lane = threadIdx.x % L, nv = p.C / V;
     const float inv = 1.f / (float)p.C;
     const long long col = (long long)q.group * p.C;
@@ -202,9 +202,9 @@ __global__ void __launch_bounds__(TPB) group_norm_fwd_kernel(GroupNormParams p, 
 
 // BIAS: the call has a bias or wants its gradient.
 template <class T, int V, int ITEMS, int L, bool GATE, bool BIAS>
-__global__ void __launch_bounds__(TPB, ITEMS == 1 ? (V == 1 ? 4 : 2) : V == 1 && ITEMS < 8 ? 2 : 1) group_norm_bwd_kernel(GroupNormParams p, int per) {
+__global__ void __launch_bounds__(TPB, ITEMS == 1 ? (V == 1 ? 4 : 2) : V == 1 && ITEMS < 8 ? 2 : 1) group_norm_bwd_kernel(GroupNormParams p, int per, unsigned first) {
     constexpr int P = (V + 1) / 2, SLOTS = TPB / L;
-    const Place q = place_of<L>(p, per);
+    const Place q = place_of<L>(p, per, first + blockIdx.y);
     const int lane = threadIdx.x % L, nv = p.C / V;
     const float inv = 1.f / (float)p.C;
     const long long col = (long long)q.group * p.C;
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(TPB, ITEMS == 1 ? (V == 1 ? 4 : 2) : V == 1 &&
     auto sums = reinterpret_cast<float (*)[L][2 * V]>(sm);     // [SLOTS]
     const int keys = p.shared ? 1 : per, key = threadIdx.x / L, cols = p.shared ? p.C : p.G * p.C;
     const long long rowp = p.shared ? (long long)blockIdx.y * gridDim.x + blockIdx.x : blockIdx.x;
-    const int kg = (int)blockIdx.y * per + key;              // (unshared: the key's group)
+    const unsigned kg = (first + blockIdx.y) * per + key;    // (unshared: the key's group)
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
         __syncthreads();
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(TPB, ITEMS == 1 ? (V == 1 ? 4 : 2) : V == 1 &&
             sums[threadIdx.x / L][lane][V + e] = e & 1 ? hi : lo;
         }
         __syncthreads();
-        if (key < keys && (p.shared || kg < p.G) && lane + k * L < nv) {
+        if (key < keys && (p.shared || kg < (unsigned)p.G) && lane + k * L < nv) {
             float t[2 * V];
 #pragma unroll
             for (int e = 0; e < 2 * V; ++e) t[e] = 0.f;
@@ -327,6 +327,12 @@ __global__ void __launch_bounds__(TPB, ITEMS == 1 ? (V == 1 ? 4 : 2) : V == 1 &&
 #pragma unroll
                 for (int e = 0; e < 2 * V; ++e) t[e] += sums[s][lane][e];
             float *out = p.part + rowp * 2 * cols + (p.shared ? 0 : (long long)kg * p.C) + at[k];
+            if (p.shared && first)                           // the sums of the launch before, of other groups
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    t[e] += out[e];
+                    t[V + e] += out[cols + e];
+                }
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 out[e] = t[e];
@@ -421,25 +427,39 @@ template <class T> __global__ void __launch_bounds__(512) group_norm_bwd_long_ke
     }
 }
 
-// The sums over rows for these: a thread per column of the weight, a part of the rows per block.
-template <class T> __global__ void __launch_bounds__(256) group_norm_sums_kernel(GroupNormParams p) {
+// The sums over rows for these: a thread per column of the weight, a part of the rows (of few rows whose groups share a weight: of the
+// groups too) per block.  Sums of up to 256 terms at a time, and of up to 256 of those, so that one of many like terms keeps growing by them.
+template <class T> __global__ void __launch_bounds__(256) group_norm_sums_kernel(GroupNormParams p, int row_parts, long long each_rows, int each_groups) {
     const long long cols = p.shared ? p.C : (long long)p.G * p.C, c = (long long)blockIdx.x * 256 + threadIdx.x;
     if (c >= cols) return;
-    const long long r0 = p.rows * blockIdx.y / gridDim.y, r1 = p.rows * (blockIdx.y + 1) / gridDim.y;
-    const int g0 = p.shared ? 0 : (int)(c / p.C), g1 = p.shared ? p.G : g0 + 1, in = (int)(p.shared ? c : c % p.C);
+    const int gpart = blockIdx.y / row_parts;
+    const long long r0 = (blockIdx.y % row_parts) * each_rows, r1 = min(r0 + each_rows, p.rows);
+    const int g0 = p.shared ? gpart * each_groups : (int)(c / p.C), g1 = p.shared ? min(g0 + each_groups, p.G) : g0 + 1;
+    const int in = (int)(p.shared ? c : c % p.C);
     const float w = p.weight ? load_w(p.weight, c, p.w_bf16) : 1.f, b = p.bias ? load_w(p.bias, c, p.w_bf16) : 0.f;
-    float aw = 0.f, ab = 0.f;
-    for (long long row = r0; row < r1; ++row)
-        for (int g = g0; g < g1; ++g) {
-            const long long k = (long long)g * p.C + in;
-            const float mean = p.mean ? p.mean[row * p.G + g] : 0.f;
-            const float xh = (to_f(static_cast<const T *>(p.x)[row * p.ld_x + k]) - mean) * p.rstd[row * p.G + g];
-            float dz;
-            const float d = gated(p, to_f(static_cast<const T *>(p.dy)[row * p.ld_dy + k]), fmaf(xh, w, b),
-                                  static_cast<const T *>(p.gate) + row * p.ld_gate + k, dz);
-            aw = fmaf(d, xh, aw);
-            ab += d;
+    float aw = 0.f, ab = 0.f, mw = 0.f, mb = 0.f;
+    for (long long row = r0; row < r1; ++row) {
+        for (int from = g0; from < g1; from += 256) {
+            float sw = 0.f, sb = 0.f;
+            for (int g = from; g < min(from + 256, g1); ++g) {
+                const long long k = (long long)g * p.C + in;
+                const float mean = p.mean ? p.mean[row * p.G + g] : 0.f;
+                const float xh = (to_f(static_cast<const T *>(p.x)[row * p.ld_x + k]) - mean) * p.rstd[row * p.G + g];
+                float dz;
+                const float d = gated(p, to_f(static_cast<const T *>(p.dy)[row * p.ld_dy + k]), fmaf(xh, w, b),
+                                      static_cast<const T *>(p.gate) + row * p.ld_gate + k, dz);
+                sw = fmaf(d, xh, sw);
+                sb += d;
+            }
+            mw += sw;
+            mb += sb;
         }
+        if (row % 256 == 255 || row + 1 == r1 || g1 - g0 > 256) {
+            aw += mw;
+            ab += mb;
+            mw = mb = 0.f;
+        }
+    }
     p.part[blockIdx.y * 2 * cols + c] = aw;
     p.part[blockIdx.y * 2 * cols + cols + c] = ab;
 }
@@ -448,9 +468,12 @@ template <class T> __global__ void __launch_bounds__(256) group_norm_sums_kernel
 struct Plan {
     int V, L, items;            // items 0: the long form
     int per;
-    unsigned gx, gy;
-    int parts;                  // rows of partial sums
+    unsigned gx, gy;            // blocks down the rows, and over the parts of the groups
+    int parts;                  // rows of partial sums (the long form: row_parts times parts of the groups)
+    int row_parts, each_groups;
+    long long each_rows;
 };
+constexpr unsigned GRID_Y = 65535;       // what a grid's second axis takes: more parts take several launches, whose sums add up
 Plan plan_of(const GroupNormParams &p, bool bf16_, bool bwd) {
     const size_t es = bf16_ ? 2 : 4;
     Plan q{};
@@ -469,16 +492,15 @@ Plan plan_of(const GroupNormParams &p, bool bf16_, bool bwd) {
     const int sms = sm_count();
     if (q.items > (q.V == 8 ? 4 : 8)) {       // (eight vectors of eight and their sums do not fit the registers)
         q.items = 0;
-        q.parts = (int)(p.rows < 64 ? p.rows : 64);
+        q.each_rows = (p.rows + 63) / 64;
+        q.row_parts = (int)((p.rows + q.each_rows - 1) / q.each_rows);
+        const int most = p.shared ? 64 / q.row_parts : 1;
+        q.each_groups = (p.G - 1) / most + 1;
+        q.parts = q.row_parts * (p.shared ? (p.G - 1) / q.each_groups + 1 : 1);
         return q;
     }
     q.per = slots_per_row(p.G, TPB / q.L);
     q.gy = (unsigned)((p.G - 1) / q.per + 1);
-    if (q.gy > 65535) {                       // (a grid's second axis: more than four million groups go one by one)
-        q.items = 0;
-        q.parts = (int)(p.rows < 64 ? p.rows : 64);
-        return q;
-    }
     const int rows = TPB / q.L / q.per;                      // rows of a block's visit
     const long long visits = (p.rows + rows - 1) / rows;
     // Blocks to an SM.  Vectors: as few as keep enough rows on their way (16384 x 16 x 128 bfloat16, L2 flushed: two take 41 us forward
@@ -489,15 +511,19 @@ Plan plan_of(const GroupNormParams &p, bool bf16_, bool bwd) {
     long long gx = (long long)sms * held / q.gy;
     if (gx < 1) gx = 1;
     q.gx = (unsigned)(visits < gx ? visits : gx);
-    q.parts = (int)(p.shared ? q.gx * q.gy : q.gx);
+    q.parts = (int)(p.shared ? q.gx * (q.gy < GRID_Y ? q.gy : GRID_Y) : q.gx);
     return q;
 }
 
 template <auto KERNEL> cudaError_t launch(const GroupNormParams &p, const Plan &q, size_t smem, cudaStream_t s) {
     const cudaError_t e = allow_shared<KERNEL>(smem);
     if (e != cudaSuccess) return e;
-    KERNEL<<<dim3(q.gx, q.gy), TPB, smem, s>>>(p, q.per);
-    return cudaGetLastError();
+    for (unsigned first = 0; first < q.gy; first += GRID_Y) {
+        KERNEL<<<dim3(q.gx, q.gy - first < GRID_Y ? q.gy - first : GRID_Y), TPB, smem, s>>>(p, q.per, first);
+        const cudaError_t l = cudaGetLastError();
+        if (l != cudaSuccess) return l;
+    }
+    return cudaSuccess;
 }
 template <class T, int V, int ITEMS, int L, bool GATE, bool BIAS> cudaError_t run_bwd(const GroupNormParams &p, const Plan &q, cudaStream_t s) {
     using A = Ahead<T, V, ITEMS, GATE ? 3 : 2>;
@@ -541,7 +567,7 @@ template <class T> cudaError_t run_t(const GroupNormParams &p, const Plan &q, bo
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !p.part) return e;
     const long long cols = p.shared ? p.C : (long long)p.G * p.C;
-    group_norm_sums_kernel<T><<<dim3((unsigned)((cols + 255) / 256), q.parts), 256, 0, s>>>(p);
+    group_norm_sums_kernel<T><<<dim3((unsigned)((cols + 255) / 256), q.parts), 256, 0, s>>>(p, q.row_parts, q.each_rows, q.each_groups);
     return cudaGetLastError();
 }
 

@@ -171,3 +171,27 @@ def test_more_groups_than_a_grid_has_rows():
     groups, C = 4_200_000, 3
     s = make(1, groups, C, torch.float32, shared=True)
     check(call(s, groups, True), definition(s, groups, True), groups, C)
+
+
+@pytest.mark.parametrize("groups,C", [(4_200_000, 3), (70_000, 1023), (66_000, 2049)])
+def test_sums_of_one_sign_over_many_groups(groups, C):
+    """One weight for more groups than a grid's second axis has places, every term of dbias the same: a single float32 sum of them would
+    stop growing in steps of a term.  The sums here are nested: along any path from a term to the total at most 2^12 additions (a block's
+    rows and groups, its slots, then the blocks'), each off by half a step."""
+    x = torch.randn(1, groups * C, device=DEV)
+    w, b = torch.ones(C, device=DEV), torch.zeros(C, device=DEV)
+    dy = torch.full_like(x, 0.7)
+    y, mean, rstd = lib.group_norm_fwd(x, groups, w, b, eps=EPS)
+    out = lib.group_norm_bwd(dy, x, groups, w, b, None, mean, rstd)
+    want = float(dy[0, 0]) * groups
+    assert float((out["dbias"].double() - want).abs().max()) <= 2 ** 12 * 2.0 ** -24 * want
+    xh = ((x.view(groups, C).double() - mean.view(groups, 1)) * rstd.view(groups, 1))
+    assert rel(y.view(groups, C), xh) <= 8 * 2.0 ** -24
+    terms = xh * float(dy[0, 0])
+    assert float((out["dweight"].double() - terms.sum(0)).abs().max() / terms.abs().sum(0).max()) <= (2 ** 12 + 8) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("rows,groups,C", [(2, 4_200_000, 3), (1, 66_000, 520)])
+def test_many_groups_with_weights_of_their_own(rows, groups, C):
+    s = make(rows, groups, C, torch.bfloat16, torch.float32)
+    check(call(s, groups, True), definition(s, groups, True), rows, C)
