@@ -1,6 +1,7 @@
 // Gated recurrence (one state per channel), forward, backward and single tokens.
 //
-// All rows of a call form one axis, cut where a sequence begins, in segments of 16 to 128 rows whatever the sequences' lengths.
+// All rows of a call form one axis, cut where a sequence begins, in segments whatever the sequences' lengths: of 16 to 96 rows where
+// there are places for all their warps, up to 192 where the channels alone take most of them, and a call of up to 128 rows is one.
 // A warp has a segment's rows and 64 channels, a lane two of them, eight rows in registers and the next eight on their way:
 //
 //   local pass      what a segment does to a state: h_out = h + A h_in (A, h), or h alone where a sequence begins in it
@@ -9,16 +10,18 @@
 //
 // Warps wait for no other, and every pass is as parallel as the call has rows and channels.  The walk goes through the segments
 // from the last, whose inputs the local pass has left in L2.
-// Gates are computed twice, and the passes are bound by instructions and their latency (57 and 64 per row and pair of channels, 66 %
+// Gates are computed twice, and the passes are bound by instructions and their latency (57 and 63 per row and pair of channels, 66 %
 // of the issue slots at 20 warps to an SM; four channels to a lane, a seventh fewer instructions at 12 or 16 warps, takes as long):
-// 4 sequences of 4096 x 2048 bfloat16 take 87 us, of which local pass 41, boundary 5, walk 43 (traffic of one pass: 39); one of
-// 16384 x 1024 takes 53.  One pass was slower: clusters of blocks that carry the state through shared memory took 104 and 109 us,
+// 4 sequences of 4096 x 2048 bfloat16 take 88 us, of which local pass 42, boundary 5, walk 44 (traffic of one pass: 39); one of
+// 16384 x 1024 takes 51 to 54.  Those are channels that remember long.  A warp with one whose exponent may reach 1/4 takes the general
+// form of a decay, ten instructions more: 97 us (local pass 48, walk 49) and 58.  One pass was slower: clusters of blocks that carry the state through shared memory took 104 and 109 us,
 // tiles that take what enters from the tiles before by flags in memory 154 and 93, both waiting for each other most of the time.
 // Where a sequence begins the link is cut by selection (never by a product with 0: a state of an earlier sequence
 // may be an infinity).
 //
 // The backward does the same from the end, with G_t = dy_t + a_{t+1} G_{t+1}: its local pass takes decay and dy alone, and its walk
-// has the state before every eighth row from the forward.
+// has the state before every eighth row from the forward.  4 x 4096 x 2048 takes 134 us, 147 in the general form (139 and 160
+// instructions per row and pair in the walk).
 #include "gated_scan.cuh"
 #include "tc_common.cuh"
 
@@ -471,8 +474,9 @@ int access_of(const GatedScanParams &p, bool bf16) {
     return (int)es;
 }
 
-// Rows of a segment, such that the warps of a pass (`warps` to an SM) all run at once, or in as few rounds as make segments of at most
-// MOST rows: a last round that is not full costs as much as a full one (B4 T4096 D2048: 90 us in segments of 64, 88 so).  Up to FEW
+// Rows of a segment, such that the warps of a pass (`warps` to an SM) all run at once, or in as few rounds as make segments of about
+// MOST rows (their number is rounded down, so where fewer than two or three fit beside one another a segment has up to 192 or 144):
+// a last round that is not full costs as much as a full one (B4 T4096 D2048: 90 us in segments of 64, 88 so).  Up to FEW
 // rows are one segment, a launch instead of three: calls of 128 x 512 back to back take 22 us for 30 (with gradients 58 for 77),
 // waited for one by one 43 for 40.
 constexpr int MOST = 96, FEW = 128;

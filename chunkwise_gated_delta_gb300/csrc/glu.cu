@@ -211,7 +211,9 @@ template <int SIDE, Mode MODE, int V> __global__ void __launch_bounds__(Tiles<SI
     }
 }
 
-// dg and du of saved products: V columns per thread.
+// dg and du of saved products: V columns per thread.  They are rounded to T, as operands of products on the tensor cores have to be: the
+// weights' gradients are then 2.3e-3 off in bfloat16, where one rounding of the exact result is 1.7e-3.  (What the rounding drops,
+// carried as a second operand, would double those products' work.)
 template <class T, int V> __global__ void __launch_bounds__(256) glu_slope_kernel(GluParams p) {
     const long long per = (p.F - 1) / V + 1, i = (long long)blockIdx.x * 256 + threadIdx.x;
     if (i >= per * p.M) return;
@@ -268,8 +270,8 @@ template <int SIDE, Mode MODE, int V> cudaError_t run_side(const GluParams &p, l
     }
     return cudaLaunchKernelEx(&cfg, glu_f32_kernel<SIDE, MODE, V>, p, blocks);
 }
-// Tiles of 128 where they fill the SMs' places (two to an SM) twice over, else tiles of 64 (eight), a cluster of blocks to each
-// of up to sixteen blocks to each where those leave half of the places empty and every block has eight steps.
+// Tiles of 128 where they fill the SMs' places (two to an SM) twice over, else tiles of 64 (eight), and a cluster of up to sixteen
+// blocks to each where those leave half of the places empty and every block has eight steps.
 template <Mode MODE> cudaError_t run_f32(const GluParams &p, cudaStream_t s) {
     constexpr bool DUAL = MODE == FWD || MODE == RECOMPUTE;
     const long long ms = MODE == DW ? p.F : p.M, ns = DUAL ? p.F : p.D, ks = MODE == DW ? p.M : MODE == DX ? 2LL * p.F : p.D;

@@ -534,8 +534,8 @@ __global__ void __launch_bounds__(256) glu_join_kernel(const float *part, int sp
         if (c + k < cols) to[k] = __float2bfloat16_rn(f[k]);
 }
 
-// Where the tiles of a product (or pairs of CTAs for them) leave half of the SMs idle, K is cut into parts that fill them, each of four
-// blocks of 64 at least.
+// Where the tiles of one of the backward's products (or pairs of CTAs for them) leave half of the SMs idle, K is cut into parts that fill
+// them, each of four blocks of 64 at least.  (The forward's is not cut: its epilogue needs whole sums.)
 struct Shape {
     bool pair;
     long long tm, tn, kbs;
