@@ -125,9 +125,9 @@ template <class T, int CP, int N, bool BACK> struct Ring {
 // ------------------------------------------------------------------------------------------ forward
 // A segment's effect is kept as A >= 0 and h; A = -1 says that the link is cut and h alone counts.  (A, h) of a pair of channels
 // lie together, rows of pairs are as wide as D rounded up to even.  A product of positive decays that underflows is kept at the smallest
-// normal number: an infinity that enters then leaves as one, not as 0 times infinity.  (Of a finite state that is 2^-126 of itself, where
+// positive number: an infinity that enters then leaves as one, not as 0 times infinity.  (Of a finite state that is 2^-149 of itself, where
 // a test for infinities in the chain of segments would take 2 us of the 51 of the long prompt.)
-constexpr float LEAST = 1.17549435e-38f;
+constexpr float LEAST = 1.40129846e-45f;
 __device__ __forceinline__ void store_segment(const GatedScanParams &p, const Where &w, f2 a, f2 h, bool cut) {
     float4 q;
     unpack2(a, q.x, q.z);

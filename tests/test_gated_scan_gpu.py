@@ -366,3 +366,14 @@ def test_an_infinite_state_stays_infinite(lens):
     keep[:first, [5, 7, 9, 11]] = False
     for k in ("y", "dx", "ddecay", "dgate"):
         assert torch.equal(got[k][0][keep], clean[k][0][keep]), k
+
+
+def test_a_huge_state_decays_to_nothing():
+    """A product of decays that underflows, times a state near the largest float32: what is left of it is below the rounding of what comes in."""
+    T, D = 400, 34
+    s = make(T, 1, D, torch.float32)
+    s["rate"][:] = 0.0
+    s["h0"][:] = 1e38
+    want = definition(s, [(0, T)])
+    y, ht = lib.gated_scan_fwd(*(s[k].view(1, T, D) for k in ("x", "decay", "gate")), s["rate"], s["h0"], scale=SCALE)
+    assert rel(ht, want["ht"]) <= STATE and rel(y[0, 200:], want["y"][200:]) <= STATE
